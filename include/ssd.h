@@ -371,6 +371,127 @@ ssd_status ssd_chunk_scan_fwd_noalloc(const void *X, const void *dt, const float
                                       int64_t nheads, int64_t headdim, int64_t dstate,
                                       int64_t ngroups, ssd_dtype dtype, void *stream);
 
+/*
+ * The decode step of a beam search: ssd_step_fused out of place, each row from
+ * the state of the beam it continues. Row b's state comes from row parent[b]
+ * of state_in (and its conv state from that row of conv_in); the updated ones
+ * go to row b of state_out (conv_out). A search keeps two states and swaps
+ * them, so reordering costs no pass of its own; the same call spreads the
+ * states that a prompt left over the beams.
+ *
+ *   state_in  (src_rows, nheads, headdim, dstate)  float32
+ *   state_out (batch, nheads, headdim, dstate)     float32   output
+ *   parent (batch)  int32, DEVICE memory: a row of state_in; one row may be
+ *          the parent of several. A value outside [0, src_rows) starts from
+ *          a zero state (and zero conv state), as at a sequence's start.
+ *   conv_in (src_rows, nheads * headdim, 3), conv_out (batch, ...)  dtype; both
+ *          NULL, as conv_b, where conv_w is NULL (no convolution)
+ * Other arguments, shapes, alignment and errors as ssd_step_fused. The inputs
+ * may not overlap the outputs (SSD_ERR_UNSUPPORTED for the states).
+ * With src_rows == 0 state_in and conv_in may be NULL.
+ */
+ssd_status ssd_step_beam(const float *state_in, float *state_out, const int32_t *parent, int64_t src_rows,
+                         const void *conv_in, void *conv_out, const void *x, const float *conv_w,
+                         const float *conv_b, const void *dt, const float *dt_bias, int dt_softplus,
+                         const float *A, const void *B, const void *C, const float *D, const void *z, void *y,
+                         int64_t batch, int64_t nheads, int64_t headdim, int64_t dstate, int64_t ngroups,
+                         ssd_dtype dtype, void *stream);
+
+/*
+ * Beam search's choice: of all beams k and vocabulary entries v of a sequence,
+ * the `beams` largest
+ *
+ *   cand[k, v] = scores[k] + logits[k, v] - log sum_u exp(logits[k, u])
+ *
+ * largest first, equal ones by the lowest k * vocab + v (within one beam the
+ * order is that of the logits). A beam with finished[k] has one candidate,
+ * (k, eos) at scores[k]; its logits are not read. What is not a number counts
+ * as -inf (a NaN logit or score; every candidate of a beam whose sum of
+ * exponentials is infinite or zero). Where fewer than `beams` candidates lie
+ * above -inf, the rest are the lowest at -inf.
+ *
+ *   logits (batch, beams, vocab)   dtype
+ *   scores (batch, beams)          float32   the beams' log-probabilities; -inf for a beam
+ *                                            not yet in use (all but the first of a new sequence)
+ *   finished (batch, beams)        uint8 (0 or not), or NULL: none
+ *   eos                            the end token, or -1 (then finished must be NULL)
+ *   next_scores (batch, beams)     float32   outputs: the scores chosen,
+ *   parent (batch, beams)          int32     the beam each continues, as a row of the
+ *                                            batch * beams states (ssd_step_beam's parent),
+ *   token (batch, beams)           int32     the token,
+ *   next_finished (batch, beams)   uint8     and whether it is finished; may be NULL
+ *
+ * Sums of exponentials are accumulated in 32 bits per 2048 logits and in 64
+ * across them; scores are compared in 64 bits. beams at most 16, vocab at most
+ * 2^28 (else SSD_ERR_UNSUPPORTED). The workspace is 256-byte aligned; the query
+ * returns (size_t)-1 for a shape that is not supported. With batch == 0 nothing is read.
+ */
+size_t ssd_beam_select_workspace_bytes(int64_t batch, int64_t beams, int64_t vocab);
+
+ssd_status ssd_beam_select(const void *logits, const float *scores, const uint8_t *finished, int64_t eos,
+                           float *next_scores, int32_t *parent, int32_t *token, uint8_t *next_finished,
+                           int64_t batch, int64_t beams, int64_t vocab, ssd_dtype dtype, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/*
+ * Root-mean-square norm of a layer's rows with the residual's addition:
+ *
+ *   h = x + residual;   y = h * weight / sqrt(mean(h^2) + eps)
+ *
+ * in fp32, the mean over each of `groups` equal pieces of the row by itself.
+ *
+ *   x (rows, dim)                  dtype
+ *   residual (rows, dim)           residual_dtype, or NULL: h = x
+ *   weight (dim)                   float32
+ *   residual_out (rows, dim)       residual_dtype  output: h, rounded once; may be
+ *                                  `residual` itself; NULL exactly where residual is
+ *   y (rows, dim)                  dtype           output, from the h before its rounding
+ *   rstd (rows, groups)            float32         output for the backward pass: 1 / sqrt(...); or NULL
+ *
+ * residual_dtype is dtype or, with bf16, also SSD_F32 (a residual stream kept
+ * in fp32); without a residual it is dtype. dim / groups at most 65536.
+ *
+ * ssd_rms_norm_mx writes y in 8 bits instead: q (rows, dim) holds e4m3 codes
+ * (OCP, largest 448) and scale (rows, dim / 32) one power of two for each 32
+ * of a row (e8m0: 2^(scale - 127)), the smallest not below 2^-127 that leaves
+ * the 32 within 448; y = q * scale. Codes are rounded to nearest even from
+ * the fp32 y. A block that holds an infinity or a NaN is NaN as a whole (scale
+ * 255, codes 0x7f). dim / groups must be a multiple of 32.
+ *
+ * ssd_mx_quantize writes any x (rows, dim) so (weights, once; activations).
+ */
+ssd_status ssd_rms_norm(const void *x, const void *residual, const float *weight, float eps, void *residual_out,
+                        void *y, float *rstd, int64_t rows, int64_t dim, int64_t groups, ssd_dtype dtype,
+                        ssd_dtype residual_dtype, void *stream);
+
+ssd_status ssd_rms_norm_mx(const void *x, const void *residual, const float *weight, float eps, void *residual_out,
+                           uint8_t *q, uint8_t *scale, int64_t rows, int64_t dim, int64_t groups, ssd_dtype dtype,
+                           ssd_dtype residual_dtype, void *stream);
+
+ssd_status ssd_mx_quantize(const void *x, uint8_t *q, uint8_t *scale, int64_t rows, int64_t dim, ssd_dtype dtype,
+                           void *stream);
+
+/*
+ * Gradients of ssd_rms_norm. With hh = h * rstd and g = dy * weight:
+ *   dh = rstd (g - hh mean(g hh)) + d_residual_out,  which is both dx and d_residual
+ *   dweight = sum over rows of dy hh
+ *
+ *   dy (rows, dim) dtype;  h (rows, dim) residual_dtype: residual_out (x where there was none);
+ *   rstd: from the forward;  d_residual_out (rows, dim) residual_dtype, or NULL (zero)
+ *   dx (rows, dim) dtype       output
+ *   d_residual (rows, dim)     output in residual_dtype where that is not dtype, or NULL;
+ *                              where it is, dx serves for both and d_residual must be NULL
+ *   dweight (dim) float32      output, summed in a fixed order
+ * The workspace is 256-byte aligned. With rows == 0, dweight = 0.
+ */
+size_t ssd_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, int64_t groups, ssd_dtype dtype,
+                                        ssd_dtype residual_dtype);
+
+ssd_status ssd_rms_norm_bwd(const void *dy, const void *h, const float *weight, const float *rstd,
+                            const void *d_residual_out, void *dx, void *d_residual, float *dweight, int64_t rows,
+                            int64_t dim, int64_t groups, ssd_dtype dtype, ssd_dtype residual_dtype, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

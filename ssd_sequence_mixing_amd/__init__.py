@@ -19,6 +19,8 @@ __all__ = [
     "ssd_chunk_scan_fwd_varlen", "ssd_chunk_scan_fwd_gated", "ssd_step_gated",
     "ssd_chunk_scan_bwd_workspace_bytes", "ssd_chunk_scan_bwd", "ssd_chunk_scan_fwd_fused",
     "ssd_chunk_scan_fwd_noalloc", "ssd_step_fused", "NOALLOC_SCRATCH_BYTES", "EXPORTS",
+    "ssd_step_beam", "ssd_beam_select_workspace_bytes", "ssd_beam_select", "ssd_rms_norm", "ssd_rms_norm_mx",
+    "ssd_mx_quantize", "ssd_rms_norm_bwd_workspace_bytes", "ssd_rms_norm_bwd",
 ]
 
 SSD_F32 = 0
@@ -32,7 +34,9 @@ EXPORTS = ("ssd_status_string", "ssd_chunk_scan_fwd_workspace_bytes", "ssd_chunk
            "ssd_chunk_scan_prepare", "ssd_chunk_scan_walk", "ssd_step",
            "ssd_chunk_scan_varlen_workspace_bytes", "ssd_chunk_scan_fwd_varlen",
            "ssd_chunk_scan_fwd_gated", "ssd_step_gated", "ssd_chunk_scan_bwd_workspace_bytes",
-           "ssd_chunk_scan_bwd", "ssd_chunk_scan_fwd_fused", "ssd_chunk_scan_fwd_noalloc", "ssd_step_fused")
+           "ssd_chunk_scan_bwd", "ssd_chunk_scan_fwd_fused", "ssd_chunk_scan_fwd_noalloc", "ssd_step_fused",
+           "ssd_step_beam", "ssd_beam_select_workspace_bytes", "ssd_beam_select", "ssd_rms_norm",
+           "ssd_rms_norm_mx", "ssd_mx_quantize", "ssd_rms_norm_bwd_workspace_bytes", "ssd_rms_norm_bwd")
 
 # SSD_NOALLOC_SCRATCH_BYTES: the static workspace of ssd_chunk_scan_fwd_noalloc.
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -123,6 +127,19 @@ def load():
     lib.ssd_chunk_scan_bwd.restype = ctypes.c_int
     lib.ssd_chunk_scan_bwd.argtypes = ([_V] * 6 + [_I] + [_V] * 10 + [_I] * 6 +
                                        [ctypes.c_int, _V, ctypes.c_size_t, _V])
+    _F, _E, _S = ctypes.c_float, ctypes.c_int, ctypes.c_size_t
+    for name, res, args in (
+            ("ssd_step_beam", _E, [_V, _V, _V, _I] + [_V] * 6 + [_V, _E] + [_V] * 6 + [_I] * 5 + [_E, _V]),
+            ("ssd_beam_select_workspace_bytes", _S, [_I] * 3),
+            ("ssd_beam_select", _E, [_V] * 3 + [_I] + [_V] * 4 + [_I] * 3 + [_E, _V, _S, _V]),
+            ("ssd_rms_norm", _E, [_V] * 3 + [_F] + [_V] * 3 + [_I] * 3 + [_E, _E, _V]),
+            ("ssd_rms_norm_mx", _E, [_V] * 3 + [_F] + [_V] * 3 + [_I] * 3 + [_E, _E, _V]),
+            ("ssd_mx_quantize", _E, [_V] * 3 + [_I] * 2 + [_E, _V]),
+            ("ssd_rms_norm_bwd_workspace_bytes", _S, [_I] * 3 + [_E] * 2),
+            ("ssd_rms_norm_bwd", _E, [_V] * 8 + [_I] * 3 + [_E, _E, _V, _S, _V]),
+    ):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = res, args
     _lib = lib
     return lib
 
@@ -533,6 +550,211 @@ def ssd_chunk_scan_bwd(X, dt, A, B, C, D, chunk: int, dY, *, initial_state=None,
     if st != 0:
         raise SSDError(st, "ssd_chunk_scan_bwd")
     return dX, ddt, dA, dB, dC, dD, dinit
+
+
+def _here(*tensors) -> None:
+    """Raises ValueError unless every tensor given is on the current GPU: the
+    stream a call goes to is this device's."""
+    import torch
+    now = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != now:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{now}")
+
+
+def _new(shape, dtype, device, stream):
+    """An output or workspace for a call on `stream`. It is allocated as that
+    stream's memory, so that it is not handed out again before the call is done."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _sized(name: str, n: int) -> int:
+    if n == ctypes.c_size_t(-1).value:
+        raise SSDError(3, name)
+    return int(n)
+
+
+def _nbytes(workspace) -> int:
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def _rows_dim(name: str, t):
+    """(product of the leading dimensions, last dimension) of a tensor whose rows lie in its last one."""
+    if t.dim() < 1 or t.shape[-1] == 0:
+        raise ValueError(f"{name} must have a last dimension of at least 1")
+    return t.numel() // t.shape[-1], t.shape[-1]
+
+
+def ssd_step_beam(state_in, state_out, parent, x, dt, A, B, C, D, *, conv_in=None, conv_out=None, conv_w=None,
+                  conv_b=None, dt_bias=None, dt_softplus: int = 0, z=None, y=None, stream=None):
+    """The decode step of a beam search: row b of state_out (batch, H, P, N) fp32 is the step from row parent[b]
+    (int32, on the GPU) of state_in (src_rows, H, P, N); a parent outside it starts from a zero state. With conv_w
+    (H*P, 4) the layer's convolution runs on x, and conv_in (src_rows, H*P, 3) is reordered and shifted into
+    conv_out (batch, H*P, 3). Other arguments as ssd_step_fused. Returns y."""
+    import torch
+    lib = load()
+    _check_step(state_out, x, dt, A, B, C, D, y=y, z=z)
+    bsz, H, P, N = state_out.shape
+    G = B.shape[1]
+    if state_in.dim() != 4:
+        raise ValueError("state_in must be (src_rows, H, P, N)")
+    src = state_in.shape[0]
+    _chk("state_in", state_in, (src, H, P, N), torch.float32)
+    _chk("parent", parent, (bsz,), torch.int32)
+    _chk("conv_in", conv_in, (src, H * P, 3), x.dtype)
+    _chk("conv_out", conv_out, (bsz, H * P, 3), x.dtype)
+    _chk("conv_w", conv_w, (H * P, 4), torch.float32)
+    _chk("conv_b", conv_b, (H * P,), torch.float32)
+    _chk("dt_bias", dt_bias, (H,), torch.float32)
+    _here(state_in, state_out, parent, x, dt, A, B, C, D, conv_in, conv_out, conv_w, conv_b, dt_bias, z, y)
+    if y is None:
+        y = _new(x.shape, x.dtype, x.device, stream)
+    st = lib.ssd_step_beam(_ptr(state_in), _ptr(state_out), _ptr(parent), src, _ptr(conv_in), _ptr(conv_out), _ptr(x),
+                           _ptr(conv_w), _ptr(conv_b), _ptr(dt), _ptr(dt_bias), int(dt_softplus), _ptr(A), _ptr(B),
+                           _ptr(C), _ptr(D), _ptr(z), _ptr(y), bsz, H, P, N, G, _dtype_code(x), _stream(stream))
+    if st != 0:
+        raise SSDError(st, "ssd_step_beam")
+    return y
+
+
+def ssd_beam_select_workspace_bytes(batch, beams, vocab) -> int:
+    return _sized("ssd_beam_select_workspace_bytes", load().ssd_beam_select_workspace_bytes(batch, beams, vocab))
+
+
+def ssd_beam_select(logits, scores, *, finished=None, eos: int = -1, workspace=None, stream=None):
+    """Beam search's choice: logits (batch, beams, vocab) bf16 or fp32, scores (batch, beams) fp32
+    log-probabilities (-inf for a beam not in use), finished (batch, beams) bool or uint8, or None.
+    Returns (next_scores fp32, parent int32, token int32, next_finished bool), each (batch, beams); parent is a
+    row of the batch * beams states, as ssd_step_beam takes it."""
+    import torch
+    lib = load()
+    if logits.dim() != 3:
+        raise ValueError("logits must be (batch, beams, vocab)")
+    bsz, K, V = logits.shape
+    _chk("scores", scores, (bsz, K), torch.float32)
+    if finished is not None:
+        _chk("finished", finished, (bsz, K), torch.bool if finished.dtype == torch.bool else torch.uint8)
+    code = _dtype_code(logits)
+    _here(logits, scores, finished, workspace)
+    if workspace is None:
+        workspace = _new((ssd_beam_select_workspace_bytes(bsz, K, V),), torch.uint8, logits.device, stream)
+    out = _new((bsz, K), torch.float32, logits.device, stream)
+    parent = _new((bsz, K), torch.int32, logits.device, stream)
+    token = _new((bsz, K), torch.int32, logits.device, stream)
+    done = _new((bsz, K), torch.bool, logits.device, stream)
+    st = lib.ssd_beam_select(_ptr(logits), _ptr(scores), _ptr(finished), int(eos), _ptr(out), _ptr(parent),
+                             _ptr(token), _ptr(done), bsz, K, V, code, _ptr(workspace), _nbytes(workspace),
+                             _stream(stream))
+    if st != 0:
+        raise SSDError(st, "ssd_beam_select")
+    return out, parent, token, done
+
+
+def _check_norm(x, weight, residual, residual_out):
+    import torch
+    rows, dim = _rows_dim("x", x)
+    code = _dtype_code(x)
+    _chk("weight", weight, (dim,), torch.float32)
+    rcode = code
+    if residual is not None:
+        rcode = _dtype_code(residual)
+        _chk("residual", residual, x.shape, residual.dtype)
+        _chk("residual_out", residual_out, x.shape, residual.dtype)
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    return rows, dim, code, rcode
+
+
+def ssd_rms_norm(x, weight, eps: float, *, residual=None, groups: int = 1, residual_out=None, y=None,
+                 want_rstd: bool = False, stream=None):
+    """y = h * weight / sqrt(mean(h^2) + eps), h = x + residual, over the last dimension of x (or each of `groups`
+    equal pieces of it). residual: x's type or fp32. Returns (y, residual_out, rstd): residual_out is h in
+    residual's type (None without one; may be passed as residual itself), rstd (rows..., groups) fp32 for the
+    backward pass, or None."""
+    import torch
+    lib = load()
+    rows, dim, code, rcode = _check_norm(x, weight, residual, residual_out)
+    _chk("y", y, x.shape, x.dtype)
+    _here(x, weight, residual, residual_out, y)
+    if y is None:
+        y = _new(x.shape, x.dtype, x.device, stream)
+    if residual is not None and residual_out is None:
+        residual_out = _new(x.shape, residual.dtype, x.device, stream)
+    rstd = _new((*x.shape[:-1], groups), torch.float32, x.device, stream) if want_rstd else None
+    st = lib.ssd_rms_norm(_ptr(x), _ptr(residual), _ptr(weight), float(eps), _ptr(residual_out), _ptr(y), _ptr(rstd),
+                          rows, dim, int(groups), code, rcode, _stream(stream))
+    if st != 0:
+        raise SSDError(st, "ssd_rms_norm")
+    return y, residual_out, rstd
+
+
+def ssd_rms_norm_mx(x, weight, eps: float, *, residual=None, groups: int = 1, residual_out=None, stream=None):
+    """ssd_rms_norm with an 8-bit output. Returns (q, scale, residual_out): q float8_e4m3fn like x, scale
+    float8_e8m0fnu (..., dim / 32), a power of two for each 32 values of a row."""
+    import torch
+    lib = load()
+    rows, dim, code, rcode = _check_norm(x, weight, residual, residual_out)
+    _here(x, weight, residual, residual_out)
+    q = _new(x.shape, torch.float8_e4m3fn, x.device, stream)
+    scale = _new((*x.shape[:-1], dim // 32), torch.float8_e8m0fnu, x.device, stream)
+    if residual is not None and residual_out is None:
+        residual_out = _new(x.shape, residual.dtype, x.device, stream)
+    st = lib.ssd_rms_norm_mx(_ptr(x), _ptr(residual), _ptr(weight), float(eps), _ptr(residual_out), _ptr(q),
+                             _ptr(scale), rows, dim, int(groups), code, rcode, _stream(stream))
+    if st != 0:
+        raise SSDError(st, "ssd_rms_norm_mx")
+    return q, scale, residual_out
+
+
+def ssd_mx_quantize(x, *, stream=None):
+    """x (..., dim), dim a multiple of 32, in 8 bits: (q float8_e4m3fn, scale float8_e8m0fnu), as ssd_rms_norm_mx."""
+    import torch
+    lib = load()
+    rows, dim = _rows_dim("x", x)
+    code = _dtype_code(x)
+    _here(x)
+    q = _new(x.shape, torch.float8_e4m3fn, x.device, stream)
+    scale = _new((*x.shape[:-1], dim // 32), torch.float8_e8m0fnu, x.device, stream)
+    st = lib.ssd_mx_quantize(_ptr(x), _ptr(q), _ptr(scale), rows, dim, code, _stream(stream))
+    if st != 0:
+        raise SSDError(st, "ssd_mx_quantize")
+    return q, scale
+
+
+def ssd_rms_norm_bwd_workspace_bytes(rows, dim, groups, dtype: int, residual_dtype: int) -> int:
+    return _sized("ssd_rms_norm_bwd_workspace_bytes",
+                  load().ssd_rms_norm_bwd_workspace_bytes(rows, dim, groups, dtype, residual_dtype))
+
+
+def ssd_rms_norm_bwd(dy, h, weight, rstd, *, d_residual_out=None, groups: int = 1, workspace=None, stream=None):
+    """Gradients of ssd_rms_norm: dy like y, h its residual_out (its x, where it had no residual), rstd from it,
+    d_residual_out like h or None. Returns (dx, d_residual, dweight): dx in dy's type; d_residual is the same
+    gradient in h's type where that differs, else None (dx serves for both); dweight fp32."""
+    import torch
+    lib = load()
+    rows, dim = _rows_dim("dy", dy)
+    code, rcode = _dtype_code(dy), _dtype_code(h)
+    _chk("h", h, dy.shape, h.dtype)
+    _chk("weight", weight, (dim,), torch.float32)
+    _chk("rstd", rstd, (*dy.shape[:-1], groups), torch.float32)
+    _chk("d_residual_out", d_residual_out, dy.shape, h.dtype)
+    _here(dy, h, weight, rstd, d_residual_out, workspace)
+    need = ssd_rms_norm_bwd_workspace_bytes(rows, dim, int(groups), code, rcode)
+    if workspace is None and need:
+        workspace = _new((need,), torch.uint8, dy.device, stream)
+    dx = _new(dy.shape, dy.dtype, dy.device, stream)
+    dh = _new(dy.shape, h.dtype, dy.device, stream) if rcode != code else None
+    dw = _new((dim,), torch.float32, dy.device, stream)
+    st = lib.ssd_rms_norm_bwd(_ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(d_residual_out), _ptr(dx), _ptr(dh),
+                              _ptr(dw), rows, dim, int(groups), code, rcode, _ptr(workspace), _nbytes(workspace),
+                              _stream(stream))
+    if st != 0:
+        raise SSDError(st, "ssd_rms_norm_bwd")
+    return dx, dh, dw
 
 
 def raw_call(name: str, *args) -> int:

@@ -243,7 +243,15 @@ ssd_status fwd_impl(const void *X, const float *conv_w, const float *conv_b, con
 ssd_status step_impl(float *state, void *conv_state, const void *x, const float *conv_w, const float *conv_b,
                      const void *dt, const float *dt_bias, int dt_softplus, const float *A, const void *B,
                      const void *C, const float *D, const void *z, void *y, int64_t batch, int64_t nheads,
-                     int64_t headdim, int64_t dstate, int64_t ngroups, ssd_dtype dtype, void *stream);
+                     int64_t headdim, int64_t dstate, int64_t ngroups, ssd_dtype dtype, void *stream,
+                     const int32_t *parent = nullptr, const float *state_in = nullptr,
+                     const void *conv_in = nullptr, int64_t src_rows = 0);
+
+// Whether [a, a + na) and [b, b + nb) share a byte (a NULL one does not).
+bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+    const uintptr_t pa = (uintptr_t)a, pb = (uintptr_t)b;
+    return a && b && na > 0 && nb > 0 && pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
+}
 
 }  // namespace
 
@@ -424,6 +432,21 @@ ssd_status ssd_step_fused(float *state, void *conv_state, const void *x, const f
                      nheads, headdim, dstate, ngroups, dtype, stream);
 }
 
+ssd_status ssd_step_beam(const float *state_in, float *state_out, const int32_t *parent, int64_t src_rows,
+                         const void *conv_in, void *conv_out, const void *x, const float *conv_w,
+                         const float *conv_b, const void *dt, const float *dt_bias, int dt_softplus,
+                         const float *A, const void *B, const void *C, const float *D, const void *z, void *y,
+                         int64_t batch, int64_t nheads, int64_t headdim, int64_t dstate, int64_t ngroups,
+                         ssd_dtype dtype, void *stream) {
+    if (src_rows < 0 || src_rows > (int64_t)INT32_MAX) return SSD_ERR_SHAPE;
+    if (batch != 0 && (!parent || (src_rows > 0 && !state_in))) return SSD_ERR_NULL;
+    if (batch != 0 && conv_w && (!conv_out || (src_rows > 0 && !conv_in))) return SSD_ERR_NULL;
+    if (!conv_w && (conv_in || conv_out || conv_b)) return SSD_ERR_NULL;
+    if (!aligned16(state_in) || !aligned16(conv_in) || !aligned16(parent)) return SSD_ERR_ALIGN;
+    return step_impl(state_out, conv_out, x, conv_w, conv_b, dt, dt_bias, dt_softplus, A, B, C, D, z, y, batch,
+                     nheads, headdim, dstate, ngroups, dtype, stream, parent, state_in, conv_in, src_rows);
+}
+
 }  // extern "C"
 
 namespace {
@@ -431,7 +454,8 @@ namespace {
 ssd_status step_impl(float *state, void *conv_state, const void *x, const float *conv_w, const float *conv_b,
                      const void *dt, const float *dt_bias, int dt_softplus, const float *A, const void *B,
                      const void *C, const float *D, const void *z, void *y, int64_t batch, int64_t nheads,
-                     int64_t headdim, int64_t dstate, int64_t ngroups, ssd_dtype dtype, void *stream) {
+                     int64_t headdim, int64_t dstate, int64_t ngroups, ssd_dtype dtype, void *stream,
+                     const int32_t *parent, const float *state_in, const void *conv_in, int64_t src_rows) {
     if (dt_softplus < 0 || dt_softplus > 2) return SSD_ERR_UNSUPPORTED;
     if (batch != 0 && (!state || !x || !dt || !A || !B || !C || !D || !y)) return SSD_ERR_NULL;
     if (!valid_dtype((int)dtype)) return SSD_ERR_UNSUPPORTED;
@@ -447,7 +471,16 @@ ssd_status step_impl(float *state, void *conv_state, const void *x, const float 
     if (batch > (int64_t)UINT32_MAX || nheads > 65536 || headdim > 4096) return SSD_ERR_UNSUPPORTED;
     const int64_t rows = batch * nheads * headdim;
     if (rows > (int64_t)UINT32_MAX) return SSD_ERR_UNSUPPORTED;
+    if (parent) {
+        // a parent's state may be read after another row's has been written
+        const int64_t per = nheads * headdim, es = esize(dtype);
+        if (src_rows > INT64_MAX / 4 / (per * dstate)) return SSD_ERR_UNSUPPORTED;
+        if (overlap(state_in, src_rows * per * dstate * 4, state, batch * per * dstate * 4) ||
+            overlap(conv_in, src_rows * per * 3 * es, conv_state, batch * per * 3 * es))
+            return SSD_ERR_UNSUPPORTED;
+    }
     ssd::StepArgs a;
+    a.parent = parent; a.state_in = state_in; a.conv_in = conv_in; a.src_rows = src_rows;
     a.state = state; a.x = x; a.dt = dt; a.B = B; a.C = C; a.A = A; a.D = D; a.y = y;
     a.batch = batch; a.H = nheads; a.P = headdim; a.N = dstate; a.G = ngroups; a.dtype = dtype;
     a.dt_bias = dt_bias; a.softplus = dt_softplus; a.z = z;

@@ -1,0 +1,342 @@
+// Beam search's choice of the next tokens for gfx950: over all beams k and
+// vocabulary entries v of a sequence, the `beams` largest
+//
+//   cand[k, v] = score[k] + logits[k, v] - log sum_u exp(logits[k, u])
+//
+// in order, equal ones by the lowest k V + v. A finished beam has the one
+// candidate (k, eos) at score[k]; whatever is not a number counts as -inf.
+//
+// Bound: HBM, one read of the logits. k_beam_top gives each wavefront 2048
+// logits of a row, which stay in registers: it sums their exponentials and
+// finds their `beams` largest. Within a row cand orders as the logits do, so
+// that needs no sum. A filter leaves few to be sorted: the beams-th largest of
+// the 64 lanes' own maxima is a lower bound on the beams-th largest value, and
+// of 2048 values about 18 reach it at 16 beams. k_beam_pick (one work-group
+// per sequence, a wavefront per beam) merges a row's lists the same way,
+// forms the scores and merges the beams.
+//
+// The sums of exponentials are fp32 within a wavefront and 64-bit across a
+// row, and scores are compared in 64 bits, so that two candidates change places only
+// where they are closer than the sums' own error (~1e-8 relative).
+#include "ssd_common.h"
+#include "ssd_internal.h"
+
+namespace ssd {
+
+constexpr int kTile = 2048;        // logits a wavefront holds at a time, 32 a lane
+constexpr int kPerLane = kTile / 64;
+
+// Order-preserving bits of a float (no NaN): larger floats, larger bits; 0 is below all.
+__device__ __forceinline__ uint32_t ord32(float v) {
+    const uint32_t u = __float_as_uint(v);
+    return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_ord32(uint32_t o) {
+    return __uint_as_float((o & 0x80000000u) ? (o ^ 0x80000000u) : ~o);
+}
+constexpr uint32_t kNone = 0x007fffffu;  // ord32(-inf)
+// Larger value first, then lower index: one 64-bit comparison. 0 is no entry.
+__device__ __forceinline__ uint64_t key_of(uint32_t ord, uint32_t idx) { return ((uint64_t)ord << 32) | (uint32_t)~idx; }
+
+__device__ __forceinline__ uint32_t xor32(uint32_t v, int m) { return (uint32_t)__shfl_xor((int)v, m, 64); }
+__device__ __forceinline__ uint64_t xor64(uint64_t v, int m) {
+    return ((uint64_t)xor32((uint32_t)(v >> 32), m) << 32) | xor32((uint32_t)v, m);
+}
+
+// Bitonic sort of one value per lane, largest in lane 0.
+template <typename U>
+__device__ __forceinline__ U sort_desc(U v, int lane) {
+#pragma unroll
+    for (int k = 2; k <= 64; k <<= 1) {
+#pragma unroll
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            U o;
+            if constexpr (sizeof(U) == 8) o = xor64(v, j); else o = xor32(v, j);
+            const bool keep_max = ((lane & k) == 0) == ((lane & j) == 0);
+            v = (keep_max == (v > o)) ? v : o;
+        }
+    }
+    return v;
+}
+
+__device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        const uint64_t o = xor64(v, off);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+
+// The sorted list in lanes 0 .. K-1 and the n <= 64 - K keys in buf, merged.
+__device__ __forceinline__ uint64_t merge_into(uint64_t best, const uint64_t *buf, int n, int K, int lane) {
+    uint64_t v = lane < K ? best : 0;
+    if (lane >= K && lane - K < n) v = buf[lane - K];
+    return sort_desc(v, lane);
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_beam_top(BeamArgs a) {
+    constexpr int VE = 16 / (int)sizeof(T);    // logits per 16-byte load
+    constexpr int NL = kPerLane / VE;          // loads per lane and tile
+    __shared__ uint64_t bufs[4][64];
+    const int lane = threadIdx.x & 63;
+    uint64_t *buf = bufs[threadIdx.x >> 6];
+    const int64_t gl = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t row = gl / a.lists;
+    const int li = (int)(gl - row * a.lists);
+    if (row >= a.rows || (a.finished && a.finished[row])) return;
+    const int K = a.beams, V = a.V;
+    const T *rp = reinterpret_cast<const T *>(a.logits) + row * V;
+    uint64_t best = 0;
+    float M = -INFINITY, S = 0.f;
+    for (int j = 0; j < a.tiles; ++j) {
+        const int base = (li * a.tiles + j) * kTile;
+        if (base >= V) break;
+        float v[kPerLane];
+        if (base + kTile <= V) {
+            // a row of an odd number of logits begins at any multiple of its type. The split goes by
+            // the place in the row all the same, so that equal rows have bit-equal sums (and tie)
+            typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+            u32x4 raw[NL];
+#pragma unroll
+            for (int l = 0; l < NL; ++l) raw[l] = *reinterpret_cast<const u32x4_any *>(rp + base + (l * 64 + lane) * VE);
+#pragma unroll
+            for (int e = 0; e < kPerLane; ++e) {
+                float f;
+                if constexpr (sizeof(T) == 2) {
+                    const uint32_t w = raw[e / VE][(e % VE) >> 1];
+                    f = __uint_as_float((e & 1) ? (w & 0xffff0000u) : (w << 16));
+                } else {
+                    const uint32_t w = raw[e / VE][e % VE];
+                    f = __uint_as_float(w);
+                }
+                v[e] = f == f ? f : -INFINITY;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < kPerLane; ++e) {
+                const int i = base + ((e / VE) * 64 + lane) * VE + e % VE;
+                const float f = i < V ? (float)rp[i] : -INFINITY;
+                v[e] = f == f ? f : -INFINITY;
+            }
+        }
+        float lm = v[0];
+#pragma unroll
+        for (int e = 1; e < kPerLane; ++e) lm = fmaxf(lm, v[e]);
+        float wm = lm;
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) wm = fmaxf(wm, __shfl_xor(wm, off, 64));
+        const float Mn = fmaxf(M, wm);
+        if (Mn > -INFINITY) {  // per lane: a share of the row's sum, relative to Mn
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < kPerLane; ++e) s += fast_exp2((v[e] - Mn) * kLog2e);
+            S = (M > -INFINITY ? S * fast_exp2((M - Mn) * kLog2e) : 0.f) + s;
+            M = Mn;
+        }
+        // lower bound on the K-th largest of the tile and of the list so far
+        uint32_t bound = (uint32_t)__builtin_amdgcn_readlane((int)sort_desc(ord32(lm), lane), K - 1);
+        const uint32_t kth = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(best >> 32), K - 1);
+        bound = bound > kth ? bound : kth;
+        bound = bound > kNone ? bound : kNone + 1;  // -inf is no candidate
+        int n = 0;
+#pragma unroll
+        for (int e = 0; e < kPerLane; ++e) {
+            const int i = base + ((e / VE) * 64 + lane) * VE + e % VE;
+            const bool in = i < V && ord32(v[e]) >= bound;
+            const uint64_t mask = __ballot(in);
+            if (mask) {
+                const int at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+                if (in && at < 64 - K) buf[at] = key_of(ord32(v[e]), (uint32_t)i);
+                n += __popcll(mask);
+            }
+        }
+        if (n <= 64 - K) {
+            __builtin_amdgcn_wave_barrier();
+            best = merge_into(best, buf, n, K, lane);
+            __builtin_amdgcn_wave_barrier();
+        } else {
+            // many equal or ordered logits: the K largest one by one
+            uint64_t fresh = 0, last = ~0ull;
+            for (int k = 0; k < K; ++k) {
+                uint64_t top = 0;
+#pragma unroll
+                for (int e = 0; e < kPerLane; ++e) {
+                    const int i = base + ((e / VE) * 64 + lane) * VE + e % VE;
+                    const uint64_t q = (i < V) ? key_of(ord32(v[e]), (uint32_t)i) : 0;
+                    if (q < last && q > top) top = q;
+                }
+                last = wave_max64(top);
+                if (lane == k) fresh = last;
+                if (last == 0) break;
+            }
+            if (lane < K) buf[lane] = fresh;
+            __builtin_amdgcn_wave_barrier();
+            best = merge_into(best, buf, K, K, lane);
+            __builtin_amdgcn_wave_barrier();
+        }
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) S += __shfl_xor(S, off, 64);
+    if (lane < K) a.keys[gl * K + lane] = best;
+    if (lane == 0) a.sums[gl] = make_float2(M, S);
+}
+
+template <typename T>
+__global__ __launch_bounds__(1024) void k_beam_pick(BeamArgs a) {
+    constexpr int kMost = 16;  // beams
+    __shared__ uint64_t bufs[kMost][64];
+    __shared__ double sc[kMost][kMost];
+    __shared__ uint32_t ix[kMost][kMost];
+    __shared__ int cnt[kMost];
+    __shared__ int live[kMost];   // 1: the row's candidates are its logits; 2: finished; 0: none
+    const int lane = threadIdx.x & 63, k = threadIdx.x >> 6;
+    const int K = a.beams, V = a.V;
+    const int64_t b = blockIdx.x, row = b * K + k;
+    const float score = a.scores[row];
+    const bool alive = score > -INFINITY;  // false for NaN too
+    if (a.finished && a.finished[row]) {
+        if (lane == 0) {
+            live[k] = 2;
+            cnt[k] = alive ? 1 : 0;
+            sc[k][0] = (double)score;
+            ix[k][0] = (uint32_t)a.eos;
+        }
+    } else {
+        // log-sum-exp of the row
+        const bool in = lane < a.lists;
+        float2 ms = make_float2(-INFINITY, 0.f);
+        if (in) ms = a.sums[row * a.lists + lane];
+        const float m = ms.x, s = ms.y;
+        float M = m;
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, 64));
+        double S = m > -INFINITY ? (double)s * exp((double)m - (double)M) : 0.0;
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) S += __shfl_xor(S, off, 64);
+        const double lse = (double)M + log(S);
+        const bool ok = alive && lse - lse == 0.0;  // a finite sum
+        uint64_t best = 0;
+        if (ok) {
+            uint64_t key[kMost];
+#pragma unroll
+            for (int r = 0; r < kMost; ++r) key[r] = (in && r < K) ? a.keys[(row * a.lists + lane) * K + r] : 0;
+            const uint64_t heads = sort_desc(key[0], lane);
+            const uint64_t bound = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(heads >> 32), K - 1) << 32) |
+                                   (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)heads, K - 1);
+            int n = 0;
+#pragma unroll
+            for (int r = 0; r < kMost; ++r) {
+                // keys differ, so at most K - 1 lists and the bound's own reach it
+                const bool hit = key[r] && key[r] >= bound;
+                const uint64_t mask = __ballot(hit);
+                const int c = __popcll(mask);
+                if (c) {
+                    if (n + c > 64 - K) {
+                        __builtin_amdgcn_wave_barrier();
+                        best = merge_into(best, bufs[k], n, K, lane);
+                        __builtin_amdgcn_wave_barrier();
+                        n = 0;
+                    }
+                    const int at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+                    if (hit) bufs[k][at] = key[r];
+                    n += c;
+                }
+            }
+            __builtin_amdgcn_wave_barrier();
+            best = merge_into(best, bufs[k], n, K, lane);
+        }
+        const float l = from_ord32((uint32_t)(best >> 32));
+        const bool use = ok && lane < K && best && l > -INFINITY;
+        if (use) {
+            sc[k][lane] = (double)score + ((double)l - lse);
+            ix[k][lane] = (uint32_t)~(uint32_t)best;
+        }
+        const uint64_t used = __ballot(use);  // a leading run of lanes: the list is sorted
+        if (lane == 0) {
+            cnt[k] = __popcll(used);
+            live[k] = ok ? 1 : 0;
+        }
+    }
+    __syncthreads();
+    if (k != 0) return;
+    // the beams' lists, merged: lane j holds the head of beam j's
+    int at = 0, got = 0;
+    double hs = -INFINITY;
+    uint32_t hi = 0xffffffffu;  // k V + v; beams in order, so equal scores go to the lower lane's
+    const int mine = lane < K ? cnt[lane] : 0;
+    if (mine > 0) hs = sc[lane][0], hi = ix[lane][0];
+    for (; got < K; ++got) {
+        double s = hs;
+        uint32_t who = (mine > at) ? (uint32_t)lane : 0xffffu;
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) {
+            const double os = __shfl_xor(s, off, 16);
+            const uint32_t ow = (uint32_t)__shfl_xor((int)who, off, 16);
+            const bool take = ow != 0xffffu && (who == 0xffffu || os > s || (os == s && ow < who));
+            s = take ? os : s;
+            who = take ? ow : who;
+        }
+        who = (uint32_t)__builtin_amdgcn_readfirstlane((int)who);
+        if (who == 0xffffu) break;
+        if (lane == (int)who) {
+            const int64_t o = b * K + got;
+            a.out_scores[o] = (float)hs;
+            a.parent[o] = (int)(b * K + lane);
+            a.token[o] = (int)hi;
+            if (a.out_finished)
+                a.out_finished[o] = ((a.finished && a.finished[b * K + lane]) || (int)hi == a.eos) ? 1 : 0;
+            ++at;
+            if (at < mine) hs = sc[lane][at], hi = ix[lane][at];
+        }
+    }
+    // fewer candidates than beams: the lowest of those at -inf. Fewer than K
+    // are not, so the first 2 K positions hold enough.
+    for (int64_t i0 = 0; got < K && i0 < (int64_t)K * V; i0 += 64) {
+        const int64_t i = i0 + lane;
+        bool none = false;
+        if (i < (int64_t)K * V) {
+            const int kk = (int)(i / V), v = (int)(i - (int64_t)kk * V);
+            if (cnt[kk] == 0) none = true;
+            else if (live[kk] == 2) none = v != a.eos;
+            else {
+                const float f = (float)reinterpret_cast<const T *>(a.logits)[(b * K + kk) * V + v];
+                none = !(f > -INFINITY);
+            }
+        }
+        const uint64_t mask = __ballot(none);
+        const int o = got + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+        if (none && o < K) {
+            const int kk = (int)(i / V), v = (int)(i - (int64_t)kk * V);
+            a.out_scores[b * K + o] = -INFINITY;
+            a.parent[b * K + o] = (int)(b * K + kk);
+            a.token[b * K + o] = v;
+            if (a.out_finished)
+                a.out_finished[b * K + o] = ((a.finished && a.finished[b * K + kk]) || v == a.eos) ? 1 : 0;
+        }
+        got += __popcll(mask);
+    }
+}
+
+// Lists per row (at most 64, the lanes that merge them) and tiles per list.
+void beam_plan(int64_t V, int *lists, int *tiles) {
+    const int64_t t = (V + kTile - 1) / kTile;
+    *tiles = (int)((t + 63) / 64);
+    *lists = (int)((t + *tiles - 1) / *tiles);
+}
+
+template <typename T>
+static ssd_status run_beam(const BeamArgs &a, int64_t batch, hipStream_t s) {
+    const int64_t waves = a.rows * a.lists;
+    if (launch(k_beam_top<T>, dim3((unsigned)((waves + 3) / 4)), dim3(256), s, a) != hipSuccess) return SSD_ERR_HIP;
+    return launch(k_beam_pick<T>, dim3((unsigned)batch), dim3((unsigned)(64 * a.beams)), s, a) == hipSuccess
+               ? SSD_OK
+               : SSD_ERR_HIP;
+}
+
+ssd_status launch_beam_select(const BeamArgs &a, int64_t batch, ssd_dtype dtype, hipStream_t s) {
+    return dtype == SSD_BF16 ? run_beam<bf16>(a, batch, s) : run_beam<float>(a, batch, s);
+}
+
+}  // namespace ssd

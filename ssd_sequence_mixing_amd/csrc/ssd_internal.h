@@ -93,6 +93,12 @@ struct StepArgs {
     const float *conv_b;       // its bias (H P), or null (zero)
     int64_t batch, H, P, N, G;
     ssd_dtype dtype;
+    // beam search: row b's state (and conv state) comes from row parent[b] of
+    // state_in (conv_in), of which there are src_rows; null for a step in place
+    const int *parent;
+    const float *state_in;
+    const void *conv_in;
+    int64_t src_rows;
 };
 
 // Backward pass (ssd_bwd.hip).
@@ -170,6 +176,50 @@ ssd_status launch_walk_rs(const FwdArgs &f, hipStream_t s);
 // The end states of a split sequence's segments 0 .. S - 2 (each entered with
 // zero, the first with f.init) into f.seg (ssd_seg_states.hip).
 ssd_status launch_seg_states(const FwdArgs &f, hipStream_t s);
+// RMS norm (ssd_norm.hip). rows counts (row, group) pairs of Dg values each.
+struct NormArgs {
+    const void *x, *res;        // res may be null: no residual
+    const float *w;             // (groups, Dg)
+    void *res_out, *y;          // y null where q is given
+    uint8_t *q, *scale;         // 8-bit output, or null
+    float *rstd;                // (rows) or null
+    int64_t rows, groups;
+    int Dg;
+    float eps;
+    ssd_dtype dtype, res_dtype;
+};
+ssd_status launch_rms_norm(const NormArgs &a, hipStream_t s);
+ssd_status launch_mx_quantize(const void *x, uint8_t *q, uint8_t *scale, int64_t n, ssd_dtype dtype, hipStream_t s);
+
+struct NormBwdArgs {
+    const void *dy, *h, *dres;  // dres may be null
+    const float *w, *rstd;      // rstd (rows, groups)
+    void *dx, *dh;              // dh may be null; written where h's type is not dy's
+    float *dw;
+    float *part;                // workspace: (nb, groups, Dg)
+    int64_t rows, groups;
+    int Dg, nb;
+    ssd_dtype dtype, res_dtype;
+};
+int norm_bwd_blocks(int64_t rows, int64_t groups, int64_t n);
+ssd_status launch_rms_norm_bwd(const NormBwdArgs &a, hipStream_t s);
+
+// Beam search's selection (ssd_beam.hip).
+struct BeamArgs {
+    const void *logits;         // (rows, V), rows = batch x beams
+    const float *scores;        // (rows)
+    const uint8_t *finished;    // (rows) or null
+    float *out_scores;
+    int *parent, *token;
+    uint8_t *out_finished;      // or null
+    uint64_t *keys;             // workspace: (rows, lists, beams)
+    float2 *sums;               // workspace: (rows, lists) maximum and sum of exponentials
+    int64_t rows;
+    int beams, V, eos, lists, tiles;
+};
+void beam_plan(int64_t V, int *lists, int *tiles);
+ssd_status launch_beam_select(const BeamArgs &a, int64_t batch, ssd_dtype dtype, hipStream_t s);
+
 // One recurrent decode step.
 ssd_status launch_step(const StepArgs &a, hipStream_t s);
 

@@ -1,0 +1,418 @@
+// Root-mean-square norm of a layer's rows for gfx950, with the residual's
+// addition in front and an 8-bit output behind, its backward pass, and the
+// 8-bit quantiser by itself.
+//
+//   h = x + r;  inv = 1 / sqrt(mean(h^2) + eps);  y = h inv w
+//
+// over each of `groups` equal pieces of a row of D values (a tensor-parallel
+// layer's norm takes one piece per group). Everything is held in fp32; r's
+// sum is rounded once, to the stored h, and y once, to its storage type.
+//
+// 8 bits: every 32 consecutive y share a power of two 2^p, p the smallest
+// whole number >= -127 with max|y| <= 448 * 2^p (448 is e4m3's largest value,
+// so nothing saturates and nothing is clipped), stored as p + 127 (e8m0), and
+// the code of y is e4m3(y 2^-p), rounded to nearest even; y 2^-p is exact. These are the operands the
+// matrix cores' scaled products take as they are. A block that holds a value
+// that is not finite gets the scale 255 (NaN) and codes 0x7f (NaN).
+//
+// Bound: HBM, one read and one write of every row. A row stays in registers
+// between the sum and the scaling, so it is read once: W wavefronts take one
+// row, each lane NC chunks of 8 consecutive values (one 16-byte load in bf16).
+// With many rows one wavefront takes a row (no barrier, NC loads in flight);
+// with few rows the time is latency, and a row is spread over 4.
+#include "ssd_common.h"
+#include "ssd_internal.h"
+
+namespace ssd {
+
+constexpr int kNormThreads = 256;
+
+// 8 values of one chunk as fp32. V: the chunk is 8 consecutive values, 16-byte
+// aligned; else the values are taken one by one, `step` apart, where i < n.
+template <typename T, bool V>
+__device__ __forceinline__ void ld8(float (&v)[8], const T *p, int i, int step, int n) {
+    if constexpr (V) {
+        if (i < n) {
+            if constexpr (sizeof(T) == 2) {
+                const bf16x8 q = *reinterpret_cast<const bf16x8 *>(p + i);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = (float)q[e];
+            } else {
+                const f32x4 a = *reinterpret_cast<const f32x4 *>(p + i);
+                const f32x4 b = *reinterpret_cast<const f32x4 *>(p + i + 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = (i + e * step < n) ? (float)p[i + e * step] : 0.f;
+    }
+}
+
+template <typename T, bool V>
+__device__ __forceinline__ void st8(const float (&v)[8], T *p, int i, int step, int n) {
+    if constexpr (V) {
+        if (i >= n) return;
+        if constexpr (sizeof(T) == 2) {
+            bf16x8 q;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q[e] = (bf16)v[e];
+            *reinterpret_cast<bf16x8 *>(p + i) = q;
+        } else {
+            *reinterpret_cast<f32x4 *>(p + i) = f32x4{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<f32x4 *>(p + i + 4) = f32x4{v[4], v[5], v[6], v[7]};
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (i + e * step < n) p[i + e * step] = (T)v[e];
+    }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+    return v;
+}
+
+// Sum over the W wavefronts of a row; red holds one value per wavefront.
+template <int W>
+__device__ __forceinline__ float row_sum(float v, float *red) {
+    v = wave_sum(v);
+    if constexpr (W > 1) {
+        const int w = threadIdx.x >> 6;
+        __syncthreads();  // the values of the sum before have been read
+        if ((threadIdx.x & 63) == 0) red[w] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) v += red[k];
+    }
+    return v;
+}
+
+// The codes of 8 values and the scale of their block of 32 (this lane and the
+// 3 beside it in its group of 4).
+__device__ __forceinline__ void mx_block(const float (&v)[8], u32x2 &codes, uint32_t &scale) {
+    uint32_t top = 0;  // largest magnitude as bits: NaN > infinity > every finite value
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+    top = max(top, (uint32_t)__shfl_xor((int)top, 1, 64));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 2, 64));
+    if (top >= 0x7f800000u) {
+        codes = u32x2{0x7f7f7f7fu, 0x7f7f7f7fu};
+        scale = 255;
+        return;
+    }
+    // top = 1.m 2^(E-127) <= 1.75 * 2^(p+8): p = E - 135, one more where 1.m > 1.75
+    int p = (int)(top >> 23) - 135 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+    p = max(p, -127);
+    const float inv = __uint_as_float((uint32_t)(127 - p) << 23);  // 2^-p, p in [-127, 120]
+    int lo = 0, hi = 0;
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, lo, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, lo, true);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * inv, v[5] * inv, hi, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * inv, v[7] * inv, hi, true);
+    codes = u32x2{(uint32_t)lo, (uint32_t)hi};
+    scale = (uint32_t)(p + 127);
+}
+
+// TX: storage type of x and y; TR: of the residual. W wavefronts per row, NC
+// chunks of 8 values per lane. MX: 8-bit output instead of y.
+template <typename TX, typename TR, int W, int NC, bool V, bool MX>
+__global__ __launch_bounds__(W > 4 ? W * 64 : kNormThreads) void k_rms_norm(NormArgs a) {
+    constexpr int RPB = W > 4 ? 1 : kNormThreads / (64 * W);  // rows per work-group
+    __shared__ float red[W > 1 ? W : 1];
+    const int t = threadIdx.x % (64 * W);
+    const int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / (64 * W);
+    if (r >= a.rows) return;  // only where W == 1: a row per work-group never ends early
+    const int n = a.Dg;
+    const int64_t at = r * n;
+    const TX *x = reinterpret_cast<const TX *>(a.x) + at;
+    const TR *res = a.res ? reinterpret_cast<const TR *>(a.res) + at : nullptr;
+    const float *wt = a.w + (r % a.groups) * n;
+    constexpr int kStep = 64 * W;  // distance of a lane's values where they are taken one by one
+    auto first = [&](int c) { return V ? (c * kStep + t) * 8 : c * kStep * 8 + t; };
+    float h[NC][8];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) ld8<TX, V>(h[c], x, first(c), kStep, n);
+    if (res) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            float q[8];
+            ld8<TR, V>(q, res, first(c), kStep, n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[c][e] += q[e];
+        }
+    }
+    float wv[NC][8];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) ld8<float, V>(wv[c], wt, first(c), kStep, n);
+    float sq = 0.f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sq += h[c][e] * h[c][e];
+    if (res) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) st8<TR, V>(h[c], reinterpret_cast<TR *>(a.res_out) + at, first(c), kStep, n);
+    }
+    sq = row_sum<W>(sq, red);
+    const float inv = 1.f / sqrtf(sq / (float)n + a.eps);
+    if (a.rstd && t == 0) a.rstd[r] = inv;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = h[c][e] * inv * wv[c][e];
+        if constexpr (MX) {
+            u32x2 codes;
+            uint32_t scale;
+            mx_block(y, codes, scale);  // every lane: its neighbours read its values
+            const int i = first(c);
+            if (i < n) {
+                *reinterpret_cast<u32x2 *>(a.q + at + i) = codes;
+                if ((t & 3) == 0) a.scale[(at + i) >> 5] = (uint8_t)scale;
+            }
+        } else {
+            st8<TX, V>(y, reinterpret_cast<TX *>(a.y) + at, first(c), kStep, n);
+        }
+    }
+}
+
+// y = x in 8 bits (no norm): one chunk of 8 values per lane.
+template <typename TX>
+__global__ __launch_bounds__(kNormThreads) void k_mx_quantize(const TX *x, uint8_t *q, uint8_t *scale, int64_t n) {
+    const int64_t i = ((int64_t)blockIdx.x * kNormThreads + threadIdx.x) * 8;
+    float v[8];
+    ld8<TX, true>(v, x + (i < n ? i : 0), i < n ? 0 : 8, 0, 8);
+    u32x2 codes;
+    uint32_t s;
+    mx_block(v, codes, s);
+    if (i < n) {
+        *reinterpret_cast<u32x2 *>(q + i) = codes;
+        if ((threadIdx.x & 3) == 0) scale[i >> 5] = (uint8_t)s;
+    }
+}
+
+// The gradients, from the stored h and inv. With hh = h inv and g = dy w:
+//   dh = inv (g - hh mean(g hh)) + dr_out;   dw = sum over rows of dy hh
+// A work-group takes every nb-th row of one group (blockIdx.y) and keeps its
+// share of dw in registers, lane by lane the columns it reads; the shares are
+// added in a fixed order (wavefronts, then work-groups in k_rms_norm_dw), so
+// the same inputs give the same bits.
+template <typename TX, typename TR, int W, int NC, bool V>
+__global__ __launch_bounds__(W > 4 ? W * 64 : kNormThreads) void k_rms_norm_bwd(NormBwdArgs a) {
+    constexpr int RPB = W > 4 ? 1 : kNormThreads / (64 * W);
+    constexpr bool kTwo = sizeof(TX) != sizeof(TR);  // h's gradient in its own type beside x's
+    constexpr int kStep = 64 * W;
+    __shared__ float red[W > 1 ? W : 1];
+    __shared__ float share[RPB > 1 ? kStep * NC * 8 : 1];
+    const int t = threadIdx.x % kStep, slot = threadIdx.x / kStep;
+    const int n = a.Dg, g = blockIdx.y;
+    const float *wt = a.w + (int64_t)g * n;
+    auto first = [&](int c) { return V ? (c * kStep + t) * 8 : c * kStep * 8 + t; };
+    float dw[NC][8];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[c][e] = 0.f;
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += (int64_t)gridDim.x * RPB) {
+        const int64_t r = r0 + slot;
+        if (RPB > 1 && r >= a.rows) break;  // W == 1: no barrier in the loop
+        const int64_t at = (r * a.groups + g) * n;
+        const float inv = a.rstd[r * a.groups + g];
+        float hh[NC][8], gw[NC][8];
+        float dot = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            ld8<TR, V>(hh[c], reinterpret_cast<const TR *>(a.h) + at, first(c), kStep, n);
+            ld8<TX, V>(gw[c], reinterpret_cast<const TX *>(a.dy) + at, first(c), kStep, n);
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            float wv[8];
+            ld8<float, V>(wv, wt, first(c), kStep, n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                hh[c][e] *= inv;
+                dw[c][e] += gw[c][e] * hh[c][e];
+                gw[c][e] *= wv[e];
+                dot += gw[c][e] * hh[c][e];
+            }
+        }
+        dot = row_sum<W>(dot, red) / (float)n;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            float dr[8];
+            if (a.dres) {
+                ld8<TR, V>(dr, reinterpret_cast<const TR *>(a.dres) + at, first(c), kStep, n);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) dr[e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dr[e] += inv * (gw[c][e] - hh[c][e] * dot);
+            st8<TX, V>(dr, reinterpret_cast<TX *>(a.dx) + at, first(c), kStep, n);
+            if constexpr (kTwo) {
+                if (a.dh) st8<TR, V>(dr, reinterpret_cast<TR *>(a.dh) + at, first(c), kStep, n);
+            }
+        }
+    }
+    float *part = a.part + ((int64_t)blockIdx.x * a.groups + g) * n;
+    if constexpr (RPB > 1) {
+        for (int s = 1; s < RPB; ++s) {
+            __syncthreads();
+            if (slot == s) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) share[(c * 8 + e) * kStep + t] = dw[c][e];
+            }
+            __syncthreads();
+            if (slot == 0) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dw[c][e] += share[(c * 8 + e) * kStep + t];
+            }
+        }
+        if (slot != 0) return;
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) st8<float, V>(dw[c], part, first(c), kStep, n);
+}
+
+// dw[d] = the nb shares of column d, added by 16 threads and then by one, in
+// order. One work-group takes 64 columns.
+__global__ __launch_bounds__(1024) void k_rms_norm_dw(const float *part, float *dw, int nb, int64_t D) {
+    __shared__ float red[16][64];
+    const int c = threadIdx.x & 63, k = threadIdx.x >> 6;
+    const int64_t d = (int64_t)blockIdx.x * 64 + c;
+    float s = 0.f;
+    if (d < D) {
+#pragma unroll 8
+        for (int b = k; b < nb; b += 16) s += part[(int64_t)b * D + d];
+    }
+    red[k][c] = s;
+    __syncthreads();
+    if (k == 0 && d < D) {
+#pragma unroll
+        for (int j = 1; j < 16; ++j) s += red[j][c];
+        dw[d] = s;
+    }
+}
+
+// How a row of n values is spread: wavefronts per row and chunks per lane.
+struct NormPlan {
+    int W, NC;
+};
+// One wavefront per row while a row fits 8 chunks a lane and there are rows
+// for every SIMD (1024); with fewer rows, 4 wavefronts share one, which
+// shortens the chain of a row. Beyond 16384 values 16 wavefronts take a row.
+static NormPlan norm_plan(int64_t rows, int64_t n) {
+    if (n > 16384) return {16, n > 32768 ? 8 : 4};
+    const int W = (n <= 512 || (n <= 4096 && rows >= 1024)) ? 1 : 4;
+    const int64_t c = (n + 512 * W - 1) / (512 * W);
+    return {W, c <= 1 ? 1 : c <= 2 ? 2 : c <= 4 ? 4 : 8};
+}
+
+template <typename TX, typename TR, bool V, bool MX>
+static ssd_status run_norm(const NormArgs &a, hipStream_t s) {
+    const NormPlan p = norm_plan(a.rows, a.Dg);
+    const int rpb = p.W > 4 ? 1 : kNormThreads / (64 * p.W);
+    const dim3 grid((unsigned)((a.rows + rpb - 1) / rpb)), block(p.W > 4 ? 64 * p.W : kNormThreads);
+    auto go = [&](auto k) { return launch(k, grid, block, s, a) == hipSuccess ? SSD_OK : SSD_ERR_HIP; };
+    if (p.W == 1) {
+        switch (p.NC) {
+            case 1: return go(k_rms_norm<TX, TR, 1, 1, V, MX>);
+            case 2: return go(k_rms_norm<TX, TR, 1, 2, V, MX>);
+            case 4: return go(k_rms_norm<TX, TR, 1, 4, V, MX>);
+            default: return go(k_rms_norm<TX, TR, 1, 8, V, MX>);
+        }
+    }
+    if (p.W == 4) {
+        switch (p.NC) {
+            case 1: return go(k_rms_norm<TX, TR, 4, 1, V, MX>);
+            case 2: return go(k_rms_norm<TX, TR, 4, 2, V, MX>);
+            case 4: return go(k_rms_norm<TX, TR, 4, 4, V, MX>);
+            default: return go(k_rms_norm<TX, TR, 4, 8, V, MX>);
+        }
+    }
+    return p.NC == 4 ? go(k_rms_norm<TX, TR, 16, 4, V, MX>) : go(k_rms_norm<TX, TR, 16, 8, V, MX>);
+}
+
+template <typename TX, typename TR>
+static ssd_status norm_t(const NormArgs &a, hipStream_t s) {
+    if (a.q) return run_norm<TX, TR, true, true>(a, s);
+    return a.Dg % 8 == 0 ? run_norm<TX, TR, true, false>(a, s) : run_norm<TX, TR, false, false>(a, s);
+}
+
+ssd_status launch_rms_norm(const NormArgs &a, hipStream_t s) {
+    if (a.dtype == SSD_F32) return norm_t<float, float>(a, s);
+    return a.res_dtype == SSD_F32 ? norm_t<bf16, float>(a, s) : norm_t<bf16, bf16>(a, s);
+}
+
+ssd_status launch_mx_quantize(const void *x, uint8_t *q, uint8_t *scale, int64_t n, ssd_dtype dtype, hipStream_t s) {
+    const dim3 grid((unsigned)((n / 8 + kNormThreads - 1) / kNormThreads)), block(kNormThreads);
+    const hipError_t e = dtype == SSD_BF16
+                             ? launch(k_mx_quantize<bf16>, grid, block, s, (const bf16 *)x, q, scale, n)
+                             : launch(k_mx_quantize<float>, grid, block, s, (const float *)x, q, scale, n);
+    return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+}
+
+// Work-groups per group of columns in the backward: enough to fill the chip
+// (1024, 4 to a CU, over all groups), no more than there are rows for.
+int norm_bwd_blocks(int64_t rows, int64_t groups, int64_t n) {
+    const int rpb = norm_plan(rows, n).W == 1 ? 4 : 1;
+    const int64_t most = (rows + rpb - 1) / rpb;
+    int64_t want = (1024 + groups - 1) / groups;
+    return (int)(want < most ? want : most);
+}
+
+template <typename TX, typename TR, bool V>
+static ssd_status run_norm_bwd(const NormBwdArgs &a, hipStream_t s) {
+    const NormPlan p = norm_plan(a.rows, a.Dg);
+    const dim3 grid((unsigned)a.nb, (unsigned)a.groups), block(p.W > 4 ? 64 * p.W : kNormThreads);
+    auto go = [&](auto k) { return launch(k, grid, block, s, a) == hipSuccess ? SSD_OK : SSD_ERR_HIP; };
+    if (p.W == 1) {
+        switch (p.NC) {
+            case 1: return go(k_rms_norm_bwd<TX, TR, 1, 1, V>);
+            case 2: return go(k_rms_norm_bwd<TX, TR, 1, 2, V>);
+            case 4: return go(k_rms_norm_bwd<TX, TR, 1, 4, V>);
+            default: return go(k_rms_norm_bwd<TX, TR, 1, 8, V>);
+        }
+    }
+    if (p.W == 4) {
+        switch (p.NC) {
+            case 1: return go(k_rms_norm_bwd<TX, TR, 4, 1, V>);
+            case 2: return go(k_rms_norm_bwd<TX, TR, 4, 2, V>);
+            case 4: return go(k_rms_norm_bwd<TX, TR, 4, 4, V>);
+            default: return go(k_rms_norm_bwd<TX, TR, 4, 8, V>);
+        }
+    }
+    return p.NC == 4 ? go(k_rms_norm_bwd<TX, TR, 16, 4, V>) : go(k_rms_norm_bwd<TX, TR, 16, 8, V>);
+}
+
+template <typename TX, typename TR>
+static ssd_status norm_bwd_t(const NormBwdArgs &a, hipStream_t s) {
+    return a.Dg % 8 == 0 ? run_norm_bwd<TX, TR, true>(a, s) : run_norm_bwd<TX, TR, false>(a, s);
+}
+
+ssd_status launch_rms_norm_bwd(const NormBwdArgs &a, hipStream_t s) {
+    ssd_status st = a.dtype == SSD_F32         ? norm_bwd_t<float, float>(a, s)
+                    : a.res_dtype == SSD_F32 ? norm_bwd_t<bf16, float>(a, s)
+                                             : norm_bwd_t<bf16, bf16>(a, s);
+    if (st != SSD_OK) return st;
+    const int64_t D = (int64_t)a.Dg * a.groups;
+    return launch(k_rms_norm_dw, dim3((unsigned)((D + 63) / 64)), dim3(1024), s, (const float *)a.part, a.dw, a.nb,
+                  D) == hipSuccess
+               ? SSD_OK
+               : SSD_ERR_HIP;
+}
+
+}  // namespace ssd

@@ -5,6 +5,8 @@
 //   a = exp(dt[b,h] A[h]);  s[p,n] <- a s[p,n] + dt x[p] B[g,n];
 //   y[p] = sum_n s[p,n] C[g,n] + D[h] x[p]
 //
+// from the state of row parent[b] (kBeam: beam search's reordering of states,
+// which costs no pass of its own) or of row b in place, and
 // optionally with the layer's prologue and epilogue fused in: dt =
 // softplus(dt + dt_bias[h]), the input x <- SiLU(b + w . [x_{t-3}, x_{t-2},
 // x_{t-1}, x_t]) of the layer's causal convolution (the 3 earlier raw inputs
@@ -32,7 +34,7 @@ struct StepShape {
     static constexpr int RPB = (kStepThreads / 64) * RPW * kStepUnroll;  // rows per work-group
 };
 
-template <typename TI, int N>
+template <typename TI, int N, bool kBeam>
 __global__ __launch_bounds__(kStepThreads) void k_step(StepArgs a, int pblocks) {
     using Tr = Traits<TI>;
     using S = StepShape<TI, N>;
@@ -51,14 +53,25 @@ __global__ __launch_bounds__(kStepThreads) void k_step(StepArgs a, int pblocks) 
     const float dec = fast_exp2(dtv * a.A[h] * kLog2e);
     const float Dh = a.D[h];
     float *srow = a.state + bh * P * N;
+    // kBeam: the row the state comes from; out of range, a sequence that begins
+    // (zero state). The states' addresses then wait for this one scalar load.
+    int64_t from = bb;
+    bool begun = true;
+    const float *sin = srow;
+    if constexpr (kBeam) {
+        from = a.parent[bb];
+        begun = from >= 0 && from < a.src_rows;
+        if (!begun) from = 0;
+        sin = a.state_in + (from * H + h) * P * N;
+    }
 
     int p[kStepUnroll];
     f32x4 s[kStepUnroll];
 #pragma unroll
     for (int u = 0; u < kStepUnroll; ++u) {
         p[u] = pb * RPB + (u * (kStepThreads / 64) + w) * RPW + sub;
-        s[u] = (p[u] < P)
-                   ? __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(srow + (int64_t)p[u] * N) + c4)
+        s[u] = (p[u] < P && begun)
+                   ? __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(sin + (int64_t)p[u] * N) + c4)
                    : f32x4{0.f, 0.f, 0.f, 0.f};
     }
     const TI *bp = reinterpret_cast<const TI *>(a.B) + (bb * G + g) * N + 4 * c4;
@@ -80,8 +93,10 @@ __global__ __launch_bounds__(kStepThreads) void k_step(StepArgs a, int pblocks) 
             // after the reads have been used.
             const int64_t ch = (int64_t)h * P + p[u];
             TI *cst = reinterpret_cast<TI *>(a.conv_state) + (bb * H * P + ch) * 3;
-            const TI s1 = cst[1], s2 = cst[2];
-            const float s0 = Tr::to_f32(cst[0]);
+            const TI *old = cst;
+            if constexpr (kBeam) old = reinterpret_cast<const TI *>(a.conv_in) + (from * H * P + ch) * 3;
+            const TI s1 = begun ? old[1] : Tr::from_f32(0.f), s2 = begun ? old[2] : Tr::from_f32(0.f);
+            const float s0 = begun ? Tr::to_f32(old[0]) : 0.f;
             const f32x4 wv = *reinterpret_cast<const f32x4 *>(a.conv_w + 4 * ch);
             const float v = (a.conv_b ? a.conv_b[ch] : 0.f) + wv[0] * s0 + wv[1] * Tr::to_f32(s1) +
                             wv[2] * Tr::to_f32(s2) + wv[3] * xv;
@@ -112,33 +127,34 @@ __global__ __launch_bounds__(kStepThreads) void k_step(StepArgs a, int pblocks) 
     }
 }
 
-template <typename TI, int N>
+template <typename TI, int N, bool kBeam>
 static ssd_status run_step(const StepArgs &a, hipStream_t s) {
     constexpr int RPB = StepShape<TI, N>::RPB;
     const int pblocks = (int)((a.P + RPB - 1) / RPB);
     const int64_t blocks = a.batch * a.H * pblocks;
-    return launch(k_step<TI, N>, dim3((unsigned)blocks), dim3(kStepThreads), s, a, pblocks) ==
+    return launch(k_step<TI, N, kBeam>, dim3((unsigned)blocks), dim3(kStepThreads), s, a, pblocks) ==
                    hipSuccess
                ? SSD_OK
                : SSD_ERR_HIP;
 }
 
-template <typename TI>
+template <typename TI, bool kBeam>
 static ssd_status step_n(const StepArgs &a, hipStream_t s) {
     switch (a.N) {
-        case 4: return run_step<TI, 4>(a, s);
-        case 8: return run_step<TI, 8>(a, s);
-        case 16: return run_step<TI, 16>(a, s);
-        case 32: return run_step<TI, 32>(a, s);
-        case 64: return run_step<TI, 64>(a, s);
-        case 128: return run_step<TI, 128>(a, s);
-        case 256: return run_step<TI, 256>(a, s);
+        case 4: return run_step<TI, 4, kBeam>(a, s);
+        case 8: return run_step<TI, 8, kBeam>(a, s);
+        case 16: return run_step<TI, 16, kBeam>(a, s);
+        case 32: return run_step<TI, 32, kBeam>(a, s);
+        case 64: return run_step<TI, 64, kBeam>(a, s);
+        case 128: return run_step<TI, 128, kBeam>(a, s);
+        case 256: return run_step<TI, 256, kBeam>(a, s);
         default: return SSD_ERR_UNSUPPORTED;
     }
 }
 
 ssd_status launch_step(const StepArgs &a, hipStream_t s) {
-    return a.dtype == SSD_BF16 ? step_n<bf16>(a, s) : step_n<float>(a, s);
+    if (a.parent) return a.dtype == SSD_BF16 ? step_n<bf16, true>(a, s) : step_n<float, true>(a, s);
+    return a.dtype == SSD_BF16 ? step_n<bf16, false>(a, s) : step_n<float, false>(a, s);
 }
 
 }  // namespace ssd
