@@ -492,6 +492,65 @@ ssd_status ssd_rms_norm_bwd(const void *dy, const void *h, const float *weight, 
                             int64_t dim, int64_t groups, ssd_dtype dtype, ssd_dtype residual_dtype, void *workspace,
                             size_t workspace_bytes, void *stream);
 
+/*
+ * Matrix product of a layer's projection, with bias, activation and residual
+ * in its epilogue:
+ *
+ *   z = x w^T + bias;   y = act(z) + residual
+ *
+ *   x (rows, in)         dtype
+ *   w (out, in)          dtype
+ *   bias (out)           float32, or NULL (zero)
+ *   act                  SSD_ACT_NONE, SSD_ACT_SILU (z / (1 + e^-z)) or SSD_ACT_GELU (z (1 + erf(z / sqrt 2)) / 2)
+ *   residual (rows, out) dtype, or NULL (zero)
+ *   y (rows, out)        dtype  output, rounded once
+ *   preact (rows, out)   dtype  output: z, for the backward pass; or NULL
+ *
+ * Sums in fp32: bf16 operands on the bf16 matrix cores, fp32 ones on the
+ * fp32 matrix cores. Any sizes; rows that do not begin at multiples of 16 bytes
+ * (in * sizeof(dtype) not a multiple of 16) cost a copy of both operands in the
+ * workspace. rows at most 2^24, in and out at most 2^20. The same inputs give
+ * the same bits. The workspace (256-byte aligned) is empty for most shapes.
+ *
+ * ssd_linear_mx is the same product of 8-bit operands as ssd_rms_norm_mx and
+ * ssd_mx_quantize write them (weights once): xq (rows, in), wq (out, in) e4m3
+ * codes, xscale (rows, in / 32), wscale (out, in / 32); in a multiple of 32;
+ * residual and y bf16. Sums are fp32 but for one thing: the matrix cores add
+ * the products of 8 consecutive codes in fixed point, 13 bits below the largest of
+ * the 8 (about 1e-4 of a result of ordinary data, far below the codes' own rounding).
+ */
+typedef enum { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1, SSD_ACT_GELU = 2 } ssd_act;
+
+size_t ssd_linear_workspace_bytes(int64_t rows, int64_t in, int64_t out, ssd_dtype dtype);
+
+ssd_status ssd_linear(const void *x, const void *w, const float *bias, int act, const void *residual, void *y,
+                      void *preact, int64_t rows, int64_t in, int64_t out, ssd_dtype dtype, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+size_t ssd_linear_mx_workspace_bytes(int64_t rows, int64_t in, int64_t out);
+
+ssd_status ssd_linear_mx(const uint8_t *xq, const uint8_t *xscale, const uint8_t *wq, const uint8_t *wscale,
+                         const float *bias, int act, const void *residual, void *y, int64_t rows, int64_t in,
+                         int64_t out, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of ssd_linear (the residual's is dy itself). With dz = dy act'(z):
+ *   dx = dz w;   dw = dz^T x;   dbias = sum over rows of dz
+ *
+ *   dy (rows, out), x (rows, in), w (out, in)   dtype; w is read only for dx, x only for dw
+ *   preact (rows, out)   dtype: z, as the forward kept it; not read with SSD_ACT_NONE
+ *   dx (rows, in), dw (out, in)  dtype   outputs, each NULL to leave it out
+ *   dbias (out)          float32         output, or NULL
+ * dz is rounded to dtype as an operand of the two products (in bf16; dbias sums
+ * it in fp32 before that). rows, in and out at most 2^20. The workspace query
+ * is for all three gradients. With rows == 0, dw and dbias are zero.
+ */
+size_t ssd_linear_bwd_workspace_bytes(int64_t rows, int64_t in, int64_t out, int act, ssd_dtype dtype);
+
+ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, int act, const void *preact, void *dx,
+                          void *dw, float *dbias, int64_t rows, int64_t in, int64_t out, ssd_dtype dtype,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

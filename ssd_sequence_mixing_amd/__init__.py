@@ -20,7 +20,9 @@ __all__ = [
     "ssd_chunk_scan_bwd_workspace_bytes", "ssd_chunk_scan_bwd", "ssd_chunk_scan_fwd_fused",
     "ssd_chunk_scan_fwd_noalloc", "ssd_step_fused", "NOALLOC_SCRATCH_BYTES", "EXPORTS",
     "ssd_step_beam", "ssd_beam_select_workspace_bytes", "ssd_beam_select", "ssd_rms_norm", "ssd_rms_norm_mx",
-    "ssd_mx_quantize", "ssd_rms_norm_bwd_workspace_bytes", "ssd_rms_norm_bwd",
+    "ssd_mx_quantize", "ssd_rms_norm_bwd_workspace_bytes", "ssd_rms_norm_bwd", "ssd_linear_workspace_bytes",
+    "ssd_linear", "ssd_linear_mx_workspace_bytes", "ssd_linear_mx", "ssd_linear_bwd_workspace_bytes",
+    "ssd_linear_bwd", "ACTS",
 ]
 
 SSD_F32 = 0
@@ -36,10 +38,15 @@ EXPORTS = ("ssd_status_string", "ssd_chunk_scan_fwd_workspace_bytes", "ssd_chunk
            "ssd_chunk_scan_fwd_gated", "ssd_step_gated", "ssd_chunk_scan_bwd_workspace_bytes",
            "ssd_chunk_scan_bwd", "ssd_chunk_scan_fwd_fused", "ssd_chunk_scan_fwd_noalloc", "ssd_step_fused",
            "ssd_step_beam", "ssd_beam_select_workspace_bytes", "ssd_beam_select", "ssd_rms_norm",
-           "ssd_rms_norm_mx", "ssd_mx_quantize", "ssd_rms_norm_bwd_workspace_bytes", "ssd_rms_norm_bwd")
+           "ssd_rms_norm_mx", "ssd_mx_quantize", "ssd_rms_norm_bwd_workspace_bytes", "ssd_rms_norm_bwd",
+           "ssd_linear_workspace_bytes", "ssd_linear", "ssd_linear_mx_workspace_bytes", "ssd_linear_mx",
+           "ssd_linear_bwd_workspace_bytes", "ssd_linear_bwd")
 
 # SSD_NOALLOC_SCRATCH_BYTES: the static workspace of ssd_chunk_scan_fwd_noalloc.
 NOALLOC_SCRATCH_BYTES = 64 << 20
+
+# ssd_act: the activations of ssd_linear's epilogue.
+ACTS = {"none": 0, "silu": 1, "gelu": 2}
 
 _V = ctypes.c_void_p
 _I = ctypes.c_int64
@@ -137,6 +144,12 @@ def load():
             ("ssd_mx_quantize", _E, [_V] * 3 + [_I] * 2 + [_E, _V]),
             ("ssd_rms_norm_bwd_workspace_bytes", _S, [_I] * 3 + [_E] * 2),
             ("ssd_rms_norm_bwd", _E, [_V] * 8 + [_I] * 3 + [_E, _E, _V, _S, _V]),
+            ("ssd_linear_workspace_bytes", _S, [_I] * 3 + [_E]),
+            ("ssd_linear", _E, [_V] * 3 + [_E] + [_V] * 3 + [_I] * 3 + [_E, _V, _S, _V]),
+            ("ssd_linear_mx_workspace_bytes", _S, [_I] * 3),
+            ("ssd_linear_mx", _E, [_V] * 5 + [_E] + [_V] * 2 + [_I] * 3 + [_V, _S, _V]),
+            ("ssd_linear_bwd_workspace_bytes", _S, [_I] * 3 + [_E, _E]),
+            ("ssd_linear_bwd", _E, [_V] * 3 + [_E] + [_V] * 4 + [_I] * 3 + [_E, _V, _S, _V]),
     ):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
@@ -755,6 +768,122 @@ def ssd_rms_norm_bwd(dy, h, weight, rstd, *, d_residual_out=None, groups: int = 
     if st != 0:
         raise SSDError(st, "ssd_rms_norm_bwd")
     return dx, dh, dw
+
+
+def _act_code(act: str) -> int:
+    if act not in ACTS:
+        raise ValueError(f"act {act!r}: one of {sorted(ACTS)}")
+    return ACTS[act]
+
+
+def ssd_linear_workspace_bytes(rows, in_, out, dtype: int) -> int:
+    return _sized("ssd_linear_workspace_bytes", load().ssd_linear_workspace_bytes(rows, in_, out, dtype))
+
+
+def ssd_linear(x, w, *, bias=None, act: str = "none", residual=None, y=None, want_preact: bool = False, workspace=None,
+               stream=None):
+    """y = act(x w^T + bias) + residual: x (..., in) and w (out, in) bf16 or fp32, bias (out) fp32, act "none", "silu"
+    or "gelu", residual (..., out) in x's type. Returns (y, preact): preact is x w^T + bias for ssd_linear_bwd, or
+    None."""
+    import torch
+    lib = load()
+    rows, k = _rows_dim("x", x)
+    if w.dim() != 2 or w.shape[1] != k:
+        raise ValueError(f"w: shape {tuple(w.shape)}, expected (out, {k})")
+    n = w.shape[0]
+    shape = (*x.shape[:-1], n)
+    code = _dtype_code(x)
+    _chk("w", w, (n, k), x.dtype)
+    _chk("bias", bias, (n,), torch.float32)
+    _chk("residual", residual, shape, x.dtype)
+    _chk("y", y, shape, x.dtype)
+    _here(x, w, bias, residual, y, workspace)
+    if y is None:
+        y = _new(shape, x.dtype, x.device, stream)
+    pre = _new(shape, x.dtype, x.device, stream) if want_preact else None
+    if workspace is None:
+        need = ssd_linear_workspace_bytes(rows, k, n, code)
+        if need:
+            workspace = _new((need,), torch.uint8, x.device, stream)
+    st = lib.ssd_linear(_ptr(x), _ptr(w), _ptr(bias), _act_code(act), _ptr(residual), _ptr(y), _ptr(pre), rows, k, n,
+                        code, _ptr(workspace), _nbytes(workspace), _stream(stream))
+    if st != 0:
+        raise SSDError(st, "ssd_linear")
+    return y, pre
+
+
+def ssd_linear_mx_workspace_bytes(rows, in_, out) -> int:
+    return _sized("ssd_linear_mx_workspace_bytes", load().ssd_linear_mx_workspace_bytes(rows, in_, out))
+
+
+def ssd_linear_mx(xq, xscale, wq, wscale, *, bias=None, act: str = "none", residual=None, y=None, workspace=None,
+                  stream=None):
+    """ssd_linear from 8-bit operands as ssd_rms_norm_mx and ssd_mx_quantize return them: xq (..., in) and wq
+    (out, in) float8_e4m3fn, xscale (..., in / 32) and wscale (out, in / 32) float8_e8m0fnu; residual and y bf16.
+    Returns y."""
+    import torch
+    lib = load()
+    rows, k = _rows_dim("xq", xq)
+    if wq.dim() != 2 or wq.shape[1] != k:
+        raise ValueError(f"wq: shape {tuple(wq.shape)}, expected (out, {k})")
+    n = wq.shape[0]
+    shape = (*xq.shape[:-1], n)
+    _chk("xq", xq, xq.shape, torch.float8_e4m3fn)
+    _chk("xscale", xscale, (*xq.shape[:-1], k // 32), torch.float8_e8m0fnu)
+    _chk("wq", wq, (n, k), torch.float8_e4m3fn)
+    _chk("wscale", wscale, (n, k // 32), torch.float8_e8m0fnu)
+    _chk("bias", bias, (n,), torch.float32)
+    _chk("residual", residual, shape, torch.bfloat16)
+    _chk("y", y, shape, torch.bfloat16)
+    _here(xq, xscale, wq, wscale, bias, residual, y, workspace)
+    if y is None:
+        y = _new(shape, torch.bfloat16, xq.device, stream)
+    if workspace is None:
+        need = ssd_linear_mx_workspace_bytes(rows, k, n)
+        if need:
+            workspace = _new((need,), torch.uint8, xq.device, stream)
+    st = lib.ssd_linear_mx(_ptr(xq), _ptr(xscale), _ptr(wq), _ptr(wscale), _ptr(bias), _act_code(act), _ptr(residual),
+                           _ptr(y), rows, k, n, _ptr(workspace), _nbytes(workspace), _stream(stream))
+    if st != 0:
+        raise SSDError(st, "ssd_linear_mx")
+    return y
+
+
+def ssd_linear_bwd_workspace_bytes(rows, in_, out, act: str, dtype: int) -> int:
+    return _sized("ssd_linear_bwd_workspace_bytes",
+                  load().ssd_linear_bwd_workspace_bytes(rows, in_, out, _act_code(act), dtype))
+
+
+def ssd_linear_bwd(dy, x, w, *, act: str = "none", preact=None, want_x: bool = True, want_w: bool = True,
+                   want_bias: bool = False, workspace=None, stream=None):
+    """Gradients of ssd_linear: dy (..., out), x (..., in), w (out, in), preact as the forward returned it (act other
+    than "none"). Returns (dx, dw, dbias fp32), None for one that is not wanted; the residual's gradient is dy."""
+    import torch
+    lib = load()
+    rows, k = _rows_dim("x", x)
+    if w.dim() != 2 or w.shape[1] != k:
+        raise ValueError(f"w: shape {tuple(w.shape)}, expected (out, {k})")
+    n = w.shape[0]
+    shape = (*x.shape[:-1], n)
+    code, acode = _dtype_code(x), _act_code(act)
+    _chk("w", w, (n, k), x.dtype)
+    _chk("dy", dy, shape, x.dtype)
+    if acode and preact is None:
+        raise ValueError("act needs preact")
+    _chk("preact", preact, shape, x.dtype)
+    _here(dy, x, w, preact, workspace)
+    dx = _new(x.shape, x.dtype, x.device, stream) if want_x else None
+    dw = _new((n, k), x.dtype, x.device, stream) if want_w else None
+    db = _new((n,), torch.float32, x.device, stream) if want_bias else None
+    if workspace is None:
+        need = ssd_linear_bwd_workspace_bytes(rows, k, n, act, code)
+        if need:
+            workspace = _new((need,), torch.uint8, x.device, stream)
+    st = lib.ssd_linear_bwd(_ptr(dy), _ptr(x), _ptr(w), acode, _ptr(preact), _ptr(dx), _ptr(dw), _ptr(db), rows, k, n,
+                            code, _ptr(workspace), _nbytes(workspace), _stream(stream))
+    if st != 0:
+        raise SSDError(st, "ssd_linear_bwd")
+    return dx, dw, db
 
 
 def raw_call(name: str, *args) -> int:

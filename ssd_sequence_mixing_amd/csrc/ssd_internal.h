@@ -204,6 +204,34 @@ struct NormBwdArgs {
 int norm_bwd_blocks(int64_t rows, int64_t groups, int64_t n);
 ssd_status launch_rms_norm_bwd(const NormBwdArgs &a, hipStream_t s);
 
+// out[d] = sum over b < nb of part[b][d], in a fixed order (fp32).
+ssd_status launch_column_sums(const float *part, float *out, int nb, int64_t D, hipStream_t s);
+
+// Matrix products (ssd_linear.hip): y (M x N) = act(x w^T + bias) + res.
+struct LinearArgs {
+    const void *x, *w;          // rows of ldx / ldw bytes (multiples of 16), kbytes of them along k
+    const uint8_t *xscale, *wscale;  // 8-bit operands: a scale for each 32 along k, rows of lds bytes
+    int64_t ldx, ldw, lds;
+    const float *bias;          // (N) or null
+    const void *res;            // (M x N) or null
+    void *y, *pre;              // pre: z before the activation, or null
+    float *part;                // workspace: (splits, M, N) where the sum over k is split
+    int M, N, act;
+    uint32_t kbytes;
+    int nm, nn, steps, splits, steps_per_split;
+};
+struct LinearPlan {
+    int tile;                   // edge of a work-group's tile of y; 0: the few-rows kernel
+    int nm, nn;                 // tiles
+    int steps, splits, steps_per_split;
+};
+LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes);
+ssd_status launch_linear(LinearArgs a, const LinearPlan &p, bool mx, ssd_dtype dtype, hipStream_t s);
+ssd_status launch_pad(const void *in, void *out, int64_t rows, int64_t n, int64_t ldo, int es, hipStream_t s);
+ssd_status launch_transpose(const void *in, void *out, int64_t R, int64_t C, int64_t ldo, ssd_dtype dtype, hipStream_t s);
+ssd_status launch_dz(const void *dy, const void *pre, int act, void *dz, void *dzt, float *part, int64_t M, int64_t N,
+                     int64_t ldz, int64_t ldt, ssd_dtype dtype, hipStream_t s);
+
 // Beam search's selection (ssd_beam.hip).
 struct BeamArgs {
     const void *logits;         // (rows, V), rows = batch x beams

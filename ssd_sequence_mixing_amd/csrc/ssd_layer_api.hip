@@ -18,15 +18,21 @@ bool valid_dtype(int d) { return d == SSD_F32 || d == SSD_BF16; }
 
 int64_t align256(int64_t v) { return (v + 255) & ~(int64_t)255; }
 
-__global__ void k_clear(float *p, int64_t n) {
+int64_t esize(ssd_dtype d) { return d == SSD_BF16 ? 2 : 4; }
+
+__global__ void k_clear(uint16_t *p, int64_t n) {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i < n) p[i] = 0.f;
+    if (i < n) p[i] = 0;
 }
 
-ssd_status clear(float *p, int64_t n, hipStream_t s) {
-    if (n == 0) return SSD_OK;
-    return ssd::launch(k_clear, dim3((unsigned)((n + 255) / 256)), dim3(256), s, p, n) == hipSuccess ? SSD_OK
-                                                                                                     : SSD_ERR_HIP;
+// Zeros over an even number of bytes.
+ssd_status clear(void *p, int64_t bytes, hipStream_t s) {
+    if (!p || bytes == 0) return SSD_OK;
+    const int64_t n = bytes / 2;
+    return ssd::launch(k_clear, dim3((unsigned)((n + 255) / 256)), dim3(256), s, static_cast<uint16_t *>(p), n) ==
+                   hipSuccess
+               ? SSD_OK
+               : SSD_ERR_HIP;
 }
 
 ssd_status check_workspace(int64_t need, const void *workspace, size_t workspace_bytes) {
@@ -77,9 +83,208 @@ int64_t beam_bytes(int64_t batch, int64_t beams, int64_t vocab, int *lists, int 
     return align256(n * beams * 8) + align256(n * 8);
 }
 
+constexpr int64_t kMostDim = (int64_t)1 << 20;   // in and out: 256 rows stay under 2 GiB
+constexpr int64_t kMostRows = (int64_t)1 << 24;
+
+ssd_status check_linear(int64_t rows, int64_t in, int64_t out, int act, int64_t most_rows) {
+    if (act < SSD_ACT_NONE || act > SSD_ACT_GELU) return SSD_ERR_UNSUPPORTED;
+    if (rows < 0 || in <= 0 || out <= 0) return SSD_ERR_SHAPE;
+    if (rows > most_rows || in > kMostDim || out > kMostDim) return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+int64_t align16(int64_t v) { return (v + 15) & ~(int64_t)15; }
+
+// Workspace of a product: copies of the operands where their rows do not
+// begin at multiples of 16 bytes, and the parts of a split sum.
+struct LinearLayout {
+    ssd::LinearPlan plan;
+    int64_t ld, xpad, wpad, xs, ws, part, total;
+};
+LinearLayout linear_layout(int64_t rows, int64_t in, int64_t out, ssd_dtype dtype) {
+    LinearLayout l = {};
+    if (rows == 0) return l;
+    const int64_t bytes = in * esize(dtype);
+    l.ld = align16(bytes);
+    if (l.ld != bytes) {
+        l.xpad = align256(rows * l.ld);
+        l.wpad = align256(out * l.ld);
+    }
+    l.plan = ssd::linear_plan(rows, out, l.ld);
+    if (l.plan.splits > 1) l.part = align256(l.plan.splits * rows * out * 4);
+    l.total = l.xpad + l.wpad + l.part;
+    return l;
+}
+// 8-bit operands: the tile kernel takes a step's 4 scales of a row as one word.
+LinearLayout linear_mx_layout(int64_t rows, int64_t in, int64_t out) {
+    LinearLayout l = {};
+    if (rows == 0) return l;
+    l.plan = ssd::linear_plan(rows, out, in);
+    l.ld = in / 32;
+    if (l.plan.tile && l.ld % 4 != 0) {
+        l.ld = (l.ld + 3) & ~(int64_t)3;
+        l.xs = align256(rows * l.ld);
+        l.ws = align256(out * l.ld);
+    }
+    if (l.plan.splits > 1) l.part = align256(l.plan.splits * rows * out * 4);
+    l.total = l.xs + l.ws + l.part;
+    return l;
+}
+
+// Workspace of the gradients: dz by rows (where it is not dy itself) and dz,
+// x and w transposed (rows of ldt / ldz values), the 64-row shares of
+// dbias, and the parts of the two products' sums, one after the other.
+struct LinearBwdLayout {
+    ssd::LinearPlan px, pw;
+    int64_t ldz, ldt, dz, dzt, wt, xt, db, part, total;
+    bool own_dz;
+};
+LinearBwdLayout linear_bwd_layout(int64_t rows, int64_t in, int64_t out, int act, bool want_dx, bool want_dw,
+                                  bool want_db, ssd_dtype dtype) {
+    LinearBwdLayout l = {};
+    if (rows == 0) return l;
+    const int64_t es = esize(dtype);
+    l.ldz = align16(out * es) / es;
+    l.ldt = align16(rows * es) / es;
+    l.own_dz = want_dx && (act != SSD_ACT_NONE || l.ldz != out);
+    if (l.own_dz) l.dz = align256(rows * l.ldz * es);
+    int64_t px = 0, pw = 0;
+    if (want_dx) {
+        l.wt = align256(in * l.ldz * es);
+        l.px = ssd::linear_plan(rows, in, l.ldz * es);
+        if (l.px.splits > 1) px = align256(l.px.splits * rows * in * 4);
+    }
+    if (want_dw) {
+        l.dzt = align256(out * l.ldt * es);
+        l.xt = align256(in * l.ldt * es);
+        l.pw = ssd::linear_plan(out, in, l.ldt * es);
+        if (l.pw.splits > 1) pw = align256(l.pw.splits * out * in * 4);
+    }
+    if (want_db) l.db = align256((rows + 63) / 64 * out * 4);
+    l.part = px > pw ? px : pw;
+    l.total = l.dz + l.dzt + l.wt + l.xt + l.db + l.part;
+    return l;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t ssd_linear_workspace_bytes(int64_t rows, int64_t in, int64_t out, ssd_dtype dtype) {
+    if (!valid_dtype((int)dtype) || check_linear(rows, in, out, SSD_ACT_NONE, kMostRows) != SSD_OK) return (size_t)-1;
+    return (size_t)linear_layout(rows, in, out, dtype).total;
+}
+
+ssd_status ssd_linear(const void *x, const void *w, const float *bias, int act, const void *residual, void *y,
+                      void *preact, int64_t rows, int64_t in, int64_t out, ssd_dtype dtype, void *workspace,
+                      size_t workspace_bytes, void *stream) {
+    if (rows != 0 && (!x || !w || !y)) return SSD_ERR_NULL;
+    if (!valid_dtype((int)dtype)) return SSD_ERR_UNSUPPORTED;
+    ssd_status st = check_linear(rows, in, out, act, kMostRows);
+    if (st != SSD_OK) return st;
+    if (misaligned((const char *)x, (const char *)w, (const char *)bias, (const char *)residual, (const char *)y,
+                   (const char *)preact))
+        return SSD_ERR_ALIGN;
+    const LinearLayout l = linear_layout(rows, in, out, dtype);
+    if ((st = check_workspace(l.total, workspace, workspace_bytes)) != SSD_OK) return st;
+    if (rows == 0) return SSD_OK;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    ssd::LinearArgs a = {};
+    a.x = x; a.w = w; a.bias = bias; a.res = residual; a.y = y; a.pre = preact; a.act = act;
+    a.M = (int)rows; a.N = (int)out; a.ldx = a.ldw = l.ld; a.kbytes = (uint32_t)l.ld;
+    if (l.xpad) {
+        const int es = (int)esize(dtype);
+        if ((st = ssd::launch_pad(x, ws, rows, in, l.ld / es, es, s)) != SSD_OK) return st;
+        if ((st = ssd::launch_pad(w, ws + l.xpad, out, in, l.ld / es, es, s)) != SSD_OK) return st;
+        a.x = ws;
+        a.w = ws + l.xpad;
+    }
+    a.part = reinterpret_cast<float *>(ws + l.xpad + l.wpad);
+    return ssd::launch_linear(a, l.plan, false, dtype, s);
+}
+
+size_t ssd_linear_mx_workspace_bytes(int64_t rows, int64_t in, int64_t out) {
+    if (check_linear(rows, in, out, SSD_ACT_NONE, kMostRows) != SSD_OK || in % 32 != 0) return (size_t)-1;
+    return (size_t)linear_mx_layout(rows, in, out).total;
+}
+
+ssd_status ssd_linear_mx(const uint8_t *xq, const uint8_t *xscale, const uint8_t *wq, const uint8_t *wscale,
+                         const float *bias, int act, const void *residual, void *y, int64_t rows, int64_t in,
+                         int64_t out, void *workspace, size_t workspace_bytes, void *stream) {
+    if (rows != 0 && (!xq || !xscale || !wq || !wscale || !y)) return SSD_ERR_NULL;
+    ssd_status st = check_linear(rows, in, out, act, kMostRows);
+    if (st != SSD_OK) return st;
+    if (in % 32 != 0) return SSD_ERR_SHAPE;
+    if (misaligned((const char *)xq, (const char *)xscale, (const char *)wq, (const char *)wscale,
+                   (const char *)bias, (const char *)residual, (const char *)y))
+        return SSD_ERR_ALIGN;
+    const LinearLayout l = linear_mx_layout(rows, in, out);
+    if ((st = check_workspace(l.total, workspace, workspace_bytes)) != SSD_OK) return st;
+    if (rows == 0) return SSD_OK;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    ssd::LinearArgs a = {};
+    a.x = xq; a.w = wq; a.xscale = xscale; a.wscale = wscale; a.bias = bias; a.res = residual; a.y = y; a.act = act;
+    a.M = (int)rows; a.N = (int)out; a.ldx = a.ldw = in; a.lds = l.ld; a.kbytes = (uint32_t)in;
+    if (l.xs) {
+        if ((st = ssd::launch_pad(xscale, ws, rows, in / 32, l.ld, 1, s)) != SSD_OK) return st;
+        if ((st = ssd::launch_pad(wscale, ws + l.xs, out, in / 32, l.ld, 1, s)) != SSD_OK) return st;
+        a.xscale = reinterpret_cast<uint8_t *>(ws);
+        a.wscale = reinterpret_cast<uint8_t *>(ws + l.xs);
+    }
+    a.part = reinterpret_cast<float *>(ws + l.xs + l.ws);
+    return ssd::launch_linear(a, l.plan, true, SSD_BF16, s);
+}
+
+size_t ssd_linear_bwd_workspace_bytes(int64_t rows, int64_t in, int64_t out, int act, ssd_dtype dtype) {
+    if (!valid_dtype((int)dtype) || check_linear(rows, in, out, act, kMostDim) != SSD_OK) return (size_t)-1;
+    return (size_t)linear_bwd_layout(rows, in, out, act, true, true, true, dtype).total;
+}
+
+ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, int act, const void *preact, void *dx,
+                          void *dw, float *dbias, int64_t rows, int64_t in, int64_t out, ssd_dtype dtype,
+                          void *workspace, size_t workspace_bytes, void *stream) {
+    if (rows != 0 && (!dy || (dx && !w) || (dw && !x) || (act != SSD_ACT_NONE && !preact))) return SSD_ERR_NULL;
+    if (!valid_dtype((int)dtype)) return SSD_ERR_UNSUPPORTED;
+    ssd_status st = check_linear(rows, in, out, act, kMostDim);
+    if (st != SSD_OK) return st;
+    if (misaligned((const char *)dy, (const char *)x, (const char *)w, (const char *)preact, (const char *)dx,
+                   (const char *)dw, (const char *)dbias))
+        return SSD_ERR_ALIGN;
+    const LinearBwdLayout l = linear_bwd_layout(rows, in, out, act, dx, dw, dbias, dtype);
+    if ((st = check_workspace(l.total, workspace, workspace_bytes)) != SSD_OK) return st;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const int64_t es = esize(dtype);
+    if (rows == 0) {
+        if ((st = clear(dw, out * in * es, s)) != SSD_OK) return st;
+        return clear(dbias, out * 4, s);
+    }
+    char *ws = static_cast<char *>(workspace);
+    char *dz = ws, *dzt = dz + l.dz, *wt = dzt + l.dzt, *xt = wt + l.wt;
+    float *db = reinterpret_cast<float *>(xt + l.xt), *part = reinterpret_cast<float *>(xt + l.xt + l.db);
+    if (l.dz || l.dzt || l.db) {
+        st = ssd::launch_dz(dy, preact, act, l.dz ? dz : nullptr, l.dzt ? dzt : nullptr, l.db ? db : nullptr, rows, out,
+                            l.ldz, l.ldt, dtype, s);
+        if (st != SSD_OK) return st;
+    }
+    if (dbias && (st = ssd::launch_column_sums(db, dbias, (int)((rows + 63) / 64), out, s)) != SSD_OK) return st;
+    if (dx) {
+        if ((st = ssd::launch_transpose(w, wt, out, in, l.ldz, dtype, s)) != SSD_OK) return st;
+        ssd::LinearArgs a = {};
+        a.x = l.dz ? dz : dy; a.w = wt; a.y = dx; a.part = part; a.M = (int)rows; a.N = (int)in;
+        a.ldx = a.ldw = l.ldz * es; a.kbytes = (uint32_t)a.ldx;
+        if ((st = ssd::launch_linear(a, l.px, false, dtype, s)) != SSD_OK) return st;
+    }
+    if (dw) {
+        if ((st = ssd::launch_transpose(x, xt, rows, in, l.ldt, dtype, s)) != SSD_OK) return st;
+        ssd::LinearArgs a = {};
+        a.x = dzt; a.w = xt; a.y = dw; a.part = part; a.M = (int)out; a.N = (int)in;
+        a.ldx = a.ldw = l.ldt * es; a.kbytes = (uint32_t)a.ldx;
+        if ((st = ssd::launch_linear(a, l.pw, false, dtype, s)) != SSD_OK) return st;
+    }
+    return SSD_OK;
+}
 
 ssd_status ssd_rms_norm(const void *x, const void *residual, const float *weight, float eps, void *residual_out,
                         void *y, float *rstd, int64_t rows, int64_t dim, int64_t groups, ssd_dtype dtype,
@@ -127,7 +332,7 @@ ssd_status ssd_rms_norm_bwd(const void *dy, const void *h, const float *weight, 
     const int64_t need = (int64_t)ssd_rms_norm_bwd_workspace_bytes(rows, dim, groups, dtype, residual_dtype);
     if ((st = check_workspace(need, workspace, workspace_bytes)) != SSD_OK) return st;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    if (rows == 0) return clear(dweight, dim, s);
+    if (rows == 0) return clear(dweight, dim * 4, s);
     ssd::NormBwdArgs a = {};
     a.dy = dy; a.h = h; a.dres = d_residual_out; a.w = weight; a.rstd = rstd; a.dx = dx; a.dh = d_residual;
     a.dw = dweight; a.part = static_cast<float *>(workspace); a.rows = rows; a.groups = groups;

@@ -1,0 +1,506 @@
+// Matrix products of a layer's projections for gfx950, with the epilogue fused:
+//
+//   z[m, n] = sum_k x[m, k] w[n, k] + bias[n];   y = act(z) + r[m, n]
+//
+// from bf16, fp32 or 8-bit operands (e4m3 codes with one power of two for each
+// 32 along k), and the pieces of the backward pass. Sums are fp32 (matrix
+// cores); y is rounded once, at the end, and z once where it is kept.
+//
+// k_tile: a work-group forms a BM x BN tile of y. A step takes 128 bytes of
+// every row of x and w (64 bf16, 32 fp32 or 128 codes): they go straight from
+// memory to LDS (16 bytes a lane, no registers), one step ahead of the one
+// being multiplied, into the other of two buffers. A row's 8 chunks of 16
+// bytes lie at chunk ^ (row % 8), so that the 8 rows that one LDS cycle reads
+// lie in different banks; since the loads write LDS in lane order, the lanes
+// permute the addresses they load from. Lane l = 16 kg + r takes chunks kg and
+// kg + 4 of its row: that is the order of k that the 8-bit product's scales
+// imply (lane kg's scale is that of k in [32 kg, 32 kg + 32)), and any order
+// does for the other types as long as x and w share it. The 8-bit product
+// (twice the bf16 rate) adds 8 consecutive k in fixed point, 13 bits below the
+// largest of the 8 products, and everything else in fp32: measured on random
+// codes, 2^-15.7 of the sum of magnitudes on average, some 1e-4 of a result at
+// in = 2048, where the codes' own rounding is 2.6e-2. Products in bf16 (every
+// code is a bf16) would be exact at half the rate.
+//
+// The product is formed as w x^T, so that a lane holds 4 consecutive n of one
+// row; the epilogue turns 16 x (columns of a wavefront) at a time through LDS
+// into whole lines of rows.
+//
+// k_skinny (up to 64 rows, decoding): the time is one read of w. A
+// work-group takes 16 rows of w, its 8 wavefronts split k, and both operands
+// go from memory to the matrix cores' registers; the 8 shares are added
+// through LDS.
+#include "ssd_common.h"
+#include "ssd_internal.h"
+
+namespace ssd {
+
+constexpr int kBF16 = 0, kF32 = 1, kMX = 2;
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void lds_void;
+
+// 128 bytes (lane's 2 x 16) of a row of w against those of a row of x.
+template <int KIND>
+__device__ __forceinline__ f32x4 mma2(u32x4 wl, u32x4 wh, u32x4 xl, u32x4 xh, f32x4 c, int sw, int sx) {
+    if constexpr (KIND == kBF16) {
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wl), __builtin_bit_cast(bf16x8, xl), c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wh), __builtin_bit_cast(bf16x8, xh), c, 0, 0, 0);
+    } else if constexpr (KIND == kF32) {
+        const f32x4 a = __builtin_bit_cast(f32x4, wl), b = __builtin_bit_cast(f32x4, xl);
+        const f32x4 d = __builtin_bit_cast(f32x4, wh), e = __builtin_bit_cast(f32x4, xh);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(d[i], e[i], c, 0, 0, 0);
+    } else {
+        typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
+        const u32x8 w = __builtin_shufflevector(wl, wh, 0, 1, 2, 3, 4, 5, 6, 7);
+        const u32x8 x = __builtin_shufflevector(xl, xh, 0, 1, 2, 3, 4, 5, 6, 7);
+        c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8, w), __builtin_bit_cast(i32x8, x),
+                                                             c, 0, 0, 0, sw, 0, sx);
+    }
+    return c;
+}
+
+__device__ __forceinline__ float act_of(float z, int act) {
+    if (act == SSD_ACT_SILU) return z / (1.f + expf(-z));
+    if (act == SSD_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    return z;
+}
+// d act / dz
+__device__ __forceinline__ float act_slope(float z, int act) {
+    if (act == SSD_ACT_SILU) {
+        const float g = 1.f / (1.f + expf(-z));
+        return g * (1.f + z * (1.f - g));
+    }
+    if (act == SSD_ACT_GELU)
+        return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.3989422804014327f * expf(-0.5f * z * z);
+    return 1.f;
+}
+
+template <typename TO>
+__device__ __forceinline__ void put4(TO *p, const float (&v)[4], int n, bool whole) {
+    if (whole) {
+        if constexpr (sizeof(TO) == 2) {
+            *reinterpret_cast<bf16x4 *>(p) = bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
+        } else {
+            *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p[i] = (TO)v[i];
+    }
+}
+
+// The epilogue of 4 consecutive columns n .. n + 3 of row m.
+template <typename TO>
+__device__ __forceinline__ void finish4(const LinearArgs &a, int m, int n, float (&v)[4]) {
+    const int left = a.N - n;
+    if (m >= a.M || left <= 0) return;
+    const int64_t at = (int64_t)m * a.N + n;
+    const bool whole = (a.N & 3) == 0;  // then n is a multiple of 4 too: every group of 4 is whole and aligned
+    if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < left) v[i] += a.bias[n + i];
+    }
+    if (a.pre) put4<TO>(reinterpret_cast<TO *>(a.pre) + at, v, left, whole);
+    if (a.act != SSD_ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = act_of(v[i], a.act);
+    }
+    if (a.res) {
+        const TO *r = reinterpret_cast<const TO *>(a.res) + at;
+        if (whole) {
+            if constexpr (sizeof(TO) == 2) {
+                const bf16x4 q = *reinterpret_cast<const bf16x4 *>(r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += (float)q[i];
+            } else {
+                const f32x4 q = *reinterpret_cast<const f32x4 *>(r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += q[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < left) v[i] += (float)r[i];
+        }
+    }
+    put4<TO>(reinterpret_cast<TO *>(a.y) + at, v, left, whole);
+}
+
+// Tile number of a work-group: consecutive ones on one XCD (work-groups are
+// dealt to the 8 XCDs in turn), walked down columns of 8 tiles of m, so that
+// an XCD's L2 sees few rows of x and w at a time.
+__device__ __forceinline__ void tile_of(int id, int nm, int nn, int &tm, int &tn) {
+    const int total = nm * nn, per = total >> 3, more = total & 7;
+    const int xcd = id & 7, k = id >> 3;
+    const int t = xcd * per + (xcd < more ? xcd : more) + k;
+    constexpr int G = 8;
+    const int band = t / (G * nn), in = t - band * G * nn;
+    const int rows = min(G, nm - band * G);
+    tm = band * G + in % rows;
+    tn = in / rows;
+}
+
+template <int KIND, typename TO, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
+    constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
+    constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // loads per wavefront and step, 8 rows each
+    static_assert(LA * 8 * NW == BM && LB * 8 * NW == BN, "rows divide over the wavefronts");
+    static_assert(KIND != kMX || BM + BN == 64 * NW, "one load of scales per wavefront and step");
+    // one array per buffer: the compiler then knows that reads of one do not wait for the loads into the other
+    __shared__ __attribute__((aligned(128))) char s0[(BM + BN) * 128];
+    __shared__ __attribute__((aligned(128))) char s1[(BM + BN) * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t q0[KIND == kMX ? (BM + BN) * 4 : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t q1[KIND == kMX ? (BM + BN) * 4 : 16];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int r = lane & 15, kg = lane >> 4;
+    int tm, tn;
+    tile_of(blockIdx.x, a.nm, a.nn, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+    const int64_t rows_a = min(BM, a.M - m0), rows_b = min(BN, a.N - n0);
+    const rsrc_t ra = make_rsrc(reinterpret_cast<const char *>(a.x) + (int64_t)m0 * a.ldx, (uint32_t)(rows_a * a.ldx));
+    const rsrc_t rb = make_rsrc(reinterpret_cast<const char *>(a.w) + (int64_t)n0 * a.ldw, (uint32_t)(rows_b * a.ldw));
+    const uint32_t ldx = (uint32_t)a.ldx, ldw = (uint32_t)a.ldw;
+    // this lane's chunk of the 8 rows of a load
+    const uint32_t chunk = (uint32_t)(((lane & 7) ^ (lane >> 3)) << 4);
+    const uint32_t va = (uint32_t)(lane >> 3) * ldx + chunk, vb = (uint32_t)(lane >> 3) * ldw + chunk;
+    rsrc_t rs = ra;
+    uint32_t vs = 0;
+    if constexpr (KIND == kMX) {
+        // scales: wavefronts below BM / 64 take rows of x, the others rows of w; 4 bytes a row and step
+        const bool of_x = w < BM / 64;
+        const int row0 = of_x ? m0 + w * 64 : n0 + (w - BM / 64) * 64, most = of_x ? a.M : a.N;
+        const int64_t rows = max(0, min(64, most - row0));
+        const uint8_t *p = (of_x ? a.xscale + (int64_t)row0 * a.lds : a.wscale + (int64_t)row0 * a.lds);
+        rs = make_rsrc(rows > 0 ? p : a.xscale, (uint32_t)(rows * a.lds));
+        vs = (uint32_t)lane * (uint32_t)a.lds;
+    }
+    const int per = a.steps_per_split, first = (int)blockIdx.y * per;
+    const int steps = min(per, a.steps - first);
+
+    auto fetch = [&](int s, char *buf, uint8_t *sc) {
+        const uint32_t k0 = (uint32_t)(first + s) * 128u;
+        // the last step may end inside its 128 bytes: chunks behind the row's end become zeros. Only k0,
+        // which lies inside every range, goes into the scalar offset: that one is subtracted from the
+        // range before the comparison
+        const uint32_t off = oob_if(k0 + chunk >= a.kbytes, 0);
+#pragma unroll
+        for (int j = 0; j < LA; ++j) {
+            const int row = (w * LA + j) * 8;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(buf + row * 128), 16, (va + (uint32_t)row * ldx) | off, k0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < LB; ++j) {
+            const int row = (w * LB + j) * 8;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)(buf + (BM + row) * 128), 16, (vb + (uint32_t)row * ldw) | off, k0, 0, 0);
+        }
+        if constexpr (KIND == kMX)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(sc + w * 256), 4, vs + (uint32_t)(first + s) * 4u, 0, 0, 0);
+    };
+
+    const int wm = w / WN, wn = w % WN;
+    const int pa = (wm * TM * 16 + r) * 128 + ((kg ^ (r & 7)) << 4);       // chunk kg of row r; kg + 4 is at ^ 64
+    const int pb = (BM + wn * TN * 16 + r) * 128 + ((kg ^ (r & 7)) << 4);
+    f32x4 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    auto multiply = [&](const char *buf, const uint8_t *sc) {
+        u32x4 wl[TN], wh[TN];
+        int sw[TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            wl[j] = *reinterpret_cast<const u32x4 *>(buf + pb + j * 2048);
+            wh[j] = *reinterpret_cast<const u32x4 *>(buf + (pb ^ 64) + j * 2048);
+            sw[j] = KIND == kMX ? sc[(BM + (wn * TN + j) * 16 + r) * 4 + kg] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const u32x4 xl = *reinterpret_cast<const u32x4 *>(buf + pa + i * 2048);
+            const u32x4 xh = *reinterpret_cast<const u32x4 *>(buf + (pa ^ 64) + i * 2048);
+            const int sx = KIND == kMX ? sc[((wm * TM + i) * 16 + r) * 4 + kg] : 0;
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = mma2<KIND>(wl[j], wh[j], xl, xh, acc[i][j], sw[j], sx);
+        }
+    };
+
+    if (steps > 0) fetch(0, s0, q0);
+    for (int s = 0; s < steps; s += 2) {
+        __syncthreads();  // step s has arrived, and everybody is done with the other buffer
+        if (s + 1 < steps) fetch(s + 1, s1, q1);
+        multiply(s0, q0);
+        if (s + 1 >= steps) break;
+        __syncthreads();
+        if (s + 2 < steps) fetch(s + 2, s0, q0);
+        multiply(s1, q1);
+    }
+    __syncthreads();
+
+    // epilogue: 16 rows of the wavefront's columns at a time through LDS
+    constexpr int CW = TN * 16, LDC = CW + 4;
+    static_assert(NW * 16 * LDC * 4 <= (BM + BN) * 128, "the wavefronts' pieces fit one buffer");
+    float *piece = reinterpret_cast<float *>(s0) + w * 16 * LDC;
+    const int mw = m0 + wm * TM * 16, nw = n0 + wn * CW;
+    constexpr int LPR = CW / 4, RPI = 64 / LPR;  // lanes per row, rows per pass
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) *reinterpret_cast<f32x4 *>(piece + r * LDC + j * 16 + kg * 4) = acc[i][j];
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int p = 0; p < 16 / RPI; ++p) {
+            const int row = p * RPI + lane / LPR, col = (lane % LPR) * 4;
+            const f32x4 c = *reinterpret_cast<const f32x4 *>(piece + row * LDC + col);
+            float v[4] = {c[0], c[1], c[2], c[3]};
+            const int m = mw + i * 16 + row, n = nw + col;
+            if (a.part) {
+                if (m < a.M && n < a.N) {
+                    float *o = a.part + ((int64_t)blockIdx.y * a.M + m) * a.N + n;
+                    put4<float>(o, v, a.N - n, (a.N & 3) == 0);
+                }
+            } else {
+                finish4<TO>(a, m, n, v);
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// The splits' parts of y, added in order, and the epilogue: 4 columns a thread.
+template <typename TO>
+__global__ __launch_bounds__(256) void k_join(LinearArgs a) {
+    const int n4 = (a.N + 3) / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)a.M * n4) return;
+    const int m = (int)(i / n4), n = (int)(i - (int64_t)m * n4) * 4;
+    const int64_t step = (int64_t)a.M * a.N;
+    const float *p = a.part + (int64_t)m * a.N + n;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if ((a.N & 3) == 0) {
+        for (int s = 0; s < a.splits; ++s, p += step) {
+            const f32x4 c = *reinterpret_cast<const f32x4 *>(p);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += c[e];
+        }
+    } else {
+        for (int s = 0; s < a.splits; ++s, p += step)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n + e < a.N) v[e] += p[e];
+    }
+    finish4<TO>(a, m, n, v);
+}
+
+template <int KIND, typename TO, int MT>
+__global__ __launch_bounds__(512) void k_skinny(LinearArgs a) {
+    __shared__ __attribute__((aligned(16))) float red[8][MT][64][4];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int r = lane & 15, kg = lane >> 4;
+    const int n0 = blockIdx.x * 16;
+    const rsrc_t rw = make_rsrc(reinterpret_cast<const char *>(a.w) + (int64_t)n0 * a.ldw, (uint32_t)(min(16, a.N - n0) * a.ldw));
+    const rsrc_t rx = make_rsrc(a.x, (uint32_t)(a.M * a.ldx));
+    rsrc_t rsw = rw, rsx = rx;
+    if constexpr (KIND == kMX) {
+        rsw = make_rsrc(a.wscale + (int64_t)n0 * a.lds, (uint32_t)(min(16, a.N - n0) * a.lds));
+        rsx = make_rsrc(a.xscale, (uint32_t)(a.M * a.lds));
+    }
+    f32x4 acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const uint32_t ldx = (uint32_t)a.ldx, ldw = (uint32_t)a.ldw, ldsc = (uint32_t)a.lds;
+    // U steps' operands are loaded before the first is used; steps behind the last load zeros
+    constexpr int U = MT == 1 ? 4 : 2;
+    for (int s0 = w; s0 < a.steps; s0 += 8 * U) {
+        u32x4 wl[U], wh[U], xl[U][MT], xh[U][MT];
+        int sw[U], sx[U][MT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t c0 = (uint32_t)(s0 + 8 * u) * 128u + kg * 16u, c1 = c0 + 64u;
+            const uint32_t o0 = oob_if(c0 >= a.kbytes, c0), o1 = oob_if(c1 >= a.kbytes, c1);
+            const uint32_t b = (uint32_t)(s0 + 8 * u) * 4u + kg, ob = oob_if(b >= ldsc, b);
+            wl[u] = buf_ld128(rw, o0 + r * ldw);
+            wh[u] = buf_ld128(rw, o1 + r * ldw);
+            sw[u] = KIND == kMX ? (int)__builtin_amdgcn_raw_buffer_load_b8(rsw, ob + r * ldsc, 0, 0) : 0;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const uint32_t row = (uint32_t)(i * 16 + r);
+                xl[u][i] = buf_ld128(rx, o0 + row * ldx);
+                xh[u][i] = buf_ld128(rx, o1 + row * ldx);
+                sx[u][i] = KIND == kMX ? (int)__builtin_amdgcn_raw_buffer_load_b8(rsx, ob + row * ldsc, 0, 0) : 0;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) acc[i] = mma2<KIND>(wl[u], wh[u], xl[u][i], xh[u][i], acc[i], sw[u], sx[u][i]);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4 *>(red[w][i][lane]) = acc[i];
+    __syncthreads();
+    if (w < MT) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const f32x4 c = *reinterpret_cast<const f32x4 *>(red[k][w][lane]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += c[e];
+        }
+        finish4<TO>(a, w * 16 + r, n0 + kg * 4, v);
+    }
+}
+
+// Rows of `bytes` bytes copied to rows of ldo bytes (a multiple of 16), zeros
+// behind them: operands whose rows do not begin at multiples of 16 bytes.
+// ES bytes at a time.
+template <typename U>
+__global__ __launch_bounds__(256) void k_pad(const U *in, U *out, int64_t rows, int n, int ldo) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= rows * ldo) return;
+    const int64_t row = i / ldo;
+    const int c = (int)(i - row * ldo);
+    out[i] = c < n ? in[row * n + c] : (U)0;
+}
+
+// out (C x ldo) = in (R x C) transposed, zeros behind column R. 64 x 64 a work-group.
+template <typename T>
+__global__ __launch_bounds__(256) void k_transpose(const T *in, T *out, int R, int C, int ldo) {
+    __shared__ T sm[64][64 + 4 / sizeof(T)];
+    const int r0 = blockIdx.x * 64, c0 = blockIdx.y * 64, x = threadIdx.x & 63, y = threadIdx.x >> 6;
+    for (int i = y; i < 64; i += 4)
+        sm[i][x] = (r0 + i < R && c0 + x < C) ? in[(int64_t)(r0 + i) * C + c0 + x] : (T)0.f;
+    __syncthreads();
+    for (int i = y; i < 64; i += 4)
+        if (c0 + i < C && r0 + x < ldo) out[(int64_t)(c0 + i) * ldo + r0 + x] = sm[x][i];
+}
+
+// dz = dy act'(z) of 64 x 64: rows (M x ldz), the transpose (N x ldt), both
+// zeros behind their rows, and the 64 rows' share of db (fp32, before dz is
+// rounded).
+template <typename T>
+__global__ __launch_bounds__(256) void k_dz(const T *dy, const T *pre, int act, T *dz, T *dzt, float *part, int M, int N,
+                                            int ldz, int ldt) {
+    __shared__ T sm[64][64 + 4 / sizeof(T)];
+    __shared__ float col[4][64];
+    const int m0 = blockIdx.x * 64, n0 = blockIdx.y * 64, x = threadIdx.x & 63, y = threadIdx.x >> 6;
+    const int n = n0 + x;
+    float sum = 0.f;
+    for (int i = y; i < 64; i += 4) {
+        float v = 0.f;
+        if (m0 + i < M && n < N) {
+            const int64_t at = (int64_t)(m0 + i) * N + n;
+            v = (float)dy[at];
+            if (act != SSD_ACT_NONE) v *= act_slope((float)pre[at], act);
+        }
+        sum += v;
+        sm[i][x] = (T)v;
+        if (dz && m0 + i < M && n < ldz) dz[(int64_t)(m0 + i) * ldz + n] = (T)v;
+    }
+    col[y][x] = sum;
+    __syncthreads();
+    if (part && y == 0 && n < N) part[(int64_t)blockIdx.x * N + n] = col[0][x] + col[1][x] + col[2][x] + col[3][x];
+    if (dzt)
+        for (int i = y; i < 64; i += 4)
+            if (n0 + i < N && m0 + x < ldt) dzt[(int64_t)(n0 + i) * ldt + m0 + x] = sm[x][i];
+}
+
+static int kind_of(int dtype) { return dtype == SSD_BF16 ? kBF16 : kF32; }
+
+// How a product is formed. tile: 0 = k_skinny, else the tile's edge.
+// The model of a tile kernel's time, in units of one 128-byte step of a
+// 256-tile: work-groups run in rounds over the 256 CUs (two 128-tiles share a
+// CU), each round its steps and a fixed share for the start and the epilogue,
+// and a split adds the traffic of its fp32 parts.
+LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes) {
+    LinearPlan p = {};
+    p.steps = (int)((kbytes + 127) / 128);
+    p.splits = 1;
+    p.steps_per_split = p.steps;
+    if (M <= 64) return p;
+    double best = 1e300;
+    for (int tile = 128; tile <= 256; tile *= 2) {
+        const int64_t nm = (M + tile - 1) / tile, nn = (N + tile - 1) / tile;
+        for (int splits = 1; splits <= 32 && splits <= p.steps; splits += splits < 8 ? 1 : 4) {
+            const int per = (p.steps + splits - 1) / splits;
+            const int real = (p.steps + per - 1) / per;
+            if (real != splits) continue;
+            const double slots = tile == 256 ? 256 : 512;
+            const double rounds = (double)((int64_t)((nm * nn * splits + slots - 1) / slots));
+            double t = rounds * (per + 6) * (tile == 256 ? 1.0 : 0.6);
+            if (splits > 1) t += 6 + 2.0 * splits * M * N * 4 / 4.0e6;
+            if (t < best) {
+                best = t;
+                p.tile = tile;
+                p.splits = splits;
+                p.steps_per_split = per;
+                p.nm = (int)nm;
+                p.nn = (int)nn;
+            }
+        }
+    }
+    return p;
+}
+
+template <int KIND, typename TO>
+static ssd_status run_linear(const LinearArgs &a, const LinearPlan &p, hipStream_t s) {
+    hipError_t e;
+    if (p.tile == 0) {
+        const dim3 grid((unsigned)((a.N + 15) / 16)), block(512);
+        e = a.M <= 16   ? launch(k_skinny<KIND, TO, 1>, grid, block, s, a)
+            : a.M <= 32 ? launch(k_skinny<KIND, TO, 2>, grid, block, s, a)
+                        : launch(k_skinny<KIND, TO, 4>, grid, block, s, a);
+    } else {
+        const dim3 grid((unsigned)(p.nm * p.nn), (unsigned)p.splits);
+        e = p.tile == 256 ? launch(k_tile<KIND, TO, 256, 256, 2, 4>, grid, dim3(512), s, a)
+                          : launch(k_tile<KIND, TO, 128, 128, 2, 2>, grid, dim3(256), s, a);
+        if (e == hipSuccess && p.splits > 1) {
+            const int64_t n = (int64_t)a.M * ((a.N + 3) / 4);
+            e = launch(k_join<TO>, dim3((unsigned)((n + 255) / 256)), dim3(256), s, a);
+        }
+    }
+    return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+}
+
+ssd_status launch_linear(LinearArgs a, const LinearPlan &p, bool mx, ssd_dtype dtype, hipStream_t s) {
+    a.nm = p.nm; a.nn = p.nn; a.steps = p.steps; a.splits = p.splits; a.steps_per_split = p.steps_per_split;
+    if (p.splits == 1) a.part = nullptr;
+    if (mx) return run_linear<kMX, bf16>(a, p, s);
+    return dtype == SSD_BF16 ? run_linear<kBF16, bf16>(a, p, s) : run_linear<kF32, float>(a, p, s);
+}
+
+ssd_status launch_pad(const void *in, void *out, int64_t rows, int64_t n, int64_t ldo, int es, hipStream_t s) {
+    const dim3 grid((unsigned)((rows * ldo + 255) / 256)), block(256);
+    hipError_t e;
+    if (es == 1) e = launch(k_pad<uint8_t>, grid, block, s, (const uint8_t *)in, (uint8_t *)out, rows, (int)n, (int)ldo);
+    else if (es == 2) e = launch(k_pad<uint16_t>, grid, block, s, (const uint16_t *)in, (uint16_t *)out, rows, (int)n, (int)ldo);
+    else e = launch(k_pad<uint32_t>, grid, block, s, (const uint32_t *)in, (uint32_t *)out, rows, (int)n, (int)ldo);
+    return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+}
+
+ssd_status launch_transpose(const void *in, void *out, int64_t R, int64_t C, int64_t ldo, ssd_dtype dtype, hipStream_t s) {
+    const dim3 grid((unsigned)((ldo + 63) / 64), (unsigned)((C + 63) / 64)), block(256);
+    const hipError_t e =
+        dtype == SSD_BF16
+            ? launch(k_transpose<bf16>, grid, block, s, (const bf16 *)in, (bf16 *)out, (int)R, (int)C, (int)ldo)
+            : launch(k_transpose<float>, grid, block, s, (const float *)in, (float *)out, (int)R, (int)C, (int)ldo);
+    return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+}
+
+ssd_status launch_dz(const void *dy, const void *pre, int act, void *dz, void *dzt, float *part, int64_t M, int64_t N,
+                     int64_t ldz, int64_t ldt, ssd_dtype dtype, hipStream_t s) {
+    const int64_t nm = ((dzt ? ldt : M) + 63) / 64, nn = ((dz ? ldz : N) + 63) / 64;
+    const dim3 grid((unsigned)nm, (unsigned)nn), block(256);
+    const hipError_t e = dtype == SSD_BF16
+                             ? launch(k_dz<bf16>, grid, block, s, (const bf16 *)dy, (const bf16 *)pre, act, (bf16 *)dz,
+                                      (bf16 *)dzt, part, (int)M, (int)N, (int)ldz, (int)ldt)
+                             : launch(k_dz<float>, grid, block, s, (const float *)dy, (const float *)pre, act, (float *)dz,
+                                      (float *)dzt, part, (int)M, (int)N, (int)ldz, (int)ldt);
+    return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+}
+
+}  // namespace ssd

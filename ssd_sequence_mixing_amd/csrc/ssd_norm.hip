@@ -203,7 +203,7 @@ __global__ __launch_bounds__(kNormThreads) void k_mx_quantize(const TX *x, uint8
 //   dh = inv (g - hh mean(g hh)) + dr_out;   dw = sum over rows of dy hh
 // A work-group takes every nb-th row of one group (blockIdx.y) and keeps its
 // share of dw in registers, lane by lane the columns it reads; the shares are
-// added in a fixed order (wavefronts, then work-groups in k_rms_norm_dw), so
+// added in a fixed order (wavefronts, then work-groups in k_column_sums), so
 // the same inputs give the same bits.
 template <typename TX, typename TR, int W, int NC, bool V>
 __global__ __launch_bounds__(W > 4 ? W * 64 : kNormThreads) void k_rms_norm_bwd(NormBwdArgs a) {
@@ -287,9 +287,9 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : kNormThreads) void k_rms_norm_bwd(
     for (int c = 0; c < NC; ++c) st8<float, V>(dw[c], part, first(c), kStep, n);
 }
 
-// dw[d] = the nb shares of column d, added by 16 threads and then by one, in
+// out[d] = the nb shares of column d, added by 16 threads and then by one, in
 // order. One work-group takes 64 columns.
-__global__ __launch_bounds__(1024) void k_rms_norm_dw(const float *part, float *dw, int nb, int64_t D) {
+__global__ __launch_bounds__(1024) void k_column_sums(const float *part, float *out, int nb, int64_t D) {
     __shared__ float red[16][64];
     const int c = threadIdx.x & 63, k = threadIdx.x >> 6;
     const int64_t d = (int64_t)blockIdx.x * 64 + c;
@@ -303,8 +303,14 @@ __global__ __launch_bounds__(1024) void k_rms_norm_dw(const float *part, float *
     if (k == 0 && d < D) {
 #pragma unroll
         for (int j = 1; j < 16; ++j) s += red[j][c];
-        dw[d] = s;
+        out[d] = s;
     }
+}
+
+ssd_status launch_column_sums(const float *part, float *out, int nb, int64_t D, hipStream_t s) {
+    return launch(k_column_sums, dim3((unsigned)((D + 63) / 64)), dim3(1024), s, part, out, nb, D) == hipSuccess
+               ? SSD_OK
+               : SSD_ERR_HIP;
 }
 
 // How a row of n values is spread: wavefronts per row and chunks per lane.
@@ -408,11 +414,7 @@ ssd_status launch_rms_norm_bwd(const NormBwdArgs &a, hipStream_t s) {
                     : a.res_dtype == SSD_F32 ? norm_bwd_t<bf16, float>(a, s)
                                              : norm_bwd_t<bf16, bf16>(a, s);
     if (st != SSD_OK) return st;
-    const int64_t D = (int64_t)a.Dg * a.groups;
-    return launch(k_rms_norm_dw, dim3((unsigned)((D + 63) / 64)), dim3(1024), s, (const float *)a.part, a.dw, a.nb,
-                  D) == hipSuccess
-               ? SSD_OK
-               : SSD_ERR_HIP;
+    return launch_column_sums(a.part, a.dw, a.nb, (int64_t)a.Dg * a.groups, s);
 }
 
 }  // namespace ssd

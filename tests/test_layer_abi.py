@@ -140,3 +140,75 @@ def test_binding_refuses_what_the_library_would_misread():
         ssd.ssd_beam_select(torch.zeros(2, 3, 10), torch.zeros(2, 4))
     with pytest.raises(ValueError):
         ssd.ssd_beam_select(torch.zeros(2, 3, 10), torch.zeros(2, 3), finished=torch.zeros(2, 3))
+
+
+def linear(x=P, w=P, b=None, act=0, r=None, y=P, pre=None, rows=100, k=64, n=48, dtype=BF16, ws=P, wsb=1 << 40):
+    return ssd.raw_call("ssd_linear", x, w, b, act, r, y, pre, rows, k, n, dtype, ws, wsb, None)
+
+
+def linear_mx(x=P, xs=P, w=P, ws_=P, b=None, act=0, r=None, y=P, rows=100, k=64, n=48, ws=P, wsb=1 << 40):
+    return ssd.raw_call("ssd_linear_mx", x, xs, w, ws_, b, act, r, y, rows, k, n, ws, wsb, None)
+
+
+def linear_bwd(dy=P, x=P, w=P, act=1, pre=P, dx=P, dw=P, db=P, rows=100, k=64, n=48, dtype=BF16, ws=P, wsb=1 << 40):
+    return ssd.raw_call("ssd_linear_bwd", dy, x, w, act, pre, dx, dw, db, rows, k, n, dtype, ws, wsb, None)
+
+
+COMMON = [(dict(rows=-1), ESHAPE), (dict(k=0), ESHAPE), (dict(n=-3), ESHAPE), (dict(act=3), EUNSUP), (dict(act=-1), EUNSUP),
+          (dict(rows=(1 << 24) + 1), EUNSUP), (dict(k=1 << 21), EUNSUP), (dict(n=1 << 40), EUNSUP)]
+
+
+@pytest.mark.parametrize("kw,code", COMMON + [
+    (dict(x=None), ENULL), (dict(w=None), ENULL), (dict(y=None), ENULL), (dict(dtype=5), EUNSUP),
+    (dict(x=P + 2), EALIGN), (dict(w=P + 8), EALIGN), (dict(b=P + 4), EALIGN), (dict(r=P + 2), EALIGN),
+    (dict(pre=P + 2), EALIGN), (dict(k=63, ws=None), EWS), (dict(k=63, wsb=100), EWS), (dict(k=63, ws=P + 16), EALIGN),
+    (dict(rows=0, x=None, w=None, y=None), OK)])
+def test_linear_checks(kw, code):
+    assert linear(**kw) == code
+
+
+@pytest.mark.parametrize("kw,code", COMMON + [
+    (dict(x=None), ENULL), (dict(xs=None), ENULL), (dict(w=None), ENULL), (dict(ws_=None), ENULL), (dict(y=None), ENULL),
+    (dict(k=72), ESHAPE), (dict(xs=P + 4), EALIGN), (dict(ws_=P + 4), EALIGN), (dict(rows=0, y=None), OK)])
+def test_linear_mx_checks(kw, code):
+    assert linear_mx(**kw) == code
+
+
+@pytest.mark.parametrize("kw,code", COMMON + [
+    (dict(dy=None), ENULL), (dict(x=None), ENULL), (dict(w=None), ENULL), (dict(pre=None), ENULL), (dict(dtype=5), EUNSUP),
+    (dict(dx=P + 2), EALIGN), (dict(dw=P + 2), EALIGN), (dict(db=P + 4), EALIGN), (dict(pre=P + 2), EALIGN),
+    (dict(ws=None), EWS), (dict(wsb=1000), EWS), (dict(ws=P + 128), EALIGN), (dict(rows=0, dw=None, db=None), OK)])
+def test_linear_bwd_checks(kw, code):
+    assert linear_bwd(**kw) == code
+
+
+def test_linear_workspaces():
+    q = ssd.load().ssd_linear_workspace_bytes
+    assert q(8, 2048, 8512, BF16) == 0 and q(8192, 4096, 2048, BF16) == 0
+    # rows of 1003 fp32 values: both operands copied to rows of 1004
+    assert q(64, 1003, 515, F32) == 64 * 1004 * 4 + -(-515 * 1004 * 4 // 256) * 256
+    assert q(0, 1003, 515, F32) == 0 and q(-1, 64, 64, F32) == NONE and q(8, 64, 64, 9) == NONE
+    q = ssd.load().ssd_linear_mx_workspace_bytes
+    assert q(8, 96, 64) == 0 and q(8, 40, 64) == NONE
+    for rows in (0, 1, 1 << 20, (1 << 20) + 1, 1 << 40, -1):
+        for dim in (1, 7, 1 << 20, (1 << 20) + 1, 0):
+            ssd.load().ssd_linear_bwd_workspace_bytes(rows, dim, dim, 1, BF16)
+
+
+def test_linear_binding_refuses():
+    import torch
+    x, w = torch.zeros(4, 64), torch.zeros(8, 64)
+    with pytest.raises(ValueError):
+        ssd.ssd_linear(x, w[:, :32])
+    with pytest.raises(ValueError):
+        ssd.ssd_linear(x, w, bias=torch.zeros(64))
+    with pytest.raises(ValueError):
+        ssd.ssd_linear(x, w.bfloat16())
+    with pytest.raises(ValueError):
+        ssd.ssd_linear(x, w, residual=torch.zeros(4, 64))
+    with pytest.raises(ValueError):
+        ssd.ssd_linear(x, w, act="relu")
+    with pytest.raises(ValueError):
+        ssd.ssd_linear_bwd(torch.zeros(4, 8), x, w, act="silu")
+    with pytest.raises(ValueError):
+        ssd.ssd_linear_mx(x, x, w, w)
