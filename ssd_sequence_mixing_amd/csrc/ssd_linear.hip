@@ -30,14 +30,25 @@
 // work-group takes 16 rows of w, its 8 wavefronts split k, and both operands
 // go from memory to the matrix cores' registers; the 8 shares are added
 // through LDS.
+#include <type_traits>
+
 #include "ssd_common.h"
 #include "ssd_internal.h"
 
 namespace ssd {
 
 constexpr int kBF16 = 0, kF32 = 1, kMX = 2;
+constexpr int kParts = 3;  // beside the activations
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void lds_void;
+
+// 16 (4) bytes a lane from base + voff + soff, zeros behind `bytes`, to consecutive places from dst on.
+__device__ __forceinline__ void to_lds16(const void *base, uint32_t bytes, void *dst, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(base, bytes), (lds_void *)dst, 16, voff, soff, 0, 0);
+}
+__device__ __forceinline__ void to_lds4(const void *base, uint32_t bytes, void *dst, uint32_t voff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(base, bytes), (lds_void *)dst, 4, voff, 0, 0, 0);
+}
 
 // 128 bytes (lane's 2 x 16) of a row of w against those of a row of x.
 template <int KIND>
@@ -62,7 +73,7 @@ __device__ __forceinline__ f32x4 mma2(u32x4 wl, u32x4 wh, u32x4 xl, u32x4 xh, f3
     return c;
 }
 
-__device__ __forceinline__ float act_of(float z, int act) {
+__device__ __forceinline__ float act_of(float z, int act) {  // act: a constant where it is called
     if (act == SSD_ACT_SILU) return z / (1.f + expf(-z));
     if (act == SSD_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
     return z;
@@ -93,42 +104,67 @@ __device__ __forceinline__ void put4(TO *p, const float (&v)[4], int n, bool who
     }
 }
 
-// The epilogue of 4 consecutive columns n .. n + 3 of row m.
 template <typename TO>
-__device__ __forceinline__ void finish4(const LinearArgs &a, int m, int n, float (&v)[4]) {
+__device__ __forceinline__ void get4(float (&v)[4], const TO *p, int n, bool whole) {
+    if (whole) {
+        if constexpr (sizeof(TO) == 2) {
+            const bf16x4 q = *reinterpret_cast<const bf16x4 *>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = (float)q[i];
+        } else {
+            const f32x4 q = *reinterpret_cast<const f32x4 *>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = q[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = i < n ? (float)p[i] : 0.f;
+    }
+}
+
+// The epilogue of 4 consecutive columns n .. n + 3 of row m, with their bias
+// and residual (zeros where there is none) already loaded. kWhole: N is a
+// multiple of 4, so every group of 4 is whole and aligned.
+template <typename TO, int ACT, bool kWhole>
+__device__ __forceinline__ void finish4(const LinearArgs &a, int m, int n, float (&v)[4], const float (&bias)[4],
+                                        const float (&res)[4]) {
     const int left = a.N - n;
     if (m >= a.M || left <= 0) return;
     const int64_t at = (int64_t)m * a.N + n;
-    const bool whole = (a.N & 3) == 0;  // then n is a multiple of 4 too: every group of 4 is whole and aligned
-    if (a.bias) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < left) v[i] += a.bias[n + i];
+    for (int i = 0; i < 4; ++i) v[i] += bias[i];
+    if (a.pre) put4<TO>(reinterpret_cast<TO *>(a.pre) + at, v, left, kWhole);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = act_of(v[i], ACT) + res[i];
+    put4<TO>(reinterpret_cast<TO *>(a.y) + at, v, left, kWhole);
+}
+__device__ __forceinline__ void bias4(const LinearArgs &a, int n, float (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (a.bias && n + i < a.N) ? a.bias[n + i] : 0.f;
+}
+template <typename TO, bool kWhole>
+__device__ __forceinline__ void res4(const LinearArgs &a, int m, int n, float (&v)[4]) {
+    if (a.res && m < a.M && n < a.N) {
+        get4<TO>(v, reinterpret_cast<const TO *>(a.res) + (int64_t)m * a.N + n, a.N - n, kWhole);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = 0.f;
     }
-    if (a.pre) put4<TO>(reinterpret_cast<TO *>(a.pre) + at, v, left, whole);
-    if (a.act != SSD_ACT_NONE) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = act_of(v[i], a.act);
-    }
-    if (a.res) {
-        const TO *r = reinterpret_cast<const TO *>(a.res) + at;
-        if (whole) {
-            if constexpr (sizeof(TO) == 2) {
-                const bf16x4 q = *reinterpret_cast<const bf16x4 *>(r);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] += (float)q[i];
-            } else {
-                const f32x4 q = *reinterpret_cast<const f32x4 *>(r);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] += q[i];
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < left) v[i] += (float)r[i];
-        }
-    }
-    put4<TO>(reinterpret_cast<TO *>(a.y) + at, v, left, whole);
+}
+// Everything for one group of 4.
+template <typename TO>
+__device__ __forceinline__ void finish4_any(const LinearArgs &a, int m, int n, float (&v)[4]) {
+    float bias[4], res[4];
+    bias4(a, n, bias);
+    auto go = [&](auto whole) {
+        constexpr bool kWhole = decltype(whole)::value;
+        res4<TO, kWhole>(a, m, n, res);
+        if (a.act == SSD_ACT_SILU) finish4<TO, SSD_ACT_SILU, kWhole>(a, m, n, v, bias, res);
+        else if (a.act == SSD_ACT_GELU) finish4<TO, SSD_ACT_GELU, kWhole>(a, m, n, v, bias, res);
+        else finish4<TO, SSD_ACT_NONE, kWhole>(a, m, n, v, bias, res);
+    };
+    if ((a.N & 3) == 0) go(std::true_type{});
+    else go(std::false_type{});
 }
 
 // Tile number of a work-group: consecutive ones on one XCD (work-groups are
@@ -145,7 +181,8 @@ __device__ __forceinline__ void tile_of(int id, int nm, int nn, int &tm, int &tn
     tn = in / rows;
 }
 
-template <int KIND, typename TO, int BM, int BN, int WM, int WN>
+// EPI: the activation, or kParts to store the fp32 parts of a split sum
+template <int KIND, typename TO, int BM, int BN, int WM, int WN, int EPI>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
     constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // loads per wavefront and step, 8 rows each
@@ -161,45 +198,62 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
     int tm, tn;
     tile_of(blockIdx.x, a.nm, a.nn, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
-    const int64_t rows_a = min(BM, a.M - m0), rows_b = min(BN, a.N - n0);
-    const rsrc_t ra = make_rsrc(reinterpret_cast<const char *>(a.x) + (int64_t)m0 * a.ldx, (uint32_t)(rows_a * a.ldx));
-    const rsrc_t rb = make_rsrc(reinterpret_cast<const char *>(a.w) + (int64_t)n0 * a.ldw, (uint32_t)(rows_b * a.ldw));
-    const uint32_t ldx = (uint32_t)a.ldx, ldw = (uint32_t)a.ldw;
+    // A load takes 8 rows; each has a resource of its own that ends with the operand, so that one
+    // offset per lane serves all. Loads whole behind the operand take its first 8 rows of this tile
+    // instead: their rows of y are not stored.
+    const char *xrow[LA], *wrow[LB];
+    uint32_t xlen[LA], wlen[LB];
+#pragma unroll
+    for (int j = 0; j < LA; ++j) {
+        int row = m0 + (w * LA + j) * 8;
+        row = row < a.M ? row : m0;
+        xrow[j] = reinterpret_cast<const char *>(a.x) + (int64_t)row * a.ldx;
+        xlen[j] = (uint32_t)(min(8, a.M - row) * a.ldx);
+    }
+#pragma unroll
+    for (int j = 0; j < LB; ++j) {
+        int row = n0 + (w * LB + j) * 8;
+        row = row < a.N ? row : n0;
+        wrow[j] = reinterpret_cast<const char *>(a.w) + (int64_t)row * a.ldw;
+        wlen[j] = (uint32_t)(min(8, a.N - row) * a.ldw);
+    }
     // this lane's chunk of the 8 rows of a load
     const uint32_t chunk = (uint32_t)(((lane & 7) ^ (lane >> 3)) << 4);
-    const uint32_t va = (uint32_t)(lane >> 3) * ldx + chunk, vb = (uint32_t)(lane >> 3) * ldw + chunk;
-    rsrc_t rs = ra;
-    uint32_t vs = 0;
+    const uint32_t va = (uint32_t)(lane >> 3) * (uint32_t)a.ldx + chunk, vb = (uint32_t)(lane >> 3) * (uint32_t)a.ldw + chunk;
+    const uint8_t *srow = nullptr;
+    uint32_t slen = 0, vs = 0;
     if constexpr (KIND == kMX) {
         // scales: wavefronts below BM / 64 take rows of x, the others rows of w; 4 bytes a row and step
         const bool of_x = w < BM / 64;
         const int row0 = of_x ? m0 + w * 64 : n0 + (w - BM / 64) * 64, most = of_x ? a.M : a.N;
         const int64_t rows = max(0, min(64, most - row0));
         const uint8_t *p = (of_x ? a.xscale + (int64_t)row0 * a.lds : a.wscale + (int64_t)row0 * a.lds);
-        rs = make_rsrc(rows > 0 ? p : a.xscale, (uint32_t)(rows * a.lds));
+        srow = rows > 0 ? p : a.xscale;
+        slen = (uint32_t)(rows * a.lds);
         vs = (uint32_t)lane * (uint32_t)a.lds;
     }
     const int per = a.steps_per_split, first = (int)blockIdx.y * per;
     const int steps = min(per, a.steps - first);
 
     auto fetch = [&](int s, char *buf, uint8_t *sc) {
-        const uint32_t k0 = (uint32_t)(first + s) * 128u;
-        // the last step may end inside its 128 bytes: chunks behind the row's end become zeros. Only k0,
-        // which lies inside every range, goes into the scalar offset: that one is subtracted from the
-        // range before the comparison
-        const uint32_t off = oob_if(k0 + chunk >= a.kbytes, 0);
+        // a step behind the last loads zeros, and so do the chunks behind the row's end where the last
+        // ends inside its 128 bytes. Only k0, which lies inside every range, goes into the scalar offset:
+        // that one is subtracted from the range before the comparison
+        const bool live = s < steps;
+        const uint32_t k0 = live ? (uint32_t)(first + s) * 128u : 0u;
+        const uint32_t off = oob_if(!live || k0 + chunk >= a.kbytes, 0);
 #pragma unroll
         for (int j = 0; j < LA; ++j) {
             const int row = (w * LA + j) * 8;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(buf + row * 128), 16, (va + (uint32_t)row * ldx) | off, k0, 0, 0);
+            to_lds16(xrow[j], xlen[j], buf + row * 128, va | off, k0);
         }
 #pragma unroll
         for (int j = 0; j < LB; ++j) {
             const int row = (w * LB + j) * 8;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)(buf + (BM + row) * 128), 16, (vb + (uint32_t)row * ldw) | off, k0, 0, 0);
+            to_lds16(wrow[j], wlen[j], buf + (BM + row) * 128, vb | off, k0);
         }
         if constexpr (KIND == kMX)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(sc + w * 256), 4, vs + (uint32_t)(first + s) * 4u, 0, 0, 0);
+            to_lds4(srow, slen, sc + w * 256, (vs + (uint32_t)(first + s) * 4u) | oob_if(!live, 0));
     };
 
     const int wm = w / WN, wn = w % WN;
@@ -211,34 +265,76 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    auto multiply = [&](const char *buf, const uint8_t *sc) {
-        u32x4 wl[TN], wh[TN];
-        int sw[TN];
+    // A step's products go in NQ parts, TQ of the wavefront's row blocks each. The
+    // operands of a part are read while the part before it is multiplied: the first
+    // part of the next step (and its w) during this step's last, right behind the
+    // barrier, so that the matrix cores have work across it.
+    constexpr int NQ = KIND == kMX ? TM : 4, TQ = TM / NQ;  // 8 bits: registers for the scales, too
+    static_assert(TQ * NQ == TM && NQ % 2 == 0, "parts of a step");
+    struct WRegs {
+        u32x4 l[TN], h[TN];
+        int s[TN];
+    } w0, w1;
+    struct XRegs {
+        u32x4 l[TQ], h[TQ];
+        int s[TQ];
+    } x0, x1;
+    auto read_w = [&](WRegs &f, const char *buf, const uint8_t *sc) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-            wl[j] = *reinterpret_cast<const u32x4 *>(buf + pb + j * 2048);
-            wh[j] = *reinterpret_cast<const u32x4 *>(buf + (pb ^ 64) + j * 2048);
-            sw[j] = KIND == kMX ? sc[(BM + (wn * TN + j) * 16 + r) * 4 + kg] : 0;
-        }
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const u32x4 xl = *reinterpret_cast<const u32x4 *>(buf + pa + i * 2048);
-            const u32x4 xh = *reinterpret_cast<const u32x4 *>(buf + (pa ^ 64) + i * 2048);
-            const int sx = KIND == kMX ? sc[((wm * TM + i) * 16 + r) * 4 + kg] : 0;
-#pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] = mma2<KIND>(wl[j], wh[j], xl, xh, acc[i][j], sw[j], sx);
+            f.l[j] = *reinterpret_cast<const u32x4 *>(buf + pb + j * 2048);
+            f.h[j] = *reinterpret_cast<const u32x4 *>(buf + (pb ^ 64) + j * 2048);
+            f.s[j] = KIND == kMX ? sc[(BM + (wn * TN + j) * 16 + r) * 4 + kg] : 0;
         }
     };
+    auto read_x = [&](XRegs &f, const char *buf, const uint8_t *sc, int q) {
+#pragma unroll
+        for (int i = 0; i < TQ; ++i) {
+            f.l[i] = *reinterpret_cast<const u32x4 *>(buf + pa + (q * TQ + i) * 2048);
+            f.h[i] = *reinterpret_cast<const u32x4 *>(buf + (pa ^ 64) + (q * TQ + i) * 2048);
+            f.s[i] = KIND == kMX ? sc[((wm * TM + q * TQ + i) * 16 + r) * 4 + kg] : 0;
+        }
+    };
+    auto multiply = [&](const WRegs &wf, const XRegs &xf, int q) {
+#pragma unroll
+        for (int i = 0; i < TQ; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                acc[q * TQ + i][j] = mma2<KIND>(wf.l[j], wf.h[j], xf.l[i], xf.h[i], acc[q * TQ + i][j], wf.s[j], xf.s[i]);
+    };
+    auto step = [&](int s, char *buf, uint8_t *sc, char *nbuf, uint8_t *nsc, WRegs &wf, WRegs &nwf) {
+#pragma unroll
+        for (int q = 0; q < NQ - 1; ++q) {
+            read_x((q & 1) ? x0 : x1, buf, sc, q + 1);
+            __builtin_amdgcn_sched_barrier(0);  // the compiler would move every read down to its first use
+            multiply(wf, (q & 1) ? x1 : x0, q);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        __syncthreads();  // step s + 1 has arrived, and everybody has read all of step s
+        __builtin_amdgcn_sched_barrier(0);
+        read_w(nwf, nbuf, nsc);
+        read_x(x0, nbuf, nsc, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        fetch(s + 2, buf, sc);
+        multiply(wf, x1, NQ - 1);
+        // the loads between the products, not in front of them
+#pragma unroll
+        for (int j = 0; j < LA + LB; ++j) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
 
-    if (steps > 0) fetch(0, s0, q0);
+    // pairs of steps, without a branch: the accumulators then stay where they are
+    fetch(0, s0, q0);
+    __syncthreads();
+    fetch(1, s1, q1);
+    read_w(w0, s0, q0);
+    read_x(x0, s0, q0, 0);
     for (int s = 0; s < steps; s += 2) {
-        __syncthreads();  // step s has arrived, and everybody is done with the other buffer
-        if (s + 1 < steps) fetch(s + 1, s1, q1);
-        multiply(s0, q0);
-        if (s + 1 >= steps) break;
-        __syncthreads();
-        if (s + 2 < steps) fetch(s + 2, s0, q0);
-        multiply(s1, q1);
+        step(s, s0, q0, s1, q1, w0, w1);
+        step(s + 1, s1, q1, s0, q0, w1, w0);
     }
     __syncthreads();
 
@@ -246,28 +342,74 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
     constexpr int CW = TN * 16, LDC = CW + 4;
     static_assert(NW * 16 * LDC * 4 <= (BM + BN) * 128, "the wavefronts' pieces fit one buffer");
     float *piece = reinterpret_cast<float *>(s0) + w * 16 * LDC;
-    const int mw = m0 + wm * TM * 16, nw = n0 + wn * CW;
-    constexpr int LPR = CW / 4, RPI = 64 / LPR;  // lanes per row, rows per pass
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
+    constexpr int LPR = CW / 4, RPI = 64 / LPR, NP = 16 / RPI;  // lanes per row, rows per pass, passes
+    const int mw = m0 + wm * TM * 16 + lane / LPR, col = (lane % LPR) * 4, n = n0 + wn * CW + col;
+    auto stage = [&](int i) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) *reinterpret_cast<f32x4 *>(piece + r * LDC + j * 16 + kg * 4) = acc[i][j];
         __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-        for (int p = 0; p < 16 / RPI; ++p) {
-            const int row = p * RPI + lane / LPR, col = (lane % LPR) * 4;
-            const f32x4 c = *reinterpret_cast<const f32x4 *>(piece + row * LDC + col);
-            float v[4] = {c[0], c[1], c[2], c[3]};
-            const int m = mw + i * 16 + row, n = nw + col;
-            if (a.part) {
-                if (m < a.M && n < a.N) {
-                    float *o = a.part + ((int64_t)blockIdx.y * a.M + m) * a.N + n;
-                    put4<float>(o, v, a.N - n, (a.N & 3) == 0);
-                }
-            } else {
-                finish4<TO>(a, m, n, v);
+    };
+    auto staged = [&](int p, float (&v)[4]) {
+        const f32x4 c = *reinterpret_cast<const f32x4 *>(piece + (p * RPI + lane / LPR) * LDC + col);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = c[e];
+    };
+    if constexpr (EPI == kParts) {
+        const bool whole = (a.N & 3) == 0;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            stage(i);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                float v[4];
+                staged(p, v);
+                const int m = mw + i * 16 + p * RPI;
+                if (m < a.M && n < a.N) put4<float>(a.part + ((int64_t)blockIdx.y * a.M + m) * a.N + n, v, a.N - n, whole);
             }
+            __builtin_amdgcn_wave_barrier();
         }
+        return;
+    }
+    float bias[4];
+    bias4(a, n, bias);
+    if (EPI == SSD_ACT_NONE && (a.N & 3) == 0) {
+        // the next 16 rows' residual is on its way while 16 rows are finished
+        float res[2][NP][4];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) res4<TO, true>(a, mw + p * RPI, n, res[0][p]);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            stage(i);
+            if (i + 1 < TM) {
+#pragma unroll
+                for (int p = 0; p < NP; ++p) res4<TO, true>(a, mw + (i + 1) * 16 + p * RPI, n, res[(i + 1) & 1][p]);
+            }
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                float v[4];
+                staged(p, v);
+                finish4<TO, SSD_ACT_NONE, true>(a, mw + i * 16 + p * RPI, n, v, bias, res[i & 1][p]);
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
+        return;
+    }
+    // rolled: unrolled, the activation's code would not fit the instruction cache (8192 x 2048 x 8512 took 349 us, not 286)
+    auto rows = [&](int i, auto whole) {
+        constexpr bool kWhole = decltype(whole)::value;
+#pragma unroll 1
+        for (int p = 0; p < NP; ++p) {
+            float v[4], res[4];
+            res4<TO, kWhole>(a, mw + i * 16 + p * RPI, n, res);
+            staged(p, v);
+            finish4<TO, EPI, kWhole>(a, mw + i * 16 + p * RPI, n, v, bias, res);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        stage(i);
+        if ((a.N & 3) == 0) rows(i, std::true_type{});
+        else rows(i, std::false_type{});
         __builtin_amdgcn_wave_barrier();
     }
 }
@@ -294,7 +436,7 @@ __global__ __launch_bounds__(256) void k_join(LinearArgs a) {
             for (int e = 0; e < 4; ++e)
                 if (n + e < a.N) v[e] += p[e];
     }
-    finish4<TO>(a, m, n, v);
+    finish4_any<TO>(a, m, n, v);
 }
 
 template <int KIND, typename TO, int MT>
@@ -351,7 +493,7 @@ __global__ __launch_bounds__(512) void k_skinny(LinearArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] += c[e];
         }
-        finish4<TO>(a, w * 16 + r, n0 + kg * 4, v);
+        finish4_any<TO>(a, w * 16 + r, n0 + kg * 4, v);
     }
 }
 
@@ -456,8 +598,15 @@ static ssd_status run_linear(const LinearArgs &a, const LinearPlan &p, hipStream
                         : launch(k_skinny<KIND, TO, 4>, grid, block, s, a);
     } else {
         const dim3 grid((unsigned)(p.nm * p.nn), (unsigned)p.splits);
-        e = p.tile == 256 ? launch(k_tile<KIND, TO, 256, 256, 2, 4>, grid, dim3(512), s, a)
-                          : launch(k_tile<KIND, TO, 128, 128, 2, 2>, grid, dim3(256), s, a);
+        auto go = [&](auto epi) {
+            constexpr int EPI = decltype(epi)::value;
+            return p.tile == 256 ? launch(k_tile<KIND, TO, 256, 256, 2, 4, EPI>, grid, dim3(512), s, a)
+                                 : launch(k_tile<KIND, TO, 128, 128, 2, 2, EPI>, grid, dim3(256), s, a);
+        };
+        e = p.splits > 1                 ? go(std::integral_constant<int, kParts>{})
+            : a.act == SSD_ACT_SILU ? go(std::integral_constant<int, SSD_ACT_SILU>{})
+            : a.act == SSD_ACT_GELU ? go(std::integral_constant<int, SSD_ACT_GELU>{})
+                                    : go(std::integral_constant<int, SSD_ACT_NONE>{});
         if (e == hipSuccess && p.splits > 1) {
             const int64_t n = (int64_t)a.M * ((a.N + 3) / 4);
             e = launch(k_join<TO>, dim3((unsigned)((n + 255) / 256)), dim3(256), s, a);
