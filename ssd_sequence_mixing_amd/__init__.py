@@ -30,6 +30,8 @@ SSD_BF16 = 1
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libssd.so")
 _lib = None
+torch = None   # imported by load(): libssd binds to torch's HIP runtime
+_CODES = {}    # storage types
 
 # Entry points include/ssd.h declares.
 EXPORTS = ("ssd_status_string", "ssd_chunk_scan_fwd_workspace_bytes", "ssd_chunk_scan_fwd",
@@ -84,14 +86,16 @@ def load():
     bring in a second HIP runtime (torch asks for its copy under another
     name), and device memory and streams owned by one runtime are not valid
     in the other."""
-    global _lib
+    global _lib, torch
     if _lib is not None:
         return _lib
     if not os.path.exists(_LIB_PATH):
         raise FileNotFoundError(
             f"{_LIB_PATH} is missing: build it with `python -m ssd_sequence_mixing_amd.build` "
             "(or __graft_entry__.build()). There is no fallback path.")
-    import torch  # noqa: F401  (see the docstring: one HIP runtime per process)
+    import torch as t  # see the docstring: one HIP runtime per process
+    torch = t
+    _CODES.update({t.bfloat16: SSD_BF16, t.float32: SSD_F32})
     lib = ctypes.CDLL(_LIB_PATH)
     runtimes = _hip_runtimes_mapped()
     if len(runtimes) > 1:
@@ -162,18 +166,19 @@ def ssd_status_string(code: int) -> str:
 
 
 def _dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return SSD_BF16
-    if t.dtype == torch.float32:
-        return SSD_F32
-    raise TypeError(f"unsupported storage dtype {t.dtype}; use torch.bfloat16 or torch.float32")
+    code = _CODES.get(t.dtype)
+    if code is None:
+        load()
+        if t.dtype not in _CODES:
+            raise TypeError(f"unsupported storage dtype {t.dtype}; use torch.bfloat16 or torch.float32")
+        code = _CODES[t.dtype]
+    return code
 
 
 def _chk(name: str, t, shape, dtype) -> None:
     """Raises ValueError unless tensor t (when given) has this shape and dtype:
     the C ABI takes raw pointers and trusts the sizes it is told."""
-    if t is None:
+    if t is None or (t.shape == shape and t.dtype == dtype):
         return
     if tuple(t.shape) != tuple(int(d) for d in shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(int(d) for d in shape)}")
@@ -187,7 +192,6 @@ def _check_scan(X, dt, A, B, C, D, *, Y=None, final_state=None, initial_state=No
     X (b, T, H, P) and B (b, T, G, N), or for a packed batch X (total, H, P) and
     B (total, G, N) with packed_seqs sequences. X, dt, B, C, Y, z, dY share one
     storage dtype; A, D and the states are fp32."""
-    import torch
     if packed_seqs is None:
         if X.dim() != 4 or B.dim() != 4:
             raise ValueError("X must be (batch, T, H, P) and B (batch, T, G, N)")
@@ -217,7 +221,6 @@ def _check_scan(X, dt, A, B, C, D, *, Y=None, final_state=None, initial_state=No
 def _check_step(state, x, dt, A, B, C, D, y=None, z=None):
     """Shapes and dtypes of a decode step's tensors against state (b, H, P, N)
     and B (b, G, N)."""
-    import torch
     if state.dim() != 4 or B.dim() != 3:
         raise ValueError("state must be (batch, H, P, N) and B (batch, G, N)")
     bsz, H, P, N = state.shape
@@ -246,9 +249,8 @@ def _ptr(t) -> Optional[int]:
 
 
 def _stream(stream) -> Optional[int]:
-    import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -268,7 +270,6 @@ def ssd_chunk_scan_fwd(X, dt, A, B, C, D, chunk: int, Y=None, final_state=None, 
 
     Returns (Y, final_state); final_state is None when want_final is False and
     none was passed in."""
-    import torch
     lib = load()
     _check_scan(X, dt, A, B, C, D, Y=Y, final_state=final_state)
     bsz, T, H, P = X.shape
@@ -315,7 +316,6 @@ def ssd_step_fused(state, conv_state, x, dt, A, B, C, D, *, conv_w, conv_b=None,
     (b, H*P, 3) in x's dtype holds the 3 earlier raw inputs (oldest first) and
     is shifted in place, as is the fp32 state. conv_w (H*P, 4), conv_b (H*P)
     fp32. Returns y."""
-    import torch
     lib = load()
     _check_step(state, x, dt, A, B, C, D, y=y, z=z)
     bsz, H, P, N = state.shape
@@ -336,7 +336,6 @@ def ssd_step_fused(state, conv_state, x, dt, A, B, C, D, *, conv_w, conv_b=None,
 
 
 def _workspace(workspace, need, device):
-    import torch
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -345,7 +344,6 @@ def _workspace(workspace, need, device):
 
 def ssd_chunk_scan_prepare(dt, A, B, C, chunk: int, headdim: int, *, workspace=None, stream=None):
     """Phase 1 of the forward: fills and returns the workspace."""
-    import torch
     lib = load()
     if dt.dim() != 3 or B.dim() != 4:
         raise ValueError("dt must be (batch, T, H) and B (batch, T, G, N)")
@@ -367,7 +365,6 @@ def ssd_chunk_scan_prepare(dt, A, B, C, chunk: int, headdim: int, *, workspace=N
 def ssd_chunk_scan_walk(X, B, C, D, workspace, chunk: int, initial_state=None, Y=None,
                         final_state=None, *, want_final: bool = True, stream=None):
     """Phase 2 of the forward: the chunk walk over a prepared workspace."""
-    import torch
     lib = load()
     if X.dim() != 4 or B.dim() != 4:
         raise ValueError("X must be (batch, T, H, P) and B (batch, T, G, N)")
@@ -395,7 +392,6 @@ def ssd_chunk_scan_walk(X, B, C, D, workspace, chunk: int, initial_state=None, Y
 
 def ssd_step(state, x, dt, A, B, C, D, y=None, *, stream=None):
     """One decode step; `state` (b, H, P, N) fp32 is updated in place. Returns y."""
-    import torch
     lib = load()
     _check_step(state, x, dt, A, B, C, D, y=y)
     bsz, H, P, N = state.shape
@@ -427,7 +423,6 @@ def ssd_chunk_scan_fwd_varlen(X, dt, A, B, C, D, chunk: int, cu_seqlens, max_seq
     lengths; max_seqlen the longest sequence (a host int, so that no device value
     has to be read here). Returns (Y, final_state) with final_state
     (num_seqs, H, P, N) fp32."""
-    import torch
     lib = load()
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be a 1-d int32 tensor of num_seqs + 1 offsets")
@@ -456,7 +451,6 @@ def ssd_chunk_scan_fwd_gated(X, dt, A, B, C, D, chunk: int, *, dt_bias=None, dt_
                              Y=None, final_state=None, want_final: bool = True, workspace=None, stream=None):
     """ssd_chunk_scan_fwd with the fused prologue (dt_bias, dt_softplus: 0 none,
     1 softplus(dt + bias), 2 softplus(dt) + bias) and output gate Y * silu(z)."""
-    import torch
     lib = load()
     _check_scan(X, dt, A, B, C, D, Y=Y, final_state=final_state, z=z)
     _chk("dt_bias", dt_bias, (X.shape[2],), torch.float32)
@@ -482,7 +476,6 @@ def ssd_chunk_scan_fwd_fused(X, dt, A, B, C, D, chunk: int, *, conv_w=None, conv
                              workspace=None, stream=None):
     """ssd_chunk_scan_fwd_gated with the input activation fused in: X is taken before the
     causal 4-tap depthwise convolution (conv_w (H*P, 4), conv_b (H*P) fp32) and SiLU."""
-    import torch
     lib = load()
     _check_scan(X, dt, A, B, C, D, Y=Y, final_state=final_state, z=z)
     _chk("dt_bias", dt_bias, (X.shape[2],), torch.float32)
@@ -509,7 +502,6 @@ def ssd_chunk_scan_fwd_fused(X, dt, A, B, C, D, chunk: int, *, conv_w=None, conv
 def ssd_step_gated(state, x, dt, A, B, C, D, *, dt_bias=None, dt_softplus: int = 0, z=None, y=None,
                    stream=None):
     """ssd_step with the fused prologue and output gate (see ssd_chunk_scan_fwd_gated)."""
-    import torch
     lib = load()
     _check_step(state, x, dt, A, B, C, D, y=y, z=z)
     _chk("dt_bias", dt_bias, (state.shape[1],), torch.float32)
@@ -540,7 +532,6 @@ def ssd_chunk_scan_bwd(X, dt, A, B, C, D, chunk: int, dY, *, initial_state=None,
     """Gradients of <dY, Y> + <dF, final_state> for ssd_chunk_scan_fwd(X, dt, A, B, C, D, chunk)
     from initial_state (zero when None). Returns (dX, ddt, dA, dB, dC, dD, d_initial_state);
     the last is None unless want_initial_grad."""
-    import torch
     lib = load()
     _check_scan(X, dt, A, B, C, D, dY=dY, final_state=d_final_state, initial_state=initial_state)
     bsz, T, H, P = X.shape
@@ -565,34 +556,59 @@ def ssd_chunk_scan_bwd(X, dt, A, B, C, D, chunk: int, dY, *, initial_state=None,
     return dX, ddt, dA, dB, dC, dD, dinit
 
 
-def _here(*tensors) -> None:
-    """Raises ValueError unless every tensor given is on the current GPU: the
-    stream a call goes to is this device's."""
-    import torch
-    now = torch.cuda.current_device() if torch.cuda.is_initialized() else None
-    for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != now:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{now}")
+def _device(t) -> int:
+    """The GPU that t is on, which has to be the current one: the stream a call goes to is that device's."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on the GPU")
+    now = torch.cuda.current_device()
+    if dev != now:
+        raise ValueError(f"tensor on cuda:{dev}, but the current device is cuda:{now}")
+    return dev
 
 
-def _new(shape, dtype, device, stream):
+def _in(dev: int, name: str, t, shape, dtype) -> Optional[int]:
+    """The address of an argument (None for None) that is checked: shape, type, device, contiguous."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype:
+        _chk(name, t, shape, dtype)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _scratch(workspace, need: int, like, dev: int, stream):
+    """(tensor, address, bytes) of a call's workspace: the caller's, or a new one."""
+    if workspace is None:
+        if not need:
+            return None, None, 0
+        workspace = _new((need,), torch.uint8, like, stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous and on the device of the tensors")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _new(shape, dtype, like, stream):
     """An output or workspace for a call on `stream`. It is allocated as that
     stream's memory, so that it is not handed out again before the call is done."""
-    import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _like(t, stream):
+    """_new of the shape and type of t, which is contiguous."""
+    return torch.empty_like(t) if stream is None else _new(t.shape, t.dtype, t, stream)
 
 
 def _sized(name: str, n: int) -> int:
     if n == ctypes.c_size_t(-1).value:
         raise SSDError(3, name)
     return int(n)
-
-
-def _nbytes(workspace) -> int:
-    return 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
 def _rows_dim(name: str, t):
@@ -608,29 +624,28 @@ def ssd_step_beam(state_in, state_out, parent, x, dt, A, B, C, D, *, conv_in=Non
     (int32, on the GPU) of state_in (src_rows, H, P, N); a parent outside it starts from a zero state. With conv_w
     (H*P, 4) the layer's convolution runs on x, and conv_in (src_rows, H*P, 3) is reordered and shifted into
     conv_out (batch, H*P, 3). Other arguments as ssd_step_fused. Returns y."""
-    import torch
     lib = load()
-    _check_step(state_out, x, dt, A, B, C, D, y=y, z=z)
+    if state_in.dim() != 4 or state_out.dim() != 4 or B.dim() != 3:
+        raise ValueError("state_in must be (src_rows, H, P, N), state_out (batch, H, P, N) and B (batch, G, N)")
     bsz, H, P, N = state_out.shape
-    G = B.shape[1]
-    if state_in.dim() != 4:
-        raise ValueError("state_in must be (src_rows, H, P, N)")
-    src = state_in.shape[0]
-    _chk("state_in", state_in, (src, H, P, N), torch.float32)
-    _chk("parent", parent, (bsz,), torch.int32)
-    _chk("conv_in", conv_in, (src, H * P, 3), x.dtype)
-    _chk("conv_out", conv_out, (bsz, H * P, 3), x.dtype)
-    _chk("conv_w", conv_w, (H * P, 4), torch.float32)
-    _chk("conv_b", conv_b, (H * P,), torch.float32)
-    _chk("dt_bias", dt_bias, (H,), torch.float32)
-    _here(state_in, state_out, parent, x, dt, A, B, C, D, conv_in, conv_out, conv_w, conv_b, dt_bias, z, y)
+    G, src = B.shape[1], state_in.shape[0]
+    st, f32 = x.dtype, torch.float32
+    code = _dtype_code(x)
+    dev = _device(state_out)
+    p_y = _in(dev, "y", y, (bsz, H, P), st)
     if y is None:
-        y = _new(x.shape, x.dtype, x.device, stream)
-    st = lib.ssd_step_beam(_ptr(state_in), _ptr(state_out), _ptr(parent), src, _ptr(conv_in), _ptr(conv_out), _ptr(x),
-                           _ptr(conv_w), _ptr(conv_b), _ptr(dt), _ptr(dt_bias), int(dt_softplus), _ptr(A), _ptr(B),
-                           _ptr(C), _ptr(D), _ptr(z), _ptr(y), bsz, H, P, N, G, _dtype_code(x), _stream(stream))
-    if st != 0:
-        raise SSDError(st, "ssd_step_beam")
+        y = _like(x, stream)
+        p_y = y.data_ptr()
+    rc = lib.ssd_step_beam(
+        _in(dev, "state_in", state_in, (src, H, P, N), f32), _in(dev, "state_out", state_out, (bsz, H, P, N), f32),
+        _in(dev, "parent", parent, (bsz,), torch.int32), src, _in(dev, "conv_in", conv_in, (src, H * P, 3), st),
+        _in(dev, "conv_out", conv_out, (bsz, H * P, 3), st), _in(dev, "x", x, (bsz, H, P), st),
+        _in(dev, "conv_w", conv_w, (H * P, 4), f32), _in(dev, "conv_b", conv_b, (H * P,), f32),
+        _in(dev, "dt", dt, (bsz, H), st), _in(dev, "dt_bias", dt_bias, (H,), f32), int(dt_softplus),
+        _in(dev, "A", A, (H,), f32), _in(dev, "B", B, (bsz, G, N), st), _in(dev, "C", C, (bsz, G, N), st),
+        _in(dev, "D", D, (H,), f32), _in(dev, "z", z, (bsz, H, P), st), p_y, bsz, H, P, N, G, code, _stream(stream))
+    if rc != 0:
+        raise SSDError(rc, "ssd_step_beam")
     return y
 
 
@@ -643,43 +658,51 @@ def ssd_beam_select(logits, scores, *, finished=None, eos: int = -1, workspace=N
     log-probabilities (-inf for a beam not in use), finished (batch, beams) bool or uint8, or None.
     Returns (next_scores fp32, parent int32, token int32, next_finished bool), each (batch, beams); parent is a
     row of the batch * beams states, as ssd_step_beam takes it."""
-    import torch
     lib = load()
     if logits.dim() != 3:
         raise ValueError("logits must be (batch, beams, vocab)")
-    bsz, K, V = logits.shape
-    _chk("scores", scores, (bsz, K), torch.float32)
-    if finished is not None:
-        _chk("finished", finished, (bsz, K), torch.bool if finished.dtype == torch.bool else torch.uint8)
+    bsz, K, V = shape = logits.shape
+    rows = (bsz, K)
     code = _dtype_code(logits)
-    _here(logits, scores, finished, workspace)
-    if workspace is None:
-        workspace = _new((ssd_beam_select_workspace_bytes(bsz, K, V),), torch.uint8, logits.device, stream)
-    out = _new((bsz, K), torch.float32, logits.device, stream)
-    parent = _new((bsz, K), torch.int32, logits.device, stream)
-    token = _new((bsz, K), torch.int32, logits.device, stream)
-    done = _new((bsz, K), torch.bool, logits.device, stream)
-    st = lib.ssd_beam_select(_ptr(logits), _ptr(scores), _ptr(finished), int(eos), _ptr(out), _ptr(parent),
-                             _ptr(token), _ptr(done), bsz, K, V, code, _ptr(workspace), _nbytes(workspace),
-                             _stream(stream))
+    if finished is not None and finished.dtype not in (torch.bool, torch.uint8):
+        raise ValueError(f"finished: dtype {finished.dtype}, expected bool or uint8")
+    dev = _device(logits)
+    p_l, p_s = _in(dev, "logits", logits, shape, logits.dtype), _in(dev, "scores", scores, rows, torch.float32)
+    p_f = None if finished is None else _in(dev, "finished", finished, rows, finished.dtype)
+    need = 0 if workspace is not None else ssd_beam_select_workspace_bytes(bsz, K, V)
+    workspace, p_w, nbytes = _scratch(workspace, need, logits, dev, stream)
+    out = _like(scores, stream)
+    parent = _new(rows, torch.int32, logits, stream)
+    token = _like(parent, stream)
+    done = _new(rows, torch.bool, logits, stream)
+    st = lib.ssd_beam_select(p_l, p_s, p_f, int(eos), out.data_ptr(), parent.data_ptr(), token.data_ptr(),
+                             done.data_ptr(), bsz, K, V, code, p_w, nbytes, _stream(stream))
     if st != 0:
         raise SSDError(st, "ssd_beam_select")
     return out, parent, token, done
 
 
-def _check_norm(x, weight, residual, residual_out):
-    import torch
+def _norm_args(x, weight, residual, residual_out, stream):
+    """The checked arguments that both norms share: (rows, dim, codes of x and residual, device, addresses of x,
+    weight, residual and residual_out, residual_out)."""
     rows, dim = _rows_dim("x", x)
-    code = _dtype_code(x)
-    _chk("weight", weight, (dim,), torch.float32)
-    rcode = code
-    if residual is not None:
+    shape = x.shape
+    code = rcode = _dtype_code(x)
+    dev = _device(x)
+    p_x, p_w = _in(dev, "x", x, shape, x.dtype), _in(dev, "weight", weight, (dim,), torch.float32)
+    p_r = p_ro = None
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out without a residual")
+    else:
         rcode = _dtype_code(residual)
-        _chk("residual", residual, x.shape, residual.dtype)
-        _chk("residual_out", residual_out, x.shape, residual.dtype)
-    elif residual_out is not None:
-        raise ValueError("residual_out without a residual")
-    return rows, dim, code, rcode
+        p_r = _in(dev, "residual", residual, shape, residual.dtype)
+        if residual_out is None:
+            residual_out = _like(residual, stream)
+            p_ro = residual_out.data_ptr()
+        else:
+            p_ro = _in(dev, "residual_out", residual_out, shape, residual.dtype)
+    return rows, dim, code, rcode, dev, p_x, p_w, p_r, p_ro, residual_out
 
 
 def ssd_rms_norm(x, weight, eps: float, *, residual=None, groups: int = 1, residual_out=None, y=None,
@@ -688,36 +711,33 @@ def ssd_rms_norm(x, weight, eps: float, *, residual=None, groups: int = 1, resid
     equal pieces of it). residual: x's type or fp32. Returns (y, residual_out, rstd): residual_out is h in
     residual's type (None without one; may be passed as residual itself), rstd (rows..., groups) fp32 for the
     backward pass, or None."""
-    import torch
     lib = load()
-    rows, dim, code, rcode = _check_norm(x, weight, residual, residual_out)
-    _chk("y", y, x.shape, x.dtype)
-    _here(x, weight, residual, residual_out, y)
+    rows, dim, code, rcode, dev, p_x, p_w, p_r, p_ro, residual_out = _norm_args(x, weight, residual, residual_out, stream)
+    p_y = _in(dev, "y", y, x.shape, x.dtype)
     if y is None:
-        y = _new(x.shape, x.dtype, x.device, stream)
-    if residual is not None and residual_out is None:
-        residual_out = _new(x.shape, residual.dtype, x.device, stream)
-    rstd = _new((*x.shape[:-1], groups), torch.float32, x.device, stream) if want_rstd else None
-    st = lib.ssd_rms_norm(_ptr(x), _ptr(residual), _ptr(weight), float(eps), _ptr(residual_out), _ptr(y), _ptr(rstd),
-                          rows, dim, int(groups), code, rcode, _stream(stream))
+        y = _like(x, stream)
+        p_y = y.data_ptr()
+    rstd = _new((*x.shape[:-1], groups), torch.float32, x, stream) if want_rstd else None
+    st = lib.ssd_rms_norm(p_x, p_r, p_w, eps, p_ro, p_y, None if rstd is None else rstd.data_ptr(), rows, dim, groups,
+                          code, rcode, _stream(stream))
     if st != 0:
         raise SSDError(st, "ssd_rms_norm")
     return y, residual_out, rstd
 
 
+def _new_mx(x, dim: int, stream):
+    return (_new(x.shape, torch.float8_e4m3fn, x, stream),
+            _new((*x.shape[:-1], dim // 32), torch.float8_e8m0fnu, x, stream))
+
+
 def ssd_rms_norm_mx(x, weight, eps: float, *, residual=None, groups: int = 1, residual_out=None, stream=None):
     """ssd_rms_norm with an 8-bit output. Returns (q, scale, residual_out): q float8_e4m3fn like x, scale
     float8_e8m0fnu (..., dim / 32), a power of two for each 32 values of a row."""
-    import torch
     lib = load()
-    rows, dim, code, rcode = _check_norm(x, weight, residual, residual_out)
-    _here(x, weight, residual, residual_out)
-    q = _new(x.shape, torch.float8_e4m3fn, x.device, stream)
-    scale = _new((*x.shape[:-1], dim // 32), torch.float8_e8m0fnu, x.device, stream)
-    if residual is not None and residual_out is None:
-        residual_out = _new(x.shape, residual.dtype, x.device, stream)
-    st = lib.ssd_rms_norm_mx(_ptr(x), _ptr(residual), _ptr(weight), float(eps), _ptr(residual_out), _ptr(q),
-                             _ptr(scale), rows, dim, int(groups), code, rcode, _stream(stream))
+    rows, dim, code, rcode, dev, p_x, p_w, p_r, p_ro, residual_out = _norm_args(x, weight, residual, residual_out, stream)
+    q, scale = _new_mx(x, dim, stream)
+    st = lib.ssd_rms_norm_mx(p_x, p_r, p_w, eps, p_ro, q.data_ptr(), scale.data_ptr(), rows, dim, groups, code, rcode,
+                             _stream(stream))
     if st != 0:
         raise SSDError(st, "ssd_rms_norm_mx")
     return q, scale, residual_out
@@ -725,14 +745,12 @@ def ssd_rms_norm_mx(x, weight, eps: float, *, residual=None, groups: int = 1, re
 
 def ssd_mx_quantize(x, *, stream=None):
     """x (..., dim), dim a multiple of 32, in 8 bits: (q float8_e4m3fn, scale float8_e8m0fnu), as ssd_rms_norm_mx."""
-    import torch
     lib = load()
     rows, dim = _rows_dim("x", x)
     code = _dtype_code(x)
-    _here(x)
-    q = _new(x.shape, torch.float8_e4m3fn, x.device, stream)
-    scale = _new((*x.shape[:-1], dim // 32), torch.float8_e8m0fnu, x.device, stream)
-    st = lib.ssd_mx_quantize(_ptr(x), _ptr(q), _ptr(scale), rows, dim, code, _stream(stream))
+    p_x = _in(_device(x), "x", x, x.shape, x.dtype)
+    q, scale = _new_mx(x, dim, stream)
+    st = lib.ssd_mx_quantize(p_x, q.data_ptr(), scale.data_ptr(), rows, dim, code, _stream(stream))
     if st != 0:
         raise SSDError(st, "ssd_mx_quantize")
     return q, scale
@@ -747,24 +765,21 @@ def ssd_rms_norm_bwd(dy, h, weight, rstd, *, d_residual_out=None, groups: int = 
     """Gradients of ssd_rms_norm: dy like y, h its residual_out (its x, where it had no residual), rstd from it,
     d_residual_out like h or None. Returns (dx, d_residual, dweight): dx in dy's type; d_residual is the same
     gradient in h's type where that differs, else None (dx serves for both); dweight fp32."""
-    import torch
     lib = load()
     rows, dim = _rows_dim("dy", dy)
+    shape = dy.shape
     code, rcode = _dtype_code(dy), _dtype_code(h)
-    _chk("h", h, dy.shape, h.dtype)
-    _chk("weight", weight, (dim,), torch.float32)
-    _chk("rstd", rstd, (*dy.shape[:-1], groups), torch.float32)
-    _chk("d_residual_out", d_residual_out, dy.shape, h.dtype)
-    _here(dy, h, weight, rstd, d_residual_out, workspace)
-    need = ssd_rms_norm_bwd_workspace_bytes(rows, dim, int(groups), code, rcode)
-    if workspace is None and need:
-        workspace = _new((need,), torch.uint8, dy.device, stream)
-    dx = _new(dy.shape, dy.dtype, dy.device, stream)
-    dh = _new(dy.shape, h.dtype, dy.device, stream) if rcode != code else None
-    dw = _new((dim,), torch.float32, dy.device, stream)
-    st = lib.ssd_rms_norm_bwd(_ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(d_residual_out), _ptr(dx), _ptr(dh),
-                              _ptr(dw), rows, dim, int(groups), code, rcode, _ptr(workspace), _nbytes(workspace),
-                              _stream(stream))
+    dev = _device(dy)
+    need = 0 if workspace is not None else ssd_rms_norm_bwd_workspace_bytes(rows, dim, groups, code, rcode)
+    workspace, p_ws, nbytes = _scratch(workspace, need, dy, dev, stream)
+    dx = _new(shape, dy.dtype, dy, stream)
+    dh = _new(shape, h.dtype, dy, stream) if rcode != code else None
+    dw = _new((dim,), torch.float32, dy, stream)
+    st = lib.ssd_rms_norm_bwd(
+        _in(dev, "dy", dy, shape, dy.dtype), _in(dev, "h", h, shape, h.dtype),
+        _in(dev, "weight", weight, (dim,), torch.float32), _in(dev, "rstd", rstd, (*shape[:-1], groups), torch.float32),
+        _in(dev, "d_residual_out", d_residual_out, shape, h.dtype), dx.data_ptr(), None if dh is None else dh.data_ptr(),
+        dw.data_ptr(), rows, dim, groups, code, rcode, p_ws, nbytes, _stream(stream))
     if st != 0:
         raise SSDError(st, "ssd_rms_norm_bwd")
     return dx, dh, dw
@@ -776,6 +791,15 @@ def _act_code(act: str) -> int:
     return ACTS[act]
 
 
+def _linear_dims(x, w, what: str):
+    """(rows, in, out, shape of y) of a product of x (..., in) and w (out, in)."""
+    rows, k = _rows_dim("x", x)
+    if w.dim() != 2 or w.shape[1] != k:
+        raise ValueError(f"{what}: shape {tuple(w.shape)}, expected (out, {k})")
+    n = w.shape[0]
+    return rows, k, n, (*x.shape[:-1], n)
+
+
 def ssd_linear_workspace_bytes(rows, in_, out, dtype: int) -> int:
     return _sized("ssd_linear_workspace_bytes", load().ssd_linear_workspace_bytes(rows, in_, out, dtype))
 
@@ -785,30 +809,22 @@ def ssd_linear(x, w, *, bias=None, act: str = "none", residual=None, y=None, wan
     """y = act(x w^T + bias) + residual: x (..., in) and w (out, in) bf16 or fp32, bias (out) fp32, act "none", "silu"
     or "gelu", residual (..., out) in x's type. Returns (y, preact): preact is x w^T + bias for ssd_linear_bwd, or
     None."""
-    import torch
     lib = load()
-    rows, k = _rows_dim("x", x)
-    if w.dim() != 2 or w.shape[1] != k:
-        raise ValueError(f"w: shape {tuple(w.shape)}, expected (out, {k})")
-    n = w.shape[0]
-    shape = (*x.shape[:-1], n)
-    code = _dtype_code(x)
-    _chk("w", w, (n, k), x.dtype)
-    _chk("bias", bias, (n,), torch.float32)
-    _chk("residual", residual, shape, x.dtype)
-    _chk("y", y, shape, x.dtype)
-    _here(x, w, bias, residual, y, workspace)
+    rows, k, n, shape = _linear_dims(x, w, "w")
+    st, code, acode = x.dtype, _dtype_code(x), _act_code(act)
+    dev = _device(x)
+    p_y = _in(dev, "y", y, shape, st)
     if y is None:
-        y = _new(shape, x.dtype, x.device, stream)
-    pre = _new(shape, x.dtype, x.device, stream) if want_preact else None
-    if workspace is None:
-        need = ssd_linear_workspace_bytes(rows, k, n, code)
-        if need:
-            workspace = _new((need,), torch.uint8, x.device, stream)
-    st = lib.ssd_linear(_ptr(x), _ptr(w), _ptr(bias), _act_code(act), _ptr(residual), _ptr(y), _ptr(pre), rows, k, n,
-                        code, _ptr(workspace), _nbytes(workspace), _stream(stream))
-    if st != 0:
-        raise SSDError(st, "ssd_linear")
+        y = _new(shape, st, x, stream)
+        p_y = y.data_ptr()
+    pre = _new(shape, st, x, stream) if want_preact else None
+    need = 0 if workspace is not None else ssd_linear_workspace_bytes(rows, k, n, code)
+    workspace, p_ws, nbytes = _scratch(workspace, need, x, dev, stream)
+    rc = lib.ssd_linear(_in(dev, "x", x, x.shape, st), _in(dev, "w", w, (n, k), st),
+                        _in(dev, "bias", bias, (n,), torch.float32), acode, _in(dev, "residual", residual, shape, st), p_y,
+                        None if pre is None else pre.data_ptr(), rows, k, n, code, p_ws, nbytes, _stream(stream))
+    if rc != 0:
+        raise SSDError(rc, "ssd_linear")
     return y, pre
 
 
@@ -821,31 +837,24 @@ def ssd_linear_mx(xq, xscale, wq, wscale, *, bias=None, act: str = "none", resid
     """ssd_linear from 8-bit operands as ssd_rms_norm_mx and ssd_mx_quantize return them: xq (..., in) and wq
     (out, in) float8_e4m3fn, xscale (..., in / 32) and wscale (out, in / 32) float8_e8m0fnu; residual and y bf16.
     Returns y."""
-    import torch
     lib = load()
-    rows, k = _rows_dim("xq", xq)
-    if wq.dim() != 2 or wq.shape[1] != k:
-        raise ValueError(f"wq: shape {tuple(wq.shape)}, expected (out, {k})")
-    n = wq.shape[0]
-    shape = (*xq.shape[:-1], n)
-    _chk("xq", xq, xq.shape, torch.float8_e4m3fn)
-    _chk("xscale", xscale, (*xq.shape[:-1], k // 32), torch.float8_e8m0fnu)
-    _chk("wq", wq, (n, k), torch.float8_e4m3fn)
-    _chk("wscale", wscale, (n, k // 32), torch.float8_e8m0fnu)
-    _chk("bias", bias, (n,), torch.float32)
-    _chk("residual", residual, shape, torch.bfloat16)
-    _chk("y", y, shape, torch.bfloat16)
-    _here(xq, xscale, wq, wscale, bias, residual, y, workspace)
+    rows, k, n, shape = _linear_dims(xq, wq, "wq")
+    acode = _act_code(act)
+    q8, s8, f32, b16 = torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.float32, torch.bfloat16
+    sshape = (*xq.shape[:-1], k // 32)
+    dev = _device(xq)
+    p_y = _in(dev, "y", y, shape, b16)
     if y is None:
-        y = _new(shape, torch.bfloat16, xq.device, stream)
-    if workspace is None:
-        need = ssd_linear_mx_workspace_bytes(rows, k, n)
-        if need:
-            workspace = _new((need,), torch.uint8, xq.device, stream)
-    st = lib.ssd_linear_mx(_ptr(xq), _ptr(xscale), _ptr(wq), _ptr(wscale), _ptr(bias), _act_code(act), _ptr(residual),
-                           _ptr(y), rows, k, n, _ptr(workspace), _nbytes(workspace), _stream(stream))
-    if st != 0:
-        raise SSDError(st, "ssd_linear_mx")
+        y = _new(shape, b16, xq, stream)
+        p_y = y.data_ptr()
+    need = 0 if workspace is not None else ssd_linear_mx_workspace_bytes(rows, k, n)
+    workspace, p_ws, nbytes = _scratch(workspace, need, xq, dev, stream)
+    rc = lib.ssd_linear_mx(_in(dev, "xq", xq, xq.shape, q8), _in(dev, "xscale", xscale, sshape, s8),
+                           _in(dev, "wq", wq, (n, k), q8), _in(dev, "wscale", wscale, (n, k // 32), s8),
+                           _in(dev, "bias", bias, (n,), f32), acode, _in(dev, "residual", residual, shape, b16), p_y,
+                           rows, k, n, p_ws, nbytes, _stream(stream))
+    if rc != 0:
+        raise SSDError(rc, "ssd_linear_mx")
     return y
 
 
@@ -858,31 +867,22 @@ def ssd_linear_bwd(dy, x, w, *, act: str = "none", preact=None, want_x: bool = T
                    want_bias: bool = False, workspace=None, stream=None):
     """Gradients of ssd_linear: dy (..., out), x (..., in), w (out, in), preact as the forward returned it (act other
     than "none"). Returns (dx, dw, dbias fp32), None for one that is not wanted; the residual's gradient is dy."""
-    import torch
     lib = load()
-    rows, k = _rows_dim("x", x)
-    if w.dim() != 2 or w.shape[1] != k:
-        raise ValueError(f"w: shape {tuple(w.shape)}, expected (out, {k})")
-    n = w.shape[0]
-    shape = (*x.shape[:-1], n)
-    code, acode = _dtype_code(x), _act_code(act)
-    _chk("w", w, (n, k), x.dtype)
-    _chk("dy", dy, shape, x.dtype)
+    rows, k, n, shape = _linear_dims(x, w, "w")
+    st, code, acode = x.dtype, _dtype_code(x), _act_code(act)
     if acode and preact is None:
         raise ValueError("act needs preact")
-    _chk("preact", preact, shape, x.dtype)
-    _here(dy, x, w, preact, workspace)
-    dx = _new(x.shape, x.dtype, x.device, stream) if want_x else None
-    dw = _new((n, k), x.dtype, x.device, stream) if want_w else None
-    db = _new((n,), torch.float32, x.device, stream) if want_bias else None
-    if workspace is None:
-        need = ssd_linear_bwd_workspace_bytes(rows, k, n, act, code)
-        if need:
-            workspace = _new((need,), torch.uint8, x.device, stream)
-    st = lib.ssd_linear_bwd(_ptr(dy), _ptr(x), _ptr(w), acode, _ptr(preact), _ptr(dx), _ptr(dw), _ptr(db), rows, k, n,
-                            code, _ptr(workspace), _nbytes(workspace), _stream(stream))
-    if st != 0:
-        raise SSDError(st, "ssd_linear_bwd")
+    dev = _device(x)
+    dx = _new(x.shape, st, x, stream) if want_x else None
+    dw = _new((n, k), st, x, stream) if want_w else None
+    db = _new((n,), torch.float32, x, stream) if want_bias else None
+    need = 0 if workspace is not None else ssd_linear_bwd_workspace_bytes(rows, k, n, act, code)
+    workspace, p_ws, nbytes = _scratch(workspace, need, x, dev, stream)
+    rc = lib.ssd_linear_bwd(_in(dev, "dy", dy, shape, st), _in(dev, "x", x, x.shape, st), _in(dev, "w", w, (n, k), st),
+                            acode, _in(dev, "preact", preact, shape, st), _ptr(dx), _ptr(dw), _ptr(db), rows, k, n,
+                            code, p_ws, nbytes, _stream(stream))
+    if rc != 0:
+        raise SSDError(rc, "ssd_linear_bwd")
     return dx, dw, db
 
 
