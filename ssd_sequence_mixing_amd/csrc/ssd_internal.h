@@ -218,19 +218,24 @@ struct LinearArgs {
     float *part;                // workspace: (splits, M, N) where the sum over k is split
     int M, N, act;
     uint32_t kbytes;
+    bool xt, wt;                // bf16: x (w) is given as (krows x M) ((krows x N)), rows along k
+    int krows;
     int nm, nn, steps, splits, steps_per_split;
 };
 struct LinearPlan {
-    int tile;                   // edge of a work-group's tile of y; 0: the few-rows kernel
+    int bm, bn;                 // a work-group's tile of y; 0: the few-rows kernel
     int nm, nn;                 // tiles
     int steps, splits, steps_per_split;
 };
-LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes);
+// along_k: an operand has its rows along k (the few-rows kernel takes none of these).
+LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, bool along_k);
 ssd_status launch_linear(LinearArgs a, const LinearPlan &p, bool mx, ssd_dtype dtype, hipStream_t s);
 ssd_status launch_pad(const void *in, void *out, int64_t rows, int64_t n, int64_t ldo, int es, hipStream_t s);
-ssd_status launch_transpose(const void *in, void *out, int64_t R, int64_t C, int64_t ldo, ssd_dtype dtype, hipStream_t s);
-ssd_status launch_dz(const void *dy, const void *pre, int act, void *dz, void *dzt, float *part, int64_t M, int64_t N,
-                     int64_t ldz, int64_t ldt, ssd_dtype dtype, hipStream_t s);
+// fp32 only.
+ssd_status launch_transpose(const void *in, void *out, int64_t R, int64_t C, int64_t ldo, hipStream_t s);
+// dz (null: not wanted) and the 64-row shares of db (null: not wanted).
+ssd_status launch_dz(const void *dy, const void *pre, int act, void *dz, float *part, int64_t M, int64_t N, int64_t ldz,
+                     ssd_dtype dtype, hipStream_t s);
 
 // Beam search's selection (ssd_beam.hip).
 struct BeamArgs {

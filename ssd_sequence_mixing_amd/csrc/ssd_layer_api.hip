@@ -110,7 +110,7 @@ LinearLayout linear_layout(int64_t rows, int64_t in, int64_t out, ssd_dtype dtyp
         l.xpad = align256(rows * l.ld);
         l.wpad = align256(out * l.ld);
     }
-    l.plan = ssd::linear_plan(rows, out, l.ld);
+    l.plan = ssd::linear_plan(rows, out, l.ld, false);
     if (l.plan.splits > 1) l.part = align256(l.plan.splits * rows * out * 4);
     l.total = l.xpad + l.wpad + l.part;
     return l;
@@ -119,9 +119,9 @@ LinearLayout linear_layout(int64_t rows, int64_t in, int64_t out, ssd_dtype dtyp
 LinearLayout linear_mx_layout(int64_t rows, int64_t in, int64_t out) {
     LinearLayout l = {};
     if (rows == 0) return l;
-    l.plan = ssd::linear_plan(rows, out, in);
+    l.plan = ssd::linear_plan(rows, out, in, false);
     l.ld = in / 32;
-    if (l.plan.tile && l.ld % 4 != 0) {
+    if (l.plan.bm && l.ld % 4 != 0) {
         l.ld = (l.ld + 3) & ~(int64_t)3;
         l.xs = align256(rows * l.ld);
         l.ws = align256(out * l.ld);
@@ -131,38 +131,39 @@ LinearLayout linear_mx_layout(int64_t rows, int64_t in, int64_t out) {
     return l;
 }
 
-// Workspace of the gradients: dz by rows (where it is not dy itself) and dz,
-// x and w transposed (rows of ldt / ldz values), the 64-row shares of
-// dbias, and the parts of the two products' sums, one after the other.
+// Workspace of the gradients, one after the other: dz (where it is not dy
+// itself); bf16: copies of w and x with rows of 16-byte multiples, where theirs are
+// not; fp32: dz, w and x transposed (rows of ldt / ldz values); the 64-row
+// shares of dbias; the parts of the two products' sums.
 struct LinearBwdLayout {
     ssd::LinearPlan px, pw;
-    int64_t ldz, ldt, dz, dzt, wt, xt, db, part, total;
-    bool own_dz;
+    int64_t ldz, ldt, ldk, dz, dzt, w, x, db, part, total;
 };
 LinearBwdLayout linear_bwd_layout(int64_t rows, int64_t in, int64_t out, int act, bool want_dx, bool want_dw,
                                   bool want_db, ssd_dtype dtype) {
     LinearBwdLayout l = {};
     if (rows == 0) return l;
     const int64_t es = esize(dtype);
+    const bool bf = dtype == SSD_BF16;
     l.ldz = align16(out * es) / es;
     l.ldt = align16(rows * es) / es;
-    l.own_dz = want_dx && (act != SSD_ACT_NONE || l.ldz != out);
-    if (l.own_dz) l.dz = align256(rows * l.ldz * es);
+    l.ldk = align16(in * es) / es;
+    if ((want_dx || want_dw) && (act != SSD_ACT_NONE || l.ldz != out)) l.dz = align256(rows * l.ldz * es);
     int64_t px = 0, pw = 0;
     if (want_dx) {
-        l.wt = align256(in * l.ldz * es);
-        l.px = ssd::linear_plan(rows, in, l.ldz * es);
+        l.w = bf ? (l.ldk != in ? align256(out * l.ldk * es) : 0) : align256(in * l.ldz * es);
+        l.px = ssd::linear_plan(rows, in, l.ldz * es, bf);
         if (l.px.splits > 1) px = align256(l.px.splits * rows * in * 4);
     }
     if (want_dw) {
-        l.dzt = align256(out * l.ldt * es);
-        l.xt = align256(in * l.ldt * es);
-        l.pw = ssd::linear_plan(out, in, l.ldt * es);
+        l.x = bf ? (l.ldk != in ? align256(rows * l.ldk * es) : 0) : align256(in * l.ldt * es);
+        if (!bf) l.dzt = align256(l.ldz * l.ldt * es);
+        l.pw = ssd::linear_plan(out, in, l.ldt * es, bf);
         if (l.pw.splits > 1) pw = align256(l.pw.splits * out * in * 4);
     }
     if (want_db) l.db = align256((rows + 63) / 64 * out * 4);
     l.part = px > pw ? px : pw;
-    l.total = l.dz + l.dzt + l.wt + l.xt + l.db + l.part;
+    l.total = l.dz + l.dzt + l.w + l.x + l.db + l.part;
     return l;
 }
 
@@ -261,26 +262,45 @@ ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, int act,
         return clear(dbias, out * 4, s);
     }
     char *ws = static_cast<char *>(workspace);
-    char *dz = ws, *dzt = dz + l.dz, *wt = dzt + l.dzt, *xt = wt + l.wt;
-    float *db = reinterpret_cast<float *>(xt + l.xt), *part = reinterpret_cast<float *>(xt + l.xt + l.db);
-    if (l.dz || l.dzt || l.db) {
-        st = ssd::launch_dz(dy, preact, act, l.dz ? dz : nullptr, l.dzt ? dzt : nullptr, l.db ? db : nullptr, rows, out,
-                            l.ldz, l.ldt, dtype, s);
+    char *dz = ws, *dzt = dz + l.dz, *wc = dzt + l.dzt, *xc = wc + l.w;
+    float *db = reinterpret_cast<float *>(xc + l.x), *part = reinterpret_cast<float *>(xc + l.x + l.db);
+    const bool bf = dtype == SSD_BF16;
+    if (l.dz || l.db) {
+        st = ssd::launch_dz(dy, preact, act, l.dz ? dz : nullptr, l.db ? db : nullptr, rows, out, l.ldz, dtype, s);
         if (st != SSD_OK) return st;
     }
     if (dbias && (st = ssd::launch_column_sums(db, dbias, (int)((rows + 63) / 64), out, s)) != SSD_OK) return st;
+    const void *z = l.dz ? dz : dy;
     if (dx) {
-        if ((st = ssd::launch_transpose(w, wt, out, in, l.ldz, dtype, s)) != SSD_OK) return st;
         ssd::LinearArgs a = {};
-        a.x = l.dz ? dz : dy; a.w = wt; a.y = dx; a.part = part; a.M = (int)rows; a.N = (int)in;
-        a.ldx = a.ldw = l.ldz * es; a.kbytes = (uint32_t)a.ldx;
+        a.x = z; a.y = dx; a.part = part; a.M = (int)rows; a.N = (int)in; a.ldx = l.ldz * es; a.kbytes = (uint32_t)a.ldx;
+        a.w = w;
+        if (l.w) {
+            st = bf ? ssd::launch_pad(w, wc, out, in, l.ldk, 2, s) : ssd::launch_transpose(w, wc, out, in, l.ldz, s);
+            if (st != SSD_OK) return st;
+            a.w = wc;
+        }
+        a.ldw = bf ? l.ldk * es : a.ldx;
+        a.wt = bf;
+        a.krows = (int)out;
         if ((st = ssd::launch_linear(a, l.px, false, dtype, s)) != SSD_OK) return st;
     }
     if (dw) {
-        if ((st = ssd::launch_transpose(x, xt, rows, in, l.ldt, dtype, s)) != SSD_OK) return st;
         ssd::LinearArgs a = {};
-        a.x = dzt; a.w = xt; a.y = dw; a.part = part; a.M = (int)out; a.N = (int)in;
-        a.ldx = a.ldw = l.ldt * es; a.kbytes = (uint32_t)a.ldx;
+        a.y = dw; a.part = part; a.M = (int)out; a.N = (int)in; a.kbytes = (uint32_t)(l.ldt * es);
+        a.x = z; a.w = x;
+        if (l.x) {
+            st = bf ? ssd::launch_pad(x, xc, rows, in, l.ldk, 2, s) : ssd::launch_transpose(x, xc, rows, in, l.ldt, s);
+            if (st != SSD_OK) return st;
+            a.w = xc;
+        }
+        if (bf) {
+            a.ldx = l.ldz * es; a.ldw = l.ldk * es; a.xt = a.wt = true; a.krows = (int)rows;
+        } else {
+            // z has rows of ldz values, and only `out` of them are rows of the transpose
+            if ((st = ssd::launch_transpose(z, dzt, rows, l.dz ? l.ldz : out, l.ldt, s)) != SSD_OK) return st;
+            a.x = dzt; a.ldx = a.ldw = l.ldt * es;
+        }
         if ((st = ssd::launch_linear(a, l.pw, false, dtype, s)) != SSD_OK) return st;
     }
     return SSD_OK;

@@ -50,6 +50,22 @@ __device__ __forceinline__ void to_lds4(const void *base, uint32_t bytes, void *
     __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(base, bytes), (lds_void *)dst, 4, voff, 0, 0, 0);
 }
 
+// Every wavefront's loads into LDS have arrived (a barrier alone does not wait
+// for them), and its reads too.
+__device__ __forceinline__ void arrive() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __syncthreads();
+}
+
+// 4 consecutive rows of one column a lane: in each group of 16, lane j gives the
+// address of 8 bytes of row j / 4 and receives the column of its own number.
+__device__ __forceinline__ u32x2 lds_transposed(const char *p) {
+    typedef short v4i16 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
+    const v4i16 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16 *)p);
+    return __builtin_bit_cast(u32x2, v);
+}
+
 // 128 bytes (lane's 2 x 16) of a row of w against those of a row of x.
 template <int KIND>
 __device__ __forceinline__ f32x4 mma2(u32x4 wl, u32x4 wh, u32x4 xl, u32x4 xh, f32x4 c, int sw, int sx) {
@@ -181,18 +197,24 @@ __device__ __forceinline__ void tile_of(int id, int nm, int nn, int &tm, int &tn
     tn = in / rows;
 }
 
-// EPI: the activation, or kParts to store the fp32 parts of a split sum
-template <int KIND, typename TO, int BM, int BN, int WM, int WN, int EPI>
+// EPI: the activation, or kParts to store the fp32 parts of a split sum.
+// XT, WT (bf16): x or w is given with its rows along k (k x M, k x N), as the
+// backward pass has them. A step then takes 64 rows of BM (BN) columns, and
+// the lanes' 8 values along k are read down the columns with LDS's transposing
+// read. Its 16 lanes take 32 bytes of 4 rows: the chunks of row k lie at
+// chunk ^ 2 (k % 4), so that the 4 rows lie in different banks.
+template <int KIND, typename TO, int BM, int BN, int WM, int WN, int EPI, bool XT, bool WT>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
     constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // loads per wavefront and step, 8 rows each
     static_assert(LA * 8 * NW == BM && LB * 8 * NW == BN, "rows divide over the wavefronts");
-    static_assert(KIND != kMX || BM + BN == 64 * NW, "one load of scales per wavefront and step");
+    static_assert(KIND != kMX || (BM % 64 == 0 && BN % 64 == 0 && BM + BN <= 64 * NW), "one load of scales per wavefront and step");
+    static_assert(KIND == kBF16 || (!XT && !WT), "the transposing read is of 16 bits");
     // one array per buffer: the compiler then knows that reads of one do not wait for the loads into the other
     __shared__ __attribute__((aligned(128))) char s0[(BM + BN) * 128];
     __shared__ __attribute__((aligned(128))) char s1[(BM + BN) * 128];
-    __shared__ __attribute__((aligned(16))) uint8_t q0[KIND == kMX ? (BM + BN) * 4 : 16];
-    __shared__ __attribute__((aligned(16))) uint8_t q1[KIND == kMX ? (BM + BN) * 4 : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t q0[KIND == kMX ? 256 * NW : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t q1[KIND == kMX ? 256 * NW : 16];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int r = lane & 15, kg = lane >> 4;
     int tm, tn;
@@ -202,31 +224,41 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
     // offset per lane serves all. Loads whole behind the operand take its first 8 rows of this tile
     // instead: their rows of y are not stored.
     const char *xrow[LA], *wrow[LB];
-    uint32_t xlen[LA], wlen[LB];
-#pragma unroll
-    for (int j = 0; j < LA; ++j) {
-        int row = m0 + (w * LA + j) * 8;
-        row = row < a.M ? row : m0;
-        xrow[j] = reinterpret_cast<const char *>(a.x) + (int64_t)row * a.ldx;
-        xlen[j] = (uint32_t)(min(8, a.M - row) * a.ldx);
-    }
-#pragma unroll
-    for (int j = 0; j < LB; ++j) {
-        int row = n0 + (w * LB + j) * 8;
-        row = row < a.N ? row : n0;
-        wrow[j] = reinterpret_cast<const char *>(a.w) + (int64_t)row * a.ldw;
-        wlen[j] = (uint32_t)(min(8, a.N - row) * a.ldw);
-    }
+    uint32_t xlen[LA], wlen[LB], xoff[LA], woff[LB];
     // this lane's chunk of the 8 rows of a load
     const uint32_t chunk = (uint32_t)(((lane & 7) ^ (lane >> 3)) << 4);
     const uint32_t va = (uint32_t)(lane >> 3) * (uint32_t)a.ldx + chunk, vb = (uint32_t)(lane >> 3) * (uint32_t)a.ldw + chunk;
+#pragma unroll
+    for (int j = 0; j < LA; ++j) {
+        if constexpr (XT) {
+            const int g = (w * LA + j) * 64 + lane, k = g / (BM / 8), c = g % (BM / 8);
+            xoff[j] = (uint32_t)k * (uint32_t)a.ldx + (uint32_t)((c ^ (2 * (k & 3))) << 4);
+        } else {
+            int row = m0 + (w * LA + j) * 8;
+            row = row < a.M ? row : m0;
+            xrow[j] = reinterpret_cast<const char *>(a.x) + (int64_t)row * a.ldx;
+            xlen[j] = (uint32_t)(min(8, a.M - row) * a.ldx);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < LB; ++j) {
+        if constexpr (WT) {
+            const int g = (w * LB + j) * 64 + lane, k = g / (BN / 8), c = g % (BN / 8);
+            woff[j] = (uint32_t)k * (uint32_t)a.ldw + (uint32_t)((c ^ (2 * (k & 3))) << 4);
+        } else {
+            int row = n0 + (w * LB + j) * 8;
+            row = row < a.N ? row : n0;
+            wrow[j] = reinterpret_cast<const char *>(a.w) + (int64_t)row * a.ldw;
+            wlen[j] = (uint32_t)(min(8, a.N - row) * a.ldw);
+        }
+    }
     const uint8_t *srow = nullptr;
     uint32_t slen = 0, vs = 0;
     if constexpr (KIND == kMX) {
         // scales: wavefronts below BM / 64 take rows of x, the others rows of w; 4 bytes a row and step
         const bool of_x = w < BM / 64;
         const int row0 = of_x ? m0 + w * 64 : n0 + (w - BM / 64) * 64, most = of_x ? a.M : a.N;
-        const int64_t rows = max(0, min(64, most - row0));
+        const int64_t rows = w < (BM + BN) / 64 ? max(0, min(64, most - row0)) : 0;
         const uint8_t *p = (of_x ? a.xscale + (int64_t)row0 * a.lds : a.wscale + (int64_t)row0 * a.lds);
         srow = rows > 0 ? p : a.xscale;
         slen = (uint32_t)(rows * a.lds);
@@ -242,15 +274,30 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
         const bool live = s < steps;
         const uint32_t k0 = live ? (uint32_t)(first + s) * 128u : 0u;
         const uint32_t off = oob_if(!live || k0 + chunk >= a.kbytes, 0);
+        // rows along k: the 64 rows of the step, from the tile's first column on; zeros behind the last row
+        const int k1 = (int)(k0 >> 1);
+        const int rows = max(0, live ? min(64, a.krows - k1) : 0);
+        const char *xt = nullptr, *wt = nullptr;
+        uint32_t xtl = 0, wtl = 0;
+        if constexpr (XT) {
+            xt = reinterpret_cast<const char *>(a.x) + (int64_t)k1 * a.ldx + m0 * 2;
+            xtl = (uint32_t)max(0, rows * (int)a.ldx - m0 * 2);
+        }
+        if constexpr (WT) {
+            wt = reinterpret_cast<const char *>(a.w) + (int64_t)k1 * a.ldw + n0 * 2;
+            wtl = (uint32_t)max(0, rows * (int)a.ldw - n0 * 2);
+        }
 #pragma unroll
         for (int j = 0; j < LA; ++j) {
-            const int row = (w * LA + j) * 8;
-            to_lds16(xrow[j], xlen[j], buf + row * 128, va | off, k0);
+            char *to = buf + (w * LA + j) * 1024;
+            if constexpr (XT) to_lds16(xt, xtl, to, xoff[j], 0);
+            else to_lds16(xrow[j], xlen[j], to, va | off, k0);
         }
 #pragma unroll
         for (int j = 0; j < LB; ++j) {
-            const int row = (w * LB + j) * 8;
-            to_lds16(wrow[j], wlen[j], buf + (BM + row) * 128, vb | off, k0);
+            char *to = buf + BM * 128 + (w * LB + j) * 1024;
+            if constexpr (WT) to_lds16(wt, wtl, to, woff[j], 0);
+            else to_lds16(wrow[j], wlen[j], to, vb | off, k0);
         }
         if constexpr (KIND == kMX)
             to_lds4(srow, slen, sc + w * 256, (vs + (uint32_t)(first + s) * 4u) | oob_if(!live, 0));
@@ -279,9 +326,23 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
         u32x4 l[TQ], h[TQ];
         int s[TQ];
     } x0, x1;
+    // rows along k: this lane's 8 bytes of row 8 kg + j / 4, at block b of 16 columns
+    const int tk = 8 * kg + (r >> 2), tx = 2 * (r >> 2), tc = (r >> 1) & 1, th = (r & 1) * 8;
+    auto down = [&](u32x4 &l, u32x4 &h, const char *part, int b, int width) {
+        const char *p = part + tk * width + (((2 * b + tc) ^ tx) << 4) + th;
+        const u32x2 l0 = lds_transposed(p), l1 = lds_transposed(p + 4 * width);
+        const u32x2 h0 = lds_transposed(p + 32 * width), h1 = lds_transposed(p + 36 * width);
+        l = __builtin_shufflevector(l0, l1, 0, 1, 2, 3);
+        h = __builtin_shufflevector(h0, h1, 0, 1, 2, 3);
+    };
     auto read_w = [&](WRegs &f, const char *buf, const uint8_t *sc) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
+            f.s[j] = 0;
+            if constexpr (WT) {
+                down(f.l[j], f.h[j], buf + BM * 128, wn * TN + j, BN * 2);
+                continue;
+            }
             f.l[j] = *reinterpret_cast<const u32x4 *>(buf + pb + j * 2048);
             f.h[j] = *reinterpret_cast<const u32x4 *>(buf + (pb ^ 64) + j * 2048);
             f.s[j] = KIND == kMX ? sc[(BM + (wn * TN + j) * 16 + r) * 4 + kg] : 0;
@@ -290,6 +351,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
     auto read_x = [&](XRegs &f, const char *buf, const uint8_t *sc, int q) {
 #pragma unroll
         for (int i = 0; i < TQ; ++i) {
+            f.s[i] = 0;
+            if constexpr (XT) {
+                down(f.l[i], f.h[i], buf, wm * TM + q * TQ + i, BM * 2);
+                continue;
+            }
             f.l[i] = *reinterpret_cast<const u32x4 *>(buf + pa + (q * TQ + i) * 2048);
             f.h[i] = *reinterpret_cast<const u32x4 *>(buf + (pa ^ 64) + (q * TQ + i) * 2048);
             f.s[i] = KIND == kMX ? sc[((wm * TM + q * TQ + i) * 16 + r) * 4 + kg] : 0;
@@ -310,7 +376,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
             multiply(wf, (q & 1) ? x1 : x0, q);
             __builtin_amdgcn_sched_barrier(0);
         }
-        __syncthreads();  // step s + 1 has arrived, and everybody has read all of step s
+        arrive();  // step s + 1 is there, and everybody has read all of step s
         __builtin_amdgcn_sched_barrier(0);
         read_w(nwf, nbuf, nsc);
         read_x(x0, nbuf, nsc, 0);
@@ -328,7 +394,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
 
     // pairs of steps, without a branch: the accumulators then stay where they are
     fetch(0, s0, q0);
-    __syncthreads();
+    arrive();
     fetch(1, s1, q1);
     read_w(w0, s0, q0);
     read_x(x0, s0, q0, 0);
@@ -336,21 +402,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
         step(s, s0, q0, s1, q1, w0, w1);
         step(s + 1, s1, q1, s0, q0, w1, w0);
     }
-    __syncthreads();
+    arrive();
 
     // epilogue: 16 rows of the wavefront's columns at a time through LDS
     constexpr int CW = TN * 16, LDC = CW + 4;
     static_assert(NW * 16 * LDC * 4 <= (BM + BN) * 128, "the wavefronts' pieces fit one buffer");
     float *piece = reinterpret_cast<float *>(s0) + w * 16 * LDC;
-    constexpr int LPR = CW / 4, RPI = 64 / LPR, NP = 16 / RPI;  // lanes per row, rows per pass, passes
-    const int mw = m0 + wm * TM * 16 + lane / LPR, col = (lane % LPR) * 4, n = n0 + wn * CW + col;
+    // a lane's group of 4 columns in pass p over the 16 rows
+    constexpr int LPR = CW / 4, NP = CW / 16;
+    const int mw = m0 + wm * TM * 16, nw = n0 + wn * CW;
+    auto row_of = [&](int p) { return (p * 64 + lane) / LPR; };
+    auto col_of = [&](int p) { return ((p * 64 + lane) % LPR) * 4; };
     auto stage = [&](int i) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) *reinterpret_cast<f32x4 *>(piece + r * LDC + j * 16 + kg * 4) = acc[i][j];
         __builtin_amdgcn_wave_barrier();
     };
     auto staged = [&](int p, float (&v)[4]) {
-        const f32x4 c = *reinterpret_cast<const f32x4 *>(piece + (p * RPI + lane / LPR) * LDC + col);
+        const f32x4 c = *reinterpret_cast<const f32x4 *>(piece + row_of(p) * LDC + col_of(p));
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = c[e];
     };
@@ -363,32 +432,34 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
             for (int p = 0; p < NP; ++p) {
                 float v[4];
                 staged(p, v);
-                const int m = mw + i * 16 + p * RPI;
+                const int m = mw + i * 16 + row_of(p), n = nw + col_of(p);
                 if (m < a.M && n < a.N) put4<float>(a.part + ((int64_t)blockIdx.y * a.M + m) * a.N + n, v, a.N - n, whole);
             }
             __builtin_amdgcn_wave_barrier();
         }
         return;
     }
-    float bias[4];
-    bias4(a, n, bias);
     if (EPI == SSD_ACT_NONE && (a.N & 3) == 0) {
         // the next 16 rows' residual is on its way while 16 rows are finished
-        float res[2][NP][4];
+        float bias[NP][4], res[2][NP][4];
 #pragma unroll
-        for (int p = 0; p < NP; ++p) res4<TO, true>(a, mw + p * RPI, n, res[0][p]);
+        for (int p = 0; p < NP; ++p) {
+            bias4(a, nw + col_of(p), bias[p]);
+            res4<TO, true>(a, mw + row_of(p), nw + col_of(p), res[0][p]);
+        }
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             stage(i);
             if (i + 1 < TM) {
 #pragma unroll
-                for (int p = 0; p < NP; ++p) res4<TO, true>(a, mw + (i + 1) * 16 + p * RPI, n, res[(i + 1) & 1][p]);
+                for (int p = 0; p < NP; ++p)
+                    res4<TO, true>(a, mw + (i + 1) * 16 + row_of(p), nw + col_of(p), res[(i + 1) & 1][p]);
             }
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
                 float v[4];
                 staged(p, v);
-                finish4<TO, SSD_ACT_NONE, true>(a, mw + i * 16 + p * RPI, n, v, bias, res[i & 1][p]);
+                finish4<TO, SSD_ACT_NONE, true>(a, mw + i * 16 + row_of(p), nw + col_of(p), v, bias[p], res[i & 1][p]);
             }
             __builtin_amdgcn_wave_barrier();
         }
@@ -399,10 +470,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
         constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll 1
         for (int p = 0; p < NP; ++p) {
-            float v[4], res[4];
-            res4<TO, kWhole>(a, mw + i * 16 + p * RPI, n, res);
+            float v[4], bias[4], res[4];
+            const int m = mw + i * 16 + row_of(p), n = nw + col_of(p);
+            bias4(a, n, bias);
+            res4<TO, kWhole>(a, m, n, res);
             staged(p, v);
-            finish4<TO, EPI, kWhole>(a, mw + i * 16 + p * RPI, n, v, bias, res);
+            finish4<TO, EPI, kWhole>(a, m, n, v, bias, res);
         }
     };
 #pragma unroll
@@ -510,6 +583,8 @@ __global__ __launch_bounds__(256) void k_pad(const U *in, U *out, int64_t rows, 
 }
 
 // out (C x ldo) = in (R x C) transposed, zeros behind column R. 64 x 64 a work-group.
+// fp32's gradients take it: its products are bound by the matrix cores (16 times
+// slower than bf16), beside which these copies are small.
 template <typename T>
 __global__ __launch_bounds__(256) void k_transpose(const T *in, T *out, int R, int C, int ldo) {
     __shared__ T sm[64][64 + 4 / sizeof(T)];
@@ -521,63 +596,96 @@ __global__ __launch_bounds__(256) void k_transpose(const T *in, T *out, int R, i
         if (c0 + i < C && r0 + x < ldo) out[(int64_t)(c0 + i) * ldo + r0 + x] = sm[x][i];
 }
 
-// dz = dy act'(z) of 64 x 64: rows (M x ldz), the transpose (N x ldt), both
-// zeros behind their rows, and the 64 rows' share of db (fp32, before dz is
-// rounded).
-template <typename T>
-__global__ __launch_bounds__(256) void k_dz(const T *dy, const T *pre, int act, T *dz, T *dzt, float *part, int M, int N,
-                                            int ldz, int ldt) {
-    __shared__ T sm[64][64 + 4 / sizeof(T)];
-    __shared__ float col[4][64];
-    const int m0 = blockIdx.x * 64, n0 = blockIdx.y * 64, x = threadIdx.x & 63, y = threadIdx.x >> 6;
-    const int n = n0 + x;
-    float sum = 0.f;
+// dz = dy act'(z), rows of ldz values with zeros behind column N, and the
+// shares of db of each 64 rows (fp32, before dz is rounded). A work-group
+// takes 64 rows of 512 columns, a lane 8 columns (V: N is a multiple of 8 and
+// they are one load) of every fourth row.
+template <typename T, bool V, int ACT>
+__global__ __launch_bounds__(256) void k_dz(const T *dy, const T *pre, T *dz, float *part, int M, int N, int ldz) {
+    __shared__ float col[4][64][8];
+    const int lane = threadIdx.x & 63, y = threadIdx.x >> 6;
+    const int m0 = blockIdx.x * 64, n = blockIdx.y * 512 + lane * 8;
+    float sum[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] = 0.f;
+#pragma unroll 4
     for (int i = y; i < 64; i += 4) {
-        float v = 0.f;
-        if (m0 + i < M && n < N) {
-            const int64_t at = (int64_t)(m0 + i) * N + n;
-            v = (float)dy[at];
-            if (act != SSD_ACT_NONE) v *= act_slope((float)pre[at], act);
+        const int m = m0 + i;
+        if (m >= M || n >= ldz) continue;
+        const int64_t at = (int64_t)m * N + n;
+        float v[8], z[8];
+        if constexpr (V) {
+            float lo[4], hi[4];
+            get4<T>(lo, dy + at, 4, true);
+            get4<T>(hi, dy + at + 4, 4, true);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = lo[e], v[4 + e] = hi[e];
+            if constexpr (ACT != SSD_ACT_NONE) {
+                get4<T>(lo, pre + at, 4, true);
+                get4<T>(hi, pre + at + 4, 4, true);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[e] = lo[e], z[4 + e] = hi[e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[e] = n + e < N ? (float)dy[at + e] : 0.f;
+                z[e] = (ACT != SSD_ACT_NONE && n + e < N) ? (float)pre[at + e] : 0.f;
+            }
         }
-        sum += v;
-        sm[i][x] = (T)v;
-        if (dz && m0 + i < M && n < ldz) dz[(int64_t)(m0 + i) * ldz + n] = (T)v;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (ACT != SSD_ACT_NONE) v[e] *= act_slope(z[e], ACT);
+            sum[e] += v[e];
+        }
+        if (dz) {
+            const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+            T *o = dz + (int64_t)m * ldz + n;  // ldz is a multiple of 16 bytes
+            put4<T>(o, lo, 4, true);
+            if (n + 4 < ldz) put4<T>(o + 4, hi, 4, true);
+        }
     }
-    col[y][x] = sum;
+    if (!part) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) col[y][lane][e] = sum[e];
     __syncthreads();
-    if (part && y == 0 && n < N) part[(int64_t)blockIdx.x * N + n] = col[0][x] + col[1][x] + col[2][x] + col[3][x];
-    if (dzt)
-        for (int i = y; i < 64; i += 4)
-            if (n0 + i < N && m0 + x < ldt) dzt[(int64_t)(n0 + i) * ldt + m0 + x] = sm[x][i];
+    if (y == 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (n + e < N)
+                part[(int64_t)blockIdx.x * N + n + e] = col[0][lane][e] + col[1][lane][e] + col[2][lane][e] + col[3][lane][e];
+    }
 }
 
-static int kind_of(int dtype) { return dtype == SSD_BF16 ? kBF16 : kF32; }
-
-// How a product is formed. tile: 0 = k_skinny, else the tile's edge.
+// How a product is formed. bm = 0: k_skinny, else a work-group's tile of y.
 // The model of a tile kernel's time, in units of one 128-byte step of a
-// 256-tile: work-groups run in rounds over the 256 CUs (two 128-tiles share a
-// CU), each round its steps and a fixed share for the start and the epilogue,
-// and a split adds the traffic of its fp32 parts.
-LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes) {
+// 256 x 256 tile: work-groups run in rounds over the 256 CUs (two of the
+// 128 x 128 tiles share a CU), each round its steps and a fixed share for the
+// start and the epilogue, and a split adds the traffic of its fp32 parts.
+LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, bool along_k) {
     LinearPlan p = {};
     p.steps = (int)((kbytes + 127) / 128);
     p.splits = 1;
     p.steps_per_split = p.steps;
-    if (M <= 64) return p;
+    if (M <= 64 && !along_k) return p;
+    struct Tile {
+        int bm, bn;
+        double slots, cost;
+    };
+    const Tile tiles[] = {{256, 256, 256, 1.0}, {256, 192, 256, 0.8}, {128, 128, 512, 0.6}};
     double best = 1e300;
-    for (int tile = 128; tile <= 256; tile *= 2) {
-        const int64_t nm = (M + tile - 1) / tile, nn = (N + tile - 1) / tile;
+    for (const Tile &c : tiles) {
+        const int64_t nm = (M + c.bm - 1) / c.bm, nn = (N + c.bn - 1) / c.bn;
         for (int splits = 1; splits <= 32 && splits <= p.steps; splits += splits < 8 ? 1 : 4) {
-            const int per = (p.steps + splits - 1) / splits;
-            const int real = (p.steps + per - 1) / per;
-            if (real != splits) continue;
-            const double slots = tile == 256 ? 256 : 512;
-            const double rounds = (double)((int64_t)((nm * nn * splits + slots - 1) / slots));
-            double t = rounds * (per + 6) * (tile == 256 ? 1.0 : 0.6);
+            const int per = ((p.steps + splits - 1) / splits + 1) & ~1;  // steps go in pairs
+            if (splits > 1 && (p.steps + per - 1) / per != splits) continue;
+            const double rounds = (double)((int64_t)((nm * nn * splits + c.slots - 1) / c.slots));
+            double t = rounds * (per + 6) * c.cost;
             if (splits > 1) t += 6 + 2.0 * splits * M * N * 4 / 4.0e6;
             if (t < best) {
                 best = t;
-                p.tile = tile;
+                p.bm = c.bm;
+                p.bn = c.bn;
                 p.splits = splits;
                 p.steps_per_split = per;
                 p.nm = (int)nm;
@@ -588,30 +696,39 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes) {
     return p;
 }
 
-template <int KIND, typename TO>
-static ssd_status run_linear(const LinearArgs &a, const LinearPlan &p, hipStream_t s) {
+template <int KIND, typename TO, bool XT, bool WT>
+static ssd_status run_tile(const LinearArgs &a, const LinearPlan &p, hipStream_t s) {
+    const dim3 grid((unsigned)(p.nm * p.nn), (unsigned)p.splits);
+    auto go = [&](auto epi) {
+        constexpr int EPI = decltype(epi)::value;
+        if (p.bm == 128) return launch(k_tile<KIND, TO, 128, 128, 2, 2, EPI, XT, WT>, grid, dim3(256), s, a);
+        if (p.bn == 192) return launch(k_tile<KIND, TO, 256, 192, 2, 4, EPI, XT, WT>, grid, dim3(512), s, a);
+        return launch(k_tile<KIND, TO, 256, 256, 2, 4, EPI, XT, WT>, grid, dim3(512), s, a);
+    };
     hipError_t e;
-    if (p.tile == 0) {
-        const dim3 grid((unsigned)((a.N + 15) / 16)), block(512);
-        e = a.M <= 16   ? launch(k_skinny<KIND, TO, 1>, grid, block, s, a)
-            : a.M <= 32 ? launch(k_skinny<KIND, TO, 2>, grid, block, s, a)
-                        : launch(k_skinny<KIND, TO, 4>, grid, block, s, a);
+    if (p.splits > 1) {
+        e = go(std::integral_constant<int, kParts>{});
+    } else if constexpr (XT || WT) {  // gradients have no activation
+        e = go(std::integral_constant<int, SSD_ACT_NONE>{});
     } else {
-        const dim3 grid((unsigned)(p.nm * p.nn), (unsigned)p.splits);
-        auto go = [&](auto epi) {
-            constexpr int EPI = decltype(epi)::value;
-            return p.tile == 256 ? launch(k_tile<KIND, TO, 256, 256, 2, 4, EPI>, grid, dim3(512), s, a)
-                                 : launch(k_tile<KIND, TO, 128, 128, 2, 2, EPI>, grid, dim3(256), s, a);
-        };
-        e = p.splits > 1                 ? go(std::integral_constant<int, kParts>{})
-            : a.act == SSD_ACT_SILU ? go(std::integral_constant<int, SSD_ACT_SILU>{})
+        e = a.act == SSD_ACT_SILU   ? go(std::integral_constant<int, SSD_ACT_SILU>{})
             : a.act == SSD_ACT_GELU ? go(std::integral_constant<int, SSD_ACT_GELU>{})
                                     : go(std::integral_constant<int, SSD_ACT_NONE>{});
-        if (e == hipSuccess && p.splits > 1) {
-            const int64_t n = (int64_t)a.M * ((a.N + 3) / 4);
-            e = launch(k_join<TO>, dim3((unsigned)((n + 255) / 256)), dim3(256), s, a);
-        }
     }
+    if (e == hipSuccess && p.splits > 1) {
+        const int64_t n = (int64_t)a.M * ((a.N + 3) / 4);
+        e = launch(k_join<TO>, dim3((unsigned)((n + 255) / 256)), dim3(256), s, a);
+    }
+    return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+}
+
+template <int KIND, typename TO>
+static ssd_status run_linear(const LinearArgs &a, const LinearPlan &p, hipStream_t s) {
+    if (p.bm) return run_tile<KIND, TO, false, false>(a, p, s);
+    const dim3 grid((unsigned)((a.N + 15) / 16)), block(512);
+    const hipError_t e = a.M <= 16   ? launch(k_skinny<KIND, TO, 1>, grid, block, s, a)
+                         : a.M <= 32 ? launch(k_skinny<KIND, TO, 2>, grid, block, s, a)
+                                     : launch(k_skinny<KIND, TO, 4>, grid, block, s, a);
     return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 
@@ -619,6 +736,7 @@ ssd_status launch_linear(LinearArgs a, const LinearPlan &p, bool mx, ssd_dtype d
     a.nm = p.nm; a.nn = p.nn; a.steps = p.steps; a.splits = p.splits; a.steps_per_split = p.steps_per_split;
     if (p.splits == 1) a.part = nullptr;
     if (mx) return run_linear<kMX, bf16>(a, p, s);
+    if (a.wt) return a.xt ? run_tile<kBF16, bf16, true, true>(a, p, s) : run_tile<kBF16, bf16, false, true>(a, p, s);
     return dtype == SSD_BF16 ? run_linear<kBF16, bf16>(a, p, s) : run_linear<kF32, float>(a, p, s);
 }
 
@@ -631,25 +749,36 @@ ssd_status launch_pad(const void *in, void *out, int64_t rows, int64_t n, int64_
     return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 
-ssd_status launch_transpose(const void *in, void *out, int64_t R, int64_t C, int64_t ldo, ssd_dtype dtype, hipStream_t s) {
+ssd_status launch_transpose(const void *in, void *out, int64_t R, int64_t C, int64_t ldo, hipStream_t s) {
     const dim3 grid((unsigned)((ldo + 63) / 64), (unsigned)((C + 63) / 64)), block(256);
-    const hipError_t e =
-        dtype == SSD_BF16
-            ? launch(k_transpose<bf16>, grid, block, s, (const bf16 *)in, (bf16 *)out, (int)R, (int)C, (int)ldo)
-            : launch(k_transpose<float>, grid, block, s, (const float *)in, (float *)out, (int)R, (int)C, (int)ldo);
-    return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+    return launch(k_transpose<float>, grid, block, s, (const float *)in, (float *)out, (int)R, (int)C, (int)ldo) ==
+                   hipSuccess
+               ? SSD_OK
+               : SSD_ERR_HIP;
 }
 
-ssd_status launch_dz(const void *dy, const void *pre, int act, void *dz, void *dzt, float *part, int64_t M, int64_t N,
-                     int64_t ldz, int64_t ldt, ssd_dtype dtype, hipStream_t s) {
-    const int64_t nm = ((dzt ? ldt : M) + 63) / 64, nn = ((dz ? ldz : N) + 63) / 64;
-    const dim3 grid((unsigned)nm, (unsigned)nn), block(256);
-    const hipError_t e = dtype == SSD_BF16
-                             ? launch(k_dz<bf16>, grid, block, s, (const bf16 *)dy, (const bf16 *)pre, act, (bf16 *)dz,
-                                      (bf16 *)dzt, part, (int)M, (int)N, (int)ldz, (int)ldt)
-                             : launch(k_dz<float>, grid, block, s, (const float *)dy, (const float *)pre, act, (float *)dz,
-                                      (float *)dzt, part, (int)M, (int)N, (int)ldz, (int)ldt);
-    return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+template <typename T>
+static ssd_status run_dz(const void *dy, const void *pre, int act, void *dz, float *part, int64_t M, int64_t N, int64_t ldz,
+                         hipStream_t s) {
+    const dim3 grid((unsigned)((M + 63) / 64), (unsigned)((ldz + 511) / 512)), block(256);
+    auto go = [&](auto k) {
+        return launch(k, grid, block, s, (const T *)dy, (const T *)pre, (T *)dz, part, (int)M, (int)N, (int)ldz) == hipSuccess
+                   ? SSD_OK
+                   : SSD_ERR_HIP;
+    };
+    if (N % 8 == 0)
+        return act == SSD_ACT_SILU   ? go(k_dz<T, true, SSD_ACT_SILU>)
+               : act == SSD_ACT_GELU ? go(k_dz<T, true, SSD_ACT_GELU>)
+                                     : go(k_dz<T, true, SSD_ACT_NONE>);
+    return act == SSD_ACT_SILU   ? go(k_dz<T, false, SSD_ACT_SILU>)
+           : act == SSD_ACT_GELU ? go(k_dz<T, false, SSD_ACT_GELU>)
+                                 : go(k_dz<T, false, SSD_ACT_NONE>);
+}
+
+ssd_status launch_dz(const void *dy, const void *pre, int act, void *dz, float *part, int64_t M, int64_t N, int64_t ldz,
+                     ssd_dtype dtype, hipStream_t s) {
+    return dtype == SSD_BF16 ? run_dz<bf16>(dy, pre, act, dz, part, M, N, ldz, s)
+                             : run_dz<float>(dy, pre, act, dz, part, M, N, ldz, s);
 }
 
 }  // namespace ssd
