@@ -50,6 +50,25 @@ __device__ __forceinline__ void to_lds4(const void *base, uint32_t bytes, void *
     __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(base, bytes), (lds_void *)dst, 4, voff, 0, 0, 0);
 }
 
+// Schedules R LDS reads one by one between the first of P matrix-core
+// instructions, and V loads between the rest.
+template <int R, int P, int V>
+__device__ __forceinline__ void mix() {
+    constexpr int each = (R + P - 1) / P, n = (R + each - 1) / each;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, each, 0);
+    }
+    constexpr int left = P > n ? P - n : 1, per = (V + left - 1) / left;
+#pragma unroll
+    for (int i = 0; i < left && V > 0; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x010, per, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // Every wavefront's loads into LDS have arrived (a barrier alone does not wait
 // for them), and its reads too.
 __device__ __forceinline__ void arrive() {
@@ -318,6 +337,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
     // barrier, so that the matrix cores have work across it.
     constexpr int NQ = KIND == kMX ? TM : 4, TQ = TM / NQ;  // 8 bits: registers for the scales, too
     static_assert(TQ * NQ == TM && NQ % 2 == 0, "parts of a step");
+    constexpr int kMma = KIND == kBF16 ? 2 : KIND == kF32 ? 8 : 1;          // matrix-core instructions of a product
+    constexpr int kReadsX = TQ * (XT ? 4 : KIND == kMX ? 3 : 2), kReadsW = TN * (WT ? 4 : KIND == kMX ? 3 : 2);
     struct WRegs {
         u32x4 l[TN], h[TN];
         int s[TN];
@@ -372,24 +393,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
 #pragma unroll
         for (int q = 0; q < NQ - 1; ++q) {
             read_x((q & 1) ? x0 : x1, buf, sc, q + 1);
-            __builtin_amdgcn_sched_barrier(0);  // the compiler would move every read down to its first use
             multiply(wf, (q & 1) ? x1 : x0, q);
-            __builtin_amdgcn_sched_barrier(0);
+            mix<kReadsX, TQ * TN * kMma, 0>();  // the compiler would move every read down to its first use
         }
         arrive();  // step s + 1 is there, and everybody has read all of step s
         __builtin_amdgcn_sched_barrier(0);
         read_w(nwf, nbuf, nsc);
         read_x(x0, nbuf, nsc, 0);
-        __builtin_amdgcn_sched_barrier(0);
         fetch(s + 2, buf, sc);
         multiply(wf, x1, NQ - 1);
-        // the loads between the products, not in front of them
-#pragma unroll
-        for (int j = 0; j < LA + LB; ++j) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+        // between the products, too: in front of them the matrix cores would wait for 8 wavefronts' reads
+        mix<kReadsW + kReadsX, TQ * TN * kMma, LA + LB>();
     };
 
     // pairs of steps, without a branch: the accumulators then stay where they are
@@ -672,7 +686,7 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, bool along_k) {
         int bm, bn;
         double slots, cost;
     };
-    const Tile tiles[] = {{256, 256, 256, 1.0}, {256, 192, 256, 0.8}, {128, 128, 512, 0.6}};
+    const Tile tiles[] = {{256, 256, 256, 1.0}, {256, 192, 256, 0.89}, {128, 128, 512, 0.68}};
     double best = 1e300;
     for (const Tile &c : tiles) {
         const int64_t nm = (M + c.bm - 1) / c.bm, nn = (N + c.bn - 1) / c.bn;
@@ -681,7 +695,7 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, bool along_k) {
             if (splits > 1 && (p.steps + per - 1) / per != splits) continue;
             const double rounds = (double)((int64_t)((nm * nn * splits + c.slots - 1) / c.slots));
             double t = rounds * (per + 6) * c.cost;
-            if (splits > 1) t += 6 + 2.0 * splits * M * N * 4 / 4.0e6;
+            if (splits > 1) t += 6 + 2.0 * splits * M * N * 4 / 6.0e6;
             if (t < best) {
                 best = t;
                 p.bm = c.bm;
