@@ -215,22 +215,26 @@ struct LinearArgs {
     const float *bias;          // (N) or null
     const void *res;            // (M x N) or null
     void *y, *pre;              // pre: z before the activation, or null
-    float *part;                // workspace: (splits, M, N) where the sum over k is split
+    float *part;                // workspace: (splits, part_stride) where the sum over k is split
     int M, N, act;
     uint32_t kbytes;
     bool xt, wt;                // bf16: x (w) is given as (krows x M) ((krows x N)), rows along k
     int krows;
     int nm, nn, steps, splits, steps_per_split;
 };
+// Floats from one part of a split sum to the next.
+__host__ __device__ inline int64_t part_stride(int64_t M, int64_t N) { return (M * N + 3) & ~(int64_t)3; }
 struct LinearPlan {
     int bm, bn;                 // a work-group's tile of y; 0: the few-rows kernel
     int nm, nn;                 // tiles
     int steps, splits, steps_per_split;
 };
 // along_k: an operand has its rows along k (the few-rows kernel takes none of these).
-LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, bool along_k);
+LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, bool f32, bool along_k);
 ssd_status launch_linear(LinearArgs a, const LinearPlan &p, bool mx, ssd_dtype dtype, hipStream_t s);
-ssd_status launch_pad(const void *in, void *out, int64_t rows, int64_t n, int64_t ldo, int es, hipStream_t s);
+// Two operands' rows (R2 may be 0) of n values of es bytes to rows of ldo values.
+ssd_status launch_pad(const void *in1, void *out1, int64_t R1, const void *in2, void *out2, int64_t R2, int64_t n,
+                      int64_t ldo, int es, hipStream_t s);
 // fp32 only.
 ssd_status launch_transpose(const void *in, void *out, int64_t R, int64_t C, int64_t ldo, hipStream_t s);
 // dz (null: not wanted) and the 64-row shares of db (null: not wanted).

@@ -110,8 +110,8 @@ LinearLayout linear_layout(int64_t rows, int64_t in, int64_t out, ssd_dtype dtyp
         l.xpad = align256(rows * l.ld);
         l.wpad = align256(out * l.ld);
     }
-    l.plan = ssd::linear_plan(rows, out, l.ld, false);
-    if (l.plan.splits > 1) l.part = align256(l.plan.splits * rows * out * 4);
+    l.plan = ssd::linear_plan(rows, out, l.ld, dtype == SSD_F32, false);
+    if (l.plan.splits > 1) l.part = align256(l.plan.splits * ssd::part_stride(rows, out) * 4);
     l.total = l.xpad + l.wpad + l.part;
     return l;
 }
@@ -119,14 +119,14 @@ LinearLayout linear_layout(int64_t rows, int64_t in, int64_t out, ssd_dtype dtyp
 LinearLayout linear_mx_layout(int64_t rows, int64_t in, int64_t out) {
     LinearLayout l = {};
     if (rows == 0) return l;
-    l.plan = ssd::linear_plan(rows, out, in, false);
+    l.plan = ssd::linear_plan(rows, out, in, false, false);
     l.ld = in / 32;
     if (l.plan.bm && l.ld % 4 != 0) {
         l.ld = (l.ld + 3) & ~(int64_t)3;
         l.xs = align256(rows * l.ld);
         l.ws = align256(out * l.ld);
     }
-    if (l.plan.splits > 1) l.part = align256(l.plan.splits * rows * out * 4);
+    if (l.plan.splits > 1) l.part = align256(l.plan.splits * ssd::part_stride(rows, out) * 4);
     l.total = l.xs + l.ws + l.part;
     return l;
 }
@@ -152,14 +152,14 @@ LinearBwdLayout linear_bwd_layout(int64_t rows, int64_t in, int64_t out, int act
     int64_t px = 0, pw = 0;
     if (want_dx) {
         l.w = bf ? (l.ldk != in ? align256(out * l.ldk * es) : 0) : align256(in * l.ldz * es);
-        l.px = ssd::linear_plan(rows, in, l.ldz * es, bf);
-        if (l.px.splits > 1) px = align256(l.px.splits * rows * in * 4);
+        l.px = ssd::linear_plan(rows, in, l.ldz * es, !bf, bf);
+        if (l.px.splits > 1) px = align256(l.px.splits * ssd::part_stride(rows, in) * 4);
     }
     if (want_dw) {
         l.x = bf ? (l.ldk != in ? align256(rows * l.ldk * es) : 0) : align256(in * l.ldt * es);
         if (!bf) l.dzt = align256(l.ldz * l.ldt * es);
-        l.pw = ssd::linear_plan(out, in, l.ldt * es, bf);
-        if (l.pw.splits > 1) pw = align256(l.pw.splits * out * in * 4);
+        l.pw = ssd::linear_plan(out, in, l.ldt * es, !bf, bf);
+        if (l.pw.splits > 1) pw = align256(l.pw.splits * ssd::part_stride(out, in) * 4);
     }
     if (want_db) l.db = align256((rows + 63) / 64 * out * 4);
     l.part = px > pw ? px : pw;
@@ -196,8 +196,8 @@ ssd_status ssd_linear(const void *x, const void *w, const float *bias, int act, 
     a.M = (int)rows; a.N = (int)out; a.ldx = a.ldw = l.ld; a.kbytes = (uint32_t)l.ld;
     if (l.xpad) {
         const int es = (int)esize(dtype);
-        if ((st = ssd::launch_pad(x, ws, rows, in, l.ld / es, es, s)) != SSD_OK) return st;
-        if ((st = ssd::launch_pad(w, ws + l.xpad, out, in, l.ld / es, es, s)) != SSD_OK) return st;
+        st = ssd::launch_pad(x, ws, rows, w, ws + l.xpad, out, in, l.ld / es, es, s);
+        if (st != SSD_OK) return st;
         a.x = ws;
         a.w = ws + l.xpad;
     }
@@ -229,8 +229,8 @@ ssd_status ssd_linear_mx(const uint8_t *xq, const uint8_t *xscale, const uint8_t
     a.x = xq; a.w = wq; a.xscale = xscale; a.wscale = wscale; a.bias = bias; a.res = residual; a.y = y; a.act = act;
     a.M = (int)rows; a.N = (int)out; a.ldx = a.ldw = in; a.lds = l.ld; a.kbytes = (uint32_t)in;
     if (l.xs) {
-        if ((st = ssd::launch_pad(xscale, ws, rows, in / 32, l.ld, 1, s)) != SSD_OK) return st;
-        if ((st = ssd::launch_pad(wscale, ws + l.xs, out, in / 32, l.ld, 1, s)) != SSD_OK) return st;
+        st = ssd::launch_pad(xscale, ws, rows, wscale, ws + l.xs, out, in / 32, l.ld, 1, s);
+        if (st != SSD_OK) return st;
         a.xscale = reinterpret_cast<uint8_t *>(ws);
         a.wscale = reinterpret_cast<uint8_t *>(ws + l.xs);
     }
@@ -276,7 +276,7 @@ ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, int act,
         a.x = z; a.y = dx; a.part = part; a.M = (int)rows; a.N = (int)in; a.ldx = l.ldz * es; a.kbytes = (uint32_t)a.ldx;
         a.w = w;
         if (l.w) {
-            st = bf ? ssd::launch_pad(w, wc, out, in, l.ldk, 2, s) : ssd::launch_transpose(w, wc, out, in, l.ldz, s);
+            st = bf ? ssd::launch_pad(w, wc, out, w, wc, 0, in, l.ldk, 2, s) : ssd::launch_transpose(w, wc, out, in, l.ldz, s);
             if (st != SSD_OK) return st;
             a.w = wc;
         }
@@ -290,7 +290,7 @@ ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, int act,
         a.y = dw; a.part = part; a.M = (int)out; a.N = (int)in; a.kbytes = (uint32_t)(l.ldt * es);
         a.x = z; a.w = x;
         if (l.x) {
-            st = bf ? ssd::launch_pad(x, xc, rows, in, l.ldk, 2, s) : ssd::launch_transpose(x, xc, rows, in, l.ldt, s);
+            st = bf ? ssd::launch_pad(x, xc, rows, x, xc, 0, in, l.ldk, 2, s) : ssd::launch_transpose(x, xc, rows, in, l.ldt, s);
             if (st != SSD_OK) return st;
             a.w = xc;
         }

@@ -26,7 +26,7 @@
 // row; the epilogue turns 16 x (columns of a wavefront) at a time through LDS
 // into whole lines of rows.
 //
-// k_skinny (up to 64 rows, decoding): the time is one read of w. A
+// k_skinny (up to 16 rows, decoding): the time is one read of w. A
 // work-group takes 16 rows of w, its 8 wavefronts split k, and both operands
 // go from memory to the matrix cores' registers; the 8 shares are added
 // through LDS.
@@ -223,7 +223,7 @@ __device__ __forceinline__ void tile_of(int id, int nm, int nn, int &tm, int &tn
 // read. Its 16 lanes take 32 bytes of 4 rows: the chunks of row k lie at
 // chunk ^ 2 (k % 4), so that the 4 rows lie in different banks.
 template <int KIND, typename TO, int BM, int BN, int WM, int WN, int EPI, bool XT, bool WT>
-__global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
+__global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearArgs a) {
     constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // loads per wavefront and step, 8 rows each
     static_assert(LA * 8 * NW == BM && LB * 8 * NW == BN, "rows divide over the wavefronts");
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
     // operands of a part are read while the part before it is multiplied: the first
     // part of the next step (and its w) during this step's last, right behind the
     // barrier, so that the matrix cores have work across it.
-    constexpr int NQ = KIND == kMX ? TM : 4, TQ = TM / NQ;  // 8 bits: registers for the scales, too
+    constexpr int NQ = (KIND == kMX || TM < 4) ? TM : 4, TQ = TM / NQ;  // 8 bits: registers for the scales, too
     static_assert(TQ * NQ == TM && NQ % 2 == 0, "parts of a step");
     constexpr int kMma = KIND == kBF16 ? 2 : KIND == kF32 ? 8 : 1;          // matrix-core instructions of a product
     constexpr int kReadsX = TQ * (XT ? 4 : KIND == kMX ? 3 : 2), kReadsW = TN * (WT ? 4 : KIND == kMX ? 3 : 2);
@@ -447,7 +447,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
                 float v[4];
                 staged(p, v);
                 const int m = mw + i * 16 + row_of(p), n = nw + col_of(p);
-                if (m < a.M && n < a.N) put4<float>(a.part + ((int64_t)blockIdx.y * a.M + m) * a.N + n, v, a.N - n, whole);
+                if (m < a.M && n < a.N) put4<float>(a.part + blockIdx.y * part_stride(a.M, a.N) + (int64_t)m * a.N + n, v, a.N - n, whole);
             }
             __builtin_amdgcn_wave_barrier();
         }
@@ -501,34 +501,49 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile(LinearArgs a) {
     }
 }
 
-// The splits' parts of y, added in order, and the epilogue: 4 columns a thread.
+// The splits' parts of y, added in order, and the epilogue. y, the residual,
+// z and a part are each one run of M N values, of which a thread takes 4; a
+// part's stride is a multiple of 4.
 template <typename TO>
 __global__ __launch_bounds__(256) void k_join(LinearArgs a) {
-    const int n4 = (a.N + 3) / 4;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)a.M * n4) return;
-    const int m = (int)(i / n4), n = (int)(i - (int64_t)m * n4) * 4;
-    const int64_t step = (int64_t)a.M * a.N;
-    const float *p = a.part + (int64_t)m * a.N + n;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if ((a.N & 3) == 0) {
-        for (int s = 0; s < a.splits; ++s, p += step) {
-            const f32x4 c = *reinterpret_cast<const f32x4 *>(p);
+    const int64_t total = (int64_t)a.M * a.N, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= total) return;
+    const int left = (int)min((int64_t)4, total - i);
+    const float *p = a.part + i;
+    float v[4] = {0.f, 0.f, 0.f, 0.f}, z[4], res[4];
+    const int64_t step = part_stride(a.M, a.N);
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s, p += step) {
+        const f32x4 c = *reinterpret_cast<const f32x4 *>(p);  // behind the last value: the stride's rest
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += c[e];
-        }
-    } else {
-        for (int s = 0; s < a.splits; ++s, p += step)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (n + e < a.N) v[e] += p[e];
+        for (int e = 0; e < 4; ++e) v[e] += c[e];
     }
-    finish4_any<TO>(a, m, n, v);
+    int n = (int)(i % a.N);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (a.bias && e < left) v[e] += a.bias[n];
+        n = n + 1 < a.N ? n + 1 : 0;
+        z[e] = v[e];
+    }
+    if (a.pre) put4<TO>(reinterpret_cast<TO *>(a.pre) + i, z, left, left == 4);
+    if (a.res) {
+        get4<TO>(res, reinterpret_cast<const TO *>(a.res) + i, left, left == 4);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) res[e] = 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (a.act == SSD_ACT_SILU) v[e] = act_of(v[e], SSD_ACT_SILU);
+        else if (a.act == SSD_ACT_GELU) v[e] = act_of(v[e], SSD_ACT_GELU);
+        v[e] += res[e];
+    }
+    put4<TO>(reinterpret_cast<TO *>(a.y) + i, v, left, left == 4);
 }
 
-template <int KIND, typename TO, int MT>
+template <int KIND, typename TO>
 __global__ __launch_bounds__(512) void k_skinny(LinearArgs a) {
-    __shared__ __attribute__((aligned(16))) float red[8][MT][64][4];
+    __shared__ __attribute__((aligned(16))) float red[8][64][4];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int r = lane & 15, kg = lane >> 4;
     const int n0 = blockIdx.x * 16;
@@ -539,15 +554,13 @@ __global__ __launch_bounds__(512) void k_skinny(LinearArgs a) {
         rsw = make_rsrc(a.wscale + (int64_t)n0 * a.lds, (uint32_t)(min(16, a.N - n0) * a.lds));
         rsx = make_rsrc(a.xscale, (uint32_t)(a.M * a.lds));
     }
-    f32x4 acc[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     const uint32_t ldx = (uint32_t)a.ldx, ldw = (uint32_t)a.ldw, ldsc = (uint32_t)a.lds;
     // U steps' operands are loaded before the first is used; steps behind the last load zeros
-    constexpr int U = MT == 1 ? 4 : 2;
+    constexpr int U = 4;
     for (int s0 = w; s0 < a.steps; s0 += 8 * U) {
-        u32x4 wl[U], wh[U], xl[U][MT], xh[U][MT];
-        int sw[U], sx[U][MT];
+        u32x4 wl[U], wh[U], xl[U], xh[U];
+        int sw[U], sx[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint32_t c0 = (uint32_t)(s0 + 8 * u) * 128u + kg * 16u, c1 = c0 + 64u;
@@ -555,45 +568,55 @@ __global__ __launch_bounds__(512) void k_skinny(LinearArgs a) {
             const uint32_t b = (uint32_t)(s0 + 8 * u) * 4u + kg, ob = oob_if(b >= ldsc, b);
             wl[u] = buf_ld128(rw, o0 + r * ldw);
             wh[u] = buf_ld128(rw, o1 + r * ldw);
+            xl[u] = buf_ld128(rx, o0 + r * ldx);
+            xh[u] = buf_ld128(rx, o1 + r * ldx);
             sw[u] = KIND == kMX ? (int)__builtin_amdgcn_raw_buffer_load_b8(rsw, ob + r * ldsc, 0, 0) : 0;
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const uint32_t row = (uint32_t)(i * 16 + r);
-                xl[u][i] = buf_ld128(rx, o0 + row * ldx);
-                xh[u][i] = buf_ld128(rx, o1 + row * ldx);
-                sx[u][i] = KIND == kMX ? (int)__builtin_amdgcn_raw_buffer_load_b8(rsx, ob + row * ldsc, 0, 0) : 0;
-            }
+            sx[u] = KIND == kMX ? (int)__builtin_amdgcn_raw_buffer_load_b8(rsx, ob + r * ldsc, 0, 0) : 0;
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < MT; ++i) acc[i] = mma2<KIND>(wl[u], wh[u], xl[u][i], xh[u][i], acc[i], sw[u], sx[u][i]);
+        for (int u = 0; u < U; ++u) acc = mma2<KIND>(wl[u], wh[u], xl[u], xh[u], acc, sw[u], sx[u]);
     }
-#pragma unroll
-    for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4 *>(red[w][i][lane]) = acc[i];
+    *reinterpret_cast<f32x4 *>(red[w][lane]) = acc;
     __syncthreads();
-    if (w < MT) {
+    if (w == 0) {
         float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const f32x4 c = *reinterpret_cast<const f32x4 *>(red[k][w][lane]);
+            const f32x4 c = *reinterpret_cast<const f32x4 *>(red[k][lane]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] += c[e];
         }
-        finish4_any<TO>(a, w * 16 + r, n0 + kg * 4, v);
+        finish4_any<TO>(a, r, n0 + kg * 4, v);
     }
 }
 
-// Rows of `bytes` bytes copied to rows of ldo bytes (a multiple of 16), zeros
-// behind them: operands whose rows do not begin at multiples of 16 bytes.
-// ES bytes at a time.
+// The rows of two operands (R1 of in1, R2 of in2, n values each) copied to rows
+// of ldo values (whole multiples of 16 bytes), zeros behind them: for operands whose
+// rows do not begin at such multiples. A wavefront takes 64 groups of 16 bytes of a row.
 template <typename U>
-__global__ __launch_bounds__(256) void k_pad(const U *in, U *out, int64_t rows, int n, int ldo) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= rows * ldo) return;
-    const int64_t row = i / ldo;
-    const int c = (int)(i - row * ldo);
-    out[i] = c < n ? in[row * n + c] : (U)0;
+__global__ __launch_bounds__(256) void k_pad(const U *in1, U *out1, int64_t R1, const U *in2, U *out2, int64_t R2, int n,
+                                             int ldo) {
+    constexpr int E = 16 / sizeof(U);
+    int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int c = ((int)blockIdx.y * 64 + (threadIdx.x & 63)) * E;
+    if (row >= R1 + R2 || c >= ldo) return;
+    const bool first = row < R1;
+    if (!first) row -= R1;
+    const U *p = (first ? in1 : in2) + row * n + c;
+    union {
+        U u[E];
+        u32x4 v;
+    } q;
+#pragma unroll
+    for (int e = 0; e < E; ++e) q.u[e] = c + e < n ? p[e] : (U)0;
+    U *o = (first ? out1 : out2) + row * ldo + c;
+    if (sizeof(U) > 1) {
+        *reinterpret_cast<u32x4 *>(o) = q.v;
+    } else {  // scales: rows of multiples of 4
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (c + e < ldo) o[e] = q.u[e];
+    }
 }
 
 // out (C x ldo) = in (R x C) transposed, zeros behind column R. 64 x 64 a work-group.
@@ -672,21 +695,25 @@ __global__ __launch_bounds__(256) void k_dz(const T *dy, const T *pre, T *dz, fl
 }
 
 // How a product is formed. bm = 0: k_skinny, else a work-group's tile of y.
-// The model of a tile kernel's time, in units of one 128-byte step of a
-// 256 x 256 tile: work-groups run in rounds over the 256 CUs (two of the
-// 128 x 128 tiles share a CU), each round its steps and a fixed share for the
-// start and the epilogue, and a split adds the traffic of its fp32 parts.
-LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, bool along_k) {
+// The model of a tile kernel's time, in microseconds: work-groups run in rounds over
+// the 256 CUs (2 of the 128-tiles, 4 of the 64-tiles share a CU), each round
+// its steps of 128 bytes along k and a fixed share for the start and the
+// epilogue; a split of the sum over k adds a launch and the traffic of its fp32
+// parts. A step's time is measured (large products on a warm GPU): of the bf16 and
+// 8-bit tiles the matrix cores' for the largest one, more and more LDS's and
+// the loads' for the smaller ones; of fp32 the matrix cores' for each.
+LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, bool f32, bool along_k) {
     LinearPlan p = {};
     p.steps = (int)((kbytes + 127) / 128);
     p.splits = 1;
     p.steps_per_split = p.steps;
-    if (M <= 64 && !along_k) return p;
+    if (M <= 16 && !along_k) return p;
     struct Tile {
         int bm, bn;
-        double slots, cost;
+        double slots, step, step32, fixed;
     };
-    const Tile tiles[] = {{256, 256, 256, 1.0}, {256, 192, 256, 0.89}, {128, 128, 512, 0.68}};
+    const Tile tiles[] = {{256, 256, 256, 1.6, 8.0, 14}, {256, 192, 256, 1.42, 6.0, 12},
+                          {128, 128, 512, 1.09, 4.0, 8}, {64, 64, 1024, 0.8, 2.0, 5}};
     double best = 1e300;
     for (const Tile &c : tiles) {
         const int64_t nm = (M + c.bm - 1) / c.bm, nn = (N + c.bn - 1) / c.bn;
@@ -694,8 +721,8 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, bool along_k) {
             const int per = ((p.steps + splits - 1) / splits + 1) & ~1;  // steps go in pairs
             if (splits > 1 && (p.steps + per - 1) / per != splits) continue;
             const double rounds = (double)((int64_t)((nm * nn * splits + c.slots - 1) / c.slots));
-            double t = rounds * (per + 6) * c.cost;
-            if (splits > 1) t += 6 + 2.0 * splits * M * N * 4 / 6.0e6;
+            double t = rounds * (per * (f32 ? c.step32 : c.step) + c.fixed);
+            if (splits > 1) t += 5 + 2.0 * splits * M * N * 4 / 5.0e6;
             if (t < best) {
                 best = t;
                 p.bm = c.bm;
@@ -715,6 +742,7 @@ static ssd_status run_tile(const LinearArgs &a, const LinearPlan &p, hipStream_t
     const dim3 grid((unsigned)(p.nm * p.nn), (unsigned)p.splits);
     auto go = [&](auto epi) {
         constexpr int EPI = decltype(epi)::value;
+        if (p.bm == 64) return launch(k_tile<KIND, TO, 64, 64, 2, 2, EPI, XT, WT>, grid, dim3(256), s, a);
         if (p.bm == 128) return launch(k_tile<KIND, TO, 128, 128, 2, 2, EPI, XT, WT>, grid, dim3(256), s, a);
         if (p.bn == 192) return launch(k_tile<KIND, TO, 256, 192, 2, 4, EPI, XT, WT>, grid, dim3(512), s, a);
         return launch(k_tile<KIND, TO, 256, 256, 2, 4, EPI, XT, WT>, grid, dim3(512), s, a);
@@ -730,7 +758,7 @@ static ssd_status run_tile(const LinearArgs &a, const LinearPlan &p, hipStream_t
                                     : go(std::integral_constant<int, SSD_ACT_NONE>{});
     }
     if (e == hipSuccess && p.splits > 1) {
-        const int64_t n = (int64_t)a.M * ((a.N + 3) / 4);
+        const int64_t n = ((int64_t)a.M * a.N + 3) / 4;
         e = launch(k_join<TO>, dim3((unsigned)((n + 255) / 256)), dim3(256), s, a);
     }
     return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
@@ -740,10 +768,7 @@ template <int KIND, typename TO>
 static ssd_status run_linear(const LinearArgs &a, const LinearPlan &p, hipStream_t s) {
     if (p.bm) return run_tile<KIND, TO, false, false>(a, p, s);
     const dim3 grid((unsigned)((a.N + 15) / 16)), block(512);
-    const hipError_t e = a.M <= 16   ? launch(k_skinny<KIND, TO, 1>, grid, block, s, a)
-                         : a.M <= 32 ? launch(k_skinny<KIND, TO, 2>, grid, block, s, a)
-                                     : launch(k_skinny<KIND, TO, 4>, grid, block, s, a);
-    return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+    return launch(k_skinny<KIND, TO>, grid, block, s, a) == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 
 ssd_status launch_linear(LinearArgs a, const LinearPlan &p, bool mx, ssd_dtype dtype, hipStream_t s) {
@@ -754,13 +779,19 @@ ssd_status launch_linear(LinearArgs a, const LinearPlan &p, bool mx, ssd_dtype d
     return dtype == SSD_BF16 ? run_linear<kBF16, bf16>(a, p, s) : run_linear<kF32, float>(a, p, s);
 }
 
-ssd_status launch_pad(const void *in, void *out, int64_t rows, int64_t n, int64_t ldo, int es, hipStream_t s) {
-    const dim3 grid((unsigned)((rows * ldo + 255) / 256)), block(256);
-    hipError_t e;
-    if (es == 1) e = launch(k_pad<uint8_t>, grid, block, s, (const uint8_t *)in, (uint8_t *)out, rows, (int)n, (int)ldo);
-    else if (es == 2) e = launch(k_pad<uint16_t>, grid, block, s, (const uint16_t *)in, (uint16_t *)out, rows, (int)n, (int)ldo);
-    else e = launch(k_pad<uint32_t>, grid, block, s, (const uint32_t *)in, (uint32_t *)out, rows, (int)n, (int)ldo);
-    return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+template <typename U>
+static ssd_status run_pad(const void *in1, void *out1, int64_t R1, const void *in2, void *out2, int64_t R2, int64_t n,
+                          int64_t ldo, hipStream_t s) {
+    return launch(k_pad<U>, dim3((unsigned)((R1 + R2 + 3) / 4), (unsigned)((ldo * sizeof(U) + 1023) / 1024)), dim3(256), s, (const U *)in1, (U *)out1, R1,
+                  (const U *)in2, (U *)out2, R2, (int)n, (int)ldo) == hipSuccess
+               ? SSD_OK
+               : SSD_ERR_HIP;
+}
+ssd_status launch_pad(const void *in1, void *out1, int64_t R1, const void *in2, void *out2, int64_t R2, int64_t n,
+                      int64_t ldo, int es, hipStream_t s) {
+    if (es == 1) return run_pad<uint8_t>(in1, out1, R1, in2, out2, R2, n, ldo, s);
+    if (es == 2) return run_pad<uint16_t>(in1, out1, R1, in2, out2, R2, n, ldo, s);
+    return run_pad<uint32_t>(in1, out1, R1, in2, out2, R2, n, ldo, s);
 }
 
 ssd_status launch_transpose(const void *in, void *out, int64_t R, int64_t C, int64_t ldo, hipStream_t s) {
