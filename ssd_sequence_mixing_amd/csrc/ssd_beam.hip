@@ -18,6 +18,8 @@
 // The sums of exponentials are fp32 within a wavefront and 64-bit across a
 // row, and scores are compared in 64 bits, so that two candidates change places only
 // where they are closer than the sums' own error (~1e-8 relative).
+#include <float.h>
+
 #include "ssd_common.h"
 #include "ssd_internal.h"
 
@@ -38,33 +40,82 @@ constexpr uint32_t kNone = 0x007fffffu;  // ord32(-inf)
 // Larger value first, then lower index: one 64-bit comparison. 0 is no entry.
 __device__ __forceinline__ uint64_t key_of(uint32_t ord, uint32_t idx) { return ((uint64_t)ord << 32) | (uint32_t)~idx; }
 
-__device__ __forceinline__ uint32_t xor32(uint32_t v, int m) { return (uint32_t)__shfl_xor((int)v, m, 64); }
-__device__ __forceinline__ uint64_t xor64(uint64_t v, int m) {
-    return ((uint64_t)xor32((uint32_t)(v >> 32), m) << 32) | xor32((uint32_t)v, m);
-}
-
-// Bitonic sort of one value per lane, largest in lane 0.
-template <typename U>
-__device__ __forceinline__ U sort_desc(U v, int lane) {
-#pragma unroll
-    for (int k = 2; k <= 64; k <<= 1) {
-#pragma unroll
-        for (int j = k >> 1; j > 0; j >>= 1) {
-            U o;
-            if constexpr (sizeof(U) == 8) o = xor64(v, j); else o = xor32(v, j);
-            const bool keep_max = ((lane & k) == 0) == ((lane & j) == 0);
-            v = (keep_max == (v > o)) ? v : o;
-        }
+// The value of lane ^ m, on the vector unit (a shuffle through LDS would take some 10
+// times as long): within quads, halves and rows of 16 by DPP, across rows by
+// swapping halves of two registers.
+template <int m>
+__device__ __forceinline__ uint32_t xor32(uint32_t v) {
+    const int i = (int)v;
+    if constexpr (m == 1) return (uint32_t)__builtin_amdgcn_mov_dpp(i, 0xb1, 0xf, 0xf, true);        // quad 1 0 3 2
+    if constexpr (m == 2) return (uint32_t)__builtin_amdgcn_mov_dpp(i, 0x4e, 0xf, 0xf, true);        // quad 2 3 0 1
+    if constexpr (m == 4) return xor32<1>(xor32<2>((uint32_t)__builtin_amdgcn_mov_dpp(i, 0x141, 0xf, 0xf, true)));  // 7 - l, then ^ 3
+    if constexpr (m == 8) return (uint32_t)__builtin_amdgcn_mov_dpp(i, 0x128, 0xf, 0xf, true);       // rotated by 8
+    if constexpr (m == 16) {
+        const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return (threadIdx.x & 16) ? p[0] : p[1];
+    }
+    if constexpr (m == 32) {
+        const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return (threadIdx.x & 32) ? p[0] : p[1];
     }
     return v;
 }
+template <int m>
+__device__ __forceinline__ uint64_t xor64(uint64_t v) {
+    return ((uint64_t)xor32<m>((uint32_t)(v >> 32)) << 32) | xor32<m>((uint32_t)v);
+}
+template <int m>
+__device__ __forceinline__ float xorf(float v) { return __uint_as_float(xor32<m>(__float_as_uint(v))); }
+template <int m>
+__device__ __forceinline__ double xord(double v) { return __longlong_as_double((long long)xor64<m>((uint64_t)__double_as_longlong(v))); }
 
+template <typename U, int j>
+__device__ __forceinline__ U exchange(U v, int lane, bool up) {
+    U o;
+    if constexpr (sizeof(U) == 8) o = xor64<j>(v); else o = xor32<j>(v);
+    const bool keep_max = up == ((lane & j) == 0);
+    return (keep_max == (v > o)) ? v : o;
+}
+template <typename U, int j>
+__device__ __forceinline__ U merge_steps(U v, int lane, bool up) {
+    v = exchange<U, j>(v, lane, up);
+    if constexpr (j > 1) v = merge_steps<U, j / 2>(v, lane, up);
+    return v;
+}
+// Bitonic sort of one value per lane, largest in lane 0.
+template <typename U>
+__device__ __forceinline__ U sort_desc(U v, int lane) {
+    v = merge_steps<U, 1>(v, lane, (lane & 2) == 0);
+    v = merge_steps<U, 2>(v, lane, (lane & 4) == 0);
+    v = merge_steps<U, 4>(v, lane, (lane & 8) == 0);
+    v = merge_steps<U, 8>(v, lane, (lane & 16) == 0);
+    v = merge_steps<U, 16>(v, lane, (lane & 32) == 0);
+    return merge_steps<U, 32>(v, lane, true);
+}
+
+template <int m = 32>
 __device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        const uint64_t o = xor64(v, off);
-        v = o > v ? o : v;
-    }
+    const uint64_t o = xor64<m>(v);
+    v = o > v ? o : v;
+    if constexpr (m > 1) v = wave_max64<m / 2>(v);
+    return v;
+}
+template <int m = 32>
+__device__ __forceinline__ float wave_maxf(float v) {
+    v = fmaxf(v, xorf<m>(v));
+    if constexpr (m > 1) v = wave_maxf<m / 2>(v);
+    return v;
+}
+template <int m = 32>
+__device__ __forceinline__ float wave_sumf(float v) {
+    v += xorf<m>(v);
+    if constexpr (m > 1) v = wave_sumf<m / 2>(v);
+    return v;
+}
+template <int m = 32>
+__device__ __forceinline__ double wave_sumd(double v) {
+    v += xord<m>(v);
+    if constexpr (m > 1) v = wave_sumd<m / 2>(v);
     return v;
 }
 
@@ -111,44 +162,41 @@ __global__ __launch_bounds__(256) void k_beam_top(BeamArgs a) {
                     const uint32_t w = raw[e / VE][e % VE];
                     f = __uint_as_float(w);
                 }
-                v[e] = f == f ? f : -INFINITY;
+                v[e] = fmaxf(f, -INFINITY);  // NaN: -inf
             }
         } else {
 #pragma unroll
             for (int e = 0; e < kPerLane; ++e) {
                 const int i = base + ((e / VE) * 64 + lane) * VE + e % VE;
                 const float f = i < V ? (float)rp[i] : -INFINITY;
-                v[e] = f == f ? f : -INFINITY;
+                v[e] = fmaxf(f, -INFINITY);  // NaN: -inf
             }
         }
         float lm = v[0];
 #pragma unroll
         for (int e = 1; e < kPerLane; ++e) lm = fmaxf(lm, v[e]);
-        float wm = lm;
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) wm = fmaxf(wm, __shfl_xor(wm, off, 64));
-        const float Mn = fmaxf(M, wm);
-        if (Mn > -INFINITY) {  // per lane: a share of the row's sum, relative to Mn
+        // the row's sum, a share per lane, relative to the largest logit so far
+        const float Mn = fmaxf(M, wave_maxf(lm));
+        if (Mn > -INFINITY) {
             float s = 0.f;
 #pragma unroll
             for (int e = 0; e < kPerLane; ++e) s += fast_exp2((v[e] - Mn) * kLog2e);
             S = (M > -INFINITY ? S * fast_exp2((M - Mn) * kLog2e) : 0.f) + s;
             M = Mn;
         }
-        // lower bound on the K-th largest of the tile and of the list so far
+        // lower bound on the K-th largest of the tile and of the list so far; -inf is no candidate
         uint32_t bound = (uint32_t)__builtin_amdgcn_readlane((int)sort_desc(ord32(lm), lane), K - 1);
         const uint32_t kth = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(best >> 32), K - 1);
         bound = bound > kth ? bound : kth;
-        bound = bound > kNone ? bound : kNone + 1;  // -inf is no candidate
+        const float least = bound > kNone ? from_ord32(bound) : -FLT_MAX;
         int n = 0;
 #pragma unroll
         for (int e = 0; e < kPerLane; ++e) {
-            const int i = base + ((e / VE) * 64 + lane) * VE + e % VE;
-            const bool in = i < V && ord32(v[e]) >= bound;
-            const uint64_t mask = __ballot(in);
+            const uint64_t mask = __ballot(v[e] >= least);  // (places behind the row hold -inf)
             if (mask) {
+                const int i = base + ((e / VE) * 64 + lane) * VE + e % VE;
                 const int at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
-                if (in && at < 64 - K) buf[at] = key_of(ord32(v[e]), (uint32_t)i);
+                if (v[e] >= least && at < 64 - K) buf[at] = key_of(ord32(v[e]), (uint32_t)i);
                 n += __popcll(mask);
             }
         }
@@ -177,10 +225,20 @@ __global__ __launch_bounds__(256) void k_beam_top(BeamArgs a) {
             __builtin_amdgcn_wave_barrier();
         }
     }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) S += __shfl_xor(S, off, 64);
+    S = wave_sumf(S);
     if (lane < K) a.keys[gl * K + lane] = best;
     if (lane == 0) a.sums[gl] = make_float2(M, S);
+}
+
+// The larger score (equal ones: the lower lane) of 16 lanes; 0xffff: none.
+template <int m>
+__device__ __forceinline__ void better(double &s, uint32_t &who) {
+    const double os = xord<m>(s);
+    const uint32_t ow = xor32<m>(who);
+    const bool take = ow != 0xffffu && (who == 0xffffu || os > s || (os == s && ow < who));
+    s = take ? os : s;
+    who = take ? ow : who;
+    if constexpr (m > 1) better<m / 2>(s, who);
 }
 
 template <typename T>
@@ -194,6 +252,13 @@ __global__ __launch_bounds__(1024) void k_beam_pick(BeamArgs a) {
     const int lane = threadIdx.x & 63, k = threadIdx.x >> 6;
     const int K = a.beams, V = a.V;
     const int64_t b = blockIdx.x, row = b * K + k;
+    // everything the row needs, loaded at once (what k_beam_top left of a finished row is not used)
+    const bool in = lane < a.lists;
+    const int64_t list = row * a.lists + (in ? lane : 0);
+    const float2 ms = in ? a.sums[list] : make_float2(-INFINITY, 0.f);
+    uint64_t key[kMost];
+#pragma unroll
+    for (int r = 0; r < kMost; ++r) key[r] = (in && r < K) ? a.keys[list * K + r] : 0;
     const float score = a.scores[row];
     const bool alive = score > -INFINITY;  // false for NaN too
     if (a.finished && a.finished[row]) {
@@ -205,23 +270,12 @@ __global__ __launch_bounds__(1024) void k_beam_pick(BeamArgs a) {
         }
     } else {
         // log-sum-exp of the row
-        const bool in = lane < a.lists;
-        float2 ms = make_float2(-INFINITY, 0.f);
-        if (in) ms = a.sums[row * a.lists + lane];
-        const float m = ms.x, s = ms.y;
-        float M = m;
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, 64));
-        double S = m > -INFINITY ? (double)s * exp((double)m - (double)M) : 0.0;
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) S += __shfl_xor(S, off, 64);
+        const float M = wave_maxf(ms.x);
+        const double S = wave_sumd(ms.x > -INFINITY ? (double)ms.y * exp((double)ms.x - (double)M) : 0.0);
         const double lse = (double)M + log(S);
         const bool ok = alive && lse - lse == 0.0;  // a finite sum
         uint64_t best = 0;
         if (ok) {
-            uint64_t key[kMost];
-#pragma unroll
-            for (int r = 0; r < kMost; ++r) key[r] = (in && r < K) ? a.keys[(row * a.lists + lane) * K + r] : 0;
             const uint64_t heads = sort_desc(key[0], lane);
             const uint64_t bound = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(heads >> 32), K - 1) << 32) |
                                    (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)heads, K - 1);
@@ -270,14 +324,7 @@ __global__ __launch_bounds__(1024) void k_beam_pick(BeamArgs a) {
     for (; got < K; ++got) {
         double s = hs;
         uint32_t who = (mine > at) ? (uint32_t)lane : 0xffffu;
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1) {
-            const double os = __shfl_xor(s, off, 16);
-            const uint32_t ow = (uint32_t)__shfl_xor((int)who, off, 16);
-            const bool take = ow != 0xffffu && (who == 0xffffu || os > s || (os == s && ow < who));
-            s = take ? os : s;
-            who = take ? ow : who;
-        }
+        better<8>(s, who);
         who = (uint32_t)__builtin_amdgcn_readfirstlane((int)who);
         if (who == 0xffffu) break;
         if (lane == (int)who) {

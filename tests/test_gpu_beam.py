@@ -117,6 +117,22 @@ def test_select_ties_and_order(ssd, dtype, k):
     assert float((out.cpu() - best[:, :k]).abs().max()) <= TOL
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_select_of_the_types_extremes(ssd, dtype):
+    """Tokens forbidden by the type's lowest value instead of -inf: among others, for a whole row and for a whole
+    sequence (every token then has log-probability -log V); and its largest value."""
+    import torch
+    logits, scores, g = _draw(5, 3, 4500, dtype, 12)
+    low, high = torch.finfo(logits.dtype).min, torch.finfo(logits.dtype).max
+    logits.masked_fill_(torch.rand(5, 3, 4500, device="cuda", generator=g) < 0.5, low)
+    logits[1, 1] = low
+    logits[2] = low
+    logits[3, 0, 2100] = high
+    logits[4, 2] = low
+    logits[4, 2, 7] = high
+    _check(ssd, logits, scores)
+
+
 def test_select_of_values_that_are_not_numbers(ssd):
     import torch
     logits, scores, g = _draw(6, 4, 3001, "f32", 11)
