@@ -149,9 +149,12 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : kNormThreads) void k_rms_norm(Norm
             for (int e = 0; e < 8; ++e) h[c][e] += q[e];
         }
     }
-    float wv[NC][8];
+    constexpr bool kLate = W == 16;  // 1024 threads: no registers for the weights, too
+    float wv[kLate ? 1 : NC][8];
+    if constexpr (!kLate) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) ld8<float, V>(wv[c], wt, first(c), kStep, n);
+        for (int c = 0; c < NC; ++c) ld8<float, V>(wv[c], wt, first(c), kStep, n);
+    }
     float sq = 0.f;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
@@ -167,8 +170,9 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : kNormThreads) void k_rms_norm(Norm
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         float y[8];
+        if constexpr (kLate) ld8<float, V>(wv[0], wt, first(c), kStep, n);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = h[c][e] * inv * wv[c][e];
+        for (int e = 0; e < 8; ++e) y[e] = h[c][e] * inv * wv[kLate ? 0 : c][e];
         if constexpr (MX) {
             u32x2 codes;
             uint32_t scale;
@@ -199,16 +203,60 @@ __global__ __launch_bounds__(kNormThreads) void k_mx_quantize(const TX *x, uint8
     }
 }
 
+// A chunk's 8 values as they are stored.
+template <typename T> struct Raw {
+    u32x4 q[sizeof(T) / 2];
+};
+template <typename T, bool V>
+__device__ __forceinline__ void ld_raw(Raw<T> &o, const T *p, int i, int step, int n) {
+    if constexpr (V) {
+#pragma unroll
+        for (int c = 0; c < (int)sizeof(T) / 2; ++c)
+            o.q[c] = i < n ? reinterpret_cast<const u32x4 *>(p + i)[c] : u32x4{0, 0, 0, 0};
+    } else {
+        float v[8];
+        ld8<T, false>(v, p, i, step, n);
+        if constexpr (sizeof(T) == 2) {
+            bf16x8 b;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) b[e] = (bf16)v[e];
+            o.q[0] = __builtin_bit_cast(u32x4, b);
+        } else {
+            o.q[0] = __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
+            o.q[1] = __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]});
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ void unpack(float (&v)[8], const Raw<T> &r) {
+    if constexpr (sizeof(T) == 2) {
+        const u32x4 q = r.q[0];
+        const bf16x8 b = __builtin_bit_cast(bf16x8, q);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = (float)b[e];
+    } else {
+        const u32x4 q0 = r.q[0], q1 = r.q[1];
+        const f32x4 a = __builtin_bit_cast(f32x4, q0), b = __builtin_bit_cast(f32x4, q1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
+    }
+}
+
 // The gradients, from the stored h and inv. With hh = h inv and g = dy w:
 //   dh = inv (g - hh mean(g hh)) + dr_out;   dw = sum over rows of dy hh
-// A work-group takes every nb-th row of one group (blockIdx.y) and keeps its
+// A work-group takes every nb-th row (or 4 rows) of one group (blockIdx.y) and keeps its
 // share of dw in registers, lane by lane the columns it reads; the shares are
 // added in a fixed order (wavefronts, then work-groups in k_column_sums), so
-// the same inputs give the same bits.
+// the same inputs give the same bits. Bound: HBM. A row's three inputs are
+// loaded, as stored, before the row in front of it is finished (kAhead; where
+// they fit the registers): a row's time is otherwise its load, the sum over
+// the lanes and its store, one after the other.
 template <typename TX, typename TR, int W, int NC, bool V>
 __global__ __launch_bounds__(W > 4 ? W * 64 : kNormThreads) void k_rms_norm_bwd(NormBwdArgs a) {
     constexpr int RPB = W > 4 ? 1 : kNormThreads / (64 * W);
     constexpr bool kTwo = sizeof(TX) != sizeof(TR);  // h's gradient in its own type beside x's
+    constexpr bool kAhead = W <= 4 && NC * (2 * sizeof(TR) + sizeof(TX)) <= 40;  // 2 rows' inputs: up to 160 registers
+    constexpr bool kTwice = W > 4;  // long rows: the registers hold no row beside dw; it is read again
     constexpr int kStep = 64 * W;
     __shared__ float red[W > 1 ? W : 1];
     __shared__ float share[RPB > 1 ? kStep * NC * 8 : 1];
@@ -221,45 +269,77 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : kNormThreads) void k_rms_norm_bwd(
     for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[c][e] = 0.f;
-    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += (int64_t)gridDim.x * RPB) {
-        const int64_t r = r0 + slot;
-        if (RPB > 1 && r >= a.rows) break;  // W == 1: no barrier in the loop
+    struct Row {
+        Raw<TR> h[NC], dr[NC];
+        Raw<TX> dy[NC];
+        float inv;
+    };
+    auto load = [&](Row &o, int64_t r) {  // a row behind the last is loaded as zeros
+        const bool in = r < a.rows;
+        const int64_t at = in ? (r * a.groups + g) * n : 0;
+        const int m = in ? n : 0;
+        o.inv = in ? a.rstd[r * a.groups + g] : 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            ld_raw<TR, V>(o.h[c], reinterpret_cast<const TR *>(a.h) + at, first(c), kStep, m);
+            ld_raw<TX, V>(o.dy[c], reinterpret_cast<const TX *>(a.dy) + at, first(c), kStep, m);
+            ld_raw<TR, V>(o.dr[c], reinterpret_cast<const TR *>(a.dres) + at, first(c), kStep, a.dres ? m : 0);
+        }
+    };
+    const int64_t hop = (int64_t)gridDim.x * RPB;
+    Row cur, next;
+    int64_t r = (int64_t)blockIdx.x * RPB + slot;
+    if constexpr (kAhead) load(next, r);
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += hop, r += hop) {
+        if constexpr (kAhead) {
+            cur = next;
+            load(next, r + hop);
+        } else if constexpr (!kTwice) {
+            load(cur, r);
+        } else {
+            cur.inv = a.rstd[r * a.groups + g];
+        }
         const int64_t at = (r * a.groups + g) * n;
-        const float inv = a.rstd[r * a.groups + g];
-        float hh[NC][8], gw[NC][8];
+        const int m = r < a.rows ? n : 0;
+        const float inv = cur.inv;
         float dot = 0.f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            ld8<TR, V>(hh[c], reinterpret_cast<const TR *>(a.h) + at, first(c), kStep, n);
-            ld8<TX, V>(gw[c], reinterpret_cast<const TX *>(a.dy) + at, first(c), kStep, n);
-        }
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            float wv[8];
+            float hh[8], dy[8], wv[8];
+            if constexpr (kTwice) {
+                ld8<TR, V>(hh, reinterpret_cast<const TR *>(a.h) + at, first(c), kStep, n);
+                ld8<TX, V>(dy, reinterpret_cast<const TX *>(a.dy) + at, first(c), kStep, n);
+            } else {
+                unpack(hh, cur.h[c]);
+                unpack(dy, cur.dy[c]);
+            }
             ld8<float, V>(wv, wt, first(c), kStep, n);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                hh[c][e] *= inv;
-                dw[c][e] += gw[c][e] * hh[c][e];
-                gw[c][e] *= wv[e];
-                dot += gw[c][e] * hh[c][e];
+                hh[e] *= inv;
+                dw[c][e] += dy[e] * hh[e];
+                dot += dy[e] * wv[e] * hh[e];
             }
         }
         dot = row_sum<W>(dot, red) / (float)n;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            float dr[8];
-            if (a.dres) {
-                ld8<TR, V>(dr, reinterpret_cast<const TR *>(a.dres) + at, first(c), kStep, n);
+            float hh[8], dy[8], wv[8], dr[8];
+            if constexpr (kTwice) {
+                ld8<TR, V>(hh, reinterpret_cast<const TR *>(a.h) + at, first(c), kStep, n);
+                ld8<TX, V>(dy, reinterpret_cast<const TX *>(a.dy) + at, first(c), kStep, n);
+                ld8<TR, V>(dr, reinterpret_cast<const TR *>(a.dres) + at, first(c), kStep, a.dres ? n : 0);
             } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) dr[e] = 0.f;
+                unpack(hh, cur.h[c]);
+                unpack(dy, cur.dy[c]);
+                unpack(dr, cur.dr[c]);
             }
+            ld8<float, V>(wv, wt, first(c), kStep, n);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dr[e] += inv * (gw[c][e] - hh[c][e] * dot);
-            st8<TX, V>(dr, reinterpret_cast<TX *>(a.dx) + at, first(c), kStep, n);
+            for (int e = 0; e < 8; ++e) dr[e] += inv * (dy[e] * wv[e] - hh[e] * inv * dot);
+            st8<TX, V>(dr, reinterpret_cast<TX *>(a.dx) + at, first(c), kStep, m);
             if constexpr (kTwo) {
-                if (a.dh) st8<TR, V>(dr, reinterpret_cast<TR *>(a.dh) + at, first(c), kStep, n);
+                if (a.dh) st8<TR, V>(dr, reinterpret_cast<TR *>(a.dh) + at, first(c), kStep, m);
             }
         }
     }
@@ -319,12 +399,12 @@ struct NormPlan {
 };
 // One wavefront per row while a row fits 8 chunks a lane and there are rows
 // for every SIMD (1024); with fewer rows, 4 wavefronts share one, which
-// shortens the chain of a row. Beyond 16384 values 16 wavefronts take a row.
+// shortens the chain of a row. Beyond 16384 values 8 or 16 wavefronts take a row.
 static NormPlan norm_plan(int64_t rows, int64_t n) {
-    if (n > 16384) return {16, n > 32768 ? 8 : 4};
+    if (n > 16384) return {n > 32768 ? 16 : 8, 8};
     const int W = (n <= 512 || (n <= 4096 && rows >= 1024)) ? 1 : 4;
     const int64_t c = (n + 512 * W - 1) / (512 * W);
-    return {W, c <= 1 ? 1 : c <= 2 ? 2 : c <= 4 ? 4 : 8};
+    return {W, c <= 4 ? (int)c : 8};
 }
 
 template <typename TX, typename TR, bool V, bool MX>
@@ -337,6 +417,7 @@ static ssd_status run_norm(const NormArgs &a, hipStream_t s) {
         switch (p.NC) {
             case 1: return go(k_rms_norm<TX, TR, 1, 1, V, MX>);
             case 2: return go(k_rms_norm<TX, TR, 1, 2, V, MX>);
+            case 3: return go(k_rms_norm<TX, TR, 1, 3, V, MX>);
             case 4: return go(k_rms_norm<TX, TR, 1, 4, V, MX>);
             default: return go(k_rms_norm<TX, TR, 1, 8, V, MX>);
         }
@@ -345,11 +426,12 @@ static ssd_status run_norm(const NormArgs &a, hipStream_t s) {
         switch (p.NC) {
             case 1: return go(k_rms_norm<TX, TR, 4, 1, V, MX>);
             case 2: return go(k_rms_norm<TX, TR, 4, 2, V, MX>);
+            case 3: return go(k_rms_norm<TX, TR, 4, 3, V, MX>);
             case 4: return go(k_rms_norm<TX, TR, 4, 4, V, MX>);
             default: return go(k_rms_norm<TX, TR, 4, 8, V, MX>);
         }
     }
-    return p.NC == 4 ? go(k_rms_norm<TX, TR, 16, 4, V, MX>) : go(k_rms_norm<TX, TR, 16, 8, V, MX>);
+    return p.W == 8 ? go(k_rms_norm<TX, TR, 8, 8, V, MX>) : go(k_rms_norm<TX, TR, 16, 8, V, MX>);
 }
 
 template <typename TX, typename TR>
@@ -389,6 +471,7 @@ static ssd_status run_norm_bwd(const NormBwdArgs &a, hipStream_t s) {
         switch (p.NC) {
             case 1: return go(k_rms_norm_bwd<TX, TR, 1, 1, V>);
             case 2: return go(k_rms_norm_bwd<TX, TR, 1, 2, V>);
+            case 3: return go(k_rms_norm_bwd<TX, TR, 1, 3, V>);
             case 4: return go(k_rms_norm_bwd<TX, TR, 1, 4, V>);
             default: return go(k_rms_norm_bwd<TX, TR, 1, 8, V>);
         }
@@ -397,11 +480,12 @@ static ssd_status run_norm_bwd(const NormBwdArgs &a, hipStream_t s) {
         switch (p.NC) {
             case 1: return go(k_rms_norm_bwd<TX, TR, 4, 1, V>);
             case 2: return go(k_rms_norm_bwd<TX, TR, 4, 2, V>);
+            case 3: return go(k_rms_norm_bwd<TX, TR, 4, 3, V>);
             case 4: return go(k_rms_norm_bwd<TX, TR, 4, 4, V>);
             default: return go(k_rms_norm_bwd<TX, TR, 4, 8, V>);
         }
     }
-    return p.NC == 4 ? go(k_rms_norm_bwd<TX, TR, 16, 4, V>) : go(k_rms_norm_bwd<TX, TR, 16, 8, V>);
+    return p.W == 8 ? go(k_rms_norm_bwd<TX, TR, 8, 8, V>) : go(k_rms_norm_bwd<TX, TR, 16, 8, V>);
 }
 
 template <typename TX, typename TR>
