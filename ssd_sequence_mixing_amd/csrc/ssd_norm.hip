@@ -255,7 +255,7 @@ template <typename TX, typename TR, int W, int NC, bool V>
 __global__ __launch_bounds__(W > 4 ? W * 64 : kNormThreads) void k_rms_norm_bwd(NormBwdArgs a) {
     constexpr int RPB = W > 4 ? 1 : kNormThreads / (64 * W);
     constexpr bool kTwo = sizeof(TX) != sizeof(TR);  // h's gradient in its own type beside x's
-    constexpr bool kAhead = W <= 4 && NC * (2 * sizeof(TR) + sizeof(TX)) <= 40;  // 2 rows' inputs: up to 160 registers
+    constexpr bool kAhead = W <= 4 && NC * (2 * sizeof(TR) + sizeof(TX)) <= 30;  // 2 rows' inputs: up to 120 registers (8192 x 2048 with an fp32 residual: 4 chunks ahead 64 us, at once 54)
     constexpr bool kTwice = W > 4;  // long rows: the registers hold no row beside dw; it is read again
     constexpr int kStep = 64 * W;
     __shared__ float red[W > 1 ? W : 1];
@@ -397,12 +397,12 @@ ssd_status launch_column_sums(const float *part, float *out, int nb, int64_t D, 
 struct NormPlan {
     int W, NC;
 };
-// One wavefront per row while a row fits 8 chunks a lane and there are rows
+// One wavefront per row while a row fits 8 chunks a lane (4 where they are taken value by value) and there are rows
 // for every SIMD (1024); with fewer rows, 4 wavefronts share one, which
 // shortens the chain of a row. Beyond 16384 values 8 or 16 wavefronts take a row.
 static NormPlan norm_plan(int64_t rows, int64_t n) {
     if (n > 16384) return {n > 32768 ? 16 : 8, 8};
-    const int W = (n <= 512 || (n <= 4096 && rows >= 1024)) ? 1 : 4;
+    const int W = (n <= 512 || (n <= (n % 8 ? 2048 : 4096) && rows >= 1024)) ? 1 : 4;
     const int64_t c = (n + 512 * W - 1) / (512 * W);
     return {W, c <= 4 ? (int)c : 8};
 }
