@@ -221,6 +221,8 @@ struct LinearArgs {
     bool xt, wt;                // bf16: x (w) is given as (krows x M) ((krows x N)), rows along k
     int krows;
     int nm, nn, steps, splits, steps_per_split;
+    int64_t ldy;                // values from one row of y, res and pre to the next (0: N)
+    bool whole;                 // set at launch: groups of 4 columns are whole and aligned
 };
 // Floats from one part of a split sum to the next.
 __host__ __device__ inline int64_t part_stride(int64_t M, int64_t N) { return (M * N + 3) & ~(int64_t)3; }
@@ -228,6 +230,8 @@ struct LinearPlan {
     int bm, bn;                 // a work-group's tile of y; 0: the few-rows kernel
     int nm, nn;                 // tiles
     int steps, splits, steps_per_split;
+    int n_main;                 // > 0: this plan is for the first n_main columns, the next for the rest
+    int rest_bm, rest_bn, rest_nm, rest_nn;
 };
 // along_k: an operand has its rows along k (the few-rows kernel takes none of these).
 LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, bool f32, bool along_k);

@@ -50,6 +50,38 @@ __device__ __forceinline__ void to_lds4(const void *base, uint32_t bytes, void *
     __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(base, bytes), (lds_void *)dst, 4, voff, 0, 0, 0);
 }
 
+// fp32 in three bf16: x = a + b + c exactly (8 bits of the 24-bit mantissa each, cut off, not
+// rounded). A product of two such sums keeps a a', a b', b a', b b', a c' and c a': the
+// three that are left out are under 2^-21 of it, 2^-24 on average.
+struct Split {
+    bf16x8 a, b, c;
+};
+__device__ __forceinline__ Split split8(u32x4 l, u32x4 h) {
+    uint32_t a[4], b[4], c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t u = i < 2 ? l[2 * i] : h[2 * i - 4], v = i < 2 ? l[2 * i + 1] : h[2 * i - 3];
+        const float ru = __uint_as_float(u) - __uint_as_float(u & 0xffff0000u);
+        const float rv = __uint_as_float(v) - __uint_as_float(v & 0xffff0000u);
+        const uint32_t ub = __float_as_uint(ru), vb = __float_as_uint(rv);
+        const uint32_t uc = __float_as_uint(ru - __uint_as_float(ub & 0xffff0000u));
+        const uint32_t vc = __float_as_uint(rv - __uint_as_float(vb & 0xffff0000u));
+        a[i] = __builtin_amdgcn_perm(v, u, 0x07060302u);  // the upper halves of u and v
+        b[i] = __builtin_amdgcn_perm(vb, ub, 0x07060302u);
+        c[i] = __builtin_amdgcn_perm(vc, uc, 0x07060302u);
+    }
+    return {__builtin_bit_cast(bf16x8, u32x4{a[0], a[1], a[2], a[3]}), __builtin_bit_cast(bf16x8, u32x4{b[0], b[1], b[2], b[3]}),
+            __builtin_bit_cast(bf16x8, u32x4{c[0], c[1], c[2], c[3]})};
+}
+__device__ __forceinline__ f32x4 mma_split(const Split &w, const Split &x, f32x4 acc) {  // small terms first
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.c, x.a, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.a, x.c, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.b, x.b, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.b, x.a, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.a, x.b, acc, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.a, x.a, acc, 0, 0, 0);
+}
+
 // Schedules R LDS reads one by one between the first of P matrix-core
 // instructions, and V loads between the rest.
 template <int R, int P, int V>
@@ -158,14 +190,14 @@ __device__ __forceinline__ void get4(float (&v)[4], const TO *p, int n, bool who
 }
 
 // The epilogue of 4 consecutive columns n .. n + 3 of row m, with their bias
-// and residual (zeros where there is none) already loaded. kWhole: N is a
-// multiple of 4, so every group of 4 is whole and aligned.
+// and residual (zeros where there is none) already loaded. kWhole: N and
+// the rows' stride are multiples of 4, so every group of 4 is whole and aligned.
 template <typename TO, int ACT, bool kWhole>
 __device__ __forceinline__ void finish4(const LinearArgs &a, int m, int n, float (&v)[4], const float (&bias)[4],
                                         const float (&res)[4]) {
     const int left = a.N - n;
     if (m >= a.M || left <= 0) return;
-    const int64_t at = (int64_t)m * a.N + n;
+    const int64_t at = (int64_t)m * a.ldy + n;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] += bias[i];
     if (a.pre) put4<TO>(reinterpret_cast<TO *>(a.pre) + at, v, left, kWhole);
@@ -180,7 +212,7 @@ __device__ __forceinline__ void bias4(const LinearArgs &a, int n, float (&v)[4])
 template <typename TO, bool kWhole>
 __device__ __forceinline__ void res4(const LinearArgs &a, int m, int n, float (&v)[4]) {
     if (a.res && m < a.M && n < a.N) {
-        get4<TO>(v, reinterpret_cast<const TO *>(a.res) + (int64_t)m * a.N + n, a.N - n, kWhole);
+        get4<TO>(v, reinterpret_cast<const TO *>(a.res) + (int64_t)m * a.ldy + n, a.N - n, kWhole);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = 0.f;
@@ -198,7 +230,7 @@ __device__ __forceinline__ void finish4_any(const LinearArgs &a, int m, int n, f
         else if (a.act == SSD_ACT_GELU) finish4<TO, SSD_ACT_GELU, kWhole>(a, m, n, v, bias, res);
         else finish4<TO, SSD_ACT_NONE, kWhole>(a, m, n, v, bias, res);
     };
-    if ((a.N & 3) == 0) go(std::true_type{});
+    if (a.whole) go(std::true_type{});
     else go(std::false_type{});
 }
 
@@ -337,7 +369,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
     // barrier, so that the matrix cores have work across it.
     constexpr int NQ = (KIND == kMX || TM < 4) ? TM : 4, TQ = TM / NQ;  // 8 bits: registers for the scales, too
     static_assert(TQ * NQ == TM && NQ % 2 == 0, "parts of a step");
-    constexpr int kMma = KIND == kBF16 ? 2 : KIND == kF32 ? 8 : 1;          // matrix-core instructions of a product
+    constexpr int kMma = KIND == kBF16 ? 2 : KIND == kF32 ? 6 : 1;          // matrix-core instructions of a product
     constexpr int kReadsX = TQ * (XT ? 4 : KIND == kMX ? 3 : 2), kReadsW = TN * (WT ? 4 : KIND == kMX ? 3 : 2);
     struct WRegs {
         u32x4 l[TN], h[TN];
@@ -382,7 +414,21 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
             f.s[i] = KIND == kMX ? sc[((wm * TM + q * TQ + i) * 16 + r) * 4 + kg] : 0;
         }
     };
+    Split ws[KIND == kF32 ? TN : 1];
     auto multiply = [&](const WRegs &wf, const XRegs &xf, int q) {
+        if constexpr (KIND == kF32) {
+            if (q == 0) {
+#pragma unroll
+                for (int j = 0; j < TN; ++j) ws[j] = split8(wf.l[j], wf.h[j]);
+            }
+#pragma unroll
+            for (int i = 0; i < TQ; ++i) {
+                const Split xs = split8(xf.l[i], xf.h[i]);
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[q * TQ + i][j] = mma_split(ws[j], xs, acc[q * TQ + i][j]);
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < TQ; ++i)
 #pragma unroll
@@ -453,7 +499,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
         }
         return;
     }
-    if (EPI == SSD_ACT_NONE && (a.N & 3) == 0) {
+    if (EPI == SSD_ACT_NONE && a.whole) {
         // the next 16 rows' residual is on its way while 16 rows are finished
         float bias[NP][4], res[2][NP][4];
 #pragma unroll
@@ -495,7 +541,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         stage(i);
-        if ((a.N & 3) == 0) rows(i, std::true_type{});
+        if (a.whole) rows(i, std::true_type{});
         else rows(i, std::false_type{});
         __builtin_amdgcn_wave_barrier();
     }
@@ -712,29 +758,61 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, bool f32, bool alon
         int bm, bn;
         double slots, step, step32, fixed;
     };
-    const Tile tiles[] = {{256, 256, 256, 1.6, 8.0, 14}, {256, 192, 256, 1.42, 6.0, 12},
-                          {128, 128, 512, 1.09, 4.0, 8}, {64, 64, 1024, 0.8, 2.0, 5}};
+    const Tile tiles[] = {{256, 256, 256, 1.45, 0, 14}, {256, 192, 256, 1.22, 3.3, 12},
+                          {128, 128, 512, 0.9, 2.3, 8}, {64, 64, 1024, 0.6, 1.5, 5}};
+    // the time of n columns by one tile's kernel, and its plan
+    auto plan_of = [&](const Tile &c, int64_t n, int splits, LinearPlan *q) {
+        const int per = ((p.steps + splits - 1) / splits + 1) & ~1;  // steps go in pairs
+        if (splits > 1 && (p.steps + per - 1) / per != splits) return 1e300;
+        const int64_t nm = (M + c.bm - 1) / c.bm, nn = (n + c.bn - 1) / c.bn;
+        const double rounds = (double)((int64_t)((nm * nn * splits + c.slots - 1) / c.slots));
+        *q = p;
+        q->bm = c.bm;
+        q->bn = c.bn;
+        q->splits = splits;
+        q->steps_per_split = per;
+        q->nm = (int)nm;
+        q->nn = (int)nn;
+        double t = rounds * (per * (f32 ? c.step32 : c.step) + c.fixed);
+        if (splits > 1) t += 5 + 2.0 * splits * M * n * 4 / 5.0e6;
+        return t;
+    };
     double best = 1e300;
-    for (const Tile &c : tiles) {
-        const int64_t nm = (M + c.bm - 1) / c.bm, nn = (N + c.bn - 1) / c.bn;
-        for (int splits = 1; splits <= 32 && splits <= p.steps; splits += splits < 8 ? 1 : 4) {
-            const int per = ((p.steps + splits - 1) / splits + 1) & ~1;  // steps go in pairs
-            if (splits > 1 && (p.steps + per - 1) / per != splits) continue;
-            const double rounds = (double)((int64_t)((nm * nn * splits + c.slots - 1) / c.slots));
-            double t = rounds * (per * (f32 ? c.step32 : c.step) + c.fixed);
-            if (splits > 1) t += 5 + 2.0 * splits * M * N * 4 / 5.0e6;
-            if (t < best) {
-                best = t;
-                p.bm = c.bm;
-                p.bn = c.bn;
-                p.splits = splits;
-                p.steps_per_split = per;
-                p.nm = (int)nm;
-                p.nn = (int)nn;
+    LinearPlan q, top = p;
+    auto best_of = [&](int64_t n, int most_splits, LinearPlan *out) {
+        double t = 1e300;
+        for (const Tile &c : tiles) {
+            if (f32 && c.bn == 256) continue;  // its operands in three parts do not fit the registers
+            for (int splits = 1; splits <= most_splits && splits <= p.steps; splits += splits < 8 ? 1 : 4) {
+                const double u = plan_of(c, n, splits, &q);
+                if (u < t) t = u, *out = q;
+            }
+        }
+        return t;
+    };
+    best = best_of(N, 32, &top);
+    // whole rounds of the large tile, and the columns that are left by the tile that is best for them
+    // (8192 x 2048 x 8512 in 8 bits: 4 rounds and 320 columns, 184 us; 5 rounds, the last a quarter full, 194)
+    if (!along_k) {
+        const Tile &c = tiles[f32 ? 1 : 0];
+        const int64_t nm = (M + c.bm - 1) / c.bm;
+        int64_t nf = N / c.bn;
+        while (nf > 0 && nm * nf % 256 != 0) --nf;
+        LinearPlan rest;
+        if (nf > 0 && nf * c.bn < N) {
+            const double t = plan_of(c, nf * c.bn, 1, &q);
+            const LinearPlan main = q;
+            if (t + best_of(N - nf * c.bn, 1, &rest) < best) {
+                top = main;
+                top.n_main = (int)(nf * c.bn);
+                top.rest_bm = rest.bm;
+                top.rest_bn = rest.bn;
+                top.rest_nm = rest.nm;
+                top.rest_nn = rest.nn;
             }
         }
     }
-    return p;
+    return top;
 }
 
 template <int KIND, typename TO, bool XT, bool WT>
@@ -745,7 +823,8 @@ static ssd_status run_tile(const LinearArgs &a, const LinearPlan &p, hipStream_t
         if (p.bm == 64) return launch(k_tile<KIND, TO, 64, 64, 2, 2, EPI, XT, WT>, grid, dim3(256), s, a);
         if (p.bm == 128) return launch(k_tile<KIND, TO, 128, 128, 2, 2, EPI, XT, WT>, grid, dim3(256), s, a);
         if (p.bn == 192) return launch(k_tile<KIND, TO, 256, 192, 2, 4, EPI, XT, WT>, grid, dim3(512), s, a);
-        return launch(k_tile<KIND, TO, 256, 256, 2, 4, EPI, XT, WT>, grid, dim3(512), s, a);
+        if constexpr (KIND != kF32) return launch(k_tile<KIND, TO, 256, 256, 2, 4, EPI, XT, WT>, grid, dim3(512), s, a);
+        return hipErrorInvalidValue;  // no such plan
     };
     hipError_t e;
     if (p.splits > 1) {
@@ -774,6 +853,25 @@ static ssd_status run_linear(const LinearArgs &a, const LinearPlan &p, hipStream
 ssd_status launch_linear(LinearArgs a, const LinearPlan &p, bool mx, ssd_dtype dtype, hipStream_t s) {
     a.nm = p.nm; a.nn = p.nn; a.steps = p.steps; a.splits = p.splits; a.steps_per_split = p.steps_per_split;
     if (p.splits == 1) a.part = nullptr;
+    if (a.ldy == 0) a.ldy = a.N;
+    a.whole = (a.N & 3) == 0 && (a.ldy & 3) == 0;
+    if (p.n_main) {  // never with an operand along k
+        const int64_t n = p.n_main, es = dtype == SSD_BF16 ? 2 : 4;
+        LinearArgs b = a;
+        LinearPlan first = p, second = p;
+        first.n_main = second.n_main = 0;
+        second.bm = p.rest_bm; second.bn = p.rest_bn; second.nm = p.rest_nm; second.nn = p.rest_nn;
+        a.N = (int)n;
+        b.N -= (int)n;
+        b.w = static_cast<const char *>(b.w) + n * b.ldw;
+        if (mx) b.wscale += n * b.lds;
+        if (b.bias) b.bias += n;
+        if (b.res) b.res = static_cast<const char *>(b.res) + n * es;
+        if (b.pre) b.pre = static_cast<char *>(b.pre) + n * es;
+        b.y = static_cast<char *>(b.y) + n * es;
+        const ssd_status st = launch_linear(a, first, mx, dtype, s);
+        return st != SSD_OK ? st : launch_linear(b, second, mx, dtype, s);
+    }
     if (mx) return run_linear<kMX, bf16>(a, p, s);
     if (a.wt) return a.xt ? run_tile<kBF16, bf16, true, true>(a, p, s) : run_tile<kBF16, bf16, false, true>(a, p, s);
     return dtype == SSD_BF16 ? run_linear<kBF16, bf16>(a, p, s) : run_linear<kF32, float>(a, p, s);

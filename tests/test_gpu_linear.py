@@ -119,6 +119,15 @@ def test_linear_large(ssd, m, k, n):
     _forward(ssd, m, k, n, "bf16", "silu", True, True)
 
 
+@pytest.mark.parametrize("dtype,m,k,n", [("bf16", 4096, 512, 4359), ("bf16", 4096, 520, 4364), ("f32", 4096, 100, 3301)])
+def test_linear_columns_in_two_kernels(ssd, dtype, m, k, n):
+    """Whole rounds of the large tile and a rest of the columns by a smaller one: the rest's offsets in every operand,
+    with rows of y that are and are not multiples of 4."""
+    log(f"[linear] {m}x{k}x{n} {dtype}")
+    _forward(ssd, m, k, n, dtype, "none", False, False)
+    _forward(ssd, m, k, n, dtype, "gelu", True, True)
+
+
 def test_linear_leading_dimensions_and_no_rows(ssd):
     import torch
     x, w, b, _, _ = _draw(24, 64, 48, "bf16", 3)
@@ -145,7 +154,8 @@ def test_linear_infinities_stay_in_their_rows(ssd):
 
 
 @pytest.mark.parametrize("m,k,n", [(1, 32, 1), (3, 96, 20), (16, 2048, 515), (40, 160, 33), (64, 4096, 100), (65, 32, 7),
-                                   (100, 224, 130), (129, 128, 300), (700, 2048, 772), (2048, 1024, 2304)])
+                                   (100, 224, 130), (129, 128, 300), (700, 2048, 772), (2048, 1024, 2304),
+                                   (4096, 512, 4359), (2048, 96, 4100)])
 def test_linear_mx(ssd, m, k, n):
     import torch
     log(f"[linear mx] {m}x{k}x{n}")
