@@ -101,6 +101,20 @@ __device__ __forceinline__ void mix() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// Where chunk c of row k lies in a row of CPR chunks (rows along k), and which chunk lies at place p.
+template <int CPR>
+__device__ __forceinline__ int swizzled(int c, int k) {
+    if constexpr (CPR == 8) return c ^ (((k >> 1) & 1) * 2 | ((k >> 3) & 1) * 4);
+    const int q = (c ^ (2 * (k & 3))) + 8 * ((k >> 3) & 1);
+    return q >= CPR ? q - CPR : q;
+}
+template <int CPR>
+__device__ __forceinline__ int unswizzled(int p, int k) {
+    if constexpr (CPR == 8) return swizzled<8>(p, k);
+    const int q = p - 8 * ((k >> 3) & 1);
+    return (q < 0 ? q + CPR : q) ^ (2 * (k & 3));
+}
+
 // Every wavefront's loads into LDS have arrived (a barrier alone does not wait
 // for them), and its reads too.
 __device__ __forceinline__ void arrive() {
@@ -140,19 +154,46 @@ __device__ __forceinline__ f32x4 mma2(u32x4 wl, u32x4 wh, u32x4 xl, u32x4 xh, f3
     return c;
 }
 
-__device__ __forceinline__ float act_of(float z, int act) {  // act: a constant where it is called
-    if (act == SSD_ACT_SILU) return z / (1.f + expf(-z));
-    if (act == SSD_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+// The activations and their slopes (act: a constant where they are called). kFast, for values that are
+// rounded to bf16: the vector unit's 2^x and 1/x (1 ulp each), and for GELU
+//   erfc(u) = (a1 t + .. + a5 t^5) e^(-u^2),  t = 1 / (1 + p u),  u >= 0
+// (Abramowitz and Stegun 7.1.26, off by at most 1.5e-7), whose exponential the slope needs, too.
+// expf, erff and a division took k_dz from memory's time to the vector unit's.
+template <bool kFast>
+__device__ __forceinline__ float sigmoid(float z) {
+    if constexpr (kFast) return __builtin_amdgcn_rcpf(1.f + fast_exp2(-kLog2e * z));
+    return 1.f / (1.f + expf(-z));
+}
+// (1 + erf(z / sqrt 2)) / 2, and e^(-z^2 / 2)
+template <bool kFast>
+__device__ __forceinline__ float normal_cdf(float z, float &e) {
+    if constexpr (kFast) {
+        e = fast_exp2(-0.5f * kLog2e * z * z);
+        const float t = __builtin_amdgcn_rcpf(1.f + 0.3275911f * 0.70710678f * fabsf(z));
+        const float c = 0.5f * e * t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+        return z < 0.f ? c : 1.f - c;
+    }
+    e = expf(-0.5f * z * z);
+    return 0.5f * (1.f + erff(z * 0.70710678118654752f));
+}
+template <bool kFast>
+__device__ __forceinline__ float act_of(float z, int act) {
+    if (act == SSD_ACT_SILU) return kFast ? z * sigmoid<true>(z) : z / (1.f + expf(-z));
+    float e;
+    if (act == SSD_ACT_GELU) return z * normal_cdf<kFast>(z, e);
     return z;
 }
-// d act / dz
+template <bool kFast>
 __device__ __forceinline__ float act_slope(float z, int act) {
     if (act == SSD_ACT_SILU) {
-        const float g = 1.f / (1.f + expf(-z));
+        const float g = sigmoid<kFast>(z);
         return g * (1.f + z * (1.f - g));
     }
-    if (act == SSD_ACT_GELU)
-        return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.3989422804014327f * expf(-0.5f * z * z);
+    if (act == SSD_ACT_GELU) {
+        float e;
+        const float c = normal_cdf<kFast>(z, e);
+        return c + z * 0.3989422804014327f * e;
+    }
     return 1.f;
 }
 
@@ -202,7 +243,7 @@ __device__ __forceinline__ void finish4(const LinearArgs &a, int m, int n, float
     for (int i = 0; i < 4; ++i) v[i] += bias[i];
     if (a.pre) put4<TO>(reinterpret_cast<TO *>(a.pre) + at, v, left, kWhole);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = act_of(v[i], ACT) + res[i];
+    for (int i = 0; i < 4; ++i) v[i] = act_of<sizeof(TO) == 2>(v[i], ACT) + res[i];
     put4<TO>(reinterpret_cast<TO *>(a.y) + at, v, left, kWhole);
 }
 __device__ __forceinline__ void bias4(const LinearArgs &a, int n, float (&v)[4]) {
@@ -252,8 +293,9 @@ __device__ __forceinline__ void tile_of(int id, int nm, int nn, int &tm, int &tn
 // XT, WT (bf16): x or w is given with its rows along k (k x M, k x N), as the
 // backward pass has them. A step then takes 64 rows of BM (BN) columns, and
 // the lanes' 8 values along k are read down the columns with LDS's transposing
-// read. Its 16 lanes take 32 bytes of 4 rows: the chunks of row k lie at
-// chunk ^ 2 (k % 4), so that the 4 rows lie in different banks.
+// read. 32 of its lanes take 32 bytes of rows k .. k + 3 and k + 8 .. k + 11 each;
+// the chunks of a row are moved by swizzled() so that these 8 pieces of 32 bytes lie in
+// different banks (without the second four: half of the reads' cycles were conflicts).
 template <int KIND, typename TO, int BM, int BN, int WM, int WN, int EPI, bool XT, bool WT>
 __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearArgs a) {
     constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
@@ -283,7 +325,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
     for (int j = 0; j < LA; ++j) {
         if constexpr (XT) {
             const int g = (w * LA + j) * 64 + lane, k = g / (BM / 8), c = g % (BM / 8);
-            xoff[j] = (uint32_t)k * (uint32_t)a.ldx + (uint32_t)((c ^ (2 * (k & 3))) << 4);
+            xoff[j] = (uint32_t)k * (uint32_t)a.ldx + (uint32_t)(unswizzled<BM / 8>(c, k) << 4);
         } else {
             int row = m0 + (w * LA + j) * 8;
             row = row < a.M ? row : m0;
@@ -295,7 +337,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
     for (int j = 0; j < LB; ++j) {
         if constexpr (WT) {
             const int g = (w * LB + j) * 64 + lane, k = g / (BN / 8), c = g % (BN / 8);
-            woff[j] = (uint32_t)k * (uint32_t)a.ldw + (uint32_t)((c ^ (2 * (k & 3))) << 4);
+            woff[j] = (uint32_t)k * (uint32_t)a.ldw + (uint32_t)(unswizzled<BN / 8>(c, k) << 4);
         } else {
             int row = n0 + (w * LB + j) * 8;
             row = row < a.N ? row : n0;
@@ -379,10 +421,12 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
         u32x4 l[TQ], h[TQ];
         int s[TQ];
     } x0, x1;
-    // rows along k: this lane's 8 bytes of row 8 kg + j / 4, at block b of 16 columns
-    const int tk = 8 * kg + (r >> 2), tx = 2 * (r >> 2), tc = (r >> 1) & 1, th = (r & 1) * 8;
-    auto down = [&](u32x4 &l, u32x4 &h, const char *part, int b, int width) {
-        const char *p = part + tk * width + (((2 * b + tc) ^ tx) << 4) + th;
+    // rows along k: this lane's 8 bytes of rows 8 kg + r / 4 and on, at block b of 16 columns
+    const int tk = 8 * kg + (r >> 2), tc = (r >> 1) & 1, th = (r & 1) * 8;
+    auto down = [&](u32x4 &l, u32x4 &h, const char *part, int b, auto chunks) {
+        constexpr int CPR = decltype(chunks)::value, width = CPR * 16;
+        // 4 and 32 rows on the chunk lies at the same place; in rows of 8 chunks, too
+        const char *p = part + tk * width + (swizzled<CPR>(2 * b + tc, tk) << 4) + th;
         const u32x2 l0 = lds_transposed(p), l1 = lds_transposed(p + 4 * width);
         const u32x2 h0 = lds_transposed(p + 32 * width), h1 = lds_transposed(p + 36 * width);
         l = __builtin_shufflevector(l0, l1, 0, 1, 2, 3);
@@ -393,7 +437,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
         for (int j = 0; j < TN; ++j) {
             f.s[j] = 0;
             if constexpr (WT) {
-                down(f.l[j], f.h[j], buf + BM * 128, wn * TN + j, BN * 2);
+                down(f.l[j], f.h[j], buf + BM * 128, wn * TN + j, std::integral_constant<int, BN / 8>{});
                 continue;
             }
             f.l[j] = *reinterpret_cast<const u32x4 *>(buf + pb + j * 2048);
@@ -406,7 +450,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
         for (int i = 0; i < TQ; ++i) {
             f.s[i] = 0;
             if constexpr (XT) {
-                down(f.l[i], f.h[i], buf, wm * TM + q * TQ + i, BM * 2);
+                down(f.l[i], f.h[i], buf, wm * TM + q * TQ + i, std::integral_constant<int, BM / 8>{});
                 continue;
             }
             f.l[i] = *reinterpret_cast<const u32x4 *>(buf + pa + (q * TQ + i) * 2048);
@@ -580,8 +624,8 @@ __global__ __launch_bounds__(256) void k_join(LinearArgs a) {
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        if (a.act == SSD_ACT_SILU) v[e] = act_of(v[e], SSD_ACT_SILU);
-        else if (a.act == SSD_ACT_GELU) v[e] = act_of(v[e], SSD_ACT_GELU);
+        if (a.act == SSD_ACT_SILU) v[e] = act_of<sizeof(TO) == 2>(v[e], SSD_ACT_SILU);
+        else if (a.act == SSD_ACT_GELU) v[e] = act_of<sizeof(TO) == 2>(v[e], SSD_ACT_GELU);
         v[e] += res[e];
     }
     put4<TO>(reinterpret_cast<TO *>(a.y) + i, v, left, left == 4);
@@ -718,7 +762,7 @@ __global__ __launch_bounds__(256) void k_dz(const T *dy, const T *pre, T *dz, fl
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            if constexpr (ACT != SSD_ACT_NONE) v[e] *= act_slope(z[e], ACT);
+            if constexpr (ACT != SSD_ACT_NONE) v[e] *= act_slope<sizeof(T) == 2>(z[e], ACT);
             sum[e] += v[e];
         }
         if (dz) {
@@ -773,7 +817,9 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, bool f32, bool alon
         q->steps_per_split = per;
         q->nm = (int)nm;
         q->nn = (int)nn;
-        double t = rounds * (per * (f32 ? c.step32 : c.step) + c.fixed);
+        // operands along k: the small tiles' steps are slower (3352 x 16384 x 768: 128-tiles 118 us, 256-tiles 110)
+        const double slow = along_k && c.bm < 256 ? 1.15 : 1.0;
+        double t = rounds * (per * (f32 ? c.step32 : c.step) * slow + c.fixed);
         if (splits > 1) t += 5 + 2.0 * splits * M * n * 4 / 5.0e6;
         return t;
     };
