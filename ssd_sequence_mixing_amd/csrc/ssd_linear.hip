@@ -741,7 +741,10 @@ __global__ __launch_bounds__(256) void k_dz(const T *dy, const T *pre, T *dz, fl
         if (m >= M || n >= ldz) continue;
         const int64_t at = (int64_t)m * N + n;
         float v[8], z[8];
-        if constexpr (V) {
+        if (V && n >= N) {  // between the row's end and ldz
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = z[e] = 0.f;
+        } else if constexpr (V) {
             float lo[4], hi[4];
             get4<T>(lo, dy + at, 4, true);
             get4<T>(hi, dy + at + 4, 4, true);

@@ -286,3 +286,24 @@ def test_linear_on_another_stream_and_replayed(ssd):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(out, want)), k
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_linear_bwd_rows_of_dz_end_in_zeros(ssd, dtype):
+    """dz lies at the workspace's front, its rows at whole 128-byte lines: behind column n there are zeros, and nothing
+    of the next row of dy or of what lies behind its last."""
+    import torch
+    m, k, n = 70, 24, 72
+    dy, _, _, pre, g = _draw(m, n, 8, dtype, 5)
+    pre = torch.randn(m, n, device="cuda", generator=g).to(_t(dtype))
+    pre = _behind(pre, math.nan)
+    x, w = (torch.randn(*s, device="cuda", generator=g).to(_t(dtype)) for s in ((m, k), (n, k)))
+    ws = torch.full((ssd.ssd_linear_bwd_workspace_bytes(m, k, n, "silu", int(dtype == "bf16")),), 0xff,
+                    dtype=torch.uint8, device="cuda")
+    assert ws.data_ptr() % 256 == 0
+    ssd.ssd_linear_bwd(dy, x, w, act="silu", preact=pre, want_bias=True, workspace=ws)
+    ld = (n * dy.element_size() + 127) // 128 * 128
+    rows = ws[:m * ld].view(dy.dtype).view(m, -1)
+    assert rows.shape[1] > n and torch.count_nonzero(rows[:, n:]) == 0
+    ref = dy.double() * _slope(pre.double(), "silu")
+    assert torch.all((rows[:, :n].double() - ref).abs() <= HALF[dtype] * ref.abs() + 2.0 ** -18 * dy.double().abs())
