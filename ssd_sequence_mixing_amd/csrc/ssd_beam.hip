@@ -29,8 +29,9 @@ constexpr int kTile = 2048;        // logits a wavefront holds at a time, 32 a l
 constexpr int kPerLane = kTile / 64;
 
 // Order-preserving bits of a float (no NaN): larger floats, larger bits; 0 is below all.
+// Both zeros are one value (-0 + 0 = 0): they tie.
 __device__ __forceinline__ uint32_t ord32(float v) {
-    const uint32_t u = __float_as_uint(v);
+    const uint32_t u = __float_as_uint(v + 0.f);
     return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float from_ord32(uint32_t o) {

@@ -284,3 +284,15 @@ def test_beam_search_step_on_a_stream_and_replayed(ssd):
         graph.replay()
         torch.cuda.synchronize()
         assert _same(out, want), r
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_select_takes_both_zeros_as_one(ssd, dtype):
+    """-0 and 0 are equal logits: the lower index goes first, in whole tiles, in the rest of a row and across tiles."""
+    import torch
+    for v, minus, plus in ((100, 3, 7), (5000, 10, 1500), (5000, 40, 4999), (300, 299, 17), (70000, 2047, 69999)):
+        logits = torch.full((1, 2, v), -9.0, device="cuda", dtype=torch.bfloat16 if dtype == "bf16" else torch.float32)
+        logits[:, :, minus], logits[:, :, plus] = -0.0, 0.0
+        scores = torch.tensor([[0.0, -math.inf]], device="cuda")
+        _, parent, token, _ = ssd.ssd_beam_select(logits, scores)
+        assert token[0].tolist() == sorted((minus, plus)) and parent[0].tolist() == [0, 0]
