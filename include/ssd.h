@@ -438,7 +438,8 @@ ssd_status ssd_beam_select(const void *logits, const float *scores, const uint8_
  *
  *   h = x + residual;   y = h * weight / sqrt(mean(h^2) + eps)
  *
- * in fp32, the mean over each of `groups` equal pieces of the row by itself.
+ * in fp32, the mean over each of `groups` equal pieces of the row by itself
+ * (a row whose sum of squares passes fp32's range, about 2^128, gives zeros).
  *
  *   x (rows, dim)                  dtype
  *   residual (rows, dim)           residual_dtype, or NULL: h = x
@@ -506,10 +507,13 @@ ssd_status ssd_rms_norm_bwd(const void *dy, const void *h, const float *weight, 
  *   y (rows, out)        dtype  output, rounded once
  *   preact (rows, out)   dtype  output: z, for the backward pass; or NULL
  *
- * Sums in fp32: bf16 operands on the bf16 matrix cores, fp32 ones on the
- * fp32 matrix cores. Any sizes; rows that do not begin at multiples of 16 bytes
- * (in * sizeof(dtype) not a multiple of 16) cost a copy of both operands in the
- * workspace. rows at most 2^24, in and out at most 2^20. The same inputs give
+ * Sums in fp32. fp32 operands: up to 16 rows on the fp32 matrix cores; more
+ * rows as three bf16 parts of each operand and six of their nine products, which
+ * leaves out less than 2^-21 of a product (2^-24 on average), and what of an
+ * operand lies below 2^-126; an infinite operand then gives NaN in its row or column.
+ * Any sizes; with more than 16 rows, ones that do not begin at multiples of 16
+ * bytes (in * sizeof(dtype) not a multiple of 16) cost a copy of both operands in
+ * the workspace. rows at most 2^24, in and out at most 2^20. The same inputs give
  * the same bits. The workspace (256-byte aligned) is empty for most shapes.
  *
  * ssd_linear_mx is the same product of 8-bit operands as ssd_rms_norm_mx and

@@ -106,11 +106,13 @@ LinearLayout linear_layout(int64_t rows, int64_t in, int64_t out, ssd_dtype dtyp
     if (rows == 0) return l;
     const int64_t bytes = in * esize(dtype);
     l.ld = align16(bytes);
-    if (l.ld != bytes) {
+    l.plan = ssd::linear_plan(rows, out, l.ld, dtype == SSD_F32, false);
+    if (!l.plan.bm) {  // few rows: operands as they are
+        l.ld = bytes;
+    } else if (l.ld != bytes) {
         l.xpad = align256(rows * l.ld);
         l.wpad = align256(out * l.ld);
     }
-    l.plan = ssd::linear_plan(rows, out, l.ld, dtype == SSD_F32, false);
     if (l.plan.splits > 1) l.part = align256(l.plan.splits * ssd::part_stride(rows, out) * 4);
     l.total = l.xpad + l.wpad + l.part;
     return l;

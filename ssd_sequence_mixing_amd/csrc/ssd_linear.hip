@@ -631,52 +631,130 @@ __global__ __launch_bounds__(256) void k_join(LinearArgs a) {
     put4<TO>(reinterpret_cast<TO *>(a.y) + i, v, left, left == 4);
 }
 
-template <int KIND, typename TO>
+// 16 bytes from a multiple of B bytes. A load of 16 bytes from an odd multiple of 2 takes twice the
+// time of one from a multiple of 4: there the 5 words around them are loaded, and shifted. (The
+// fifth is read 2 bytes further than the 16; the callers' rows go on for at least that much.)
+template <int B>
+__device__ __forceinline__ u32x4 ld_any(const char *p) {
+    typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+    if constexpr (B == 4) return *reinterpret_cast<const u32x4_any *>(p);
+    const uint32_t by = (uint32_t)(uintptr_t)p & 2u;
+    const u32x4 q = *reinterpret_cast<const u32x4_any *>(p - by);
+    const uint32_t last = *reinterpret_cast<const uint32_t *>(p + 12 + by);  // by = 0: of the 16 themselves
+    return u32x4{__builtin_amdgcn_alignbyte(q[1], q[0], by), __builtin_amdgcn_alignbyte(q[2], q[1], by),
+                 __builtin_amdgcn_alignbyte(q[3], q[2], by), __builtin_amdgcn_alignbyte(last, q[3], by)};
+}
+// The values of 16 bytes of a row that lie before its end, zeros behind it.
+template <typename T>
+__device__ __forceinline__ u32x4 ld_rest(const char *row, uint32_t off, uint32_t end) {
+    constexpr int E = 16 / (int)sizeof(T);
+    union {
+        T e[E];
+        u32x4 v;
+    } q;
+#pragma unroll
+    for (int i = 0; i < E; ++i) q.e[i] = off + i * sizeof(T) < end ? *reinterpret_cast<const T *>(row + off + i * sizeof(T)) : (T)0.f;
+    return q.v;
+}
+
+// B: the bytes that every row begins at a multiple of. 16: loads through resources that end with
+// the operand; 4 and 2: whole steps by address and the last one value by value
+// (13 x 7469 x 3392 in bf16: 21 us, 38 with copies in rows of 16-byte multiples in front).
+// C: blocks of 16 rows of w that a work-group takes.
+template <int KIND, typename TO, int B, int C>
 __global__ __launch_bounds__(512) void k_skinny(LinearArgs a) {
     __shared__ __attribute__((aligned(16))) float red[8][64][4];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int r = lane & 15, kg = lane >> 4;
-    const int n0 = blockIdx.x * 16;
-    const rsrc_t rw = make_rsrc(reinterpret_cast<const char *>(a.w) + (int64_t)n0 * a.ldw, (uint32_t)(min(16, a.N - n0) * a.ldw));
-    const rsrc_t rx = make_rsrc(a.x, (uint32_t)(a.M * a.ldx));
-    rsrc_t rsw = rw, rsx = rx;
-    if constexpr (KIND == kMX) {
-        rsw = make_rsrc(a.wscale + (int64_t)n0 * a.lds, (uint32_t)(min(16, a.N - n0) * a.lds));
-        rsx = make_rsrc(a.xscale, (uint32_t)(a.M * a.lds));
-    }
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    const uint32_t ldx = (uint32_t)a.ldx, ldw = (uint32_t)a.ldw, ldsc = (uint32_t)a.lds;
-    // U steps' operands are loaded before the first is used; steps behind the last load zeros
-    constexpr int U = 4;
-    for (int s0 = w; s0 < a.steps; s0 += 8 * U) {
-        u32x4 wl[U], wh[U], xl[U], xh[U];
-        int sw[U], sx[U];
+    const int n0 = blockIdx.x * (16 * C);
+    const int cols = min(16 * C, a.N - n0);
+    f32x4 acc[C];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t c0 = (uint32_t)(s0 + 8 * u) * 128u + kg * 16u, c1 = c0 + 64u;
-            const uint32_t o0 = oob_if(c0 >= a.kbytes, c0), o1 = oob_if(c1 >= a.kbytes, c1);
-            const uint32_t b = (uint32_t)(s0 + 8 * u) * 4u + kg, ob = oob_if(b >= ldsc, b);
-            wl[u] = buf_ld128(rw, o0 + r * ldw);
-            wh[u] = buf_ld128(rw, o1 + r * ldw);
-            xl[u] = buf_ld128(rx, o0 + r * ldx);
-            xh[u] = buf_ld128(rx, o1 + r * ldx);
-            sw[u] = KIND == kMX ? (int)__builtin_amdgcn_raw_buffer_load_b8(rsw, ob + r * ldsc, 0, 0) : 0;
-            sx[u] = KIND == kMX ? (int)__builtin_amdgcn_raw_buffer_load_b8(rsx, ob + r * ldsc, 0, 0) : 0;
+    for (int c = 0; c < C; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // U steps' operands are loaded before the first is used; steps behind the last are zeros
+    constexpr int U = C == 1 ? 4 : 2;
+    if constexpr (B < 16) {
+        // rows behind the last take the last one's place: their results are not stored
+        const char *xr = reinterpret_cast<const char *>(a.x) + (int64_t)min(r, a.M - 1) * a.ldx;
+        const char *wr[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) wr[c] = reinterpret_cast<const char *>(a.w) + (int64_t)min(n0 + c * 16 + r, a.N - 1) * a.ldw;
+        const int whole = (int)(a.kbytes / 128u);
+        for (int s0 = w; s0 < whole; s0 += 8 * U) {
+            u32x4 wl[U][C], wh[U][C], xl[U], xh[U];
+            uint32_t keep[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool live = s0 + 8 * u < whole;
+                const uint32_t c0 = (uint32_t)(live ? s0 + 8 * u : 0) * 128u + kg * 16u;
+                keep[u] = live ? ~0u : 0u;
+#pragma unroll
+                for (int c = 0; c < C; ++c) wl[u][c] = ld_any<B>(wr[c] + c0), wh[u][c] = ld_any<B>(wr[c] + c0 + 64);
+                xl[u] = ld_any<B>(xr + c0);
+                xh[u] = ld_any<B>(xr + c0 + 64);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    acc[c] = mma2<KIND>(wl[u][c] & keep[u], wh[u][c] & keep[u], xl[u] & keep[u], xh[u] & keep[u], acc[c], 0, 0);
         }
+        if (whole < a.steps && w == whole % 8) {  // the step that the rows end in
+            const uint32_t c0 = (uint32_t)whole * 128u + kg * 16u, c1 = c0 + 64u;
+            const u32x4 xl = ld_rest<TO>(xr, c0, a.kbytes), xh = ld_rest<TO>(xr, c1, a.kbytes);
 #pragma unroll
-        for (int u = 0; u < U; ++u) acc = mma2<KIND>(wl[u], wh[u], xl[u], xh[u], acc, sw[u], sx[u]);
-    }
-    *reinterpret_cast<f32x4 *>(red[w][lane]) = acc;
-    __syncthreads();
-    if (w == 0) {
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const f32x4 c = *reinterpret_cast<const f32x4 *>(red[k][lane]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += c[e];
+            for (int c = 0; c < C; ++c)
+                acc[c] = mma2<KIND>(ld_rest<TO>(wr[c], c0, a.kbytes), ld_rest<TO>(wr[c], c1, a.kbytes), xl, xh, acc[c], 0, 0);
         }
-        finish4_any<TO>(a, r, n0 + kg * 4, v);
+    } else {
+        const rsrc_t rw = make_rsrc(reinterpret_cast<const char *>(a.w) + (int64_t)n0 * a.ldw, (uint32_t)(cols * a.ldw));
+        const rsrc_t rx = make_rsrc(a.x, (uint32_t)(a.M * a.ldx));
+        rsrc_t rsw = rw, rsx = rx;
+        if constexpr (KIND == kMX) {
+            rsw = make_rsrc(a.wscale + (int64_t)n0 * a.lds, (uint32_t)(cols * a.lds));
+            rsx = make_rsrc(a.xscale, (uint32_t)(a.M * a.lds));
+        }
+        const uint32_t ldx = (uint32_t)a.ldx, ldw = (uint32_t)a.ldw, ldsc = (uint32_t)a.lds;
+        for (int s0 = w; s0 < a.steps; s0 += 8 * U) {
+            u32x4 wl[U][C], wh[U][C], xl[U], xh[U];
+            int sw[U][C], sx[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t c0 = (uint32_t)(s0 + 8 * u) * 128u + kg * 16u, c1 = c0 + 64u;
+                const uint32_t o0 = oob_if(c0 >= a.kbytes, c0), o1 = oob_if(c1 >= a.kbytes, c1);
+                const uint32_t b = (uint32_t)(s0 + 8 * u) * 4u + kg, ob = oob_if(b >= ldsc, b);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const uint32_t row = c * 16 + r;
+                    wl[u][c] = buf_ld128(rw, o0 + row * ldw);
+                    wh[u][c] = buf_ld128(rw, o1 + row * ldw);
+                    sw[u][c] = KIND == kMX ? (int)__builtin_amdgcn_raw_buffer_load_b8(rsw, ob + row * ldsc, 0, 0) : 0;
+                }
+                xl[u] = buf_ld128(rx, o0 + r * ldx);
+                xh[u] = buf_ld128(rx, o1 + r * ldx);
+                sx[u] = KIND == kMX ? (int)__builtin_amdgcn_raw_buffer_load_b8(rsx, ob + r * ldsc, 0, 0) : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int c = 0; c < C; ++c) acc[c] = mma2<KIND>(wl[u][c], wh[u][c], xl[u], xh[u], acc[c], sw[u][c], sx[u]);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        if (c) __syncthreads();
+        *reinterpret_cast<f32x4 *>(red[w][lane]) = acc[c];
+        __syncthreads();
+        if (w == c) {
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const f32x4 q = *reinterpret_cast<const f32x4 *>(red[k][lane]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] += q[e];
+            }
+            finish4_any<TO>(a, r, n0 + c * 16 + kg * 4, v);
+        }
     }
 }
 
@@ -895,8 +973,23 @@ static ssd_status run_tile(const LinearArgs &a, const LinearPlan &p, hipStream_t
 template <int KIND, typename TO>
 static ssd_status run_linear(const LinearArgs &a, const LinearPlan &p, hipStream_t s) {
     if (p.bm) return run_tile<KIND, TO, false, false>(a, p, s);
-    const dim3 grid((unsigned)((a.N + 15) / 16)), block(512);
-    return launch(k_skinny<KIND, TO>, grid, block, s, a) == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+    auto go = [&](auto k, int columns) {
+        return launch(k, dim3((unsigned)((a.N + columns - 1) / columns)), dim3(512), s, a) == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+    };
+    auto of = [&](auto b) {
+        constexpr int B = decltype(b)::value;
+        // short rows are few steps a wavefront, beside which its start and the reads of x count: with many of
+        // them a work-group takes 32 (8 x 768 x 50257 in bf16 23.8 us -> 17.1, 8 x 1024 x 32768 17.4 -> 12.8;
+        // longer ones lose by it: 8 x 2048 x 50257 45.9 -> 51.1)
+        return a.N >= 16384 && a.steps <= 24 ? go(k_skinny<KIND, TO, B, 2>, 32) : go(k_skinny<KIND, TO, B, 1>, 16);
+    };
+    if constexpr (KIND == kBF16) {
+        if (a.kbytes % 4 != 0) return of(std::integral_constant<int, 2>{});
+    }
+    if constexpr (KIND != kMX) {
+        if (a.kbytes % 16 != 0) return of(std::integral_constant<int, 4>{});
+    }
+    return of(std::integral_constant<int, 16>{});
 }
 
 ssd_status launch_linear(LinearArgs a, const LinearPlan &p, bool mx, ssd_dtype dtype, hipStream_t s) {

@@ -307,3 +307,42 @@ def test_linear_bwd_rows_of_dz_end_in_zeros(ssd, dtype):
     assert rows.shape[1] > n and torch.count_nonzero(rows[:, n:]) == 0
     ref = dy.double() * _slope(pre.double(), "silu")
     assert torch.all((rows[:, :n].double() - ref).abs() <= HALF[dtype] * ref.abs() + 2.0 ** -18 * dy.double().abs())
+
+
+@pytest.mark.parametrize("m,k,n", [(1, 7, 1), (3, 65, 17), (5, 129, 3), (16, 7469, 100), (13, 1003, 515), (2, 4097, 33),
+                                   (8, 8191, 40), (16, 63, 16), (4, 2050, 48), (7, 64 * 33 + 1, 20)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_linear_of_few_rows_at_any_address(ssd, m, k, n, dtype):
+    """Rows of an odd number of values are taken where they are, without a workspace, and a NaN of the row behind
+    (or behind the last row) stays out of a row's end."""
+    import torch
+    log(f"[linear, few rows] {m}x{k}x{n} {dtype}")
+    assert ssd.ssd_linear_workspace_bytes(m, k, n, int(dtype == "bf16")) == 0
+    _forward(ssd, m, k, n, dtype, "none", False, False)
+    _forward(ssd, m, k, n, dtype, "silu", True, True)
+    x, w, _, _, _ = _draw(m, k, n, dtype, 9)
+    ref, _ = ssd.ssd_linear(x, w)
+    if m > 1:
+        x[1] = math.nan
+        y, _ = ssd.ssd_linear(x, w)
+        assert bool(torch.isnan(y[1]).all()) and torch.equal(y[0], ref[0]) and torch.equal(y[2:], ref[2:])
+        x[1] = 0
+    if n > 1:
+        w[1] = math.nan
+        y, _ = ssd.ssd_linear(x, w)
+        keep = [j for j in range(n) if j != 1]
+        rows = [i for i in range(m) if i != 1]
+        assert bool(torch.isnan(y[:, 1]).all()) and torch.equal(y[rows][:, keep], ref[rows][:, keep])
+
+
+@pytest.mark.parametrize("m,k,n", [(1, 768, 16384), (16, 96, 16401), (7, 67, 16417), (13, 33, 20000), (3, 1500, 16385)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_linear_of_few_rows_and_many_columns(ssd, m, k, n, dtype):
+    log(f"[linear, few rows, many columns] {m}x{k}x{n} {dtype}")
+    _forward(ssd, m, k, n, dtype, "none", False, False)
+    _forward(ssd, m, k, n, dtype, "gelu", True, True)
+
+
+@pytest.mark.parametrize("m,k,n", [(16, 96, 16401), (5, 1024, 16384)])
+def test_linear_mx_of_few_rows_and_many_columns(ssd, m, k, n):
+    test_linear_mx(ssd, m, k, n)
