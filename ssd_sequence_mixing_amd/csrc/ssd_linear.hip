@@ -22,14 +22,29 @@
 // in = 2048, where the codes' own rounding is 2.6e-2. Products in bf16 (every
 // code is a bf16) would be exact at half the rate.
 //
+// fp32 operands are split, as they are read from LDS, into three bf16 each, and
+// six of the nine products formed: 1.3 times the rate of the fp32 matrix cores
+// (8192 x 4096 x 2048: 680 us, 202 TFLOP/s; the library's fp32 product 154).
+//
 // The product is formed as w x^T, so that a lane holds 4 consecutive n of one
 // row; the epilogue turns 16 x (columns of a wavefront) at a time through LDS
 // into whole lines of rows.
 //
+// Bound: the matrix cores; in a step of the 256 x 256 tile they are busy 82% of
+// the cycles. On a warm GPU (bf16, microseconds; the library's plain product beside
+// it): 8192 x 4096 x 2048 with a residual 137 (105 without one), 8192 x 2048 x 8512
+// 269 (252), 16384 x 768 x 3352 115 (135), 64 x 2048 x 8512 13.3 (19); 8 bits
+// 8192 x 2048 x 8512 176. The rest is the start and the epilogue of each round of
+// tiles (10 to 14 us of a round, where nothing is multiplied). Measured and left: 4
+// wavefronts a tile, 32 x 32 matrix instructions, a wave priority around the
+// products, loads two steps ahead (all within 2% or slower).
+//
 // k_skinny (up to 16 rows, decoding): the time is one read of w. A
 // work-group takes 16 rows of w, its 8 wavefronts split k, and both operands
 // go from memory to the matrix cores' registers; the 8 shares are added
-// through LDS.
+// through LDS. 8 x 2048 x 8512 in bf16 (35 MB): 12 us, 2.9 TB/s, of which the
+// launch and the first loads are half; 1 x 2048 x 50257 (206 MB): 40 us, 5.1 TB/s.
+// 4 or 16 wavefronts, and loads past the caches, were slower.
 #include <type_traits>
 
 #include "ssd_common.h"
@@ -804,7 +819,8 @@ __global__ __launch_bounds__(256) void k_transpose(const T *in, T *out, int R, i
 // dz = dy act'(z), rows of ldz values with zeros behind column N, and the
 // shares of db of each 64 rows (fp32, before dz is rounded). A work-group
 // takes 64 rows of 512 columns, a lane 8 columns (V: N is a multiple of 8 and
-// they are one load) of every fourth row.
+// they are one load) of every fourth row. Bound: HBM, two reads and one
+// write (16384 x 3352 in bf16, SiLU: 330 MB in 67 us, 4.9 TB/s, what a copy reaches).
 template <typename T, bool V, int ACT>
 __global__ __launch_bounds__(256) void k_dz(const T *dy, const T *pre, T *dz, float *part, int M, int N, int ldz) {
     __shared__ float col[4][64][8];
@@ -919,7 +935,7 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, bool f32, bool alon
     };
     best = best_of(N, 32, &top);
     // whole rounds of the large tile, and the columns that are left by the tile that is best for them
-    // (8192 x 2048 x 8512 in 8 bits: 4 rounds and 320 columns, 184 us; 5 rounds, the last a quarter full, 194)
+    // (8192 x 2048 x 8512 in 8 bits: 4 rounds and 320 columns, 176 us; 5 rounds, the last a quarter full, 194)
     if (!along_k) {
         const Tile &c = tiles[f32 ? 1 : 0];
         const int64_t nm = (M + c.bm - 1) / c.bm;
