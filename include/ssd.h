@@ -511,9 +511,8 @@ ssd_status ssd_rms_norm_bwd(const void *dy, const void *h, const float *weight, 
  * rows as three bf16 parts of each operand and six of their nine products, which
  * leaves out less than 2^-21 of a product (2^-24 on average), and what of an
  * operand lies below 2^-126; an infinite operand then gives NaN in its row or column.
- * Any sizes; with more than 16 rows, ones that do not begin at multiples of 16
- * bytes (in * sizeof(dtype) not a multiple of 16) cost a copy of both operands in
- * the workspace. rows at most 2^24, in and out at most 2^20. The same inputs give
+ * Any sizes; with more than 16 rows, an odd `in` in bf16 costs a copy of both
+ * operands in the workspace (rows that do not begin at multiples of 4 bytes). rows at most 2^24, in and out at most 2^20. The same inputs give
  * the same bits. The workspace (256-byte aligned) is empty for most shapes.
  *
  * ssd_linear_mx is the same product of 8-bit operands as ssd_rms_norm_mx and

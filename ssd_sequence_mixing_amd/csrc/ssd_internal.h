@@ -209,7 +209,7 @@ ssd_status launch_column_sums(const float *part, float *out, int nb, int64_t D, 
 
 // Matrix products (ssd_linear.hip): y (M x N) = act(x w^T + bias) + res.
 struct LinearArgs {
-    const void *x, *w;          // rows of ldx / ldw bytes (multiples of 16), kbytes of them along k
+    const void *x, *w;          // rows of ldx / ldw bytes (multiples of 4; few rows: of the type), kbytes of them along k
     const uint8_t *xscale, *wscale;  // 8-bit operands: a scale for each 32 along k, rows of lds bytes
     int64_t ldx, ldw, lds;
     const float *bias;          // (N) or null

@@ -95,8 +95,8 @@ ssd_status check_linear(int64_t rows, int64_t in, int64_t out, int act, int64_t 
 
 int64_t align16(int64_t v) { return (v + 15) & ~(int64_t)15; }
 
-// Workspace of a product: copies of the operands where their rows do not
-// begin at multiples of 16 bytes, and the parts of a split sum.
+// Workspace of a product: copies of the operands, in rows of multiples of 16 bytes, where
+// theirs begin at odd multiples of 2 (and there are more than a few), and the parts of a split sum.
 struct LinearLayout {
     ssd::LinearPlan plan;
     int64_t ld, xpad, wpad, xs, ws, part, total;
@@ -107,7 +107,7 @@ LinearLayout linear_layout(int64_t rows, int64_t in, int64_t out, ssd_dtype dtyp
     const int64_t bytes = in * esize(dtype);
     l.ld = align16(bytes);
     l.plan = ssd::linear_plan(rows, out, l.ld, dtype == SSD_F32, false);
-    if (!l.plan.bm) {  // few rows: operands as they are
+    if (!l.plan.bm || bytes % 4 == 0) {  // operands as they are
         l.ld = bytes;
     } else if (l.ld != bytes) {
         l.xpad = align256(rows * l.ld);

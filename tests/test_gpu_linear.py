@@ -346,3 +346,25 @@ def test_linear_of_few_rows_and_many_columns(ssd, m, k, n, dtype):
 @pytest.mark.parametrize("m,k,n", [(16, 96, 16401), (5, 1024, 16384)])
 def test_linear_mx_of_few_rows_and_many_columns(ssd, m, k, n):
     test_linear_mx(ssd, m, k, n)
+
+
+@pytest.mark.parametrize("dtype,m,k,n", [("f32", 17, 1, 5), ("f32", 20, 3, 40), ("f32", 33, 33, 3), ("f32", 777, 1003, 515),
+                                         ("f32", 300, 2050, 260), ("f32", 40, 5001, 70), ("f32", 4096, 101, 3301),
+                                         ("f32", 1024, 95, 3100), ("bf16", 17, 2, 5), ("bf16", 65, 66, 64), ("bf16", 100, 390, 100),
+                                         ("bf16", 40, 4098, 130), ("bf16", 1000, 1022, 772), ("bf16", 4096, 514, 4364),
+                                         ("bf16", 2048, 130, 4100), ("bf16", 3000, 62, 1000)])
+def test_linear_of_rows_that_end_inside_16_bytes(ssd, dtype, m, k, n):
+    """Rows at multiples of 4 bytes are taken as they are: what lies behind a row's end (the next row, or anything
+    behind the last) stays out of it, NaN or not."""
+    import torch
+    log(f"[linear, ragged rows] {m}x{k}x{n} {dtype}")
+    _forward(ssd, m, k, n, dtype, "none", False, False)
+    _forward(ssd, m, k, n, dtype, "gelu", True, True)
+    x, w, _, _, _ = _draw(m, k, n, dtype, 9)
+    ref, _ = ssd.ssd_linear(x, w)
+    rows, cols = torch.ones(m, dtype=torch.bool, device="cuda"), torch.ones(n, dtype=torch.bool, device="cuda")
+    rows[1::3] = cols[1::2] = False
+    x[~rows], w[~cols] = math.nan, math.nan
+    y, _ = ssd.ssd_linear(x, w)
+    assert torch.equal(y[rows][:, cols], ref[rows][:, cols]) and bool(torch.isnan(y[~rows]).all())
+    assert bool(torch.isnan(y[:, ~cols]).all())

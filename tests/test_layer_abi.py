@@ -185,8 +185,10 @@ def test_linear_bwd_checks(kw, code):
 def test_linear_workspaces():
     q = ssd.load().ssd_linear_workspace_bytes
     assert q(8, 2048, 8512, BF16) == 0 and q(8192, 4096, 2048, BF16) == 0
-    # rows of 1003 fp32 values: both operands copied to rows of 1004
-    assert q(64, 1003, 515, F32) == 64 * 1004 * 4 + -(-515 * 1004 * 4 // 256) * 256
+    # rows of 1003 bf16 values: both operands copied to rows of 1008; fp32 ones and few rows are taken as they are
+    copies = -(-64 * 1008 * 2 // 256) * 256 + -(-515 * 1008 * 2 // 256) * 256
+    assert q(64, 1003, 515, BF16) - copies == q(64, 1008, 515, BF16)
+    assert q(64, 1003, 515, F32) == q(64, 1004, 515, F32) and q(16, 1003, 515, BF16) == 0
     assert q(0, 1003, 515, F32) == 0 and q(-1, 64, 64, F32) == NONE and q(8, 64, 64, 9) == NONE
     q = ssd.load().ssd_linear_mx_workspace_bytes
     assert q(8, 96, 64) == 0 and q(8, 40, 64) == NONE
