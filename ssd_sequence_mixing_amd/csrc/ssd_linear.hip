@@ -324,7 +324,7 @@ __device__ __forceinline__ void tile_of(int id, int nm, int nn, int &tm, int &tn
 // read. 32 of its lanes take 32 bytes of rows k .. k + 3 and k + 8 .. k + 11 each;
 // the chunks of a row are moved by swizzled() so that these 8 pieces of 32 bytes lie in
 // different banks (without the second four: half of the reads' cycles were conflicts).
-template <int KIND, typename TO, int BM, int BN, int WM, int WN, int EPI, bool XT, bool WT>
+template <int KIND, typename TO, int BM, int BN, int WM, int WN, int EPI, bool XT, bool WT, bool RAGGED>
 __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearArgs a) {
     constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // loads per wavefront and step, 8 rows each
@@ -424,12 +424,11 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
             to_lds4(srow, slen, sc + w * 256, (vs + (uint32_t)(first + s) * 4u) | oob_if(!live, 0));
     };
 
-    // Rows that end inside 16 bytes (their starts are multiples of 4 only): the chunk that they end in
+    // RAGGED: rows end inside 16 bytes (their starts are multiples of 4 only). The chunk that they end in
     // brings the next row's first values along. It is written once more, value by value, in the step that has it.
     // (777 x 1003 x 515 in fp32 27.2 us with copies in whole chunks in front, 21.7 so; 8192 x 4094 x 2048 in bf16
-    // 138 and 117)
-    constexpr bool kRagged = KIND != kMX && !XT && !WT;
-    int ragged = (a.kbytes & 15u) ? a.steps - 1 - first : -1;
+    // 138 and 117. A kernel of its own: the branch in a step costs 8192 x 4096 x 2048 1.5%)
+    int ragged = a.steps - 1 - first;
     if (ragged >= steps) ragged = -1;  // another split's
     auto mend = [&](char *buf) {
         for (int t = (int)threadIdx.x; t < BM + BN; t += 64 * NW) {
@@ -534,7 +533,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
             mix<kReadsX, TQ * TN * kMma, 0>();  // the compiler would move every read down to its first use
         }
         arrive();  // step s + 1 is there, and everybody has read all of step s
-        if (kRagged && s + 1 == ragged) mend(nbuf);
+        if (RAGGED && s + 1 == ragged) mend(nbuf);
         __builtin_amdgcn_sched_barrier(0);
         read_w(nwf, nbuf, nsc);
         read_x(x0, nbuf, nsc, 0);
@@ -547,7 +546,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
     // pairs of steps, without a branch: the accumulators then stay where they are
     fetch(0, s0, q0);
     arrive();
-    if (kRagged && ragged == 0) mend(s0);
+    if (RAGGED && ragged == 0) mend(s0);
     fetch(1, s1, q1);
     read_w(w0, s0, q0);
     read_x(x0, s0, q0, 0);
@@ -979,15 +978,15 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, bool f32, bool alon
     return top;
 }
 
-template <int KIND, typename TO, bool XT, bool WT>
+template <int KIND, typename TO, bool XT, bool WT, bool RAGGED>
 static ssd_status run_tile(const LinearArgs &a, const LinearPlan &p, hipStream_t s) {
     const dim3 grid((unsigned)(p.nm * p.nn), (unsigned)p.splits);
     auto go = [&](auto epi) {
         constexpr int EPI = decltype(epi)::value;
-        if (p.bm == 64) return launch(k_tile<KIND, TO, 64, 64, 2, 2, EPI, XT, WT>, grid, dim3(256), s, a);
-        if (p.bm == 128) return launch(k_tile<KIND, TO, 128, 128, 2, 2, EPI, XT, WT>, grid, dim3(256), s, a);
-        if (p.bn == 192) return launch(k_tile<KIND, TO, 256, 192, 2, 4, EPI, XT, WT>, grid, dim3(512), s, a);
-        if constexpr (KIND != kF32) return launch(k_tile<KIND, TO, 256, 256, 2, 4, EPI, XT, WT>, grid, dim3(512), s, a);
+        if (p.bm == 64) return launch(k_tile<KIND, TO, 64, 64, 2, 2, EPI, XT, WT, RAGGED>, grid, dim3(256), s, a);
+        if (p.bm == 128) return launch(k_tile<KIND, TO, 128, 128, 2, 2, EPI, XT, WT, RAGGED>, grid, dim3(256), s, a);
+        if (p.bn == 192) return launch(k_tile<KIND, TO, 256, 192, 2, 4, EPI, XT, WT, RAGGED>, grid, dim3(512), s, a);
+        if constexpr (KIND != kF32) return launch(k_tile<KIND, TO, 256, 256, 2, 4, EPI, XT, WT, RAGGED>, grid, dim3(512), s, a);
         return hipErrorInvalidValue;  // no such plan
     };
     hipError_t e;
@@ -1009,7 +1008,10 @@ static ssd_status run_tile(const LinearArgs &a, const LinearPlan &p, hipStream_t
 
 template <int KIND, typename TO>
 static ssd_status run_linear(const LinearArgs &a, const LinearPlan &p, hipStream_t s) {
-    if (p.bm) return run_tile<KIND, TO, false, false>(a, p, s);
+    if constexpr (KIND != kMX) {
+        if (p.bm && a.kbytes % 16 != 0) return run_tile<KIND, TO, false, false, true>(a, p, s);
+    }
+    if (p.bm) return run_tile<KIND, TO, false, false, false>(a, p, s);
     auto go = [&](auto k, int columns) {
         return launch(k, dim3((unsigned)((a.N + columns - 1) / columns)), dim3(512), s, a) == hipSuccess ? SSD_OK : SSD_ERR_HIP;
     };
@@ -1052,7 +1054,7 @@ ssd_status launch_linear(LinearArgs a, const LinearPlan &p, bool mx, ssd_dtype d
         return st != SSD_OK ? st : launch_linear(b, second, mx, dtype, s);
     }
     if (mx) return run_linear<kMX, bf16>(a, p, s);
-    if (a.wt) return a.xt ? run_tile<kBF16, bf16, true, true>(a, p, s) : run_tile<kBF16, bf16, false, true>(a, p, s);
+    if (a.wt) return a.xt ? run_tile<kBF16, bf16, true, true, false>(a, p, s) : run_tile<kBF16, bf16, false, true, false>(a, p, s);
     return dtype == SSD_BF16 ? run_linear<kBF16, bf16>(a, p, s) : run_linear<kF32, float>(a, p, s);
 }
 
