@@ -250,7 +250,7 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -561,20 +561,31 @@ def _device(t) -> int:
     dev = t.get_device()
     if dev < 0:
         raise ValueError("tensors must be on the GPU")
-    now = torch.cuda.current_device()
+    now = torch._C._cuda_getDevice()  # current_device() without its check that CUDA is there: a tensor is on it
     if dev != now:
         raise ValueError(f"tensor on cuda:{dev}, but the current device is cuda:{now}")
     return dev
+
+
+def _stream_on(dev: int, stream) -> Optional[int]:
+    """_stream, the current device being known."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _in(dev: int, name: str, t, shape, dtype) -> Optional[int]:
     """The address of an argument (None for None) that is checked: shape, type, device, contiguous."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype:
-        _chk(name, t, shape, dtype)
+    if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _chk(name, t, shape, dtype)
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    raise ValueError(f"{name}: tensors must be contiguous")
+
+
+def _first(name: str, t) -> int:
+    """_in of the argument that the device and the shapes are taken from."""
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensors must be contiguous")
     return t.data_ptr()
@@ -643,7 +654,7 @@ def ssd_step_beam(state_in, state_out, parent, x, dt, A, B, C, D, *, conv_in=Non
         _in(dev, "conv_w", conv_w, (H * P, 4), f32), _in(dev, "conv_b", conv_b, (H * P,), f32),
         _in(dev, "dt", dt, (bsz, H), st), _in(dev, "dt_bias", dt_bias, (H,), f32), int(dt_softplus),
         _in(dev, "A", A, (H,), f32), _in(dev, "B", B, (bsz, G, N), st), _in(dev, "C", C, (bsz, G, N), st),
-        _in(dev, "D", D, (H,), f32), _in(dev, "z", z, (bsz, H, P), st), p_y, bsz, H, P, N, G, code, _stream(stream))
+        _in(dev, "D", D, (H,), f32), _in(dev, "z", z, (bsz, H, P), st), p_y, bsz, H, P, N, G, code, _stream_on(dev, stream))
     if rc != 0:
         raise SSDError(rc, "ssd_step_beam")
     return y
@@ -667,7 +678,7 @@ def ssd_beam_select(logits, scores, *, finished=None, eos: int = -1, workspace=N
     if finished is not None and finished.dtype not in (torch.bool, torch.uint8):
         raise ValueError(f"finished: dtype {finished.dtype}, expected bool or uint8")
     dev = _device(logits)
-    p_l, p_s = _in(dev, "logits", logits, shape, logits.dtype), _in(dev, "scores", scores, rows, torch.float32)
+    p_l, p_s = _first("logits", logits), _in(dev, "scores", scores, rows, torch.float32)
     p_f = None if finished is None else _in(dev, "finished", finished, rows, finished.dtype)
     need = 0 if workspace is not None else ssd_beam_select_workspace_bytes(bsz, K, V)
     workspace, p_w, nbytes = _scratch(workspace, need, logits, dev, stream)
@@ -676,7 +687,7 @@ def ssd_beam_select(logits, scores, *, finished=None, eos: int = -1, workspace=N
     token = _like(parent, stream)
     done = _new(rows, torch.bool, logits, stream)
     st = lib.ssd_beam_select(p_l, p_s, p_f, int(eos), out.data_ptr(), parent.data_ptr(), token.data_ptr(),
-                             done.data_ptr(), bsz, K, V, code, p_w, nbytes, _stream(stream))
+                             done.data_ptr(), bsz, K, V, code, p_w, nbytes, _stream_on(dev, stream))
     if st != 0:
         raise SSDError(st, "ssd_beam_select")
     return out, parent, token, done
@@ -689,7 +700,7 @@ def _norm_args(x, weight, residual, residual_out, stream):
     shape = x.shape
     code = rcode = _dtype_code(x)
     dev = _device(x)
-    p_x, p_w = _in(dev, "x", x, shape, x.dtype), _in(dev, "weight", weight, (dim,), torch.float32)
+    p_x, p_w = _first("x", x), _in(dev, "weight", weight, (dim,), torch.float32)
     p_r = p_ro = None
     if residual is None:
         if residual_out is not None:
@@ -719,7 +730,7 @@ def ssd_rms_norm(x, weight, eps: float, *, residual=None, groups: int = 1, resid
         p_y = y.data_ptr()
     rstd = _new((*x.shape[:-1], groups), torch.float32, x, stream) if want_rstd else None
     st = lib.ssd_rms_norm(p_x, p_r, p_w, eps, p_ro, p_y, None if rstd is None else rstd.data_ptr(), rows, dim, groups,
-                          code, rcode, _stream(stream))
+                          code, rcode, _stream_on(dev, stream))
     if st != 0:
         raise SSDError(st, "ssd_rms_norm")
     return y, residual_out, rstd
@@ -737,7 +748,7 @@ def ssd_rms_norm_mx(x, weight, eps: float, *, residual=None, groups: int = 1, re
     rows, dim, code, rcode, dev, p_x, p_w, p_r, p_ro, residual_out = _norm_args(x, weight, residual, residual_out, stream)
     q, scale = _new_mx(x, dim, stream)
     st = lib.ssd_rms_norm_mx(p_x, p_r, p_w, eps, p_ro, q.data_ptr(), scale.data_ptr(), rows, dim, groups, code, rcode,
-                             _stream(stream))
+                             _stream_on(dev, stream))
     if st != 0:
         raise SSDError(st, "ssd_rms_norm_mx")
     return q, scale, residual_out
@@ -748,9 +759,10 @@ def ssd_mx_quantize(x, *, stream=None):
     lib = load()
     rows, dim = _rows_dim("x", x)
     code = _dtype_code(x)
-    p_x = _in(_device(x), "x", x, x.shape, x.dtype)
+    dev = _device(x)
+    p_x = _first("x", x)
     q, scale = _new_mx(x, dim, stream)
-    st = lib.ssd_mx_quantize(p_x, q.data_ptr(), scale.data_ptr(), rows, dim, code, _stream(stream))
+    st = lib.ssd_mx_quantize(p_x, q.data_ptr(), scale.data_ptr(), rows, dim, code, _stream_on(dev, stream))
     if st != 0:
         raise SSDError(st, "ssd_mx_quantize")
     return q, scale
@@ -776,10 +788,10 @@ def ssd_rms_norm_bwd(dy, h, weight, rstd, *, d_residual_out=None, groups: int = 
     dh = _new(shape, h.dtype, dy, stream) if rcode != code else None
     dw = _new((dim,), torch.float32, dy, stream)
     st = lib.ssd_rms_norm_bwd(
-        _in(dev, "dy", dy, shape, dy.dtype), _in(dev, "h", h, shape, h.dtype),
+        _first("dy", dy), _in(dev, "h", h, shape, h.dtype),
         _in(dev, "weight", weight, (dim,), torch.float32), _in(dev, "rstd", rstd, (*shape[:-1], groups), torch.float32),
         _in(dev, "d_residual_out", d_residual_out, shape, h.dtype), dx.data_ptr(), None if dh is None else dh.data_ptr(),
-        dw.data_ptr(), rows, dim, groups, code, rcode, p_ws, nbytes, _stream(stream))
+        dw.data_ptr(), rows, dim, groups, code, rcode, p_ws, nbytes, _stream_on(dev, stream))
     if st != 0:
         raise SSDError(st, "ssd_rms_norm_bwd")
     return dx, dh, dw
@@ -820,9 +832,9 @@ def ssd_linear(x, w, *, bias=None, act: str = "none", residual=None, y=None, wan
     pre = _new(shape, st, x, stream) if want_preact else None
     need = 0 if workspace is not None else ssd_linear_workspace_bytes(rows, k, n, code)
     workspace, p_ws, nbytes = _scratch(workspace, need, x, dev, stream)
-    rc = lib.ssd_linear(_in(dev, "x", x, x.shape, st), _in(dev, "w", w, (n, k), st),
+    rc = lib.ssd_linear(_first("x", x), _in(dev, "w", w, (n, k), st),
                         _in(dev, "bias", bias, (n,), torch.float32), acode, _in(dev, "residual", residual, shape, st), p_y,
-                        None if pre is None else pre.data_ptr(), rows, k, n, code, p_ws, nbytes, _stream(stream))
+                        None if pre is None else pre.data_ptr(), rows, k, n, code, p_ws, nbytes, _stream_on(dev, stream))
     if rc != 0:
         raise SSDError(rc, "ssd_linear")
     return y, pre
@@ -852,7 +864,7 @@ def ssd_linear_mx(xq, xscale, wq, wscale, *, bias=None, act: str = "none", resid
     rc = lib.ssd_linear_mx(_in(dev, "xq", xq, xq.shape, q8), _in(dev, "xscale", xscale, sshape, s8),
                            _in(dev, "wq", wq, (n, k), q8), _in(dev, "wscale", wscale, (n, k // 32), s8),
                            _in(dev, "bias", bias, (n,), f32), acode, _in(dev, "residual", residual, shape, b16), p_y,
-                           rows, k, n, p_ws, nbytes, _stream(stream))
+                           rows, k, n, p_ws, nbytes, _stream_on(dev, stream))
     if rc != 0:
         raise SSDError(rc, "ssd_linear_mx")
     return y
@@ -878,9 +890,9 @@ def ssd_linear_bwd(dy, x, w, *, act: str = "none", preact=None, want_x: bool = T
     db = _new((n,), torch.float32, x, stream) if want_bias else None
     need = 0 if workspace is not None else ssd_linear_bwd_workspace_bytes(rows, k, n, act, code)
     workspace, p_ws, nbytes = _scratch(workspace, need, x, dev, stream)
-    rc = lib.ssd_linear_bwd(_in(dev, "dy", dy, shape, st), _in(dev, "x", x, x.shape, st), _in(dev, "w", w, (n, k), st),
+    rc = lib.ssd_linear_bwd(_in(dev, "dy", dy, shape, st), _first("x", x), _in(dev, "w", w, (n, k), st),
                             acode, _in(dev, "preact", preact, shape, st), _ptr(dx), _ptr(dw), _ptr(db), rows, k, n,
-                            code, p_ws, nbytes, _stream(stream))
+                            code, p_ws, nbytes, _stream_on(dev, stream))
     if rc != 0:
         raise SSDError(rc, "ssd_linear_bwd")
     return dx, dw, db
