@@ -611,9 +611,11 @@ def _new(shape, dtype, like, stream):
         return like.new_empty(shape, dtype=dtype)
 
 
-def _like(t, stream):
-    """_new of the shape and type of t, which is contiguous."""
-    return torch.empty_like(t) if stream is None else _new(t.shape, t.dtype, t, stream)
+def _like(t, stream, dtype=None):
+    """_new of the shape (and type) of t, which is contiguous."""
+    if stream is not None:
+        return _new(t.shape, dtype or t.dtype, t, stream)
+    return torch.empty_like(t) if dtype is None else torch.empty_like(t, dtype=dtype)
 
 
 def _sized(name: str, n: int) -> int:
@@ -683,9 +685,9 @@ def ssd_beam_select(logits, scores, *, finished=None, eos: int = -1, workspace=N
     need = 0 if workspace is not None else ssd_beam_select_workspace_bytes(bsz, K, V)
     workspace, p_w, nbytes = _scratch(workspace, need, logits, dev, stream)
     out = _like(scores, stream)
-    parent = _new(rows, torch.int32, logits, stream)
+    parent = _like(scores, stream, torch.int32)
     token = _like(parent, stream)
-    done = _new(rows, torch.bool, logits, stream)
+    done = _like(scores, stream, torch.bool)
     st = lib.ssd_beam_select(p_l, p_s, p_f, int(eos), out.data_ptr(), parent.data_ptr(), token.data_ptr(),
                              done.data_ptr(), bsz, K, V, code, p_w, nbytes, _stream_on(dev, stream))
     if st != 0:
