@@ -241,7 +241,8 @@ ssd_status launch_pad(const void *in1, void *out1, int64_t R1, const void *in2, 
                       int64_t ldo, int es, hipStream_t s);
 // fp32 only.
 ssd_status launch_transpose(const void *in, void *out, int64_t R, int64_t C, int64_t ldo, hipStream_t s);
-// dz (null: not wanted) and the 64-row shares of db (null: not wanted).
+// dz (null: not wanted) and the shares of db, of dz_rows rows each (null: not wanted).
+int dz_rows(int64_t M, int64_t ldz);
 ssd_status launch_dz(const void *dy, const void *pre, int act, void *dz, float *part, int64_t M, int64_t N, int64_t ldz,
                      ssd_dtype dtype, hipStream_t s);
 

@@ -135,11 +135,11 @@ LinearLayout linear_mx_layout(int64_t rows, int64_t in, int64_t out) {
 
 // Workspace of the gradients, one after the other: dz (where it is not dy
 // itself); bf16: copies of w and x with rows of 16-byte multiples, where theirs are
-// not; fp32: dz, w and x transposed (rows of ldt / ldz values); the 64-row
-// shares of dbias; the parts of the two products' sums.
+// not; fp32: dz, w and x transposed (rows of ldt / ldz values); the shares of
+// dbias, of dbrows rows each; the parts of the two products' sums.
 struct LinearBwdLayout {
     ssd::LinearPlan px, pw;
-    int64_t ldz, ldt, ldk, kz, dz, dzt, w, x, db, part, total;  // kz: bytes of dz along its row that a product takes
+    int64_t ldz, ldt, ldk, kz, dbrows, dz, dzt, w, x, db, part, total;  // kz: bytes of dz along its row that a product takes
 };
 LinearBwdLayout linear_bwd_layout(int64_t rows, int64_t in, int64_t out, int act, bool want_dx, bool want_dw,
                                   bool want_db, ssd_dtype dtype) {
@@ -169,7 +169,8 @@ LinearBwdLayout linear_bwd_layout(int64_t rows, int64_t in, int64_t out, int act
         l.pw = ssd::linear_plan(out, in, l.ldt * es, !bf, bf);
         if (l.pw.splits > 1) pw = align256(l.pw.splits * ssd::part_stride(out, in) * 4);
     }
-    if (want_db) l.db = align256((rows + 63) / 64 * out * 4);
+    l.dbrows = ssd::dz_rows(rows, l.ldz);
+    if (want_db) l.db = align256((rows + l.dbrows - 1) / l.dbrows * out * 4);
     l.part = px > pw ? px : pw;
     l.total = l.dz + l.dzt + l.w + l.x + l.db + l.part;
     return l;
@@ -277,7 +278,7 @@ ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, int act,
         st = ssd::launch_dz(dy, preact, act, l.dz ? dz : nullptr, l.db ? db : nullptr, rows, out, l.ldz, dtype, s);
         if (st != SSD_OK) return st;
     }
-    if (dbias && (st = ssd::launch_column_sums(db, dbias, (int)((rows + 63) / 64), out, s)) != SSD_OK) return st;
+    if (dbias && (st = ssd::launch_column_sums(db, dbias, (int)((rows + l.dbrows - 1) / l.dbrows), out, s)) != SSD_OK) return st;
     const void *z = l.dz ? dz : dy;
     if (dx) {
         ssd::LinearArgs a = {};

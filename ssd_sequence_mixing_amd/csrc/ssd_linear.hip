@@ -837,20 +837,22 @@ __global__ __launch_bounds__(256) void k_transpose(const T *in, T *out, int R, i
 }
 
 // dz = dy act'(z), rows of ldz values with zeros behind column N, and the
-// shares of db of each 64 rows (fp32, before dz is rounded). A work-group
-// takes 64 rows of 512 columns, a lane 8 columns (V: N is a multiple of 8 and
-// they are one load) of every fourth row. Bound: HBM, two reads and one
+// shares of db of each R rows (fp32, before dz is rounded). A work-group
+// takes R rows of 512 columns, a lane 8 columns (V: N is a multiple of 8 and
+// they are one load) of every Y-th row. Bound: HBM, two reads and one
 // write (16384 x 3352 in bf16, SiLU: 330 MB in 67 us, 4.9 TB/s, what a copy reaches).
-template <typename T, bool V, int ACT>
-__global__ __launch_bounds__(256) void k_dz(const T *dy, const T *pre, T *dz, float *part, int M, int N, int ldz) {
-    __shared__ float col[4][64][8];
+// Y wavefronts: 4, or 16 where there are fewer than 4 work-groups for a CU and the time is
+// the chain of a wavefront's rows (7676 x 108 in bf16 9.1 us, with 4 of 64 rows 29.9; 933 x 430 7.8 and 25.8).
+template <typename T, bool V, int ACT, int Y>
+__global__ __launch_bounds__(64 * Y) void k_dz(const T *dy, const T *pre, T *dz, float *part, int M, int N, int ldz, int R) {
+    __shared__ float col[Y][64][8];
     const int lane = threadIdx.x & 63, y = threadIdx.x >> 6;
-    const int m0 = blockIdx.x * 64, n = blockIdx.y * 512 + lane * 8;
+    const int m0 = blockIdx.x * R, n = blockIdx.y * 512 + lane * 8;
     float sum[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] = 0.f;
 #pragma unroll 4
-    for (int i = y; i < 64; i += 4) {
+    for (int i = y; i < R; i += Y) {
         const int m = m0 + i;
         if (m >= M || n >= ldz) continue;
         const int64_t at = (int64_t)m * N + n;
@@ -895,9 +897,11 @@ __global__ __launch_bounds__(256) void k_dz(const T *dy, const T *pre, T *dz, fl
     __syncthreads();
     if (y == 0) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (n + e < N)
-                part[(int64_t)blockIdx.x * N + n + e] = col[0][lane][e] + col[1][lane][e] + col[2][lane][e] + col[3][lane][e];
+        for (int e = 0; e < 8; ++e) {
+#pragma unroll
+            for (int k = 1; k < Y; ++k) sum[e] += col[k][lane][e];
+            if (n + e < N) part[(int64_t)blockIdx.x * N + n + e] = sum[e];
+        }
     }
 }
 
@@ -1089,22 +1093,28 @@ ssd_status launch_transpose(const void *in, void *out, int64_t R, int64_t C, int
                : SSD_ERR_HIP;
 }
 
+// Rows of a share of db: 64, or 16 where those were fewer work-groups than CUs.
+int dz_rows(int64_t M, int64_t ldz) { return (M + 63) / 64 * ((ldz + 511) / 512) < 256 ? 16 : 64; }
+
 template <typename T>
 static ssd_status run_dz(const void *dy, const void *pre, int act, void *dz, float *part, int64_t M, int64_t N, int64_t ldz,
                          hipStream_t s) {
-    const dim3 grid((unsigned)((M + 63) / 64), (unsigned)((ldz + 511) / 512)), block(256);
+    const int R = dz_rows(M, ldz);
+    const dim3 grid((unsigned)((M + R - 1) / R), (unsigned)((ldz + 511) / 512));
+    const bool few = (int64_t)grid.x * grid.y < 1024;
     auto go = [&](auto k) {
-        return launch(k, grid, block, s, (const T *)dy, (const T *)pre, (T *)dz, part, (int)M, (int)N, (int)ldz) == hipSuccess
+        return launch(k, grid, dim3(few ? 1024 : 256), s, (const T *)dy, (const T *)pre, (T *)dz, part, (int)M, (int)N, (int)ldz,
+                      R) == hipSuccess
                    ? SSD_OK
                    : SSD_ERR_HIP;
     };
-    if (N % 8 == 0)
-        return act == SSD_ACT_SILU   ? go(k_dz<T, true, SSD_ACT_SILU>)
-               : act == SSD_ACT_GELU ? go(k_dz<T, true, SSD_ACT_GELU>)
-                                     : go(k_dz<T, true, SSD_ACT_NONE>);
-    return act == SSD_ACT_SILU   ? go(k_dz<T, false, SSD_ACT_SILU>)
-           : act == SSD_ACT_GELU ? go(k_dz<T, false, SSD_ACT_GELU>)
-                                 : go(k_dz<T, false, SSD_ACT_NONE>);
+    auto by_act = [&](auto v) {
+        constexpr bool V = decltype(v)::value;
+        if (act == SSD_ACT_SILU) return few ? go(k_dz<T, V, SSD_ACT_SILU, 16>) : go(k_dz<T, V, SSD_ACT_SILU, 4>);
+        if (act == SSD_ACT_GELU) return few ? go(k_dz<T, V, SSD_ACT_GELU, 16>) : go(k_dz<T, V, SSD_ACT_GELU, 4>);
+        return few ? go(k_dz<T, V, SSD_ACT_NONE, 16>) : go(k_dz<T, V, SSD_ACT_NONE, 4>);
+    };
+    return N % 8 == 0 ? by_act(std::true_type{}) : by_act(std::false_type{});
 }
 
 ssd_status launch_dz(const void *dy, const void *pre, int act, void *dz, float *part, int64_t M, int64_t N, int64_t ldz,
