@@ -450,7 +450,8 @@ ssd_status ssd_beam_select(const void *logits, const float *scores, const uint8_
  *   rstd (rows, groups)            float32         output for the backward pass: 1 / sqrt(...); or NULL
  *
  * residual_dtype is dtype or, with bf16, also SSD_F32 (a residual stream kept
- * in fp32); without a residual it is dtype. dim / groups at most 65536.
+ * in fp32); without a residual it is dtype. dim / groups at most 65536, groups
+ * at most 65535, rows * groups below 2^31 (else SSD_ERR_UNSUPPORTED).
  *
  * ssd_rms_norm_mx writes y in 8 bits instead: q (rows, dim) holds e4m3 codes
  * (OCP, largest 448) and scale (rows, dim / 32) one power of two for each 32

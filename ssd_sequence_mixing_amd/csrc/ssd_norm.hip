@@ -443,11 +443,30 @@ static NormPlan norm_plan(int64_t rows, int64_t n) {
 }
 
 template <typename TX, typename TR, bool V, bool MX>
-static ssd_status run_norm(const NormArgs &a, hipStream_t s) {
-    const NormPlan p = norm_plan(a.rows, a.Dg);
-    const int rpb = p.W > 4 ? 1 : kNormThreads / (64 * p.W);
-    const dim3 grid((unsigned)((a.rows + rpb - 1) / rpb)), block(p.W > 4 ? 64 * p.W : kNormThreads);
-    auto go = [&](auto k) { return launch(k, grid, block, s, a) == hipSuccess ? SSD_OK : SSD_ERR_HIP; };
+static ssd_status run_norm(const NormArgs &all, hipStream_t s) {
+    const NormPlan p = norm_plan(all.rows, all.Dg);
+    const int rpb = p.W > 4 ? 1 : kNormThreads / (64 * p.W), threads = p.W > 4 ? 64 * p.W : kNormThreads;
+    // rows of one launch, every group of a row among them: at least 64 times the most groups
+    const int64_t most = kMostThreads / threads * rpb / all.groups * all.groups;
+    auto go = [&](auto k) {
+        for (int64_t r0 = 0; r0 < all.rows; r0 += most) {
+            NormArgs a = all;
+            a.rows = min(most, all.rows - r0);
+            const int64_t at = r0 * all.Dg;
+            a.x = static_cast<const TX *>(all.x) + at;
+            if (all.res) a.res = static_cast<const TR *>(all.res) + at;
+            if (all.res) a.res_out = static_cast<TR *>(all.res_out) + at;
+            if constexpr (MX) {
+                a.q = all.q + at;
+                a.scale = all.scale + at / 32;
+            } else {
+                a.y = static_cast<TX *>(all.y) + at;
+            }
+            if (all.rstd) a.rstd = all.rstd + r0;
+            if (launch(k, dim3((unsigned)((a.rows + rpb - 1) / rpb)), dim3(threads), s, a) != hipSuccess) return SSD_ERR_HIP;
+        }
+        return SSD_OK;
+    };
     if (p.W == 1) {
         switch (p.NC) {
             case 1: return go(k_rms_norm<TX, TR, 1, 1, V, MX>);

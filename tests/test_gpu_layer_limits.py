@@ -1,0 +1,71 @@
+"""GPU tests of the operators around the core at counts of rows whose threads pass 2^32, the most that one launch takes
+along a dimension: the ends, both sides of that border, and the middle against the formulas in 64 bits."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+
+from tests.gpu_util import log
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-5
+HALF, U32 = 2.0 ** -8, 2.0 ** -24   # of bf16, of fp32
+
+
+@pytest.fixture(autouse=True)
+def _free():
+    import torch
+    yield
+    torch.cuda.empty_cache()
+
+
+def _spots(n, border, width):
+    """Starts of stretches of `width` of n rows: the first, around the border, the middle, the last."""
+    return [0, border - width, border, n // 2, n - width]
+
+
+@pytest.mark.parametrize("per", [8, 7])
+def test_norm_of_many_groups(ssd, per):
+    """2^26 + 8 (row, group) pairs, of a wavefront each."""
+    import torch
+    rows, groups = (1 << 23) + 1, 8
+    dim = per * groups
+    log(f"[limits] norm {rows} x {groups} x {per}")
+    g = torch.Generator(device="cuda").manual_seed(per)
+    x = torch.empty(rows, dim, device="cuda", dtype=torch.bfloat16).normal_(generator=g)
+    w = torch.rand(dim, device="cuda", generator=g) + 0.5
+    y, _, rstd = ssd.ssd_rms_norm(x, w, EPS, groups=groups, want_rstd=True)
+    for r0 in range(0, rows, 1 << 20):
+        h = x[r0:r0 + (1 << 20)].double().unflatten(1, (groups, per))
+        inv = 1 / torch.sqrt((h * h).mean(-1) + EPS)
+        ref = (h * inv[..., None]).flatten(1) * w.double()
+        assert bool(((y[r0:r0 + (1 << 20)].double() - ref).abs() <= (HALF + 32 * U32) * ref.abs()).all()), r0
+        assert bool(((rstd[r0:r0 + (1 << 20)].double() - inv).abs() <= 16 * U32 * inv).all()), r0
+
+
+def test_norm_in_eight_bits_of_many_groups(ssd):
+    """The same, with 3 groups (2^26 is no multiple of them) of 32 and a residual: equal bits to the rows by themselves."""
+    import torch
+    rows, groups = (1 << 26) // 3 + 2, 3
+    dim = 32 * groups
+    log(f"[limits] norm in 8 bits {rows} x {groups} x 32")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.empty(rows, dim, device="cuda", dtype=torch.bfloat16).normal_(generator=g)
+    res = torch.empty(rows, dim, device="cuda", dtype=torch.bfloat16).normal_(generator=g)
+    w = torch.rand(dim, device="cuda", generator=g) + 0.5
+    q, s, h = ssd.ssd_rms_norm_mx(x, w, EPS, residual=res, groups=groups)
+    for r0 in _spots(rows, (1 << 26) // 3, 1):
+        r1 = min(rows, r0 + 2)
+        a, b, c = ssd.ssd_rms_norm_mx(x[r0:r1].clone(), w, EPS, residual=res[r0:r1].clone(), groups=groups)
+        torch.cuda.synchronize()
+        assert torch.equal(a.view(torch.uint8), q[r0:r1].view(torch.uint8)) and torch.equal(c, h[r0:r1])
+        assert torch.equal(b.view(torch.uint8), s[r0:r1].view(torch.uint8))
+    step = 1 << 21
+    for r0 in range(0, rows, step):  # all of it: within half a step of e4m3, and the fp32 sum
+        hh = (x[r0:r0 + step].float() + res[r0:r0 + step].float()).unflatten(1, (groups, 32))
+        y = hh / torch.sqrt((hh * hh).mean(-1, keepdim=True) + EPS) * w.view(groups, 32)
+        sc = s[r0:r0 + step].float()[..., None]
+        got = q[r0:r0 + step].float().unflatten(1, (groups, 32)) * sc
+        assert bool(((got - y).abs() <= torch.maximum(y.abs() * 2.0 ** -4, sc * 2.0 ** -10) + 256 * U32 * y.abs()).all()), r0
