@@ -460,7 +460,8 @@ ssd_status ssd_beam_select(const void *logits, const float *scores, const uint8_
  * the fp32 y. A block that holds an infinity or a NaN is NaN as a whole (scale
  * 255, codes 0x7f). dim / groups must be a multiple of 32.
  *
- * ssd_mx_quantize writes any x (rows, dim) so (weights, once; activations).
+ * ssd_mx_quantize writes any x (rows, dim) so (weights, once; activations);
+ * rows * dim at most 2^41.
  */
 ssd_status ssd_rms_norm(const void *x, const void *residual, const float *weight, float eps, void *residual_out,
                         void *y, float *rstd, int64_t rows, int64_t dim, int64_t groups, ssd_dtype dtype,

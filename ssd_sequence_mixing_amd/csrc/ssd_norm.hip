@@ -451,7 +451,7 @@ static ssd_status run_norm(const NormArgs &all, hipStream_t s) {
     auto go = [&](auto k) {
         for (int64_t r0 = 0; r0 < all.rows; r0 += most) {
             NormArgs a = all;
-            a.rows = min(most, all.rows - r0);
+            a.rows = all.rows - r0 < most ? all.rows - r0 : most;
             const int64_t at = r0 * all.Dg;
             a.x = static_cast<const TX *>(all.x) + at;
             if (all.res) a.res = static_cast<const TR *>(all.res) + at;
@@ -499,12 +499,20 @@ ssd_status launch_rms_norm(const NormArgs &a, hipStream_t s) {
     return a.res_dtype == SSD_F32 ? norm_t<bf16, float>(a, s) : norm_t<bf16, bf16>(a, s);
 }
 
+template <typename TX>
+static ssd_status run_mx_quantize(const TX *x, uint8_t *q, uint8_t *scale, int64_t n, hipStream_t s) {
+    constexpr int64_t most = kMostThreads / kNormThreads * kNormThreads * 8;  // values of one launch
+    for (int64_t i = 0; i < n; i += most) {
+        const int64_t m = n - i < most ? n - i : most;
+        const dim3 grid((unsigned)((m / 8 + kNormThreads - 1) / kNormThreads));
+        if (launch(k_mx_quantize<TX>, grid, dim3(kNormThreads), s, x + i, q + i, scale + i / 32, m) != hipSuccess)
+            return SSD_ERR_HIP;
+    }
+    return SSD_OK;
+}
 ssd_status launch_mx_quantize(const void *x, uint8_t *q, uint8_t *scale, int64_t n, ssd_dtype dtype, hipStream_t s) {
-    const dim3 grid((unsigned)((n / 8 + kNormThreads - 1) / kNormThreads)), block(kNormThreads);
-    const hipError_t e = dtype == SSD_BF16
-                             ? launch(k_mx_quantize<bf16>, grid, block, s, (const bf16 *)x, q, scale, n)
-                             : launch(k_mx_quantize<float>, grid, block, s, (const float *)x, q, scale, n);
-    return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+    return dtype == SSD_BF16 ? run_mx_quantize(static_cast<const bf16 *>(x), q, scale, n, s)
+                             : run_mx_quantize(static_cast<const float *>(x), q, scale, n, s);
 }
 
 // Work-groups per group of columns in the backward: enough to fill the chip

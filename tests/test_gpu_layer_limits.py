@@ -69,3 +69,25 @@ def test_norm_in_eight_bits_of_many_groups(ssd):
         sc = s[r0:r0 + step].float()[..., None]
         got = q[r0:r0 + step].float().unflatten(1, (groups, 32)) * sc
         assert bool(((got - y).abs() <= torch.maximum(y.abs() * 2.0 ** -4, sc * 2.0 ** -10) + 256 * U32 * y.abs()).all()), r0
+
+
+def test_quantize_of_many_values(ssd):
+    """2^35 + 2^20 values, 8 to a thread."""
+    import torch
+    rows, dim = (1 << 15) + 1, 1 << 20
+    log(f"[limits] quantize {rows} x {dim}")
+    x = torch.zeros(rows, dim, device="cuda", dtype=torch.bfloat16)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    at = _spots(rows, 1 << 15, 1)
+    for r in at:
+        x[r].normal_(generator=g)
+    q, s = ssd.ssd_mx_quantize(x)
+    for r in at:
+        a, b = ssd.ssd_mx_quantize(x[r].clone())
+        torch.cuda.synchronize()
+        assert torch.equal(a.view(torch.uint8), q[r].view(torch.uint8)), r
+        assert torch.equal(b.view(torch.uint8), s[r].view(torch.uint8)), r
+    for r0 in range(0, rows, 1 << 12):
+        part = q[r0:r0 + (1 << 12)].view(torch.uint8)
+        seen = torch.count_nonzero(part.view(torch.int64), dim=1) > 0  # (zeros are codes 0)
+        assert torch.nonzero(seen).flatten().tolist() == sorted({r - r0 for r in at if 0 <= r - r0 < (1 << 12)})
