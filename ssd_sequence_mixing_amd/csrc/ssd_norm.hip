@@ -404,7 +404,7 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : kNormThreads) void k_rms_norm_bwd(
 __global__ __launch_bounds__(1024) void k_column_sums(const float *part, float *out, int nb, int64_t D) {
     __shared__ float red[16][16];
     const int c = threadIdx.x & 15, k = threadIdx.x >> 4;
-    const int64_t d = (int64_t)blockIdx.x * 16 + c;
+    const int64_t d = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 16 + c;
     float s = 0.f;
     if (d < D) {
 #pragma unroll 8
@@ -423,7 +423,10 @@ __global__ __launch_bounds__(1024) void k_column_sums(const float *part, float *
 }
 
 ssd_status launch_column_sums(const float *part, float *out, int nb, int64_t D, hipStream_t s) {
-    return launch(k_column_sums, dim3((unsigned)((D + 15) / 16)), dim3(1024), s, part, out, nb, D) == hipSuccess
+    // up to 2^32 columns (65535 groups of 65536): the blocks in rows of 2^20, whose threads stay below kMostThreads
+    const int64_t blocks = (D + 15) / 16, x = blocks < (1 << 20) ? blocks : 1 << 20;
+    return launch(k_column_sums, dim3((unsigned)x, (unsigned)((blocks + x - 1) / x)), dim3(1024), s, part, out, nb, D) ==
+                   hipSuccess
                ? SSD_OK
                : SSD_ERR_HIP;
 }

@@ -71,6 +71,28 @@ def test_norm_in_eight_bits_of_many_groups(ssd):
         assert bool(((got - y).abs() <= torch.maximum(y.abs() * 2.0 ** -4, sc * 2.0 ** -10) + 256 * U32 * y.abs()).all()), r0
 
 
+def test_norm_gradients_of_a_wide_row(ssd):
+    """2^26 + 65536 columns: the sums over rows of that many."""
+    import torch
+    groups, per, rows = 1025, 65536, 2
+    dim = groups * per
+    log(f"[limits] norm backward {rows} x {groups} x {per}")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x, dy = (torch.empty(rows, dim, device="cuda").normal_(generator=g) for _ in range(2))
+    w = torch.rand(dim, device="cuda", generator=g) + 0.5
+    y, _, rstd = ssd.ssd_rms_norm(x, w, EPS, groups=groups, want_rstd=True)
+    dx, _, dw = ssd.ssd_rms_norm_bwd(dy, x, w, rstd, groups=groups)
+    hh = x.double().unflatten(1, (groups, per)) * rstd.double()[..., None]
+    up = dy.double().unflatten(1, (groups, per))
+    mag = (up * hh).abs().sum(0).flatten()
+    assert bool(((dw.double() - (up * hh).sum(0).flatten()).abs() <= 64 * U32 * mag).all())
+    up = up * w.double().view(groups, per)
+    dot = (up * hh).mean(-1, keepdim=True)
+    size = (up.abs() + hh.abs() * (up * hh).abs().mean(-1, keepdim=True)) * rstd.double()[..., None]
+    ref = (up - hh * dot) * rstd.double()[..., None]
+    assert bool(((dx.double().unflatten(1, (groups, per)) - ref).abs() <= 128 * U32 * size).all())
+
+
 def test_quantize_of_many_values(ssd):
     """2^35 + 2^20 values, 8 to a thread."""
     import torch
