@@ -21,16 +21,16 @@ int64_t align256(int64_t v) { return (v + 255) & ~(int64_t)255; }
 int64_t esize(ssd_dtype d) { return d == SSD_BF16 ? 2 : 4; }
 
 __global__ void k_clear(uint16_t *p, int64_t n) {
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i < n) p[i] = 0;
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) p[i] = 0;
 }
 
-// Zeros over an even number of bytes.
+// Zeros over an even number of bytes (weights of any size: 2^33 values are more threads than a launch takes).
 ssd_status clear(void *p, int64_t bytes, hipStream_t s) {
     if (!p || bytes == 0) return SSD_OK;
-    const int64_t n = bytes / 2;
-    return ssd::launch(k_clear, dim3((unsigned)((n + 255) / 256)), dim3(256), s, static_cast<uint16_t *>(p), n) ==
-                   hipSuccess
+    const int64_t n = bytes / 2, blocks = (n + 255) / 256, most = 1 << 16;
+    return ssd::launch(k_clear, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), s,
+                       static_cast<uint16_t *>(p), n) == hipSuccess
                ? SSD_OK
                : SSD_ERR_HIP;
 }

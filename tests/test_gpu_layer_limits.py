@@ -113,3 +113,18 @@ def test_quantize_of_many_values(ssd):
         part = q[r0:r0 + (1 << 12)].view(torch.uint8)
         seen = torch.count_nonzero(part.view(torch.int64), dim=1) > 0  # (zeros are codes 0)
         assert torch.nonzero(seen).flatten().tolist() == sorted({r - r0 for r in at if 0 <= r - r0 < (1 << 12)})
+
+
+def test_gradients_of_no_rows_are_zero(ssd):
+    """2^32 fp32 weights, cleared without a row to sum."""
+    import torch
+    n = 1 << 16
+    log(f"[limits] gradients of no rows, {n} x {n}")
+    dw, db = torch.ones(n, n, device="cuda"), torch.ones(n, device="cuda")
+    rc = ssd.raw_call("ssd_linear_bwd", None, None, None, 0, None, None, ctypes.c_void_p(dw.data_ptr()),
+                      ctypes.c_void_p(db.data_ptr()), 0, n, n, ssd.SSD_F32, None, 0,
+                      ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert rc == 0
+    for r in range(0, n, 1 << 12):
+        assert float(dw[r:r + (1 << 12)].abs().max()) == 0, r
+    assert float(db.abs().max()) == 0
