@@ -129,15 +129,38 @@ __global__ __launch_bounds__(kStepThreads) void k_step(StepArgs a, int pblocks) 
     }
 }
 
+// Rows b0 .. b0 + n - 1 of a step (the rows that they come from stay what they are).
+template <typename TI>
+static StepArgs step_rows(const StepArgs &a, int64_t b0, int64_t n) {
+    StepArgs r = a;
+    const int64_t hp = a.H * a.P;
+    r.batch = n;
+    r.state += b0 * hp * a.N;
+    r.x = static_cast<const TI *>(a.x) + b0 * hp;
+    r.dt = static_cast<const TI *>(a.dt) + b0 * a.H;
+    r.B = static_cast<const TI *>(a.B) + b0 * a.G * a.N;
+    r.C = static_cast<const TI *>(a.C) + b0 * a.G * a.N;
+    r.y = static_cast<TI *>(a.y) + b0 * hp;
+    if (a.z) r.z = static_cast<const TI *>(a.z) + b0 * hp;
+    if (a.conv_w) r.conv_state = static_cast<TI *>(a.conv_state) + b0 * hp * 3;
+    if (a.parent) r.parent += b0;
+    return r;
+}
+
 template <typename TI, int N, bool kBeam>
 static ssd_status run_step(const StepArgs &a, hipStream_t s) {
     constexpr int RPB = StepShape<TI, N>::RPB;
     const int pblocks = (int)((a.P + RPB - 1) / RPB);
-    const int64_t blocks = a.batch * a.H * pblocks;
-    return launch(k_step<TI, N, kBeam>, dim3((unsigned)blocks), dim3(kStepThreads), s, a, pblocks) ==
-                   hipSuccess
-               ? SSD_OK
-               : SSD_ERR_HIP;
+    // as many rows as one launch takes, and the rest in more
+    const int64_t most = kMostThreads / kStepThreads / (a.H * pblocks);
+    if (most == 0) return SSD_ERR_UNSUPPORTED;
+    for (int64_t b0 = 0; b0 < a.batch; b0 += most) {
+        const int64_t n = a.batch - b0 < most ? a.batch - b0 : most;
+        if (launch(k_step<TI, N, kBeam>, dim3((unsigned)(n * a.H * pblocks)), dim3(kStepThreads), s,
+                   step_rows<TI>(a, b0, n), pblocks) != hipSuccess)
+            return SSD_ERR_HIP;
+    }
+    return SSD_OK;
 }
 
 template <typename TI, bool kBeam>

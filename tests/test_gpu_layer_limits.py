@@ -128,3 +128,38 @@ def test_gradients_of_no_rows_are_zero(ssd):
     for r in range(0, n, 1 << 12):
         assert float(dw[r:r + (1 << 12)].abs().max()) == 0, r
     assert float(db.abs().max()) == 0
+
+
+@pytest.mark.parametrize("beam", [False, True])
+def test_step_of_many_heads(ssd, beam):
+    """2^24 + 64 (sequence, head) pairs, of a work-group each: the step in place and from parents' rows."""
+    import torch
+    rows, H, P, N = (1 << 18) + 1, 64, 1, 4
+    log(f"[limits] step of {rows} x {H} heads, beam {beam}")
+    g = torch.Generator(device="cuda").manual_seed(6)
+
+    def draw(*shape):  # in [-1, 1)
+        return 2 * torch.rand(*shape, device="cuda", generator=g) - 1
+    state, x, z, conv = draw(rows, H, P, N), draw(rows, H, P), draw(rows, H, P), draw(rows, H * P, 3)
+    dt, A = torch.rand(rows, H, device="cuda", generator=g), -torch.rand(H, device="cuda", generator=g)
+    B, C, D, conv_w, conv_b = draw(rows, 1, N), draw(rows, 1, N), draw(H), draw(H * P, 4), draw(H * P)
+    parent = torch.arange(rows - 1, -1, -1, device="cuda", dtype=torch.int32)
+    frm = parent.long() if beam else torch.arange(rows, device="cuda")
+    s0, c0 = state.double()[frm], conv.double()[frm]
+    v = (c0 * conv_w.double()[:, :3]).sum(-1) + conv_w.double()[:, 3] * x.double().flatten(1) + conv_b.double()
+    xv = (v / (1 + torch.exp(-v))).view(rows, H, P)
+    new = torch.exp(dt.double() * A.double())[..., None, None] * s0 + (dt.double()[..., None] * xv)[..., None] * B.double()[:, None]
+    ref = ((new * C.double()[:, None]).sum(-1) + D.double()[:, None] * xv) * (z.double() / (1 + torch.exp(-z.double())))
+    kept = torch.cat([c0[..., 1:], x.double().flatten(1)[..., None]], -1)
+    kw = dict(conv_w=conv_w, conv_b=conv_b, z=z)
+    if beam:
+        out, cout = torch.empty_like(state), torch.empty_like(conv)
+        y = ssd.ssd_step_beam(state, out, parent, x, dt, A, B, C, D, conv_in=conv, conv_out=cout, **kw)
+    else:
+        out, cout = state, conv
+        y = ssd.ssd_step_fused(state, conv, x, dt, A, B, C, D, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(cout.double(), kept)
+    # fp32: under 32 roundings of magnitudes of at most 6 (states) and 29 (y)
+    assert float((out.double() - new).abs().max()) < 2.0 ** -16
+    assert float((y.double() - ref).abs().max()) < 2.0 ** -14
