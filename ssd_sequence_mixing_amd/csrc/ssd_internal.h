@@ -268,12 +268,14 @@ ssd_status launch_step(const StepArgs &a, hipStream_t s);
 // Launches a kernel and returns the status of that launch itself (not an
 // error some earlier, unrelated runtime call may have left pending).
 // A launch has fewer than 2^32 threads along a dimension. HIP refuses some of those beyond and
-// cuts others down without a word, so callers with more rows than that launch them in slices.
+// cuts others down without a word, so callers with more rows than that launch them in slices,
+// and a larger grid is refused here.
 constexpr int64_t kMostThreads = UINT32_MAX;
 template <typename T> struct ident { using type = T; };
 template <typename... Args>
 inline hipError_t launch(void (*kernel)(Args...), dim3 grid, dim3 block, hipStream_t s,
                          typename ident<Args>::type... args) {
+    if ((int64_t)grid.x * block.x > kMostThreads || (int64_t)grid.y * block.y > kMostThreads) return hipErrorInvalidConfiguration;
     void *argv[] = {(void *)&args..., nullptr};
     return hipLaunchKernel((const void *)kernel, grid, block, argv, 0, s);
 }

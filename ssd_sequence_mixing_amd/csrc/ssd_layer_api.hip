@@ -80,6 +80,9 @@ int64_t beam_bytes(int64_t batch, int64_t beams, int64_t vocab, int *lists, int 
     *why = SSD_OK;
     ssd::beam_plan(vocab, lists, tiles);
     const int64_t n = batch * beams * *lists;
+    *why = SSD_ERR_UNSUPPORTED;
+    if (n > ssd::kMostThreads / 256 * 4) return -1;  // a wavefront for each, 4 to a work-group: 137 GB of logits and more
+    *why = SSD_OK;
     return align256(n * beams * 8) + align256(n * 8);
 }
 
