@@ -171,25 +171,29 @@ __device__ __forceinline__ f32x4 mma2(u32x4 wl, u32x4 wh, u32x4 xl, u32x4 xh, f3
 
 // The activations and their slopes (act: a constant where they are called). kFast, for values that are
 // rounded to bf16: the vector unit's 2^x and 1/x (1 ulp each), and for GELU
-//   erfc(u) = (a1 t + .. + a5 t^5) e^(-u^2),  t = 1 / (1 + p u),  u >= 0
-// (Abramowitz and Stegun 7.1.26, off by at most 1.5e-7), whose exponential the slope needs, too.
-// expf, erff and a division took k_dz from memory's time to the vector unit's.
+//   erfc(u) = (a1 t + .. + a7 t^7) e^(-u^2),  t = 1 / (1 + 0.505 u),  u >= 0
+// whose exponential the slope needs, too. The form is Abramowitz and Stegun's (7.1.26); its 5 terms are
+// off by 1.5e-7 of 1, which far from zero is 4% of erfc. These 7 were fitted (least largest error, weighted)
+// to stay within 1.2e-7 of 1 and within 2^-13 of erfc itself for all u: a GELU of z = -12 is as good as one of -1.
+// expf, erff and a division took k_dz from memory's time to the vector unit's. In fp32 erfc, not 1 + erf, which
+// has nothing left below z = -5.5.
 template <bool kFast>
 __device__ __forceinline__ float sigmoid(float z) {
     if constexpr (kFast) return __builtin_amdgcn_rcpf(1.f + fast_exp2(-kLog2e * z));
     return 1.f / (1.f + expf(-z));
 }
-// (1 + erf(z / sqrt 2)) / 2, and e^(-z^2 / 2)
+// erfc(-z / sqrt 2) / 2, and e^(-z^2 / 2)
 template <bool kFast>
 __device__ __forceinline__ float normal_cdf(float z, float &e) {
     if constexpr (kFast) {
         e = fast_exp2(-0.5f * kLog2e * z * z);
-        const float t = __builtin_amdgcn_rcpf(1.f + 0.3275911f * 0.70710678f * fabsf(z));
-        const float c = 0.5f * e * t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+        const float t = __builtin_amdgcn_rcpf(1.f + 0.505f * 0.70710678f * fabsf(z));
+        const float c = 0.5f * e * t * (0.284915149f + t * (0.283997625f + t * (0.264520407f + t * (0.0839478597f +
+                        t * (0.328074515f + t * (-0.329984188f + t * 0.0845286995f))))));
         return z < 0.f ? c : 1.f - c;
     }
     e = expf(-0.5f * z * z);
-    return 0.5f * (1.f + erff(z * 0.70710678118654752f));
+    return 0.5f * erfcf(z * -0.70710678118654752f);
 }
 template <bool kFast>
 __device__ __forceinline__ float act_of(float z, int act) {
