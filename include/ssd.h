@@ -422,7 +422,7 @@ ssd_status ssd_step_beam(const float *state_in, float *state_out, const int32_t 
  *   next_finished (batch, beams)   uint8     and whether it is finished; may be NULL
  *
  * Sums of exponentials are accumulated in 32 bits per 2048 logits and in 64
- * across them; scores are compared in 64 bits. beams at most 16, vocab at most
+ * across them, each term within 2^-20 of itself; scores are compared in 64 bits. beams at most 16, vocab at most
  * 2^28, batch below 2^21, and batch * beams pieces of 2048 logits (64 of longer
  * ones for a row of more than 131072) at most 2^26 - 4 (else
  * SSD_ERR_UNSUPPORTED). The workspace is 256-byte aligned; the query returns

@@ -17,9 +17,11 @@
 // 64 x 8 x 65536 fp32 logits: 134 MB in 32 us, 4.2 TB/s, and 10 us to pick; one
 // sequence of 4 beams and 50257 bf16 logits: 7 and 6 us, latency.
 //
-// The sums of exponentials are fp32 within a wavefront and 64-bit across a
-// row, and scores are compared in 64 bits, so that two candidates change places only
-// where they are closer than the sums' own error (~1e-8 relative).
+// The sums of exponentials are fp32 within 2048 logits and 64-bit across them, and scores
+// are compared in 64 bits, so that two candidates of different beams change places only where
+// they are closer than the exponentials' own error: each is off by under 2^-20 of itself (2^x
+// in fp32 of a rounded argument), their sum by less, since the errors differ in sign. (With a
+// lane's sum in fp32 over 2^28 equal logits, it was 3e-5.)
 #include <float.h>
 
 #include "ssd_common.h"
@@ -122,6 +124,17 @@ __device__ __forceinline__ double wave_sumd(double v) {
     return v;
 }
 
+// e^d, d <= 0, to 1e-11: 2^n e^r with |r| <= ln 2 / 2 and the series up to r^9. For the rises of a list's largest
+// logit, whose factors' errors multiply: fp32's would be up to 1e-4 after 2048 of them.
+__device__ __forceinline__ double exp_neg(double d) {
+    const double y = fmax(d * 1.4426950408889634, -1100.0), n = rint(y), r = (y - n) * 0.6931471805599453;
+    double p = 1.0 / 362880;
+    const double c[] = {1.0 / 40320, 1.0 / 5040, 1.0 / 720, 1.0 / 120, 1.0 / 24, 1.0 / 6, 0.5, 1.0, 1.0};
+#pragma unroll
+    for (int i = 0; i < 9; ++i) p = fma(p, r, c[i]);
+    return ldexp(p, (int)n);
+}
+
 // The sorted list in lanes 0 .. K-1 and the n <= 64 - K keys in buf, merged.
 __device__ __forceinline__ uint64_t merge_into(uint64_t best, const uint64_t *buf, int n, int K, int lane) {
     uint64_t v = lane < K ? best : 0;
@@ -129,8 +142,10 @@ __device__ __forceinline__ uint64_t merge_into(uint64_t best, const uint64_t *bu
     return sort_desc(v, lane);
 }
 
+// At most 168 registers, as many as leave a SIMD three wavefronts: the compiler hoists exp_neg's constants out of the
+// loop and takes 193 (64 x 8 x 65536 logits: 52.4 us in all).
 template <typename T>
-__global__ __launch_bounds__(256) void k_beam_top(BeamArgs a) {
+__global__ __launch_bounds__(256, 3) void k_beam_top(BeamArgs a) {
     constexpr int VE = 16 / (int)sizeof(T);    // logits per 16-byte load
     constexpr int NL = kPerLane / VE;          // loads per lane and tile
     __shared__ uint64_t bufs[4][64];
@@ -143,7 +158,8 @@ __global__ __launch_bounds__(256) void k_beam_top(BeamArgs a) {
     const int K = a.beams, V = a.V;
     const T *rp = reinterpret_cast<const T *>(a.logits) + row * V;
     uint64_t best = 0;
-    float M = -INFINITY, S = 0.f;
+    float M = -INFINITY;
+    double S = 0.0;
     for (int j = 0; j < a.tiles; ++j) {
         const int base = (li * a.tiles + j) * kTile;
         if (base >= V) break;
@@ -178,14 +194,13 @@ __global__ __launch_bounds__(256) void k_beam_top(BeamArgs a) {
         float lm = v[0];
 #pragma unroll
         for (int e = 1; e < kPerLane; ++e) lm = fmaxf(lm, v[e]);
-        // the row's sum, a share per lane, relative to the largest logit so far
+        // these logits' sum, relative to the largest so far
         const float Mn = fmaxf(M, wave_maxf(lm));
+        float s = 0.f;
         if (Mn > -INFINITY) {
-            float s = 0.f;
 #pragma unroll
             for (int e = 0; e < kPerLane; ++e) s += fast_exp2((v[e] - Mn) * kLog2e);
-            S = (M > -INFINITY ? S * fast_exp2((M - Mn) * kLog2e) : 0.f) + s;
-            M = Mn;
+            s = wave_sumf(s);
         }
         // lower bound on the K-th largest of the tile and of the list so far; -inf is no candidate
         uint32_t bound = (uint32_t)__builtin_amdgcn_readlane((int)sort_desc(ord32(lm), lane), K - 1);
@@ -227,10 +242,15 @@ __global__ __launch_bounds__(256) void k_beam_top(BeamArgs a) {
             best = merge_into(best, buf, K, K, lane);
             __builtin_amdgcn_wave_barrier();
         }
+        // the list's, in 64 bits (here, where the logits' registers are free)
+        if (Mn > M) {
+            if (M > -INFINITY) S *= exp_neg((double)M - (double)Mn);
+            M = Mn;
+        }
+        S += (double)s;
     }
-    S = wave_sumf(S);
     if (lane < K) a.keys[gl * K + lane] = best;
-    if (lane == 0) a.sums[gl] = make_float2(M, S);
+    if (lane == 0) a.sums[gl] = S;  // relative to the first key's logit
 }
 
 // The larger score (equal ones: the lower lane) of 16 lanes; 0xffff: none.
@@ -258,7 +278,7 @@ __global__ __launch_bounds__(1024) void k_beam_pick(BeamArgs a) {
     // everything the row needs, loaded at once (what k_beam_top left of a finished row is not used)
     const bool in = lane < a.lists;
     const int64_t list = row * a.lists + (in ? lane : 0);
-    const float2 ms = in ? a.sums[list] : make_float2(-INFINITY, 0.f);
+    const double sum = in ? a.sums[list] : 0.0;
     uint64_t key[kMost];
 #pragma unroll
     for (int r = 0; r < kMost; ++r) key[r] = (in && r < K) ? a.keys[list * K + r] : 0;
@@ -273,8 +293,9 @@ __global__ __launch_bounds__(1024) void k_beam_pick(BeamArgs a) {
         }
     } else {
         // log-sum-exp of the row
-        const float M = wave_maxf(ms.x);
-        const double S = wave_sumd(ms.x > -INFINITY ? (double)ms.y * exp((double)ms.x - (double)M) : 0.0);
+        const float top = key[0] ? from_ord32((uint32_t)(key[0] >> 32)) : -INFINITY;
+        const float M = wave_maxf(top);
+        const double S = wave_sumd(top > -INFINITY ? sum * exp((double)top - (double)M) : 0.0);
         const double lse = (double)M + log(S);
         const bool ok = alive && lse - lse == 0.0;  // a finite sum
         uint64_t best = 0;

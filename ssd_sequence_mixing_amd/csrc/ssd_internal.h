@@ -255,7 +255,7 @@ struct BeamArgs {
     int *parent, *token;
     uint8_t *out_finished;      // or null
     uint64_t *keys;             // workspace: (rows, lists, beams)
-    float2 *sums;               // workspace: (rows, lists) maximum and sum of exponentials
+    double *sums;               // workspace: (rows, lists) sums of exponentials, relative to the first key's logit
     int64_t rows;
     int beams, V, eos, lists, tiles;
 };

@@ -399,7 +399,7 @@ ssd_status ssd_beam_select(const void *logits, const float *scores, const uint8_
     a.token = token; a.out_finished = next_finished; a.rows = batch * beams; a.beams = (int)beams; a.V = (int)vocab;
     a.eos = (int)eos;
     a.keys = static_cast<uint64_t *>(workspace);
-    a.sums = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + align256(a.rows * a.lists * beams * 8));
+    a.sums = reinterpret_cast<double *>(static_cast<char *>(workspace) + align256(a.rows * a.lists * beams * 8));
     return ssd::launch_beam_select(a, batch, dtype, reinterpret_cast<hipStream_t>(stream));
 }
 
