@@ -458,8 +458,9 @@ ssd_status ssd_beam_select(const void *logits, const float *scores, const uint8_
  * ssd_rms_norm_mx writes y in 8 bits instead: q (rows, dim) holds e4m3 codes
  * (OCP, largest 448) and scale (rows, dim / 32) one power of two for each 32
  * of a row (e8m0: 2^(scale - 127)), the smallest not below 2^-127 that leaves
- * the 32 within 448; y = q * scale. Codes are rounded to nearest even from
- * the fp32 y. A block that holds an infinity or a NaN is NaN as a whole (scale
+ * the 32 within 448; y = q * scale. A code is the nearest one (ties to even)
+ * to h * weight / sqrt(...), kept to 48 bits between the fp32 h and mean square
+ * and the code. A block that holds an infinity or a NaN is NaN as a whole (scale
  * 255, codes 0x7f). dim / groups must be a multiple of 32.
  *
  * ssd_mx_quantize writes any x (rows, dim) so (weights, once; activations);
