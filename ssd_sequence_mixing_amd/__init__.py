@@ -568,8 +568,13 @@ def _device(t) -> int:
 
 
 def _stream_on(dev: int, stream) -> Optional[int]:
-    """_stream, the current device being known."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    """_stream, the current device being known. A stream of another device cannot run on this one's memory."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    other = getattr(stream, "device_index", dev)
+    if other != dev:
+        raise ValueError(f"stream of cuda:{other}, but the tensors are on cuda:{dev}")
+    return _stream(stream)
 
 
 def _in(dev: int, name: str, t, shape, dtype) -> Optional[int]:
