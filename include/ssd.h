@@ -448,7 +448,7 @@ ssd_status ssd_beam_select(const void *logits, const float *scores, const uint8_
  *   weight (dim)                   float32
  *   residual_out (rows, dim)       residual_dtype  output: h, rounded once; may be
  *                                  `residual` itself; NULL exactly where residual is
- *   y (rows, dim)                  dtype           output, from the h before its rounding
+ *   y (rows, dim)                  dtype           output, from the h before its rounding; may be x itself
  *   rstd (rows, groups)            float32         output for the backward pass: 1 / sqrt(...); or NULL
  *
  * residual_dtype is dtype or, with bf16, also SSD_F32 (a residual stream kept
@@ -511,6 +511,8 @@ ssd_status ssd_rms_norm_bwd(const void *dy, const void *h, const float *weight, 
  *   residual (rows, out) dtype, or NULL (zero)
  *   y (rows, out)        dtype  output, rounded once
  *   preact (rows, out)   dtype  output: z, for the backward pass; or NULL
+ * y may be `residual` itself; else an output that overlaps an input is refused
+ * (SSD_ERR_UNSUPPORTED).
  *
  * GELU keeps its accuracy where it is small beside z: relative to the value, within
  * (z^2 + 24) 2^-23 in fp32 and 2^-12 before the rounding in bf16. SiLU and GELU below
@@ -555,7 +557,8 @@ ssd_status ssd_linear_mx(const uint8_t *xq, const uint8_t *xscale, const uint8_t
  *   dbias (out)          float32         output, or NULL
  * dz is rounded to dtype as an operand of the two products (in bf16; dbias sums
  * it in fp32 before that). rows, in and out at most 2^20. The workspace query
- * is for all three gradients. With rows == 0, dw and dbias are zero.
+ * is for all three gradients. An output that overlaps an input that is read is
+ * refused (SSD_ERR_UNSUPPORTED). With rows == 0, dw and dbias are zero.
  */
 size_t ssd_linear_bwd_workspace_bytes(int64_t rows, int64_t in, int64_t out, int act, ssd_dtype dtype);
 

@@ -247,12 +247,6 @@ ssd_status step_impl(float *state, void *conv_state, const void *x, const float 
                      const int32_t *parent = nullptr, const float *state_in = nullptr,
                      const void *conv_in = nullptr, int64_t src_rows = 0);
 
-// Whether [a, a + na) and [b, b + nb) share a byte (a NULL one does not).
-bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
-    const uintptr_t pa = (uintptr_t)a, pb = (uintptr_t)b;
-    return a && b && na > 0 && nb > 0 && pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
-}
-
 }  // namespace
 
 extern "C" {
@@ -475,8 +469,8 @@ ssd_status step_impl(float *state, void *conv_state, const void *x, const float 
         // a parent's state may be read after another row's has been written
         const int64_t per = nheads * headdim, es = esize(dtype);
         if (src_rows > INT64_MAX / 4 / (per * dstate)) return SSD_ERR_UNSUPPORTED;
-        if (overlap(state_in, src_rows * per * dstate * 4, state, batch * per * dstate * 4) ||
-            overlap(conv_in, src_rows * per * 3 * es, conv_state, batch * per * 3 * es))
+        if (ssd::overlap(state_in, src_rows * per * dstate * 4, state, batch * per * dstate * 4) ||
+            ssd::overlap(conv_in, src_rows * per * 3 * es, conv_state, batch * per * 3 * es))
             return SSD_ERR_UNSUPPORTED;
     }
     ssd::StepArgs a;

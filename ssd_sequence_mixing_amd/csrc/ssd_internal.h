@@ -265,6 +265,12 @@ ssd_status launch_beam_select(const BeamArgs &a, int64_t batch, ssd_dtype dtype,
 // One recurrent decode step.
 ssd_status launch_step(const StepArgs &a, hipStream_t s);
 
+// Whether [a, a + na) and [b, b + nb) share a byte (a NULL one does not).
+inline bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+    const uintptr_t pa = (uintptr_t)a, pb = (uintptr_t)b;
+    return a && b && na > 0 && nb > 0 && pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
+}
+
 // Launches a kernel and returns the status of that launch itself (not an
 // error some earlier, unrelated runtime call may have left pending).
 // A launch has fewer than 2^32 threads along a dimension. HIP refuses some of those beyond and

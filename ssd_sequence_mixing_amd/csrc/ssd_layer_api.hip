@@ -98,6 +98,19 @@ ssd_status check_linear(int64_t rows, int64_t in, int64_t out, int act, int64_t 
 
 int64_t align16(int64_t v) { return (v + 15) & ~(int64_t)15; }
 
+// A product's operands are read while it writes: whether an output lies on one. Bytes of each behind its address.
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+template <size_t O, size_t I>
+bool any_overlap(const Span (&out)[O], const Span (&in)[I]) {
+    for (const Span &o : out)
+        for (const Span &i : in)
+            if (ssd::overlap(o.p, o.bytes, i.p, i.bytes)) return true;
+    return false;
+}
+
 // Workspace of a product: copies of the operands, in rows of multiples of 16 bytes, where
 // theirs begin at odd multiples of 2 (and there are more than a few), and the parts of a split sum.
 struct LinearLayout {
@@ -201,14 +214,17 @@ ssd_status ssd_linear(const void *x, const void *w, const float *bias, int act, 
     const LinearLayout l = linear_layout(rows, in, out, dtype);
     if ((st = check_workspace(l.total, workspace, workspace_bytes)) != SSD_OK) return st;
     if (rows == 0) return SSD_OK;
+    const int64_t es = esize(dtype), ny = rows * out * es;
+    if (any_overlap({{y, ny}, {preact, ny}}, {{x, rows * in * es}, {w, out * in * es}, {bias, out * 4}}) ||
+        (y != residual && ssd::overlap(y, ny, residual, ny)) || ssd::overlap(preact, ny, residual, ny))
+        return SSD_ERR_UNSUPPORTED;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
     ssd::LinearArgs a = {};
     a.x = x; a.w = w; a.bias = bias; a.res = residual; a.y = y; a.pre = preact; a.act = act;
     a.M = (int)rows; a.N = (int)out; a.ldx = a.ldw = l.ld; a.kbytes = (uint32_t)l.ld;
     if (l.xpad) {
-        const int es = (int)esize(dtype);
-        st = ssd::launch_pad(x, ws, rows, w, ws + l.xpad, out, in, l.ld / es, es, s);
+        st = ssd::launch_pad(x, ws, rows, w, ws + l.xpad, out, in, l.ld / es, (int)es, s);
         if (st != SSD_OK) return st;
         a.x = ws;
         a.w = ws + l.xpad;
@@ -235,6 +251,10 @@ ssd_status ssd_linear_mx(const uint8_t *xq, const uint8_t *xscale, const uint8_t
     const LinearLayout l = linear_mx_layout(rows, in, out);
     if ((st = check_workspace(l.total, workspace, workspace_bytes)) != SSD_OK) return st;
     if (rows == 0) return SSD_OK;
+    const int64_t ny = rows * out * 2;
+    if (any_overlap({{y, ny}}, {{xq, rows * in}, {xscale, rows * in / 32}, {wq, out * in}, {wscale, out * in / 32}, {bias, out * 4}}) ||
+        (y != residual && ssd::overlap(y, ny, residual, ny)))
+        return SSD_ERR_UNSUPPORTED;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
     ssd::LinearArgs a = {};
@@ -273,6 +293,10 @@ ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, int act,
         if ((st = clear(dw, out * in * es, s)) != SSD_OK) return st;
         return clear(dbias, out * 4, s);
     }
+    const int64_t ny = rows * out * es, nx = rows * in * es, nw = out * in * es;
+    if (any_overlap({{dx, nx}, {dw, nw}, {dbias, out * 4}},
+                    {{dy, ny}, {dw ? x : nullptr, nx}, {dx ? w : nullptr, nw}, {act != SSD_ACT_NONE ? preact : nullptr, ny}}))
+        return SSD_ERR_UNSUPPORTED;
     char *ws = static_cast<char *>(workspace);
     char *dz = ws, *dzt = dz + l.dz, *wc = dzt + l.dzt, *xc = wc + l.w;
     float *db = reinterpret_cast<float *>(xc + l.x), *part = reinterpret_cast<float *>(xc + l.x + l.db);
