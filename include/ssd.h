@@ -556,7 +556,8 @@ ssd_status ssd_linear_mx(const uint8_t *xq, const uint8_t *xscale, const uint8_t
  *   dx (rows, in), dw (out, in)  dtype   outputs, each NULL to leave it out
  *   dbias (out)          float32         output, or NULL
  * dz is rounded to dtype as an operand of the two products (in bf16; dbias sums
- * it in fp32 before that). rows, in and out at most 2^20. The workspace query
+ * it in fp32 before that). fp32 operands are transposed in the workspace first,
+ * which with few rows is most of the call. rows, in and out at most 2^20. The workspace query
  * is for all three gradients. An output that overlaps an input that is read is
  * refused (SSD_ERR_UNSUPPORTED). With rows == 0, dw and dbias are zero.
  */

@@ -14,7 +14,7 @@
 // of 2048 values about 18 reach it at 16 beams. k_beam_pick (one work-group
 // per sequence, a wavefront per beam) merges a row's lists the same way,
 // forms the scores and merges the beams.
-// 64 x 8 x 65536 fp32 logits: 134 MB in 32 us, 4.2 TB/s, and 10 us to pick; one
+// 64 x 8 x 65536 fp32 logits: 134 MB in 30 us, 4.5 TB/s, and 10 us to pick; one
 // sequence of 4 beams and 50257 bf16 logits: 7 and 6 us, latency.
 //
 // The sums of exponentials are fp32 within 2048 logits and 64-bit across them, and scores

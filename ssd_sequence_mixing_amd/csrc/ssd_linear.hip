@@ -24,18 +24,19 @@
 //
 // fp32 operands are split, as they are read from LDS, into three bf16 each, and
 // six of the nine products formed: 1.3 times the rate of the fp32 matrix cores
-// (8192 x 4096 x 2048: 680 us, 202 TFLOP/s; the library's fp32 product 154).
+// (8192 x 4096 x 2048: 660 us, 208 TFLOP/s; the library's fp32 product 151).
 //
 // The product is formed as w x^T, so that a lane holds 4 consecutive n of one
 // row; the epilogue turns 16 x (columns of a wavefront) at a time through LDS
 // into whole lines of rows.
 //
-// Bound: the matrix cores; in a step of the 256 x 256 tile they are busy 82% of
-// the cycles. On a warm GPU (bf16, microseconds; the library's plain product beside
-// it): 8192 x 4096 x 2048 with a residual 137 (105 without one), 8192 x 2048 x 8512
-// 269 (252), 16384 x 768 x 3352 115 (135), 64 x 2048 x 8512 13.3 (19); 8 bits
-// 8192 x 2048 x 8512 176. The rest is the start and the epilogue of each round of
-// tiles (10 to 14 us of a round, where nothing is multiplied). Measured and left: 4
+// Bound: the matrix cores and the waits for their operands. Microseconds on a warm GPU, bf16, operands that
+// change from call to call, the library's plain product beside it: 8192 x 4096 x 2048 113 (90), with a residual
+// 135; 8192 x 2048 x 8512 263 (250); 16384 x 768 x 3352 99 (133); 64 x 2048 x 8512 13.5 (19.5); 8192 x 8192 x 8192
+// 814 (697); 8 bits 8192 x 2048 x 8512 149 to 166. The matrix cores are busy 52% of the cycles of the first (42% with
+// the residual, 37% in 8 bits), and 70% of those that another 4096 along k add to it (87% where the
+// operands stay in the last-level cache). The rest of a round of tiles is its start and its epilogue, where nothing is
+// multiplied, 10 to 14 us, and the residual's way from memory. Measured and left: 4
 // wavefronts a tile, 32 x 32 matrix instructions, a wave priority around the
 // products, loads two steps ahead (all within 2% or slower).
 //
@@ -827,8 +828,9 @@ __global__ __launch_bounds__(256) void k_pad(const U *in1, U *out1, int64_t R1, 
 }
 
 // out (C x ldo) = in (R x C) transposed, zeros behind column R. 64 x 64 a work-group.
-// fp32's gradients take it: its products are bound by the matrix cores (16 times
-// slower than bf16), beside which these copies are small.
+// fp32's gradients take it. With many rows its products are bound by the matrix cores, beside which these
+// copies are small; with few, they are most of the call (3 x 4800 x 11144: w's alone 107 us of 268, where a library
+// product takes 135 for both gradients).
 template <typename T>
 __global__ __launch_bounds__(256) void k_transpose(const T *in, T *out, int R, int C, int ldo) {
     __shared__ T sm[64][64 + 4 / sizeof(T)];
@@ -841,7 +843,9 @@ __global__ __launch_bounds__(256) void k_transpose(const T *in, T *out, int R, i
 }
 
 // dz = dy act'(z), rows of ldz values with zeros behind column N, and the
-// shares of db of each R rows (fp32, before dz is rounded). A work-group
+// shares of db of each R rows (fp32, before dz is rounded). In bf16 dz is rounded to it, as an operand of the
+// matrix cores' products has to be (two parts of it would double both products): the gradients are then off by
+// 2.3e-3 of their size on ordinary data, where rounding them alone makes 1.7e-3. A work-group
 // takes R rows of 512 columns, a lane 8 columns (V: N is a multiple of 8 and
 // they are one load) of every Y-th row. Bound: HBM, two reads and one
 // write (16384 x 3352 in bf16, SiLU: 330 MB in 67 us, 4.9 TB/s, what a copy reaches).
