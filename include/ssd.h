@@ -422,11 +422,12 @@ ssd_status ssd_step_beam(const float *state_in, float *state_out, const int32_t 
  *   next_finished (batch, beams)   uint8     and whether it is finished; may be NULL
  *
  * Sums of exponentials are accumulated in 32 bits per 2048 logits and in 64
- * across them, each term within 2^-20 of itself; scores are compared in 64 bits. beams at most 16, vocab at most
- * 2^28, batch below 2^21, and batch * beams pieces of 2048 logits (64 of longer
- * ones for a row of more than 131072) at most 2^26 - 4 (else
- * SSD_ERR_UNSUPPORTED). The workspace is 256-byte aligned; the query returns
- * (size_t)-1 for a shape that is not supported. With batch == 0 nothing is read.
+ * across them, a term e^-d below the largest within (d + 1) 2^-22 of itself;
+ * scores are compared in 64 bits. beams at most 16, vocab at most 2^28, batch
+ * below 2^21, and batch * beams pieces of 2048 logits (64 of longer ones for a
+ * row of more than 131072) at most 2^26 - 4 (else SSD_ERR_UNSUPPORTED). The
+ * workspace is 256-byte aligned; the query returns (size_t)-1 for a shape that is
+ * not supported. With batch == 0 nothing is read.
  */
 size_t ssd_beam_select_workspace_bytes(int64_t batch, int64_t beams, int64_t vocab);
 

@@ -19,9 +19,9 @@
 //
 // The sums of exponentials are fp32 within 2048 logits and 64-bit across them, and scores
 // are compared in 64 bits, so that two candidates of different beams change places only where
-// they are closer than the exponentials' own error: each is off by under 2^-20 of itself (2^x
-// in fp32 of a rounded argument), their sum by less, since the errors differ in sign. (With a
-// lane's sum in fp32 over 2^28 equal logits, it was 3e-5.)
+// they are closer than the exponentials' own error: a term e^-d is off by under (d + 1) 2^-22 of
+// itself (2^x in fp32 of a difference and a product rounded to it), the sum by less, since the
+// errors differ in sign. (With a lane's sum in fp32 over 2^28 equal logits, it was 3e-5.)
 #include <float.h>
 
 #include "ssd_common.h"

@@ -449,7 +449,7 @@ template <typename TX, typename TR, bool V, bool MX>
 static ssd_status run_norm(const NormArgs &all, hipStream_t s) {
     const NormPlan p = norm_plan(all.rows, all.Dg);
     const int rpb = p.W > 4 ? 1 : kNormThreads / (64 * p.W), threads = p.W > 4 ? 64 * p.W : kNormThreads;
-    // rows of one launch, every group of a row among them: at least 64 times the most groups
+    // rows of one launch, every group of a row among them (65535 at most)
     const int64_t most = kMostThreads / threads * rpb / all.groups * all.groups;
     auto go = [&](auto k) {
         for (int64_t r0 = 0; r0 < all.rows; r0 += most) {
