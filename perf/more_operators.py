@@ -23,8 +23,8 @@ own = False
 SCAN_VALUES = 48 << 20   # the largest batch x tokens x channels of a drawn scan
 TABLE_VALUES = 1 << 27   # the largest vocabulary x channels of a drawn table
 LOGITS = 1 << 25         # the largest rows x vocabulary of drawn logits
-LINEAR_FLOPS = 1.37e11   # the largest matrix work of a drawn product, and the most values of its output
-OUTPUTS = 1 << 25
+LINEAR_FLOPS = 1.37e11   # the largest matrix work of a drawn product
+LINEAR_VALUES = 9 << 23  # the most values that it reads and writes by rows
 CHUNK = 128              # tokens between the states that a scan keeps for its gradients
 
 
@@ -106,7 +106,7 @@ def draw(rng):
         return {"kind": kind, "rows": rows, "vocab": vocab, "history": _log(rng, 1, 8192), "dtype": dtype, "bias": bias,
                 "mask": rng.choice(["none", "one", "rows"])}
     k, n = 16 * _log(rng, 4, 512), _eights(rng, _log(rng, 64, 16384))
-    rows = max(1, min(_log(rng, 1, 16384), int(LINEAR_FLOPS / (2.0 * k * n)), OUTPUTS // n))
+    rows = max(1, min(_log(rng, 1, 16384), int(LINEAR_FLOPS / (2.0 * k * n)), LINEAR_VALUES // (k + 2 * n)))
     return {"kind": kind, "rows": rows, "in": k, "out": n, "dtype": dtype, "act": rng.choice(["none", "silu", "gelu"]),
             "bias": rng.random() < 0.5, "residual": rng.random() < 0.5}
 
