@@ -9,7 +9,7 @@ Kinds of cases:
   embed      rows of a table, scaled                                      ssd_embedding
   embed_bwd  the table's gradient                                         ssd_embedding_bwd
   logits     penalties for repeated tokens, a bias, a grammar's mask      ssd_logits_process
-  linear_i8  act(x W^T + bias) + residual from 8-bit integers             ssd_i8_quantize, ssd_linear_i8
+  linear_int  act(x W^T + bias) + residual from 8-bit integers             ssd_int_quantize, ssd_linear_int
 
 Every kind has a plain form in elementary torch operations (run with own = False), the framework's call
 (own = True), and a definition in 64 bits (exact).
@@ -61,10 +61,10 @@ def listed():
         {"name": "logits_batch", "kind": "logits", "rows": 512, "vocab": 65536, "history": 2048, "dtype": "f32",
          "bias": "one", "mask": "rows"},
         # decoding 8 sequences: the 1.3B layer's input projection, bound by its weights
-        {"name": "linear_i8_decode", "kind": "linear_i8", "rows": 8, "in": 2048, "out": 8512, "dtype": "bf16", "act": "none",
+        {"name": "linear_int_decode", "kind": "linear_int", "rows": 8, "in": 2048, "out": 8512, "dtype": "bf16", "act": "none",
          "bias": False, "residual": False},
         # a prompt batch of the 1.3B layer's output projection, added to the residual stream
-        {"name": "linear_i8_prompt", "kind": "linear_i8", "rows": 8192, "in": 4096, "out": 2048, "dtype": "bf16",
+        {"name": "linear_int_prompt", "kind": "linear_int", "rows": 8192, "in": 4096, "out": 2048, "dtype": "bf16",
          "act": "none", "bias": True, "residual": True},
     ]
 
@@ -79,7 +79,7 @@ def _eights(rng, n, odd=0.4):
 
 def draw(rng):
     kind = rng.choice(["scan", "scan", "scan_bwd", "scan_bwd", "step", "embed", "embed_bwd", "embed_bwd", "logits", "logits",
-                       "linear_i8", "linear_i8"])
+                       "linear_int", "linear_int"])
     dtype = rng.choice(["bf16", "bf16", "f32"])
     if kind in ("scan", "scan_bwd"):
         most = SCAN_VALUES // (2 if kind == "scan_bwd" else 1) // (2 if dtype == "f32" else 1)
@@ -225,8 +225,8 @@ def _framework(s):
         return {"y": ssd.ssd_logits_process(s["l"], tokens=s["tokens"], lengths=s["lengths"], prompt=s["prompt"],
                                             repetition=s["repetition"], presence=s["presence"], frequency=s["frequency"],
                                             bias=s["b"], mask=s["m"])}
-    xq, xscale = ssd.ssd_i8_quantize(s["x"])
-    return {"y": ssd.ssd_linear_i8(xq, xscale, s["wq"], s["wscale"], bias=s["b"], act=s["act"], residual=s["r"],
+    xq, xscale = ssd.ssd_int_quantize(s["x"])
+    return {"y": ssd.ssd_linear_int(xq, xscale, s["wq"], s["wscale"], bias=s["b"], act=s["act"], residual=s["r"],
                                    dtype=s["x"].dtype)}
 
 
