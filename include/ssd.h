@@ -568,6 +568,140 @@ ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, int act,
                           void *dw, float *dbias, int64_t rows, int64_t in, int64_t out, ssd_dtype dtype,
                           void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Gated linear recurrence: a mixer with one state per channel. For every
+ * sequence b and channel d, from a gate f_t and an input x_t,
+ *
+ *   h_t = a_t h_{t-1} + c_t v_t;   v_t = sigmoid(i_t) x_t;   y_t = h_t
+ *
+ *   SSD_DECAY_LOG      a = e^f, c = 1 (f <= 0: log-decays)
+ *   SSD_DECAY_SIGMOID  a = sigmoid(f), c = 1 - a
+ *   SSD_DECAY_RATE     a = e^(rate[d] sigmoid(f)), c = sqrt(1 - a^2) (rate <= 0; c = 0 where 1 - a^2 < 2^-100)
+ *
+ *   x, f, in_gate (batch, seqlen, dim)  dtype    in_gate is i, or NULL (v = x). ldx, ldf, ldi: values
+ *                   from one token to the next, at least dim, tokens of one sequence behind the last
+ *                   one's (the parts of one projection's output need no copies); aligned to their type only
+ *   rate (dim)      float32, with SSD_DECAY_RATE (else NULL)
+ *   reset (batch, seqlen)  uint8 or NULL: where it is not 0, h_{t-1} is left out (a document
+ *                   begins; several laid end to end)
+ *   initial_state (batch, dim)  float32 or NULL (zero)
+ *   y (batch, seqlen, dim)  dtype    output, contiguous
+ *   final_state (batch, dim)  float32, or NULL: h of the last token (initial_state, or zero, with seqlen == 0)
+ *   states (batch, ceil(seqlen / SSD_GATED_CHUNK), dim)  float32, or NULL: h before
+ *                   the first token of each SSD_GATED_CHUNK, for the backward pass
+ *
+ * Everything in fp32, the gates to a few 2^-24 of themselves. dim at most 2^20, seqlen below 2^31, batch * dim below 2^31. An
+ * output that overlaps an input is refused (SSD_ERR_UNSUPPORTED). The
+ * workspace is 256-byte aligned; the query returns (size_t)-1 for a shape that is not supported.
+ */
+typedef enum { SSD_DECAY_LOG = 0, SSD_DECAY_SIGMOID = 1, SSD_DECAY_RATE = 2 } ssd_decay;
+#define SSD_GATED_CHUNK 128
+
+size_t ssd_gated_scan_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, ssd_dtype dtype);
+
+ssd_status ssd_gated_scan_fwd(const void *x, int64_t ldx, const void *f, int64_t ldf, const void *in_gate, int64_t ldi,
+                              int decay, const float *rate, const uint8_t *reset, const float *initial_state, void *y,
+                              float *final_state, float *states, int64_t batch, int64_t seqlen, int64_t dim,
+                              ssd_dtype dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of <dy, y> + <d_final_state, final_state>. With g_t = dy_t + a_{t+1} g_{t+1} (without the
+ * second term where token t+1 is reset; d_final_state behind the last token):
+ *   dx = g c sigmoid(i);   d_in_gate = g c x sigmoid(i) (1 - sigmoid(i))
+ *   d log a = g (a h_{t-1} + v dc/d log a)  (h_{t-1} = 0 where reset; dc/d log a = 0, -a, -a^2 / c; 0 where c is 0)
+ *   df = d log a * (1, 1 - sigmoid(f), rate sigmoid(f) (1 - sigmoid(f)));   drate = sum of d log a * sigmoid(f)
+ *   d_initial_state = a_0 g_0 (0 where token 0 is reset)
+ *
+ *   x ... reset: as the forward had them; states: as it wrote them (with initial_state in the first)
+ *   dy (batch, seqlen, dim) dtype;  d_final_state (batch, dim) float32 or NULL (zero)
+ *   dx, df, d_in_gate (batch, seqlen, dim) dtype  outputs, contiguous; d_in_gate exactly where in_gate is
+ *   drate (dim) float32  output with SSD_DECAY_RATE (else NULL), summed in a fixed order
+ *   d_initial_state (batch, dim) float32  output, or NULL
+ * With batch or seqlen 0, drate = 0 and d_initial_state = d_final_state (or zero).
+ */
+size_t ssd_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int decay, ssd_dtype dtype);
+
+ssd_status ssd_gated_scan_bwd(const void *dy, const void *x, int64_t ldx, const void *f, int64_t ldf, const void *in_gate,
+                              int64_t ldi, int decay, const float *rate, const uint8_t *reset, const float *states,
+                              const float *d_final_state, void *dx, void *df, void *d_in_gate, float *drate,
+                              float *d_initial_state, int64_t batch, int64_t seqlen, int64_t dim, ssd_dtype dtype,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of the recurrence: row b of state_out (rows, dim) float32 from row parent[b] of state_in
+ * (src_rows, dim), or from row b where parent is NULL (src_rows then at least rows, and state_out may be
+ * state_in; any other overlap is refused). A parent outside [0, src_rows) starts from zero. x, f, in_gate
+ * (rows, dim) as above, ldx, ldf, ldi from one row to the next; y (rows, dim).
+ */
+ssd_status ssd_gated_step(const float *state_in, float *state_out, const int32_t *parent, int64_t src_rows, const void *x,
+                          int64_t ldx, const void *f, int64_t ldf, const void *in_gate, int64_t ldi, int decay,
+                          const float *rate, void *y, int64_t rows, int64_t dim, ssd_dtype dtype, void *stream);
+
+/*
+ * Embedding: y[r, :] = scale table[tokens[r], :], rounded once; zeros for a token outside [0, vocab) (padding).
+ *   tokens (rows) int32;  table (vocab, dim) dtype;  y (rows, dim) y_dtype (either type)
+ * Its gradient: dtable[v, :] = scale * sum of dy[r, :] over the rows with token v, in fp32, by ascending
+ * r in a fixed order; rows of the table without a token are zero. accumulate: added to what
+ * dtable holds instead (a tied output projection's gradient), rows without a token left as they are.
+ *   dy (rows, dim) dy_dtype;  dtable (vocab, dim) dtype  output
+ * vocab and dim at most 2^20, rows below 2^31; the workspace is 256-byte aligned.
+ */
+ssd_status ssd_embedding(const int32_t *tokens, const void *table, float scale, void *y, int64_t rows, int64_t vocab,
+                         int64_t dim, ssd_dtype dtype, ssd_dtype y_dtype, void *stream);
+
+size_t ssd_embedding_bwd_workspace_bytes(int64_t rows, int64_t vocab, int64_t dim);
+
+ssd_status ssd_embedding_bwd(const void *dy, const int32_t *tokens, float scale, void *dtable, int accumulate, int64_t rows,
+                             int64_t vocab, int64_t dim, ssd_dtype dy_dtype, ssd_dtype dtype, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/*
+ * Logits before the choice (ssd_beam_select). With n(v) how often token v stands in
+ * a row's history and g(v) how often behind its prompt, in this order, in fp32, rounded once:
+ *
+ *   l <- l / repetition where l > 0, else l * repetition       for n(v) > 0
+ *   l <- l - (frequency g(v) + presence)                       for g(v) > 0
+ *   l <- l + bias(v)
+ *   l <- -inf where bit v % 32 of the row's mask word v / 32 is 0
+ *
+ *   logits (rows, vocab)  dtype;  out (rows, vocab)  dtype, may be logits itself; what none of
+ *                         these touches keeps its bits
+ *   tokens (rows, capacity)  int32: the histories, or NULL (then the next five are NULL too); entries outside [0, vocab)
+ *                         count for nothing
+ *   lengths, prompt (rows)  int32 or NULL: how much of a row's history there is (NULL: capacity; clamped to
+ *                         [0, capacity]), and how much of that is its prompt (NULL: 0)
+ *   repetition, presence, frequency (rows)  float32 or NULL (1, 0, 0); repetition > 0
+ *   bias (bias_rows, vocab)  float32 or NULL;  mask (mask_rows, ceil(vocab / 32))  int32 or NULL;
+ *                         bias_rows, mask_rows: 1 (for all rows) or rows
+ * vocab at most 2^28, capacity below 2^31, and rows * ceil((vocab + 7) / 4096) at most 2^24 - 1.
+ */
+ssd_status ssd_logits_process(const void *logits, void *out, const int32_t *tokens, int64_t capacity, const int32_t *lengths,
+                              const int32_t *prompt, const float *repetition, const float *presence, const float *frequency,
+                              const float *bias, int64_t bias_rows, const int32_t *mask, int64_t mask_rows, int64_t rows,
+                              int64_t vocab, ssd_dtype dtype, void *stream);
+
+/*
+ * ssd_linear from 8-bit integers with one scale for each token and each output channel:
+ *
+ *   z[m, n] = xscale[m] wscale[n] sum_k xq[m, k] wq[n, k] + bias[n];   y = act(z) + residual
+ *
+ *   xq (rows, in), wq (out, in)  int8;  xscale (rows), wscale (out)  float32
+ *   residual, y (rows, out)  dtype (bf16 or fp32);  others as ssd_linear
+ * The sum over k is exact (32-bit integers) and rounded to fp32 once (split sums: once for each of up to 32 parts). in a
+ * multiple of 16, at most 131072; rows at most 2^24, out at most 2^20.
+ *
+ * ssd_int_quantize writes operands so (weights once, activations): scale = max |x| / 127
+ * of the row, rounded to fp32, q the integer nearest to x / scale (ties to even). A row of zeros has scale 0;
+ * a row with an infinity or a NaN has scale NaN and codes 0. x (rows, dim) dtype, any dim up to 2^20.
+ */
+ssd_status ssd_int_quantize(const void *x, int8_t *q, float *scale, int64_t rows, int64_t dim, ssd_dtype dtype, void *stream);
+
+size_t ssd_linear_int_workspace_bytes(int64_t rows, int64_t in, int64_t out);
+
+ssd_status ssd_linear_int(const int8_t *xq, const float *xscale, const int8_t *wq, const float *wscale, const float *bias,
+                         int act, const void *residual, void *y, int64_t rows, int64_t in, int64_t out, ssd_dtype dtype,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

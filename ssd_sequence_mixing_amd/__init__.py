@@ -22,7 +22,10 @@ __all__ = [
     "ssd_step_beam", "ssd_beam_select_workspace_bytes", "ssd_beam_select", "ssd_rms_norm", "ssd_rms_norm_mx",
     "ssd_mx_quantize", "ssd_rms_norm_bwd_workspace_bytes", "ssd_rms_norm_bwd", "ssd_linear_workspace_bytes",
     "ssd_linear", "ssd_linear_mx_workspace_bytes", "ssd_linear_mx", "ssd_linear_bwd_workspace_bytes",
-    "ssd_linear_bwd", "ACTS",
+    "ssd_linear_bwd", "ACTS", "DECAYS", "GATED_CHUNK", "ssd_gated_scan_fwd_workspace_bytes", "ssd_gated_scan_fwd",
+    "ssd_gated_scan_bwd_workspace_bytes", "ssd_gated_scan_bwd", "ssd_gated_step", "ssd_embedding",
+    "ssd_embedding_bwd_workspace_bytes", "ssd_embedding_bwd", "ssd_logits_process", "ssd_int_quantize",
+    "ssd_linear_int_workspace_bytes", "ssd_linear_int",
 ]
 
 SSD_F32 = 0
@@ -42,13 +45,21 @@ EXPORTS = ("ssd_status_string", "ssd_chunk_scan_fwd_workspace_bytes", "ssd_chunk
            "ssd_step_beam", "ssd_beam_select_workspace_bytes", "ssd_beam_select", "ssd_rms_norm",
            "ssd_rms_norm_mx", "ssd_mx_quantize", "ssd_rms_norm_bwd_workspace_bytes", "ssd_rms_norm_bwd",
            "ssd_linear_workspace_bytes", "ssd_linear", "ssd_linear_mx_workspace_bytes", "ssd_linear_mx",
-           "ssd_linear_bwd_workspace_bytes", "ssd_linear_bwd")
+           "ssd_linear_bwd_workspace_bytes", "ssd_linear_bwd", "ssd_gated_scan_fwd_workspace_bytes",
+           "ssd_gated_scan_fwd", "ssd_gated_scan_bwd_workspace_bytes", "ssd_gated_scan_bwd", "ssd_gated_step",
+           "ssd_embedding", "ssd_embedding_bwd_workspace_bytes", "ssd_embedding_bwd", "ssd_logits_process",
+           "ssd_int_quantize", "ssd_linear_int_workspace_bytes", "ssd_linear_int")
 
 # SSD_NOALLOC_SCRATCH_BYTES: the static workspace of ssd_chunk_scan_fwd_noalloc.
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 # ssd_act: the activations of ssd_linear's epilogue.
 ACTS = {"none": 0, "silu": 1, "gelu": 2}
+
+# ssd_decay: how ssd_gated_scan_fwd makes a token's decay from its gate; SSD_GATED_CHUNK: tokens
+# between the states that it keeps for its gradients.
+DECAYS = {"log": 0, "sigmoid": 1, "rate": 2}
+GATED_CHUNK = 128
 
 _V = ctypes.c_void_p
 _I = ctypes.c_int64
@@ -157,6 +168,34 @@ def load():
     ):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
+    lib.ssd_gated_scan_fwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.ssd_gated_scan_fwd_workspace_bytes.argtypes = [_I] * 3 + [ctypes.c_int]
+    lib.ssd_gated_scan_fwd.restype = ctypes.c_int
+    lib.ssd_gated_scan_fwd.argtypes = ([_V, _I] * 3 + [ctypes.c_int] + [_V] * 6 + [_I] * 3
+                                       + [ctypes.c_int, _V, ctypes.c_size_t, _V])
+    lib.ssd_gated_scan_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.ssd_gated_scan_bwd_workspace_bytes.argtypes = [_I] * 3 + [ctypes.c_int] * 2
+    lib.ssd_gated_scan_bwd.restype = ctypes.c_int
+    lib.ssd_gated_scan_bwd.argtypes = ([_V] + [_V, _I] * 3 + [ctypes.c_int] + [_V] * 9 + [_I] * 3
+                                       + [ctypes.c_int, _V, ctypes.c_size_t, _V])
+    lib.ssd_gated_step.restype = ctypes.c_int
+    lib.ssd_gated_step.argtypes = [_V] * 3 + [_I] + [_V, _I] * 3 + [ctypes.c_int] + [_V] * 2 + [_I] * 2 + [ctypes.c_int, _V]
+    lib.ssd_embedding.restype = ctypes.c_int
+    lib.ssd_embedding.argtypes = [_V, _V, ctypes.c_float, _V] + [_I] * 3 + [ctypes.c_int] * 2 + [_V]
+    lib.ssd_embedding_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.ssd_embedding_bwd_workspace_bytes.argtypes = [_I] * 3
+    lib.ssd_embedding_bwd.restype = ctypes.c_int
+    lib.ssd_embedding_bwd.argtypes = ([_V, _V, ctypes.c_float, _V, ctypes.c_int] + [_I] * 3 + [ctypes.c_int] * 2
+                                      + [_V, ctypes.c_size_t, _V])
+    lib.ssd_logits_process.restype = ctypes.c_int
+    lib.ssd_logits_process.argtypes = [_V] * 3 + [_I] + [_V] * 6 + [_I, _V] + [_I] * 3 + [ctypes.c_int, _V]
+    lib.ssd_int_quantize.restype = ctypes.c_int
+    lib.ssd_int_quantize.argtypes = [_V] * 3 + [_I] * 2 + [ctypes.c_int, _V]
+    lib.ssd_linear_int_workspace_bytes.restype = ctypes.c_size_t
+    lib.ssd_linear_int_workspace_bytes.argtypes = [_I] * 3
+    lib.ssd_linear_int.restype = ctypes.c_int
+    lib.ssd_linear_int.argtypes = ([_V] * 5 + [ctypes.c_int] + [_V] * 2 + [_I] * 3
+                                  + [ctypes.c_int, _V, ctypes.c_size_t, _V])
     _lib = lib
     return lib
 
@@ -903,6 +942,297 @@ def ssd_linear_bwd(dy, x, w, *, act: str = "none", preact=None, want_x: bool = T
     if rc != 0:
         raise SSDError(rc, "ssd_linear_bwd")
     return dx, dw, db
+
+
+def _decay_code(decay: str, rate) -> int:
+    if decay not in DECAYS:
+        raise ValueError(f"decay {decay!r}: one of {sorted(DECAYS)}")
+    if (decay == "rate") != (rate is not None):
+        raise ValueError("rate goes with decay='rate', and only with it")
+    return DECAYS[decay]
+
+
+def _tokens(dev: int, name: str, t, shape, dtype):
+    """(address, values from one token to the next) of a recurrence's input: tokens may lie apart, as the parts of
+    one projection's output do, but each is one run, and the rows of the leading dimensions follow each other."""
+    if t is None:
+        return None, 0
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _chk(name, t, shape, dtype)
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    dim = shape[-1]
+    if t.is_contiguous():
+        return t.data_ptr(), dim
+    ld = next((t.stride(k) for k in range(t.dim() - 2, -1, -1) if shape[k] > 1), dim)
+    step, ok = ld, ld >= dim and (dim == 1 or t.stride(-1) == 1)
+    for k in range(t.dim() - 2, -1, -1):
+        ok = ok and (shape[k] == 1 or t.stride(k) == step)
+        step *= shape[k]
+    if not ok:
+        raise ValueError(f"{name}: each token must be contiguous, and the tokens evenly apart (strides {t.stride()})")
+    return t.data_ptr(), ld
+
+
+def _reset(dev: int, reset, shape):
+    if reset is None:
+        return None
+    if reset.dtype not in (torch.bool, torch.uint8):
+        raise ValueError(f"reset: dtype {reset.dtype}, expected bool or uint8")
+    return _in(dev, "reset", reset, shape, reset.dtype)
+
+
+def ssd_gated_scan_fwd_workspace_bytes(batch, seqlen, dim, dtype: int) -> int:
+    return _sized("ssd_gated_scan_fwd_workspace_bytes", load().ssd_gated_scan_fwd_workspace_bytes(batch, seqlen, dim, dtype))
+
+
+def ssd_gated_scan_fwd(x, f, *, decay: str, rate=None, in_gate=None, reset=None, initial_state=None, y=None,
+                       want_states: bool = False, workspace=None, stream=None):
+    """Gated linear recurrence h_t = a_t h_(t-1) + c_t sigmoid(in_gate_t) x_t over x, f, in_gate (batch, seqlen, dim) bf16
+    or fp32 (in_gate None: x itself), whose tokens may lie apart (views of one projection's output). decay: "log" (a = e^f,
+    c = 1), "sigmoid" (a = sigmoid(f), c = 1 - a) or "rate" (a = e^(rate sigmoid(f)), c = sqrt(1 - a^2); rate (dim)
+    fp32, <= 0). reset (batch, seqlen) bool or uint8: the state is left out before that token. initial_state (batch, dim)
+    fp32 or None. Returns (y, final_state, states): y in x's type, final_state (batch, dim) fp32, and states (batch,
+    ceil(seqlen / GATED_CHUNK), dim) fp32 for ssd_gated_scan_bwd, or None."""
+    lib = load()
+    if x.dim() != 3 or x.shape[-1] == 0:
+        raise ValueError("x must be (batch, seqlen, dim)")
+    bsz, T, D = shape = x.shape
+    st, f32 = x.dtype, torch.float32
+    code, dcode = _dtype_code(x), _decay_code(decay, rate)
+    dev = _device(x)
+    (p_x, ldx), (p_f, ldf) = _tokens(dev, "x", x, shape, st), _tokens(dev, "f", f, shape, st)
+    p_i, ldi = _tokens(dev, "in_gate", in_gate, shape, st)
+    p_r, p_0 = _in(dev, "rate", rate, (D,), f32), _in(dev, "initial_state", initial_state, (bsz, D), f32)
+    p_z = _reset(dev, reset, (bsz, T))
+    p_y = _in(dev, "y", y, shape, st)
+    if y is None:
+        y = _new(shape, st, x, stream)
+        p_y = y.data_ptr()
+    final = _new((bsz, D), f32, x, stream)
+    states = _new((bsz, -(-T // GATED_CHUNK), D), f32, x, stream) if want_states else None
+    need = 0 if workspace is not None else ssd_gated_scan_fwd_workspace_bytes(bsz, T, D, code)
+    workspace, p_ws, nbytes = _scratch(workspace, need, x, dev, stream)
+    rc = lib.ssd_gated_scan_fwd(p_x, ldx, p_f, ldf, p_i, ldi, dcode, p_r, p_z, p_0, p_y, final.data_ptr(),
+                                None if states is None else states.data_ptr(), bsz, T, D, code, p_ws, nbytes, _stream_on(dev, stream))
+    if rc != 0:
+        raise SSDError(rc, "ssd_gated_scan_fwd")
+    return y, final, states
+
+
+def ssd_gated_scan_bwd_workspace_bytes(batch, seqlen, dim, decay: str, dtype: int) -> int:
+    if decay not in DECAYS:
+        raise ValueError(f"decay {decay!r}: one of {sorted(DECAYS)}")
+    return _sized("ssd_gated_scan_bwd_workspace_bytes",
+                  load().ssd_gated_scan_bwd_workspace_bytes(batch, seqlen, dim, DECAYS[decay], dtype))
+
+
+def ssd_gated_scan_bwd(dy, x, f, states, *, decay: str, rate=None, in_gate=None, reset=None, d_final_state=None,
+                       workspace=None, stream=None):
+    """Gradients of ssd_gated_scan_fwd: its x, f, decay, rate, in_gate and reset, the states it returned
+    (want_states=True), dy like y, d_final_state (batch, dim) fp32 or None. Returns (dx, df, d_in_gate, drate,
+    d_initial_state): the first three in x's type (d_in_gate None without in_gate), drate (dim) fp32 (None but for decay
+    "rate"), d_initial_state (batch, dim) fp32."""
+    lib = load()
+    if x.dim() != 3 or x.shape[-1] == 0:
+        raise ValueError("x must be (batch, seqlen, dim)")
+    bsz, T, D = shape = x.shape
+    st, f32 = x.dtype, torch.float32
+    code, dcode = _dtype_code(x), _decay_code(decay, rate)
+    dev = _device(x)
+    (p_x, ldx), (p_f, ldf) = _tokens(dev, "x", x, shape, st), _tokens(dev, "f", f, shape, st)
+    p_i, ldi = _tokens(dev, "in_gate", in_gate, shape, st)
+    p_dy, p_r, p_z = _in(dev, "dy", dy, shape, st), _in(dev, "rate", rate, (D,), f32), _reset(dev, reset, (bsz, T))
+    p_s = _in(dev, "states", states, (bsz, -(-T // GATED_CHUNK), D), f32)
+    p_d = _in(dev, "d_final_state", d_final_state, (bsz, D), f32)
+    dx, df = _new(shape, st, x, stream), _new(shape, st, x, stream)
+    di = None if in_gate is None else _new(shape, st, x, stream)
+    drate = None if rate is None else _new((D,), f32, x, stream)
+    d0 = _new((bsz, D), f32, x, stream)
+    need = 0 if workspace is not None else ssd_gated_scan_bwd_workspace_bytes(bsz, T, D, decay, code)
+    workspace, p_ws, nbytes = _scratch(workspace, need, x, dev, stream)
+    rc = lib.ssd_gated_scan_bwd(p_dy, p_x, ldx, p_f, ldf, p_i, ldi, dcode, p_r, p_z, p_s, p_d, dx.data_ptr(), df.data_ptr(),
+                                None if di is None else di.data_ptr(), None if drate is None else drate.data_ptr(),
+                                d0.data_ptr(), bsz, T, D, code, p_ws, nbytes, _stream_on(dev, stream))
+    if rc != 0:
+        raise SSDError(rc, "ssd_gated_scan_bwd")
+    return dx, df, di, drate, d0
+
+
+def ssd_gated_step(state_in, state_out, x, f, *, decay: str, rate=None, in_gate=None, parent=None, y=None, stream=None):
+    """One token of ssd_gated_scan_fwd's recurrence: row b of state_out (rows, dim) fp32 from row parent[b] (int32, on the
+    GPU) of state_in (src_rows, dim), zero where that is outside it; without parent from row b, and state_out may be
+    state_in. x, f, in_gate (rows, dim), whose rows may lie apart. Returns y (rows, dim) in x's type."""
+    lib = load()
+    if x.dim() != 2 or x.shape[-1] == 0 or state_in.dim() != 2:
+        raise ValueError("x must be (rows, dim) and state_in (src_rows, dim)")
+    rows, D = shape = x.shape
+    st, f32, src = x.dtype, torch.float32, state_in.shape[0]
+    code, dcode = _dtype_code(x), _decay_code(decay, rate)
+    dev = _device(x)
+    (p_x, ldx), (p_f, ldf) = _tokens(dev, "x", x, shape, st), _tokens(dev, "f", f, shape, st)
+    p_i, ldi = _tokens(dev, "in_gate", in_gate, shape, st)
+    p_y = _in(dev, "y", y, shape, st)
+    if y is None:
+        y = _new(shape, st, x, stream)
+        p_y = y.data_ptr()
+    rc = lib.ssd_gated_step(_in(dev, "state_in", state_in, (src, D), f32), _in(dev, "state_out", state_out, shape, f32),
+                            _in(dev, "parent", parent, (rows,), torch.int32), src, p_x, ldx, p_f, ldf, p_i, ldi, dcode,
+                            _in(dev, "rate", rate, (D,), f32), p_y, rows, D, code, _stream_on(dev, stream))
+    if rc != 0:
+        raise SSDError(rc, "ssd_gated_step")
+    return y
+
+
+def _table(name: str, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be (vocab, dim)")
+    return t.shape
+
+
+def ssd_embedding(tokens, table, *, scale: float = 1.0, dtype=None, y=None, stream=None):
+    """y[..., :] = scale * table[tokens[...], :]: tokens int32 of any shape, table (vocab, dim) bf16 or fp32, y (..., dim) in
+    `dtype` (the table's where not given). A token outside the table (padding, -1) gives zeros."""
+    lib = load()
+    V, D = _table("table", table)
+    shape = (*tokens.shape, D)
+    dtype = dtype or (table.dtype if y is None else y.dtype)
+    code = _dtype_code(table)
+    if dtype not in _CODES:
+        raise TypeError(f"dtype {dtype}: bf16 or fp32")
+    dev = _device(table)
+    p_t, p_w = _in(dev, "tokens", tokens, tokens.shape, torch.int32), _first("table", table)
+    p_y = _in(dev, "y", y, shape, dtype)
+    if y is None:
+        y = _new(shape, dtype, table, stream)
+        p_y = y.data_ptr()
+    rc = lib.ssd_embedding(p_t, p_w, scale, p_y, tokens.numel(), V, D, code, _CODES[dtype], _stream_on(dev, stream))
+    if rc != 0:
+        raise SSDError(rc, "ssd_embedding")
+    return y
+
+
+def ssd_embedding_bwd_workspace_bytes(rows, vocab, dim) -> int:
+    return _sized("ssd_embedding_bwd_workspace_bytes", load().ssd_embedding_bwd_workspace_bytes(rows, vocab, dim))
+
+
+def ssd_embedding_bwd(dy, tokens, vocab: int, *, scale: float = 1.0, dtype=None, dtable=None, accumulate: bool = False,
+                      workspace=None, stream=None):
+    """The table's gradient: dy (..., dim), tokens (...) int32 as ssd_embedding had them. Returns dtable (vocab, dim) in
+    `dtype` (dy's where not given); a given dtable is overwritten, or added to with accumulate."""
+    lib = load()
+    rows, D = _rows_dim("dy", dy)
+    if accumulate and dtable is None:
+        raise ValueError("accumulate needs dtable")
+    dtype = dtype or (dy.dtype if dtable is None else dtable.dtype)
+    code = _dtype_code(dy)
+    if dtype not in _CODES:
+        raise TypeError(f"dtype {dtype}: bf16 or fp32")
+    dev = _device(dy)
+    p_dy, p_t = _first("dy", dy), _in(dev, "tokens", tokens, dy.shape[:-1], torch.int32)
+    p_d = _in(dev, "dtable", dtable, (vocab, D), dtype)
+    if dtable is None:
+        dtable = _new((vocab, D), dtype, dy, stream)
+        p_d = dtable.data_ptr()
+    need = 0 if workspace is not None else ssd_embedding_bwd_workspace_bytes(rows, vocab, D)
+    workspace, p_ws, nbytes = _scratch(workspace, need, dy, dev, stream)
+    rc = lib.ssd_embedding_bwd(p_dy, p_t, scale, p_d, int(accumulate), rows, vocab, D, code, _CODES[dtype], p_ws, nbytes,
+                               _stream_on(dev, stream))
+    if rc != 0:
+        raise SSDError(rc, "ssd_embedding_bwd")
+    return dtable
+
+
+def _per_row(dev: int, name: str, t, rows: int, last: int, dtype):
+    """(address, rows) of an argument (last) or (1, last) for all rows, or one for each of the logits' rows."""
+    if t is None:
+        return None, 0
+    n = t.numel() // last if t.dim() and t.shape[-1] == last else 0
+    if n not in (1, rows):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {last} values for all rows or for each of {rows}")
+    return _in(dev, name, t, t.shape, dtype), n
+
+
+def ssd_logits_process(logits, *, tokens=None, lengths=None, prompt=None, repetition=None, presence=None, frequency=None,
+                       bias=None, mask=None, out=None, stream=None):
+    """What is done to logits (..., vocab) bf16 or fp32 before a choice: penalties for the tokens of each row's history
+    (tokens (rows, capacity) int32; lengths (rows) int32, the part of it that is there; prompt (rows) int32, how much of that
+    counts for `repetition` only), a bias (vocab) or (..., vocab) fp32, and a mask (ceil(vocab / 32)) or (..., ceil(vocab /
+    32)) int32 of allowed tokens, 32 to a word. repetition, presence, frequency (rows) fp32 or None. `out` may be logits
+    itself. Returns out."""
+    lib = load()
+    rows, V = _rows_dim("logits", logits)
+    code = _dtype_code(logits)
+    dev = _device(logits)
+    i32, f32 = torch.int32, torch.float32
+    p_l = _first("logits", logits)
+    cap = 0
+    if tokens is not None:
+        if tokens.dim() != 2:
+            raise ValueError("tokens must be (rows, capacity)")
+        cap = tokens.shape[1]
+    elif any(t is not None for t in (lengths, prompt, repetition, presence, frequency)):
+        raise ValueError("penalties need the rows' tokens")
+    p_t = _in(dev, "tokens", tokens, (rows, cap), i32)
+    per_row = [_in(dev, n, t, (rows,), d) for n, t, d in (
+        ("lengths", lengths, i32), ("prompt", prompt, i32), ("repetition", repetition, f32), ("presence", presence, f32),
+        ("frequency", frequency, f32))]
+    p_b, nb = _per_row(dev, "bias", bias, rows, V, f32)
+    p_m, nm = _per_row(dev, "mask", mask, rows, -(-V // 32), i32)
+    p_o = _in(dev, "out", out, logits.shape, logits.dtype)
+    if out is None:
+        out = _like(logits, stream)
+        p_o = out.data_ptr()
+    if cap == 0:  # empty histories: nothing is penalised
+        p_t, per_row = None, [None] * 5
+    rc = lib.ssd_logits_process(p_l, p_o, p_t, cap, *per_row, p_b, nb, p_m, nm, rows, V, code, _stream_on(dev, stream))
+    if rc != 0:
+        raise SSDError(rc, "ssd_logits_process")
+    return out
+
+
+def ssd_int_quantize(x, *, stream=None):
+    """x (..., dim) bf16 or fp32 in 8-bit integers: (q int8 like x, scale (...) fp32 = max |x| / 127 of each row)."""
+    lib = load()
+    rows, dim = _rows_dim("x", x)
+    code = _dtype_code(x)
+    dev = _device(x)
+    p_x = _first("x", x)
+    q, scale = _new(x.shape, torch.int8, x, stream), _new(x.shape[:-1], torch.float32, x, stream)
+    st = lib.ssd_int_quantize(p_x, q.data_ptr(), scale.data_ptr(), rows, dim, code, _stream_on(dev, stream))
+    if st != 0:
+        raise SSDError(st, "ssd_int_quantize")
+    return q, scale
+
+
+def ssd_linear_int_workspace_bytes(rows, in_, out) -> int:
+    return _sized("ssd_linear_int_workspace_bytes", load().ssd_linear_int_workspace_bytes(rows, in_, out))
+
+
+def ssd_linear_int(xq, xscale, wq, wscale, *, bias=None, act: str = "none", residual=None, dtype=None, y=None, workspace=None,
+                  stream=None):
+    """ssd_linear from 8-bit integers as ssd_int_quantize returns them: xq (..., in) and wq (out, in) int8, in a multiple of
+    16, xscale (...) and wscale (out) fp32; residual and y in `dtype` (bf16 where nothing says another). Returns y."""
+    lib = load()
+    rows, k, n, shape = _linear_dims(xq, wq, "wq")
+    acode = _act_code(act)
+    int8, f32 = torch.int8, torch.float32
+    dtype = dtype or next((t.dtype for t in (y, residual) if t is not None), torch.bfloat16)
+    if dtype not in _CODES:
+        raise TypeError(f"dtype {dtype}: bf16 or fp32")
+    dev = _device(xq)
+    p_y = _in(dev, "y", y, shape, dtype)
+    if y is None:
+        y = _new(shape, dtype, xq, stream)
+        p_y = y.data_ptr()
+    need = 0 if workspace is not None else ssd_linear_int_workspace_bytes(rows, k, n)
+    workspace, p_ws, nbytes = _scratch(workspace, need, xq, dev, stream)
+    rc = lib.ssd_linear_int(_in(dev, "xq", xq, xq.shape, int8), _in(dev, "xscale", xscale, xq.shape[:-1], f32),
+                           _in(dev, "wq", wq, (n, k), int8), _in(dev, "wscale", wscale, (n,), f32),
+                           _in(dev, "bias", bias, (n,), f32), acode, _in(dev, "residual", residual, shape, dtype), p_y,
+                           rows, k, n, _CODES[dtype], p_ws, nbytes, _stream_on(dev, stream))
+    if rc != 0:
+        raise SSDError(rc, "ssd_linear_int")
+    return y
 
 
 def raw_call(name: str, *args) -> int:

@@ -1,0 +1,362 @@
+// Embedding lookup for gfx950, y[r, :] = scale table[token[r], :], and the
+// gradient of the table from its tokens in order:
+//
+//   dtable[v, :] = scale sum over r with token[r] = v of dy[r, :]
+//
+// in a fixed order, r ascending, so that the same inputs give the same bits. A
+// token outside the table is a row of zeros, and adds to no gradient.
+//
+// k_sort: a work-group sorts up to 16384 tokens in LDS (stable, by digits of at
+// most 8 bits); the other work-groups of the launch clear the table meanwhile.
+// More tokens are sorted piece by piece and merged, 8 pieces at a time, each value
+// finding its place by binary search (k_merge). k_sums: a wavefront adds
+// the rows of `len` places of the sorted list, 256 channels of them; a token whose
+// rows lie within writes its sum to the table, the first and the last one's may go on
+// beyond it, and are kept apart for k_join. Bound: HBM, the table's write.
+#include <type_traits>
+
+#include "ssd_common.h"
+#include "ssd_internal.h"
+
+namespace ssd {
+
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64, kSortKeys = 16;
+
+// 4 consecutive values (V: aligned and whole) or one.
+template <typename T, int V>
+__device__ __forceinline__ void load(float (&v)[V], const T *p) {
+    if constexpr (V == 1) {
+        v[0] = (float)p[0];
+    } else if constexpr (sizeof(T) == 2) {
+        const bf16x4 q = *reinterpret_cast<const bf16x4 *>(p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = (float)q[e];
+    } else {
+        const f32x4 q = *reinterpret_cast<const f32x4 *>(p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = q[e];
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store(T *p, const float (&v)[V]) {
+    if constexpr (V == 1) p[0] = (T)v[0];
+    else if constexpr (sizeof(T) == 2) *reinterpret_cast<bf16x4 *>(p) = bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
+    else *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
+}
+
+// V values a lane, 64 lanes to a slice of a row. Work-groups go over the rows' slices in turn.
+template <typename TT, typename TY, int V>
+__global__ __launch_bounds__(256) void k_embed(const int *tokens, const TT *table, TY *y, float scale, int64_t rows, int vocab, int dim) {
+    const int slices = (dim + 64 * V - 1) / (64 * V);
+    const int64_t n = rows * slices, hop = (int64_t)gridDim.x * 4;
+    const int lane = threadIdx.x & 63;
+    for (int64_t k = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); k < n; k += hop) {
+        const int64_t r = k / slices;
+        const int d = ((int)(k - r * slices) * 64 + lane) * V;
+        if (d >= dim) continue;
+        const int t = tokens[r];
+        float v[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = 0.f;
+        if ((uint32_t)t < (uint32_t)vocab) {
+            load<TT, V>(v, table + (int64_t)t * dim + d);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] *= scale;
+        }
+        store<TY, V>(y + r * dim + d, v);
+    }
+}
+
+// Work-groups below `tiles` sort a piece of 2^bits tokens each: keys are
+// token << bits | place in the piece, in order of their tokens; out: token << 32 | row.
+// The others clear n16 pieces of 16 bytes, and the rest behind them.
+__global__ __launch_bounds__(kSortThreads) void k_sort(const int *tokens, uint64_t *out, int64_t rows, int vocab, int bits, int passes,
+                                                       int digit, int tiles, u32x4 *clear, int64_t n16, int rest) {
+    if ((int)blockIdx.x >= tiles) {
+        const int64_t hop = (int64_t)(gridDim.x - tiles) * kSortThreads;
+        const int64_t i0 = (int64_t)((int)blockIdx.x - tiles) * kSortThreads + threadIdx.x;
+        for (int64_t i = i0; i < n16; i += hop) clear[i] = u32x4{0, 0, 0, 0};
+        if (i0 < rest) reinterpret_cast<uint16_t *>(clear + n16)[i0] = 0;
+        return;
+    }
+    __shared__ uint32_t keys[kSortThreads * kSortKeys];
+    __shared__ uint32_t count[kSortWaves][256];
+    __shared__ uint32_t sums[kSortWaves];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t first = (int64_t)blockIdx.x << bits;
+    const int n = (int)min((int64_t)1 << bits, rows - first);
+    const int each = (n + kSortThreads - 1) / kSortThreads;  // keys of a lane, 64 places apart
+    uint32_t key[kSortKeys];
+#pragma unroll
+    for (int e = 0; e < kSortKeys; ++e) {
+        const int i = (w * each + e) * 64 + lane;
+        key[e] = ~0u;  // behind every token
+        if (e < each && i < n) {
+            const uint32_t t = (uint32_t)tokens[first + i];
+            key[e] = (t < (uint32_t)vocab ? t : (uint32_t)vocab) << bits | (uint32_t)i;
+        }
+    }
+    const uint64_t below = ((uint64_t)1 << lane) - 1;
+    const uint32_t bins = 1u << digit;
+    for (int p = 0; p < passes; ++p) {
+        const int shift = bits + p * digit;
+        for (uint32_t i = threadIdx.x; i < kSortWaves * 256; i += kSortThreads) (&count[0][0])[i] = 0;
+        __syncthreads();
+        // a key's place among its wavefront's keys of the same digit
+        uint32_t place[kSortKeys];
+#pragma unroll
+        for (int e = 0; e < kSortKeys; ++e) {
+            place[e] = 0;
+            if (e < each) {
+                const uint32_t d = (key[e] >> shift) & (bins - 1);
+                uint64_t same = ~(uint64_t)0;
+                for (int b = 0; b < digit; ++b) {
+                    const bool one = (d >> b) & 1;
+                    const uint64_t ones = __ballot(one);
+                    same &= one ? ones : ~ones;
+                }
+                const uint32_t before = count[w][d];
+                __builtin_amdgcn_wave_barrier();
+                if ((same & below) == 0) count[w][d] = before + (uint32_t)__popcll(same);
+                __builtin_amdgcn_wave_barrier();
+                place[e] = before + (uint32_t)__popcll(same & below);
+            }
+        }
+        __syncthreads();
+        // the counts' exclusive sums, digit by digit and within it wavefront by wavefront: thread t takes
+        // 4 wavefronts' counts of digit t / 4
+        const uint32_t dd = threadIdx.x >> 2, w0 = (threadIdx.x & 3) * 4;
+        uint32_t c[4], s = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[j] = count[w0 + j][dd], s += c[j];
+        uint32_t up = s;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const uint32_t v = __shfl_up(up, o, 64);
+            if (lane >= o) up += v;
+        }
+        if (lane == 63) sums[w] = up;
+        __syncthreads();
+        uint32_t base = up - s;
+        for (int j = 0; j < w; ++j) base += sums[j];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            count[w0 + j][dd] = base;
+            base += c[j];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kSortKeys; ++e)
+            if (e < each) keys[count[w][(key[e] >> shift) & (bins - 1)] + place[e]] = key[e];
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kSortKeys; ++e)
+            if (e < each) key[e] = keys[(w * each + e) * 64 + lane];
+        __syncthreads();
+    }
+#pragma unroll
+    for (int e = 0; e < kSortKeys; ++e) {
+        const int i = (w * each + e) * 64 + lane;
+        if (e < each && i < n) out[first + i] = (uint64_t)(key[e] >> bits) << 32 | (uint64_t)(first + (key[e] & ((1u << bits) - 1)));
+    }
+}
+
+// Sorted runs of `run` values (the last one shorter) merged 8 at a time: a value's place is its own in its run
+// and, of each other run, the number of values below it (no two are equal).
+__global__ __launch_bounds__(256) void k_merge(const uint64_t *in, uint64_t *out, int64_t n, int64_t run) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    const uint64_t v = in[i];
+    const int64_t mine = i / run * run, group = i / (8 * run) * (8 * run);
+    int64_t at = group + (i - mine);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int64_t b = group + j * run;
+        if (b == mine || b >= n) continue;
+        int64_t lo = 0, hi = min(run, n - b);
+        while (lo < hi) {
+            const int64_t m = (lo + hi) >> 1;
+            if (in[b + m] < v) lo = m + 1;
+            else hi = m;
+        }
+        at += lo;
+    }
+    out[at] = v;
+}
+
+// The row of the table that a token's sum goes to.
+template <typename TG, int V>
+__device__ __forceinline__ void put(const EmbedBwdArgs &a, int64_t token, int d, float (&sum)[V]) {
+    TG *p = reinterpret_cast<TG *>(a.dtable) + token * a.dim + d;
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum[e] *= a.scale;
+    if (a.accumulate) {
+        float old[V];
+        load<TG, V>(old, p);
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum[e] += old[e];
+    }
+    store<TG, V>(p, sum);
+}
+
+template <typename TY, typename TG, int V>
+__global__ __launch_bounds__(64) void k_sums(EmbedBwdArgs a) {
+    constexpr int U = 8;  // rows on their way
+    const int d = ((int)blockIdx.y * 64 + (int)threadIdx.x) * V;
+    const int64_t s = (int64_t)blockIdx.x * a.len, end = min(s + a.len, a.rows);
+    const bool live = d < a.dim;
+    auto token = [&](int64_t i) { return (uint32_t)(a.sorted[i] >> 32); };
+    uint32_t now = token(s);
+    bool head = s > 0 && token(s - 1) == now;
+    float sum[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum[e] = 0.f;
+    auto flush = [&](bool tail) {
+        if (!live || now >= (uint32_t)a.vocab) return;
+        if (head || tail) store<float, V>(a.part + ((int64_t)blockIdx.x * 2 + (head ? 0 : 1)) * a.dim + d, sum);
+        else put<TG, V>(a, now, d, sum);
+    };
+    for (int64_t i = s; i < end; i += U) {
+        float v[U][V];
+        uint32_t t[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint64_t k = i + u < end ? a.sorted[i + u] : ~(uint64_t)0;
+            t[u] = (uint32_t)(k >> 32);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[u][e] = 0.f;
+            if (live && t[u] < (uint32_t)a.vocab) load<TY, V>(v[u], reinterpret_cast<const TY *>(a.dy) + (int64_t)(uint32_t)k * a.dim + d);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i + u >= end) break;
+            if (t[u] != now) {
+                flush(false);
+                now = t[u];
+                head = false;
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum[e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum[e] += v[u][e];
+        }
+    }
+    flush(end < a.rows && token(end) == now);
+}
+
+// The sums of a token whose rows begin in piece blockIdx.x and go on beyond it, in order.
+// 4 wavefronts take a quarter of the pieces each.
+template <typename TG, int V>
+__global__ __launch_bounds__(256) void k_join(EmbedBwdArgs a) {
+    __shared__ float share[4][64][V];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t p = blockIdx.x, s = p * a.len, end = s + a.len;  // never the last piece
+    const uint64_t mine = a.sorted[end - 1] >> 32;
+    if (mine >= (uint64_t)a.vocab || mine != a.sorted[end] >> 32) return;
+    if (mine == a.sorted[s] >> 32 && s > 0 && mine == a.sorted[s - 1] >> 32) return;  // it began earlier
+    // the first place behind the token's rows, and the piece of its last one
+    int64_t lo = end, hi = a.rows;
+    while (lo < hi) {
+        const int64_t m = (lo + hi) >> 1;
+        if (a.sorted[m] >> 32 <= mine) lo = m + 1;
+        else hi = m;
+    }
+    const int64_t pieces = (lo - 1) / a.len - p, each = (pieces + 3) / 4;  // behind the first
+    const int d = ((int)blockIdx.y * 64 + lane) * V;
+    float sum[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum[e] = 0.f;
+    if (d < a.dim) {
+        if (w == 0) load<float, V>(sum, a.part + (p * 2 + 1) * a.dim + d);
+        const int64_t to = min((w + 1) * each, pieces);
+#pragma unroll 4
+        for (int64_t q = w * each; q < to; ++q) {
+            float v[V];
+            load<float, V>(v, a.part + (p + 1 + q) * 2 * a.dim + d);
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum[e] += v[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) share[w][lane][e] = sum[e];
+    __syncthreads();
+    if (w == 0 && d < a.dim) {
+#pragma unroll
+        for (int k = 1; k < 4; ++k)
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum[e] += share[k][lane][e];
+        put<TG, V>(a, (int64_t)mine, d, sum);
+    }
+}
+
+static ssd_status status_of(hipError_t e) { return e == hipSuccess ? SSD_OK : SSD_ERR_HIP; }
+template <typename F>
+static ssd_status pick_type(ssd_dtype t, F fn) {
+    return t == SSD_BF16 ? fn(bf16{}) : fn(float{});
+}
+
+ssd_status launch_embed(const int *tokens, const void *table, void *y, float scale, int64_t rows, int64_t vocab, int64_t dim,
+                        ssd_dtype dtype, ssd_dtype y_dtype, hipStream_t s) {
+    return pick_type(dtype, [&](auto tt) {
+        return pick_type(y_dtype, [&](auto ty) {
+            using TT = decltype(tt);
+            using TY = decltype(ty);
+            auto go = [&](auto k, int v) {
+                const int64_t n = rows * ((dim + 64 * v - 1) / (64 * v)), blocks = (n + 3) / 4, most = 1 << 20;
+                return status_of(launch(k, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), s, tokens, (const TT *)table,
+                                        (TY *)y, scale, rows, (int)vocab, (int)dim));
+            };
+            return dim % 4 == 0 ? go(k_embed<TT, TY, 4>, 4) : go(k_embed<TT, TY, 1>, 1);
+        });
+    });
+}
+
+EmbedPlan embed_plan(int64_t rows, int64_t vocab) {
+    EmbedPlan p = {};
+    int bits = 0;
+    while ((vocab >> bits) != 0) ++bits;  // of `vocab` itself, which stands for tokens outside the table
+    p.passes = (bits + 7) / 8;
+    p.digit = (bits + p.passes - 1) / p.passes;
+    p.bits = 32 - bits < 14 ? 32 - bits : 14;
+    p.tiles = (rows + ((int64_t)1 << p.bits) - 1) >> p.bits;
+    p.len = 16;
+    while (p.len < 256 && rows / p.len > 1024) p.len *= 2;
+    p.pieces = (rows + p.len - 1) / p.len;
+    return p;
+}
+
+ssd_status launch_embed_bwd(EmbedBwdArgs a, const EmbedPlan &p, const int *tokens, uint64_t *one, uint64_t *two, ssd_dtype dy_dtype,
+                            ssd_dtype dtype, hipStream_t s) {
+    const int64_t bytes = a.accumulate ? 0 : (int64_t)a.vocab * a.dim * (dtype == SSD_BF16 ? 2 : 4);
+    const int64_t n16 = bytes / 16, rest = bytes % 16 / 2;
+    int64_t fill = (n16 + 4 * kSortThreads - 1) / (4 * kSortThreads);
+    fill = bytes ? (fill < 1 ? 1 : fill > 2048 ? 2048 : fill) : 0;
+    if (p.tiles + fill == 0) return SSD_OK;
+    ssd_status st = status_of(launch(k_sort, dim3((unsigned)(p.tiles + fill)), dim3(kSortThreads), s, tokens, one, a.rows, a.vocab, p.bits,
+                                     p.passes, p.digit, (int)p.tiles, (u32x4 *)a.dtable, n16, (int)rest));
+    if (st != SSD_OK || a.rows == 0) return st;
+    for (int64_t run = (int64_t)1 << p.bits; run < a.rows; run *= 8) {
+        st = status_of(launch(k_merge, dim3((unsigned)((a.rows + 255) / 256)), dim3(256), s, one, two, a.rows, run));
+        if (st != SSD_OK) return st;
+        uint64_t *t = one;
+        one = two;
+        two = t;
+    }
+    a.sorted = one;
+    a.len = p.len;
+    return pick_type(dy_dtype, [&](auto ty) {
+        return pick_type(dtype, [&](auto tg) {
+            using TY = decltype(ty);
+            using TG = decltype(tg);
+            auto go = [&](auto sums, auto join, int v) {
+                const unsigned slices = (unsigned)((a.dim + 64 * v - 1) / (64 * v));
+                const ssd_status e = status_of(launch(sums, dim3((unsigned)p.pieces, slices), dim3(64), s, a));
+                if (e != SSD_OK || p.pieces < 2) return e;
+                return status_of(launch(join, dim3((unsigned)(p.pieces - 1), slices), dim3(256), s, a));
+            };
+            return a.dim % 4 == 0 ? go(k_sums<TY, TG, 4>, k_join<TG, 4>, 4) : go(k_sums<TY, TG, 1>, k_join<TG, 1>, 1);
+        });
+    });
+}
+
+}  // namespace ssd

@@ -211,6 +211,7 @@ ssd_status launch_column_sums(const float *part, float *out, int nb, int64_t D, 
 struct LinearArgs {
     const void *x, *w;          // rows of ldx / ldw bytes (multiples of 4; few rows: of the type), kbytes of them along k
     const uint8_t *xscale, *wscale;  // 8-bit operands: a scale for each 32 along k, rows of lds bytes
+    const float *xs, *ws;       // 8-bit integers: a scale for each row of x and of w
     int64_t ldx, ldw, lds;
     const float *bias;          // (N) or null
     const void *res;            // (M x N) or null
@@ -261,6 +262,81 @@ struct BeamArgs {
 };
 void beam_plan(int64_t V, int *lists, int *tiles);
 ssd_status launch_beam_select(const BeamArgs &a, int64_t batch, ssd_dtype dtype, hipStream_t s);
+
+// Gated linear recurrence (ssd_gated.hip).
+struct GatedArgs {
+    const void *x, *f, *i, *dy;  // i: null where the input is not gated; dy: the backward's
+    int64_t ldx, ldf, ldi;       // values from one token to the next
+    const uint8_t *reset;        // (batch, T) or null
+    const float *rate;           // (D), decay "rate" only
+    const float *init, *dfinal;  // (batch, D) or null
+    float *states;               // (batch, nchunks, D): written by the forward (or null), read by the backward
+    void *y, *dx, *df, *di;
+    float *final, *dinit, *drate;
+    float *part;                 // backward: shares of drate
+    int64_t batch, T, D, nchunks;
+};
+struct GatedPlan {
+    bool fits;
+    int64_t fwd_bytes, bwd_bytes;  // workspace
+    int64_t rate_bytes;            // the backward's, beside that, for the rates' gradient
+};
+GatedPlan gated_plan(int64_t batch, int64_t T, int64_t D, ssd_dtype dtype);
+ssd_status launch_gated_fwd(GatedArgs a, const GatedPlan &p, ssd_dtype dtype, int decay, void *workspace, hipStream_t s);
+ssd_status launch_gated_bwd(GatedArgs a, const GatedPlan &p, ssd_dtype dtype, int decay, void *workspace, hipStream_t s);
+struct GatedStepArgs {
+    const float *state_in;
+    float *state_out;
+    const int *parent;           // (rows), or null: each row's own
+    int64_t src;
+    const void *x, *f, *i;
+    int64_t ldx, ldf, ldi;
+    const float *rate;
+    void *y;
+    int64_t rows, D;
+};
+ssd_status launch_gated_step(const GatedStepArgs &a, ssd_dtype dtype, int decay, hipStream_t s);
+
+// Embedding (ssd_embed.hip).
+ssd_status launch_embed(const int *tokens, const void *table, void *y, float scale, int64_t rows, int64_t vocab, int64_t dim,
+                        ssd_dtype dtype, ssd_dtype y_dtype, hipStream_t s);
+struct EmbedPlan {
+    int bits, passes, digit;     // tokens of a sorted piece (2^bits), and the sort's digits
+    int64_t tiles;               // sorted pieces
+    int len;                     // rows of a piece of sums
+    int64_t pieces;
+};
+EmbedPlan embed_plan(int64_t rows, int64_t vocab);
+struct EmbedBwdArgs {
+    const void *dy;              // (rows, dim)
+    void *dtable;                // (vocab, dim)
+    const uint64_t *sorted;      // token << 32 | row
+    float *part;                 // workspace: (pieces, 2, dim): a piece's first sum where it began earlier, its last where it goes on
+    int64_t rows;
+    int vocab, dim, len, accumulate;
+    float scale;
+};
+// one, two: workspace of rows each (two: only where there are several sorted pieces)
+ssd_status launch_embed_bwd(EmbedBwdArgs a, const EmbedPlan &p, const int *tokens, uint64_t *one, uint64_t *two, ssd_dtype dy_dtype,
+                            ssd_dtype dtype, hipStream_t s);
+
+// Logits before the choice (ssd_logits.hip).
+struct LogitsArgs {
+    const void *logits;
+    void *out;
+    const int *tokens, *lengths, *prompt;                 // tokens (rows, capacity); null where not given
+    const float *repetition, *presence, *frequency;       // (rows) or null
+    const float *bias;                                    // (bias_rows, vocab) or null
+    const uint32_t *mask;                                 // (mask_rows, words) or null
+    int64_t rows, vocab, capacity, words, bias_rows, mask_rows;
+    int slices;
+};
+int64_t logits_slices(int64_t vocab);
+ssd_status launch_logits(LogitsArgs a, ssd_dtype dtype, hipStream_t s);
+
+// 8-bit integers (ssd_int.hip; the products: ssd_linear_int.hip).
+ssd_status launch_int_quantize(const void *x, int8_t *q, float *scale, int64_t rows, int64_t dim, ssd_dtype dtype, hipStream_t s);
+ssd_status launch_linear_int(const LinearArgs &a, const LinearPlan &p, ssd_dtype dtype, hipStream_t s);
 
 // One recurrent decode step.
 ssd_status launch_step(const StepArgs &a, hipStream_t s);

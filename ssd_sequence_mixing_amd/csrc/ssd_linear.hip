@@ -3,8 +3,8 @@
 //   z[m, n] = sum_k x[m, k] w[n, k] + bias[n];   y = act(z) + r[m, n]
 //
 // from bf16, fp32 or 8-bit operands (e4m3 codes with one power of two for each
-// 32 along k), and the pieces of the backward pass. Sums are fp32 (matrix
-// cores); y is rounded once, at the end, and z once where it is kept.
+// 32 along k; integers with a scale for each row), and the pieces of the backward pass. Sums are fp32 (matrix
+// cores; of integers exact, in 32 bits); y is rounded once, at the end, and z once where it is kept.
 //
 // k_tile: a work-group forms a BM x BN tile of y. A step takes 128 bytes of
 // every row of x and w (64 bf16, 32 fp32 or 128 codes): they go straight from
@@ -53,9 +53,10 @@
 
 namespace ssd {
 
-constexpr int kBF16 = 0, kF32 = 1, kMX = 2;
+constexpr int kBF16 = 0, kF32 = 1, kMX = 2, kInt = 3;
 constexpr int kParts = 3;  // beside the activations
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 
 // 16 (4) bytes a lane from base + voff + soff, zeros behind `bytes`, to consecutive places from dst on.
@@ -160,6 +161,11 @@ __device__ __forceinline__ f32x4 mma2(u32x4 wl, u32x4 wh, u32x4 xl, u32x4 xh, f3
         for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(d[i], e[i], c, 0, 0, 0);
+    } else if constexpr (KIND == kInt) {  // the accumulators' bits are integers
+        i32x4 d = __builtin_bit_cast(i32x4, c);
+        d = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, wl), __builtin_bit_cast(i32x4, xl), d, 0, 0, 0);
+        d = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, wh), __builtin_bit_cast(i32x4, xh), d, 0, 0, 0);
+        c = __builtin_bit_cast(f32x4, d);
     } else {
         typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
         const u32x8 w = __builtin_shufflevector(wl, wh, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -269,6 +275,15 @@ __device__ __forceinline__ void finish4(const LinearArgs &a, int m, int n, float
 __device__ __forceinline__ void bias4(const LinearArgs &a, int n, float (&v)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = (a.bias && n + i < a.N) ? a.bias[n + i] : 0.f;
+}
+// Sums of integers in 4 consecutive columns of row m, with their scales.
+template <int KIND>
+__device__ __forceinline__ void scale4(const LinearArgs &a, int m, int n, float (&v)[4]) {
+    if constexpr (KIND == kInt) {
+        const float xs = m < a.M ? a.xs[m] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = (float)__float_as_int(v[i]) * xs * (n + i < a.N ? a.ws[n + i] : 0.f);
+    }
 }
 template <typename TO, bool kWhole>
 __device__ __forceinline__ void res4(const LinearArgs &a, int m, int n, float (&v)[4]) {
@@ -462,7 +477,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
     // barrier, so that the matrix cores have work across it.
     constexpr int NQ = (KIND == kMX || TM < 4) ? TM : 4, TQ = TM / NQ;  // 8 bits: registers for the scales, too
     static_assert(TQ * NQ == TM && NQ % 2 == 0, "parts of a step");
-    constexpr int kMma = KIND == kBF16 ? 2 : KIND == kF32 ? 6 : 1;          // matrix-core instructions of a product
+    constexpr int kMma = (KIND == kBF16 || KIND == kInt) ? 2 : KIND == kF32 ? 6 : 1;  // matrix-core instructions of a product
     constexpr int kReadsX = TQ * (XT ? 4 : KIND == kMX ? 3 : 2), kReadsW = TN * (WT ? 4 : KIND == kMX ? 3 : 2);
     struct WRegs {
         u32x4 l[TN], h[TN];
@@ -575,10 +590,11 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
         for (int j = 0; j < TN; ++j) *reinterpret_cast<f32x4 *>(piece + r * LDC + j * 16 + kg * 4) = acc[i][j];
         __builtin_amdgcn_wave_barrier();
     };
-    auto staged = [&](int p, float (&v)[4]) {
+    auto staged = [&](int i, int p, float (&v)[4]) {
         const f32x4 c = *reinterpret_cast<const f32x4 *>(piece + row_of(p) * LDC + col_of(p));
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = c[e];
+        scale4<KIND>(a, mw + i * 16 + row_of(p), nw + col_of(p), v);
     };
     if constexpr (EPI == kParts) {
         const bool whole = (a.N & 3) == 0;
@@ -588,7 +604,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
                 float v[4];
-                staged(p, v);
+                staged(i, p, v);
                 const int m = mw + i * 16 + row_of(p), n = nw + col_of(p);
                 if (m < a.M && n < a.N) put4<float>(a.part + blockIdx.y * part_stride(a.M, a.N) + (int64_t)m * a.N + n, v, a.N - n, whole);
             }
@@ -615,7 +631,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
                 float v[4];
-                staged(p, v);
+                staged(i, p, v);
                 finish4<TO, SSD_ACT_NONE, true>(a, mw + i * 16 + row_of(p), nw + col_of(p), v, bias[p], res[i & 1][p]);
             }
             __builtin_amdgcn_wave_barrier();
@@ -631,7 +647,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
             const int m = mw + i * 16 + row_of(p), n = nw + col_of(p);
             bias4(a, n, bias);
             res4<TO, kWhole>(a, m, n, res);
-            staged(p, v);
+            staged(i, p, v);
             finish4<TO, EPI, kWhole>(a, m, n, v, bias, res);
         }
     };
@@ -646,8 +662,8 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
 
 // The splits' parts of y, added in order, and the epilogue. y, the residual,
 // z and a part are each one run of M N values, of which a thread takes 4; a
-// part's stride is a multiple of 4.
-template <typename TO>
+// part's stride is a multiple of 4. INT: a name of its own in each of the two builds of this file.
+template <bool INT, typename TO>
 __global__ __launch_bounds__(256) void k_join(LinearArgs a) {
     const int64_t total = (int64_t)a.M * a.N, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= total) return;
@@ -791,8 +807,12 @@ __global__ __launch_bounds__(512) void k_skinny(LinearArgs a) {
             for (int k = 0; k < 8; ++k) {
                 const f32x4 q = *reinterpret_cast<const f32x4 *>(red[k][lane]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] += q[e];
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (KIND == kInt) v[e] = __int_as_float(__float_as_int(v[e]) + __float_as_int(q[e]));
+                    else v[e] += q[e];
+                }
             }
+            scale4<KIND>(a, r, n0 + c * 16 + kg * 4, v);
             finish4_any<TO>(a, r, n0 + c * 16 + kg * 4, v);
         }
     }
@@ -925,6 +945,7 @@ __global__ __launch_bounds__(64 * Y) void k_dz(const T *dy, const T *pre, T *dz,
 // down to `least` of them. Of 40 products of 32 to 8192 rows the plan so chosen takes 1.6% (bf16)
 // and 2.4% (fp32) more than the best one on average, with full last rounds 4.7% and 8.9%
 // (777 x 1003 x 515 in fp32: 18 us in 4 parts, 22 in 8).
+#ifndef SSD_INT_TU
 LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, bool f32, bool along_k) {
     LinearPlan p = {};
     p.steps = (int)((kbytes + 127) / 128);
@@ -997,6 +1018,7 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, bool f32, bool alon
     }
     return top;
 }
+#endif  // SSD_INT_TU
 
 template <int KIND, typename TO, bool XT, bool WT, bool RAGGED>
 static ssd_status run_tile(const LinearArgs &a, const LinearPlan &p, hipStream_t s) {
@@ -1021,14 +1043,14 @@ static ssd_status run_tile(const LinearArgs &a, const LinearPlan &p, hipStream_t
     }
     if (e == hipSuccess && p.splits > 1) {
         const int64_t n = ((int64_t)a.M * a.N + 3) / 4;
-        e = launch(k_join<TO>, dim3((unsigned)((n + 255) / 256)), dim3(256), s, a);
+        e = launch(k_join<KIND == kInt, TO>, dim3((unsigned)((n + 255) / 256)), dim3(256), s, a);
     }
     return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 
 template <int KIND, typename TO>
 static ssd_status run_linear(const LinearArgs &a, const LinearPlan &p, hipStream_t s) {
-    if constexpr (KIND != kMX) {
+    if constexpr (KIND == kBF16 || KIND == kF32) {
         if (p.bm && a.kbytes % 16 != 0) return run_tile<KIND, TO, false, false, true>(a, p, s);
     }
     if (p.bm) return run_tile<KIND, TO, false, false, false>(a, p, s);
@@ -1045,37 +1067,54 @@ static ssd_status run_linear(const LinearArgs &a, const LinearPlan &p, hipStream
     if constexpr (KIND == kBF16) {
         if (a.kbytes % 4 != 0) return of(std::integral_constant<int, 2>{});
     }
-    if constexpr (KIND != kMX) {
+    if constexpr (KIND == kBF16 || KIND == kF32) {
         if (a.kbytes % 16 != 0) return of(std::integral_constant<int, 4>{});
     }
     return of(std::integral_constant<int, 16>{});
 }
 
-ssd_status launch_linear(LinearArgs a, const LinearPlan &p, bool mx, ssd_dtype dtype, hipStream_t s) {
-    a.nm = p.nm; a.nn = p.nn; a.steps = p.steps; a.splits = p.splits; a.steps_per_split = p.steps_per_split;
-    if (p.splits == 1) a.part = nullptr;
+// The plan's one product, or its two (n_main): one(args, plan) launches each.
+template <typename F>
+static ssd_status in_parts(LinearArgs a, const LinearPlan &p, int64_t es, F one) {
+    auto go = [&](LinearArgs b, const LinearPlan &q) {
+        b.nm = q.nm; b.nn = q.nn; b.steps = q.steps; b.splits = q.splits; b.steps_per_split = q.steps_per_split;
+        if (q.splits == 1) b.part = nullptr;
+        b.whole = (b.N & 3) == 0 && (b.ldy & 3) == 0;
+        return one(b, q);
+    };
     if (a.ldy == 0) a.ldy = a.N;
-    a.whole = (a.N & 3) == 0 && (a.ldy & 3) == 0;
-    if (p.n_main) {  // never with an operand along k
-        const int64_t n = p.n_main, es = dtype == SSD_BF16 ? 2 : 4;
-        LinearArgs b = a;
-        LinearPlan first = p, second = p;
-        first.n_main = second.n_main = 0;
-        second.bm = p.rest_bm; second.bn = p.rest_bn; second.nm = p.rest_nm; second.nn = p.rest_nn;
-        a.N = (int)n;
-        b.N -= (int)n;
-        b.w = static_cast<const char *>(b.w) + n * b.ldw;
-        if (mx) b.wscale += n * b.lds;
-        if (b.bias) b.bias += n;
-        if (b.res) b.res = static_cast<const char *>(b.res) + n * es;
-        if (b.pre) b.pre = static_cast<char *>(b.pre) + n * es;
-        b.y = static_cast<char *>(b.y) + n * es;
-        const ssd_status st = launch_linear(a, first, mx, dtype, s);
-        return st != SSD_OK ? st : launch_linear(b, second, mx, dtype, s);
-    }
-    if (mx) return run_linear<kMX, bf16>(a, p, s);
-    if (a.wt) return a.xt ? run_tile<kBF16, bf16, true, true, false>(a, p, s) : run_tile<kBF16, bf16, false, true, false>(a, p, s);
-    return dtype == SSD_BF16 ? run_linear<kBF16, bf16>(a, p, s) : run_linear<kF32, float>(a, p, s);
+    if (!p.n_main) return go(a, p);
+    // never with an operand along k
+    const int64_t n = p.n_main;
+    LinearArgs b = a;
+    LinearPlan rest = p;
+    rest.bm = p.rest_bm; rest.bn = p.rest_bn; rest.nm = p.rest_nm; rest.nn = p.rest_nn;
+    a.N = (int)n;
+    b.N -= (int)n;
+    b.w = static_cast<const char *>(b.w) + n * b.ldw;
+    if (b.wscale) b.wscale += n * b.lds;
+    if (b.ws) b.ws += n;
+    if (b.bias) b.bias += n;
+    if (b.res) b.res = static_cast<const char *>(b.res) + n * es;
+    if (b.pre) b.pre = static_cast<char *>(b.pre) + n * es;
+    b.y = static_cast<char *>(b.y) + n * es;
+    const ssd_status st = go(a, p);
+    return st != SSD_OK ? st : go(b, rest);
+}
+
+#ifdef SSD_INT_TU
+ssd_status launch_linear_int(const LinearArgs &a, const LinearPlan &p, ssd_dtype dtype, hipStream_t s) {
+    return in_parts(a, p, dtype == SSD_BF16 ? 2 : 4, [&](const LinearArgs &b, const LinearPlan &q) {
+        return dtype == SSD_BF16 ? run_linear<kInt, bf16>(b, q, s) : run_linear<kInt, float>(b, q, s);
+    });
+}
+#else
+ssd_status launch_linear(LinearArgs a, const LinearPlan &p, bool mx, ssd_dtype dtype, hipStream_t s) {
+    return in_parts(a, p, dtype == SSD_BF16 ? 2 : 4, [&](const LinearArgs &b, const LinearPlan &q) {
+        if (mx) return run_linear<kMX, bf16>(b, q, s);
+        if (b.wt) return b.xt ? run_tile<kBF16, bf16, true, true, false>(b, q, s) : run_tile<kBF16, bf16, false, true, false>(b, q, s);
+        return dtype == SSD_BF16 ? run_linear<kBF16, bf16>(b, q, s) : run_linear<kF32, float>(b, q, s);
+    });
 }
 
 template <typename U>
@@ -1130,5 +1169,6 @@ ssd_status launch_dz(const void *dy, const void *pre, int act, void *dz, float *
     return dtype == SSD_BF16 ? run_dz<bf16>(dy, pre, act, dz, part, M, N, ldz, s)
                              : run_dz<float>(dy, pre, act, dz, part, M, N, ldz, s);
 }
+#endif  // SSD_INT_TU
 
 }  // namespace ssd
