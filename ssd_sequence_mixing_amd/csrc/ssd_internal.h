@@ -275,9 +275,14 @@ struct GatedArgs {
     float *final, *dinit, *drate;
     float *part;                 // backward: shares of drate
     int64_t batch, T, D, nchunks;
+    int cols;                    // pieces of 64 channels
+    uint32_t *ticket;            // workspace, cleared before: the next chunk to take; per (batch, chunk, column) ...
+    uint64_t *pieces;            // ... its decay and its own state's end,
+    uint32_t *ends;              // ... and the state behind it
 };
 struct GatedPlan {
     bool fits;
+    int64_t cols, nchunks, tiles;  // pieces of 64 channels, chunks, and chunks of all sequences and columns
     int64_t fwd_bytes, bwd_bytes;  // workspace
     int64_t rate_bytes;            // the backward's, beside that, for the rates' gradient
 };
