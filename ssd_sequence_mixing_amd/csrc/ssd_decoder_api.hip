@@ -82,7 +82,7 @@ extern "C" {
 
 size_t ssd_gated_scan_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, ssd_dtype dtype) {
     if (check_gated(batch, seqlen, dim, SSD_DECAY_LOG, (int)dtype) != SSD_OK) return (size_t)-1;
-    return (size_t)ssd::gated_plan(batch, seqlen, dim, dtype).fwd_bytes;
+    return (size_t)ssd::gated_plan(batch, seqlen, dim, dtype).word_bytes;
 }
 
 ssd_status ssd_gated_scan_fwd(const void *x, int64_t ldx, const void *f, int64_t ldf, const void *in_gate, int64_t ldi,
@@ -100,7 +100,7 @@ ssd_status ssd_gated_scan_fwd(const void *x, int64_t ldx, const void *f, int64_t
                    (const char *)final_state, (const char *)states))
         return SSD_ERR_ALIGN;
     const ssd::GatedPlan plan = ssd::gated_plan(batch, seqlen, dim, dtype);
-    if ((st = check_workspace(plan.fwd_bytes, workspace, workspace_bytes)) != SSD_OK) return st;
+    if ((st = check_workspace(plan.word_bytes, workspace, workspace_bytes)) != SSD_OK) return st;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const int64_t nb = batch * dim * 4;
     if (any_overlap({{y, rows * dim * es}, {final_state, nb}, {states, nb * chunks(seqlen)}},
@@ -118,7 +118,7 @@ ssd_status ssd_gated_scan_fwd(const void *x, int64_t ldx, const void *f, int64_t
 size_t ssd_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int decay, ssd_dtype dtype) {
     if (check_gated(batch, seqlen, dim, decay, (int)dtype) != SSD_OK) return (size_t)-1;
     const ssd::GatedPlan p = ssd::gated_plan(batch, seqlen, dim, dtype);
-    return (size_t)(p.bwd_bytes + (decay == SSD_DECAY_RATE ? p.rate_bytes : 0));
+    return (size_t)(p.word_bytes + (decay == SSD_DECAY_RATE ? p.rate_bytes : 0));
 }
 
 ssd_status ssd_gated_scan_bwd(const void *dy, const void *x, int64_t ldx, const void *f, int64_t ldf, const void *in_gate,
@@ -138,7 +138,7 @@ ssd_status ssd_gated_scan_bwd(const void *dy, const void *x, int64_t ldx, const 
                    (const char *)dx, (const char *)df, (const char *)d_in_gate, (const char *)drate, (const char *)d_initial_state))
         return SSD_ERR_ALIGN;
     const ssd::GatedPlan plan = ssd::gated_plan(batch, seqlen, dim, dtype);
-    const int64_t need = plan.bwd_bytes + (has_rate ? plan.rate_bytes : 0);
+    const int64_t need = plan.word_bytes + (has_rate ? plan.rate_bytes : 0);
     if ((st = check_workspace(need, workspace, workspace_bytes)) != SSD_OK) return st;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const int64_t nb = batch * dim * 4, n = rows * dim * es;

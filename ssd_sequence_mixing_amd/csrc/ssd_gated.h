@@ -30,8 +30,10 @@ struct Gate {
 };
 template <bool kFine>
 __device__ __forceinline__ Gate gate_of(float v) {
-    const float e = exp_of<kFine>(-fabsf(v)), r = __builtin_amdgcn_rcpf(1.f + e), er = e * r;
-    return v < 0.f ? Gate{er, r} : Gate{r, er};
+    float e = exp_of<kFine>(-v);
+    e = e > 0x1p126f ? 0x1p126f : e;  // sigmoid(v) below 2^-126 counts as 2^-126
+    const float s = __builtin_amdgcn_rcpf(1.f + e);
+    return {s, e * s};
 }
 
 // 1 - e^(2 x) for x <= 0, given e^x: near zero by its series, where the difference would cancel (8 terms to
@@ -96,6 +98,16 @@ struct Packed {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
         return __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
     }
+    // Hides from the compiler that the values are those loaded: it would keep what was made of them in registers
+    // that it does not have, where making it again is meant.
+    __device__ __forceinline__ void forget() {
+#pragma unroll
+        for (int k = 0; k < V * (int)sizeof(T) / 4; ++k) {
+            uint32_t u = w[k];
+            asm volatile("" : "+v"(u));
+            w[k] = u;
+        }
+    }
     static __device__ __forceinline__ void store(T *p, const float (&v)[V]) {
         word o;
         if constexpr (sizeof(T) == 4) {
@@ -113,6 +125,15 @@ struct Packed<T, 1> {
     T w;
     __device__ __forceinline__ void load(const T *p) { w = *p; }
     __device__ __forceinline__ float get(int) const { return (float)w; }
+    __device__ __forceinline__ void forget() {
+        if constexpr (sizeof(T) == 4) {
+            asm volatile("" : "+v"(w));
+        } else {
+            uint32_t u = __builtin_bit_cast(uint16_t, w);
+            asm volatile("" : "+v"(u));
+            w = __builtin_bit_cast(T, (uint16_t)u);
+        }
+    }
     static __device__ __forceinline__ void store(T *p, const float (&v)[1]) { *p = (T)v[0]; }
 };
 
@@ -192,5 +213,23 @@ __device__ __forceinline__ float entering(const uint64_t *pieces, const uint32_t
         if (from + j < k) h = pass(__uint_as_float((uint32_t)w[j]), __uint_as_float((uint32_t)(w[j] >> 32)), h);
     return h;
 }
+
+// fn(types...) for the call's storage type, decay and whether the input is gated.
+template <typename F>
+static ssd_status pick_gated(ssd_dtype dtype, int decay, bool in, F fn) {
+    auto two = [&](auto t, auto dec) {
+        return in ? fn(t, dec, std::true_type{}) : fn(t, dec, std::false_type{});
+    };
+    auto one = [&](auto t) {
+        if (decay == SSD_DECAY_LOG) return two(t, std::integral_constant<int, SSD_DECAY_LOG>{});
+        if (decay == SSD_DECAY_SIGMOID) return two(t, std::integral_constant<int, SSD_DECAY_SIGMOID>{});
+        return two(t, std::integral_constant<int, SSD_DECAY_RATE>{});
+    };
+    return dtype == SSD_BF16 ? one(bf16{}) : one(float{});
+}
+inline ssd_status status_of(hipError_t e) { return e == hipSuccess ? SSD_OK : SSD_ERR_HIP; }
+
+// Lays the chunks' words out at `workspace`, and has them cleared where there are several chunks (ssd_gated.hip).
+ssd_status clear_words(GatedArgs &a, const GatedPlan &p, void *workspace, hipStream_t s);
 
 }  // namespace ssd

@@ -148,44 +148,6 @@ __device__ __forceinline__ float at(const void *p, int64_t i) {
 constexpr int kThreads = 256;
 
 template <typename T, int DECAY, bool IN>
-__global__ __launch_bounds__(kThreads) void k_gated_bwd(GatedArgs a) {
-    const int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (k >= a.batch * a.D) return;
-    const int64_t b = k / a.D, d = k - b * a.D;
-    const float rate = DECAY == SSD_DECAY_RATE ? a.rate[d] : 0.f;
-    float back = a.dfinal ? a.dfinal[k] : 0.f, drate = 0.f;
-    float before[SSD_GATED_CHUNK];
-    for (int64_t c = a.nchunks - 1; c >= 0; --c) {
-        float h = a.states[(b * a.nchunks + c) * a.D + d];
-        const int64_t t0 = c * SSD_GATED_CHUNK, n = a.T - t0 < SSD_GATED_CHUNK ? a.T - t0 : SSD_GATED_CHUNK;
-        for (int pass = 0; pass < 2; ++pass)
-            for (int64_t j = 0; j < n; ++j) {
-                const int64_t row = b * a.T + t0 + (pass ? n - 1 - j : j);
-                const Decay g = decay_of<DECAY, true, true>(at<T>(a.f, row * a.ldf + d), rate);
-                const float x = at<T>(a.x, row * a.ldx + d);
-                Gate in = {1.f, 0.f};
-                if constexpr (IN) in = gate_of<true>(at<T>(a.i, row * a.ldi + d));
-                const float v = x * in.s;
-                const bool cut = a.reset && a.reset[row];  // what lies before may be infinite or NaN: left out, not multiplied by 0
-                if (!pass) {
-                    before[j] = cut ? 0.f : h;
-                    h = (cut ? 0.f : g.a * h) + g.c * v;
-                } else {
-                    const float dh = at<T>(a.dy, row * a.D + d) + back;
-                    back = cut ? 0.f : g.a * dh;
-                    const float dla = back * before[n - 1 - j] + dh * g.slope * v;
-                    reinterpret_cast<T *>(a.dx)[row * a.D + d] = (T)(dh * g.c * in.s);
-                    if constexpr (IN) reinterpret_cast<T *>(a.di)[row * a.D + d] = (T)(dh * g.c * v * in.n);
-                    reinterpret_cast<T *>(a.df)[row * a.D + d] = (T)(dla * g.p);
-                    drate += dla * g.s;
-                }
-            }
-    }
-    if (a.dinit) a.dinit[k] = back;
-    if (DECAY == SSD_DECAY_RATE && a.part) a.part[k] = drate;
-}
-
-template <typename T, int DECAY, bool IN>
 __global__ __launch_bounds__(kThreads) void k_gated_step(GatedStepArgs a) {
     const int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (k >= a.rows * a.D) return;
@@ -200,21 +162,6 @@ __global__ __launch_bounds__(kThreads) void k_gated_step(GatedStepArgs a) {
     reinterpret_cast<T *>(a.y)[k] = (T)h;
 }
 
-// fn(types...) for the call's storage type, decay and whether the input is gated.
-template <typename F>
-static ssd_status pick(ssd_dtype dtype, int decay, bool in, F fn) {
-    auto two = [&](auto t, auto dec) {
-        return in ? fn(t, dec, std::true_type{}) : fn(t, dec, std::false_type{});
-    };
-    auto one = [&](auto t) {
-        if (decay == SSD_DECAY_LOG) return two(t, std::integral_constant<int, SSD_DECAY_LOG>{});
-        if (decay == SSD_DECAY_SIGMOID) return two(t, std::integral_constant<int, SSD_DECAY_SIGMOID>{});
-        return two(t, std::integral_constant<int, SSD_DECAY_RATE>{});
-    };
-    return dtype == SSD_BF16 ? one(bf16{}) : one(float{});
-}
-static ssd_status status_of(hipError_t e) { return e == hipSuccess ? SSD_OK : SSD_ERR_HIP; }
-
 GatedPlan gated_plan(int64_t batch, int64_t T, int64_t D, ssd_dtype) {
     GatedPlan p = {};
     p.cols = (D + kCols - 1) / kCols;
@@ -224,27 +171,26 @@ GatedPlan gated_plan(int64_t batch, int64_t T, int64_t D, ssd_dtype) {
     if (!p.fits) return p;
     p.tiles = batch * p.cols * p.nchunks;
     // the ticket, then a chunk's (a, h) and its end for each column
-    p.fwd_bytes = p.nchunks > 1 && p.tiles ? 256 + p.tiles * kCols * 12 : 0;
-    p.rate_bytes = (batch * D * 4 + 255) & ~(int64_t)255;
+    p.word_bytes = p.nchunks > 1 && p.tiles ? 256 + p.tiles * kCols * 12 : 0;
+    p.rate_bytes = batch * p.nchunks * D * 4;
     return p;
 }
 
-// The words that chunks hand their states on with, where there are several.
-static ssd_status clear_words(GatedArgs &a, const GatedPlan &p, void *workspace, hipStream_t s) {
+ssd_status clear_words(GatedArgs &a, const GatedPlan &p, void *workspace, hipStream_t s) {
     a.cols = (int)p.cols;
     if (p.nchunks == 1) return SSD_OK;
     char *ws = static_cast<char *>(workspace);
     a.ticket = reinterpret_cast<uint32_t *>(ws);
     a.pieces = reinterpret_cast<uint64_t *>(ws + 256);
     a.ends = reinterpret_cast<uint32_t *>(ws + 256 + p.tiles * kCols * 8);
-    const int64_t n16 = p.fwd_bytes / 16, blocks = (n16 + 255) / 256;
+    const int64_t n16 = p.word_bytes / 16, blocks = (n16 + 255) / 256;
     return status_of(launch(k_gated_clear, dim3((unsigned)(blocks < 1024 ? blocks : 1024)), dim3(256), s, (u32x4 *)ws, n16));
 }
 
 ssd_status launch_gated_fwd(GatedArgs a, const GatedPlan &p, ssd_dtype dtype, int decay, void *workspace, hipStream_t s) {
     const ssd_status st = clear_words(a, p, workspace, s);
     if (st != SSD_OK) return st;
-    return pick(dtype, decay, a.i != nullptr, [&](auto t, auto dec, auto in) {
+    return pick_gated(dtype, decay, a.i != nullptr, [&](auto t, auto dec, auto in) {
         using T = decltype(t);
         constexpr int DECAY = decltype(dec)::value, V = 16 / (int)sizeof(T);
         constexpr bool IN = decltype(in)::value;
@@ -253,18 +199,8 @@ ssd_status launch_gated_fwd(GatedArgs a, const GatedPlan &p, ssd_dtype dtype, in
     });
 }
 
-ssd_status launch_gated_bwd(GatedArgs a, const GatedPlan &, ssd_dtype dtype, int decay, void *workspace, hipStream_t s) {
-    a.part = static_cast<float *>(workspace);
-    const ssd_status st = pick(dtype, decay, a.i != nullptr, [&](auto t, auto dec, auto in) {
-        return status_of(launch(k_gated_bwd<decltype(t), decltype(dec)::value, decltype(in)::value>,
-                                dim3((unsigned)((a.batch * a.D + kThreads - 1) / kThreads)), dim3(kThreads), s, a));
-    });
-    if (st != SSD_OK || !a.drate) return st;
-    return launch_column_sums(a.part, a.drate, (int)a.batch, a.D, s);
-}
-
 ssd_status launch_gated_step(const GatedStepArgs &a, ssd_dtype dtype, int decay, hipStream_t s) {
-    return pick(dtype, decay, a.i != nullptr, [&](auto t, auto dec, auto in) {
+    return pick_gated(dtype, decay, a.i != nullptr, [&](auto t, auto dec, auto in) {
         return status_of(launch(k_gated_step<decltype(t), decltype(dec)::value, decltype(in)::value>,
                                 dim3((unsigned)((a.rows * a.D + kThreads - 1) / kThreads)), dim3(kThreads), s, a));
     });

@@ -273,7 +273,7 @@ struct GatedArgs {
     float *states;               // (batch, nchunks, D): written by the forward (or null), read by the backward
     void *y, *dx, *df, *di;
     float *final, *dinit, *drate;
-    float *part;                 // backward: shares of drate
+    float *part;                 // backward: shares of drate, (batch, nchunks, D)
     int64_t batch, T, D, nchunks;
     int cols;                    // pieces of 64 channels
     uint32_t *ticket;            // workspace, cleared before: the next chunk to take; per (batch, chunk, column) ...
@@ -283,8 +283,8 @@ struct GatedArgs {
 struct GatedPlan {
     bool fits;
     int64_t cols, nchunks, tiles;  // pieces of 64 channels, chunks, and chunks of all sequences and columns
-    int64_t fwd_bytes, bwd_bytes;  // workspace
-    int64_t rate_bytes;            // the backward's, beside that, for the rates' gradient
+    int64_t word_bytes;            // workspace of either pass
+    int64_t rate_bytes;            // the backward's, behind that, for the rates' gradient
 };
 GatedPlan gated_plan(int64_t batch, int64_t T, int64_t D, ssd_dtype dtype);
 ssd_status launch_gated_fwd(GatedArgs a, const GatedPlan &p, ssd_dtype dtype, int decay, void *workspace, hipStream_t s);
