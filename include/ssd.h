@@ -576,10 +576,10 @@ ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, int act,
  *
  *   SSD_DECAY_LOG      a = e^f, c = 1 (f <= 0: log-decays)
  *   SSD_DECAY_SIGMOID  a = sigmoid(f), c = 1 - a
- *   SSD_DECAY_RATE     a = e^(rate[d] sigmoid(f)), c = sqrt(1 - a^2) (rate <= 0; c = 0 where 1 - a^2 < 2^-100)
+ *   SSD_DECAY_RATE     a = e^(rate[d] sigmoid(f)), c = sqrt(1 - a^2) (a positive rate counts as 0; c = 0 where 1 - a^2 is)
  *
  *   x, f, in_gate (batch, seqlen, dim)  dtype    in_gate is i, or NULL (v = x). ldx, ldf, ldi: values
- *                   from one token to the next, at least dim, tokens of one sequence behind the last
+ *                   from one token to the next, dim to 2^22, tokens of one sequence behind the last
  *                   one's (the parts of one projection's output need no copies); aligned to their type only
  *   rate (dim)      float32, with SSD_DECAY_RATE (else NULL)
  *   reset (batch, seqlen)  uint8 or NULL: where it is not 0, h_{t-1} is left out (a document

@@ -64,10 +64,10 @@ ssd_status check_gated(int64_t batch, int64_t seqlen, int64_t dim, int decay, in
 }
 
 // The inputs of a recurrence, `rows` tokens of them: present, far enough apart, aligned to their type.
-ssd_status check_tokens(const void *x, int64_t ldx, const void *f, int64_t ldf, const void *in_gate, int64_t ldi, int decay,
-                        const float *rate, int64_t rows, int64_t dim, int64_t es) {
+ssd_status check_tokens(const void *x, int64_t ldx, const void *f, int64_t ldf, const void *in_gate, int64_t ldi, int64_t dim,
+                        int64_t es) {
     if (ldx < dim || ldf < dim || (in_gate && ldi < dim)) return SSD_ERR_SHAPE;
-    const int64_t most = INT64_MAX / 8 / (rows > 0 ? rows : 1);  // the last token's address
+    constexpr int64_t most = (int64_t)1 << 22;  // a chunk's 128 tokens within 2^31 bytes
     if (ldx > most || ldf > most || (in_gate && ldi > most)) return SSD_ERR_UNSUPPORTED;
     if (((uintptr_t)x | (uintptr_t)f | (uintptr_t)in_gate) & (uintptr_t)(es - 1)) return SSD_ERR_ALIGN;
     return SSD_OK;
@@ -95,7 +95,7 @@ ssd_status ssd_gated_scan_fwd(const void *x, int64_t ldx, const void *f, int64_t
     if (st != SSD_OK) return st;
     if (decay != SSD_DECAY_RATE && rate) return SSD_ERR_UNSUPPORTED;
     const int64_t rows = batch * seqlen, es = esize(dtype);
-    if ((st = check_tokens(x, ldx, f, ldf, in_gate, ldi, decay, rate, rows, dim, es)) != SSD_OK) return st;
+    if ((st = check_tokens(x, ldx, f, ldf, in_gate, ldi, dim, es)) != SSD_OK) return st;
     if (misaligned((const char *)y, (const char *)rate, (const char *)reset, (const char *)initial_state,
                    (const char *)final_state, (const char *)states))
         return SSD_ERR_ALIGN;
@@ -133,7 +133,7 @@ ssd_status ssd_gated_scan_bwd(const void *dy, const void *x, int64_t ldx, const 
     if (st != SSD_OK) return st;
     if (!has_rate && (rate || drate)) return SSD_ERR_UNSUPPORTED;
     const int64_t rows = batch * seqlen, es = esize(dtype);
-    if ((st = check_tokens(x, ldx, f, ldf, in_gate, ldi, decay, rate, rows, dim, es)) != SSD_OK) return st;
+    if ((st = check_tokens(x, ldx, f, ldf, in_gate, ldi, dim, es)) != SSD_OK) return st;
     if (misaligned((const char *)dy, (const char *)rate, (const char *)reset, (const char *)states, (const char *)d_final_state,
                    (const char *)dx, (const char *)df, (const char *)d_in_gate, (const char *)drate, (const char *)d_initial_state))
         return SSD_ERR_ALIGN;
@@ -167,7 +167,7 @@ ssd_status ssd_gated_step(const float *state_in, float *state_out, const int32_t
     if (rows < 0 || dim <= 0 || src_rows < 0 || (!parent && src_rows < rows)) return SSD_ERR_SHAPE;
     if (dim > kMostDim || rows > INT32_MAX / dim || src_rows > INT32_MAX) return SSD_ERR_UNSUPPORTED;
     const int64_t es = esize(dtype);
-    ssd_status st = check_tokens(x, ldx, f, ldf, in_gate, ldi, decay, rate, rows, dim, es);
+    ssd_status st = check_tokens(x, ldx, f, ldf, in_gate, ldi, dim, es);
     if (st != SSD_OK) return st;
     if (misaligned((const char *)state_in, (const char *)state_out, (const char *)parent, (const char *)rate, (const char *)y))
         return SSD_ERR_ALIGN;

@@ -36,45 +36,35 @@ __device__ __forceinline__ Gate gate_of(float v) {
     return {s, e * s};
 }
 
-// 1 - e^(2 x) for x <= 0, given e^x: near zero by its series, where the difference would cancel (8 terms to
-// x = -1/4: 2^-26 of it; 6 to -1/8: 2^-24).
+// 1 - 4^y for y <= 0, given e = 2^y: near zero by its series, where the difference would cancel (8 terms to
+// 2 y ln 2 = -1/2: 2^-26 of it; 6 to -1/4: 2^-24).
 template <bool kFine>
-__device__ __forceinline__ float one_minus_square(float x, float e) {
-    const float z = x + x;
-    float q;
-    if constexpr (kFine) q = 1 / 720.f + z * (1 / 5040.f + z * (1 / 40320.f));
-    else q = 1 / 720.f;
-    q = 1.f + z * (1 / 2.f + z * (1 / 6.f + z * (1 / 24.f + z * (1 / 120.f + z * q))));
-    return z > (kFine ? -0.5f : -0.25f) ? -z * q : __builtin_fmaf(-e, e, 1.f);
+__device__ __forceinline__ float one_minus_square(float y, float e) {
+    constexpr double l = 2 * 0.69314718055994531;
+    constexpr float k1 = l, k2 = l * l / 2, k3 = l * l * l / 6, k4 = l * l * l * l / 24, k5 = k4 * l / 5, k6 = k5 * l / 6, k7 = k6 * l / 7,
+                    k8 = k7 * l / 8;
+    float q = kFine ? k6 + y * (k7 + y * k8) : k6;
+    q = k1 + y * (k2 + y * (k3 + y * (k4 + y * (k5 + y * q))));
+    return y > (kFine ? -0.36f : -0.18f) ? -y * q : __builtin_fmaf(-e, e, 1.f);
 }
 
-// A token's decay and its input's coefficient; for the gradients slope = d c / d log a,
-// p = d log a / d f and s = sigmoid(f).
+// What a token's gate makes: its decay and its input's coefficient. rate2: rate log2 e, at most 0.
 struct Decay {
-    float a, c, slope, p, s;
+    float a, c;
 };
-template <int DECAY, bool kFine, bool kSlopes>
-__device__ __forceinline__ Decay decay_of(float f, float rate) {
-    Decay o = {};
-    if constexpr (DECAY == SSD_DECAY_LOG) {
-        o.a = exp_of<kFine>(f);
-        o.c = 1.f; o.p = 1.f;
-    } else if constexpr (DECAY == SSD_DECAY_SIGMOID) {
+template <int DECAY, bool kFine>
+__device__ __forceinline__ Decay decay_of(float f, float rate2) {
+    if constexpr (DECAY == SSD_DECAY_LOG) return {exp_of<kFine>(f), 1.f};
+    if constexpr (DECAY == SSD_DECAY_SIGMOID) {
         const Gate g = gate_of<kFine>(f);
-        o.a = g.s; o.c = g.n; o.slope = -g.s; o.p = g.n;
-    } else {
-        Gate g = {};
-        if constexpr (kSlopes) g = gate_of<kFine>(f);
-        else g.s = sigmoid_of<kFine>(f);
-        const float la = rate * g.s;
-        o.a = exp_of<kFine>(la);
-        const float c2 = one_minus_square<kFine>(la, o.a);
-        // a decay of 1 (and above: a positive rate) takes no input, and has no slope
-        const float r = c2 < 0x1p-100f ? 0.f : __builtin_amdgcn_rsqf(c2);
-        o.c = c2 * r; o.slope = -o.a * o.a * r; o.p = la * g.n; o.s = g.s;
+        return {g.s, g.n};
     }
-    return o;
+    const float y = rate2 * sigmoid_of<kFine>(f), a = fast_exp2(y);
+    const float c2 = one_minus_square<kFine>(y, a);
+    return {a, c2 * __builtin_amdgcn_rsqf(fmaxf(c2, 0x1p-100f))};
 }
+// A positive rate counts as 0; in two steps, so that its rounding does not follow that of the product.
+__device__ __forceinline__ float base2(float rate) { return (rate > 0.f ? 0.f : rate) * kLog2e; }
 
 // ---------------------------------------------------------------------------
 // A work-group takes a chunk of SSD_GATED_CHUNK tokens of 64 channels. V consecutive channels (16
@@ -108,17 +98,19 @@ struct Packed {
             w[k] = u;
         }
     }
-    static __device__ __forceinline__ void store(T *p, const float (&v)[V]) {
-        word o;
-        if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) o[e] = __float_as_uint(v[e]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < V / 2; ++e) o[e] = __builtin_bit_cast(uint32_t, bf16x2{(bf16)v[2 * e], (bf16)v[2 * e + 1]});
+    // Set in ascending order, two to a word in 16 bits. Formed here and now: the compiler would put the last steps
+    // off to the store, and keep what they are made of until then.
+    __device__ __forceinline__ void set(int e, float v) {
+        if (sizeof(T) == 2 && !(e & 1)) {
+            w[e >> 1] = __float_as_uint(v);
+            return;
         }
-        *reinterpret_cast<word *>(p) = o;
+        uint32_t u = __float_as_uint(v);
+        if constexpr (sizeof(T) == 2) u = __builtin_bit_cast(uint32_t, bf16x2{(bf16)__uint_as_float(w[e >> 1]), (bf16)v});
+        asm volatile("" : "+v"(u));
+        w[e * (int)sizeof(T) / 4] = u;
     }
+    __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<word *>(p) = w; }
 };
 template <typename T>
 struct Packed<T, 1> {
@@ -134,41 +126,90 @@ struct Packed<T, 1> {
             w = __builtin_bit_cast(T, (uint16_t)u);
         }
     }
-    static __device__ __forceinline__ void store(T *p, const float (&v)[1]) { *p = (T)v[0]; }
+    __device__ __forceinline__ void set(int, float v) {
+        w = (T)v;
+        forget();
+    }
+    __device__ __forceinline__ void store(T *p) const { *p = w; }
+};
+
+// A tensor's tokens from a chunk's first one on: token i's channel d at a 32-bit offset from one address
+// for the work-group.
+template <typename T>
+struct Tokens {
+    const char *p;
+    uint32_t ld, at;  // bytes
+    __device__ __forceinline__ Tokens(const void *q, int64_t row, int64_t ld_, int i, int d)
+        : p(reinterpret_cast<const char *>(q) + row * ld_ * (int64_t)sizeof(T)), ld((uint32_t)ld_ * (uint32_t)sizeof(T)),
+          at((uint32_t)i * ld + (uint32_t)d * (uint32_t)sizeof(T)) {}
+    __device__ __forceinline__ const T *operator[](int r) const { return reinterpret_cast<const T *>(p + (uint32_t)r * ld + at); }
+    __device__ __forceinline__ T *out(int r) const { return const_cast<T *>((*this)[r]); }
 };
 
 // v where keep is all ones, 0 where it is 0, whatever v.
 __device__ __forceinline__ float masked(float v, uint32_t keep) { return __uint_as_float(__float_as_uint(v) & keep); }
-// A state passed through a piece: decay a (exactly 0 where a reset lies in it), own state h.
-__device__ __forceinline__ float pass(float a, float h, float in) { return a == 0.f ? h : __builtin_fmaf(a, in, h); }
+// A state passed through a piece: decay a, own state h. RESET: a is 0 where one lies in the piece, and then what
+// enters may be anything.
+template <bool RESET>
+__device__ __forceinline__ float pass(float a, float h, float in) {
+    return RESET && a == 0.f ? h : __builtin_fmaf(a, in, h);
+}
+template <bool RESET>
+__device__ __forceinline__ float cut(float v, uint32_t keep) { return RESET ? masked(v, keep) : v; }
 
 // ---------------------------------------------------------------------------
 // Handing states on. Work-groups take their chunks by ticket, those of all sequences and columns before the
-// next ones along the sequence, so a chunk's predecessors have begun whenever it has. Each publishes its chunk's
+// next ones along the sequence, so a chunk's predecessors belong to work-groups that have begun whenever it does, and
+// that wait for earlier chunks only: every wait ends. A ticket is for several chunks in this order, one after the
+// other: tickets are given out one each 13 ns, which for 4096 chunks would be as long as reading them. Each publishes its chunk's
 // (a, h), waits for the state kWindow chunks back, and passes it through the (a, h) of
 // those between, always in this order: the same inputs give the same bits. A word is published once, by one
 // store that nothing else has to be ordered with, into memory that k_gated_clear has filled with ones,
 // which no published word is.
 // ---------------------------------------------------------------------------
-constexpr int kWindow = 8;
+constexpr int kWindow = 4;
 
 struct Tile {
     int64_t b;
     int chunk, col;  // along the order of the walk; first channel / kCols
 };
-// The ticket's chunk (no ticket: a single chunk, which waits for none). Every thread of the work-group calls it.
-__device__ __forceinline__ Tile take_tile(uint32_t *ticket, int64_t batch, int cols) {
-    __shared__ uint32_t mine;
-    uint32_t t = blockIdx.x;
-    if (ticket) {
-        if (threadIdx.x == 0) mine = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        t = __builtin_amdgcn_readfirstlane(mine);
+// A work-group's way through its tiles, `share` to a ticket (no ticket: one tile, of a single chunk, which waits for
+// none). Every thread holds the same.
+struct Way {
+    uint32_t now, end;
+    __device__ __forceinline__ Way(const GatedArgs &a, uint32_t *mine) {
+        uint32_t t = blockIdx.x;
+        if (a.ticket) {
+            if (threadIdx.x == 0) *mine = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __syncthreads();
+            t = __builtin_amdgcn_readfirstlane(*mine);
+            __syncthreads();
+        }
+        set(a, t);
     }
-    const uint32_t wide = (uint32_t)batch * (uint32_t)cols;
-    const uint32_t chunk = t / wide, in = t - chunk * wide;
-    const uint32_t b = in / (uint32_t)cols;
-    return {b, (int)chunk, (int)(in - b * (uint32_t)cols)};
+    __device__ __forceinline__ void set(const GatedArgs &a, uint32_t t) {
+        now = t * a.share;
+        end = min(now + a.share, a.tiles);
+    }
+    // The next ticket, where the last tile of one is under way: ask() for it early (thread 0 holds the answer),
+    // tell() it to the others in front of a barrier, go_on() behind that.
+    __device__ __forceinline__ uint32_t ask(const GatedArgs &a) const {
+        if (a.ticket && now + 1 >= end && threadIdx.x == 0)
+            return __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        return 0;
+    }
+    __device__ __forceinline__ void tell(uint32_t next, uint32_t *mine) const {
+        if (now + 1 >= end && threadIdx.x == 0) *mine = next;
+    }
+    __device__ __forceinline__ void go_on(const GatedArgs &a, const uint32_t *mine) {
+        if (++now < end) return;
+        if (a.ticket) set(a, __builtin_amdgcn_readfirstlane(*mine));
+        else now = a.tiles;
+    }
+};
+__device__ __forceinline__ Tile tile_of(uint32_t t, uint32_t batch, uint32_t cols) {
+    const uint32_t wide = batch * cols, chunk = t / wide, in = t - chunk * wide, b = in / cols;
+    return {b, (int)chunk, (int)(in - b * cols)};
 }
 
 __device__ __forceinline__ void publish(uint32_t *word, float v) {
@@ -186,39 +227,48 @@ __device__ __forceinline__ W peek(const W *word) {
     return __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The state that enters chunk k of this lane's column, first being the one that enters chunk 0. pieces and
-// ends: the column's words of chunk 0, `stride` apart.
-__device__ __forceinline__ float entering(const uint64_t *pieces, const uint32_t *ends, int64_t stride, int k, float first) {
-    const int from = k > kWindow ? k - kWindow : 0;
-    float h = first;
-    if (from > 0) {
-        uint32_t u;
-        while ((u = peek(ends + (from - 1) * stride)) == ~0u) __builtin_amdgcn_s_sleep(2);
-        h = __uint_as_float(u);
-    }
+// The words from which the state that enters chunk k of this lane's column follows: the state kWindow chunks back (none
+// where the sequence begins within them), and the pieces since. pieces and ends: the columns' words of chunk 0,
+// `stride` apart. look() asks for them, and state() waits, looking again where one was not there yet; loads that the
+// wavefront issues in between, and whose results are further away, do not stand in the way of the first look.
+template <bool RESET>
+struct Entering {
     uint64_t w[kWindow];
-    for (;;) {
-        bool all = true;
+    uint32_t end;
+    __device__ __forceinline__ void look(const uint64_t *pieces, const uint32_t *ends, int64_t stride, int lane, int k) {
+        const int from = max(k - kWindow, 0);
+        end = 0;
+        if (from > 0) end = peek(ends + (from - 1) * stride + lane);
 #pragma unroll
         for (int j = 0; j < kWindow; ++j) {
             w[j] = 0;
-            if (from + j < k) w[j] = peek(pieces + (from + j) * stride);
-            all = all && w[j] != ~(uint64_t)0;
+            if (from + j < k) w[j] = peek(pieces + (from + j) * stride + lane);
         }
-        if (all) break;
-        __builtin_amdgcn_s_sleep(2);
     }
+    // first: what enters chunk 0
+    __device__ __forceinline__ float state(const uint64_t *pieces, const uint32_t *ends, int64_t stride, int lane, int k, float first) {
+        for (;;) {
+            bool all = end != ~0u;
 #pragma unroll
-    for (int j = 0; j < kWindow; ++j)
-        if (from + j < k) h = pass(__uint_as_float((uint32_t)w[j]), __uint_as_float((uint32_t)(w[j] >> 32)), h);
-    return h;
-}
+            for (int j = 0; j < kWindow; ++j) all = all && w[j] != ~(uint64_t)0;
+            if (all) break;
+            __builtin_amdgcn_s_sleep(1);
+            look(pieces, ends, stride, lane, k);
+        }
+        float h = k > kWindow ? __uint_as_float(end) : first;
+#pragma unroll
+        for (int j = 0; j < kWindow; ++j)
+            if (max(k - kWindow, 0) + j < k) h = pass<RESET>(__uint_as_float((uint32_t)w[j]), __uint_as_float((uint32_t)(w[j] >> 32)), h);
+        return h;
+    }
+};
 
-// fn(types...) for the call's storage type, decay and whether the input is gated.
+// fn(types...) for the call's storage type, decay, whether the input is gated and whether there are resets.
 template <typename F>
-static ssd_status pick_gated(ssd_dtype dtype, int decay, bool in, F fn) {
+static ssd_status pick_gated(ssd_dtype dtype, int decay, bool in, bool reset, F fn) {
     auto two = [&](auto t, auto dec) {
-        return in ? fn(t, dec, std::true_type{}) : fn(t, dec, std::false_type{});
+        if (reset) return in ? fn(t, dec, std::true_type{}, std::true_type{}) : fn(t, dec, std::false_type{}, std::true_type{});
+        return in ? fn(t, dec, std::true_type{}, std::false_type{}) : fn(t, dec, std::false_type{}, std::false_type{});
     };
     auto one = [&](auto t) {
         if (decay == SSD_DECAY_LOG) return two(t, std::integral_constant<int, SSD_DECAY_LOG>{});

@@ -21,123 +21,155 @@ __global__ __launch_bounds__(256) void k_gated_clear(u32x4 *words, int64_t n16) 
         words[i] = i < 16 ? u32x4{0, 0, 0, 0} : u32x4{~0u, ~0u, ~0u, ~0u};
 }
 
-template <typename T, int DECAY, bool IN, int V>
-__global__ __launch_bounds__(kGatedThreads, 4) void k_gated_fwd(GatedArgs a) {
+template <typename T, int DECAY, bool IN, bool RESET, int V>
+__global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) void k_gated_fwd(GatedArgs a) {
     using S = Shape<T, V>;
     constexpr int R = S::R, LPR = S::LPR, GPW = S::GPW;
     constexpr bool kFine = sizeof(T) == 4;
     __shared__ __attribute__((aligned(16))) float ga[S::G][kCols], gh[S::G][kCols];  // the groups' decays and ends, then (gh) entering states
-    __shared__ float wa[kGatedWaves][kCols], wh[kGatedWaves][kCols], carry[kCols];
-    const Tile tile = take_tile(a.ticket, a.batch, a.cols);
+    // by turns, since a wavefront that is done with a tile writes the next one's while others still read
+    __shared__ float wa2[2][kGatedWaves][kCols], wh2[2][kGatedWaves][kCols], carry2[2][kCols];
+    __shared__ uint32_t mine;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int j = lane % LPR, g = w * GPW + lane / LPR;
-    const int D = (int)a.D, c0 = tile.col * kCols;
+    const int D = (int)a.D;
+
+    // a tile's inputs, as stored; the next tile's are asked for as soon as this one's have been used
+    Packed<T, V> x[R], f[R], in[IN ? R : 1];
+    uint8_t marks[RESET ? R : 1];
+    float rate[V];
+    auto load = [&](const Tile &tile) {
+        const int c0 = tile.col * kCols, d = min(c0 + j * V, D - V);
+        const int n = c0 + j * V < D ? min(R, (int)a.T - tile.chunk * SSD_GATED_CHUNK - g * R) : 0;
+        const int64_t row0 = tile.b * a.T + (int64_t)tile.chunk * SSD_GATED_CHUNK;
+        const Tokens<T> px(a.x, row0, a.ldx, g * R, d), pf(a.f, row0, a.ldf, g * R, d), pi(a.i, row0, a.ldi, g * R, d);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            x[r] = {}; f[r] = {};
+            if constexpr (IN) in[r] = {};
+            if constexpr (RESET) marks[r] = 0;
+            if (r < n) {
+                f[r].load(pf[r]);
+                x[r].load(px[r]);
+                if constexpr (IN) in[r].load(pi[r]);
+                if constexpr (RESET) marks[r] = a.reset[row0 + g * R + r];
+            }
+        }
+        if constexpr (DECAY == SSD_DECAY_RATE) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) rate[e] = a.rate[d + e];
+        }
+    };
+    Way way(a, &mine);
+    if (way.now >= a.tiles) return;
+    Tile tile = tile_of(way.now, (uint32_t)a.batch, (uint32_t)a.cols);
+    load(tile);
+    for (uint32_t turn = 0;; ++turn) {
+    auto &wa = wa2[turn & 1], &wh = wh2[turn & 1];
+    auto &carry = carry2[turn & 1];
+    const int c0 = tile.col * kCols;
     const bool live = c0 + j * V < D;
     const int d = min(c0 + j * V, D - V);  // this lane's channels
     const int t0 = tile.chunk * SSD_GATED_CHUNK + g * R;
     const int n = live ? min(R, (int)a.T - t0) : 0;  // its tokens
-    const int64_t row = tile.b * a.T + t0;
+    uint32_t bits = 0;
+    if constexpr (RESET) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) bits |= marks[r] ? 1u << r : 0u;
+    }
+    auto keep = [&](int r) { return bits >> r & 1 ? 0u : ~0u; };
 
-    Packed<T, V> x[R], f[R], in[IN ? R : 1];
-    uint32_t keep[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        x[r] = {}; f[r] = {};
-        if constexpr (IN) in[r] = {};
-        keep[r] = ~0u;
-        if (r < n) {
-            f[r].load(reinterpret_cast<const T *>(a.f) + (row + r) * a.ldf + d);
-            x[r].load(reinterpret_cast<const T *>(a.x) + (row + r) * a.ldx + d);
-            if constexpr (IN) in[r].load(reinterpret_cast<const T *>(a.i) + (row + r) * a.ldi + d);
-        }
-    }
-    if (a.reset) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            if (r < n && a.reset[row + r]) keep[r] = 0u;
-    }
-    float rate[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) rate[e] = DECAY == SSD_DECAY_RATE && live ? a.rate[d + e] : 0.f;
+    const uint32_t next = way.ask(a);
 
     float h[R][V], p[R][V];
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const Decay q = decay_of<DECAY, kFine, false>(f[r].get(e), rate[e]);
+            // (behind the last token these are of no use, and of no harm: nobody takes what follows it)
+            const Decay q = decay_of<DECAY, kFine>(f[r].get(e), DECAY == SSD_DECAY_RATE ? base2(rate[e]) : 0.f);
             float v = x[r].get(e);
             if constexpr (IN) v *= sigmoid_of<kFine>(in[r].get(e));
             const float u = q.c * v;
-            // tokens behind the end pass the state on
-            const float dec = r < n ? q.a : 1.f, add = r < n ? u : 0.f;
-            h[r][e] = r ? __builtin_fmaf(dec, masked(h[r ? r - 1 : 0][e], keep[r]), add) : add;
-            p[r][e] = masked(r ? p[r ? r - 1 : 0][e] * dec : dec, keep[r]);
+            h[r][e] = r ? __builtin_fmaf(q.a, cut<RESET>(h[r ? r - 1 : 0][e], keep(r)), u) : u;
+            p[r][e] = cut<RESET>(r ? p[r ? r - 1 : 0][e] * q.a : q.a, keep(r));
         }
 #pragma unroll
     for (int e = 0; e < V; ++e) ga[g][j * V + e] = p[R - 1][e], gh[g][j * V + e] = h[R - 1][e];
     __builtin_amdgcn_wave_barrier();
     // this wavefront's groups, a column to a lane
-    float qa[GPW], qh[GPW], pa = 1.f, ph = 0.f;
+    float pa = 1.f, ph = 0.f;
 #pragma unroll
     for (int k = 0; k < GPW; ++k) {
-        qa[k] = ga[w * GPW + k][lane];
-        qh[k] = gh[w * GPW + k][lane];
-        ph = pass(qa[k], qh[k], ph);
-        pa *= qa[k];
+        const float q = ga[w * GPW + k][lane];
+        ph = pass<RESET>(q, gh[w * GPW + k][lane], ph);
+        pa *= q;
     }
     wa[w][lane] = pa;
     wh[w][lane] = ph;
+    way.tell(next, &mine);
     __syncthreads();
-    if (w == 0) {
-        // the channel of this lane's column
-        const int base = c0 + lane / V * V, ch = min(base, D - V) + lane % V;
-        const bool there = base < D;
-        const int64_t at = tile.b * D + ch;
-        float first = 0.f;
-        if (a.init && there) first = a.init[at];
-        if (a.nchunks > 1) {
-            float ca = 1.f, chh = 0.f;
+    const Tile here = tile;
+    // wavefront 0 takes the chunk as a whole, a column to a lane: of the channel ch
+    const int base = c0 + lane / V * V, ch = min(base, D - V) + lane % V;
+    const bool there = base < D;
+    const int64_t stride = (int64_t)a.cols * kCols, words = here.b * a.nchunks * stride + c0;
+    float ca = 1.f, chunk_h = 0.f;
+    Entering<RESET> entering;
+    if (w == 0 && a.nchunks > 1) {
 #pragma unroll
-            for (int k = 0; k < kGatedWaves; ++k) {
-                chh = pass(wa[k][lane], wh[k][lane], chh);
-                ca *= wa[k][lane];
-            }
-            const int64_t stride = (int64_t)a.cols * kCols;
-            uint64_t *pieces = a.pieces + tile.b * a.nchunks * stride + c0 + lane;
-            uint32_t *ends = a.ends + tile.b * a.nchunks * stride + c0 + lane;
-            const int k = tile.chunk;
-            publish(pieces + k * stride, ca, chh);
-            first = entering(pieces, ends, stride, k, first);
-            publish(ends + k * stride, pass(ca, chh, first));
+        for (int k = 0; k < kGatedWaves; ++k) {
+            chunk_h = pass<RESET>(wa[k][lane], wh[k][lane], chunk_h);
+            ca *= wa[k][lane];
+        }
+        publish(a.pieces + words + here.chunk * stride + lane, ca, chunk_h);
+        entering.look(a.pieces + words, a.ends + words, stride, lane, here.chunk);
+    }
+    way.go_on(a, &mine);
+    const bool more = way.now < a.tiles;
+    if (more) {
+        tile = tile_of(way.now, (uint32_t)a.batch, (uint32_t)a.cols);
+        load(tile);
+    }
+    if (w == 0) {
+        float first = 0.f;
+        if (a.init && there) first = a.init[here.b * D + ch];
+        if (a.nchunks > 1) {
+            first = entering.state(a.pieces + words, a.ends + words, stride, lane, here.chunk, first);
+            publish(a.ends + words + here.chunk * stride + lane, pass<RESET>(ca, chunk_h, first));
         }
         carry[lane] = first;
-        if (a.states && there) a.states[(tile.b * a.nchunks + tile.chunk) * D + ch] = first;
+        if (a.states && there) a.states[(here.b * a.nchunks + here.chunk) * D + ch] = first;
     }
     __syncthreads();
     float s = carry[lane];
-    for (int k = 0; k < w; ++k) s = pass(wa[k][lane], wh[k][lane], s);
+    for (int k = 0; k < w; ++k) s = pass<RESET>(wa[k][lane], wh[k][lane], s);
 #pragma unroll
     for (int k = 0; k < GPW; ++k) {
+        const float own = gh[w * GPW + k][lane];
         gh[w * GPW + k][lane] = s;
-        s = pass(qa[k], qh[k], s);
-    }
-    if (w == kGatedWaves - 1 && a.final && tile.chunk == a.nchunks - 1) {
-        const int base = c0 + lane / V * V;
-        if (base < D) a.final[tile.b * D + min(base, D - V) + lane % V] = s;
+        s = pass<RESET>(ga[w * GPW + k][lane], own, s);
     }
     __builtin_amdgcn_wave_barrier();
+    const Tokens<T> py(a.y, here.b * a.T + (int64_t)here.chunk * SSD_GATED_CHUNK, D, g * R, d);
     uint32_t open = ~0u;
     float from[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) from[e] = gh[g][j * V + e];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        open &= keep[r];
-        float o[V];
+        open &= keep(r);
+        const bool last = r < n && t0 + r == a.T - 1 && a.final;
+        Packed<T, V> o;
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = __builtin_fmaf(p[r][e], masked(from[e], open), h[r][e]);
-        if (r < n) Packed<T, V>::store(reinterpret_cast<T *>(a.y) + (row + r) * D + d, o);
+        for (int e = 0; e < V; ++e) {
+            const float v = __builtin_fmaf(p[r][e], cut<RESET>(from[e], open), h[r][e]);
+            if (last) a.final[here.b * D + d + e] = v;
+            o.set(e, v);
+        }
+        if (r < n) o.store(py.out(r));
+    }
+    if (!more) return;
     }
 }
 
@@ -154,9 +186,9 @@ __global__ __launch_bounds__(kThreads) void k_gated_step(GatedStepArgs a) {
     const int64_t b = k / a.D, d = k - b * a.D;
     const int64_t from = a.parent ? a.parent[b] : b;
     float h = from >= 0 && from < a.src ? a.state_in[from * a.D + d] : 0.f;
-    const Decay g = decay_of<DECAY, true, true>(at<T>(a.f, b * a.ldf + d), DECAY == SSD_DECAY_RATE ? a.rate[d] : 0.f);
+    const Decay g = decay_of<DECAY, true>(at<T>(a.f, b * a.ldf + d), DECAY == SSD_DECAY_RATE ? base2(a.rate[d]) : 0.f);
     float v = at<T>(a.x, b * a.ldx + d);
-    if constexpr (IN) v *= gate_of<true>(at<T>(a.i, b * a.ldi + d)).s;
+    if constexpr (IN) v *= sigmoid_of<true>(at<T>(a.i, b * a.ldi + d));
     h = g.a * h + g.c * v;
     a.state_out[k] = h;
     reinterpret_cast<T *>(a.y)[k] = (T)h;
@@ -170,6 +202,10 @@ GatedPlan gated_plan(int64_t batch, int64_t T, int64_t D, ssd_dtype) {
     p.fits = batch == 0 || T == 0 || (batch <= most / p.cols && batch * p.cols <= most / p.nchunks);
     if (!p.fits) return p;
     p.tiles = batch * p.cols * p.nchunks;
+    // tiles of a ticket, and work-groups: 2 for each CU
+    p.share = p.nchunks > 1 && p.tiles > 1024 ? 2 : 1;
+    p.groups = (p.tiles + p.share - 1) / p.share;
+    if (p.nchunks > 1 && p.groups > 512) p.groups = 512;
     // the ticket, then a chunk's (a, h) and its end for each column
     p.word_bytes = p.nchunks > 1 && p.tiles ? 256 + p.tiles * kCols * 12 : 0;
     p.rate_bytes = batch * p.nchunks * D * 4;
@@ -178,6 +214,8 @@ GatedPlan gated_plan(int64_t batch, int64_t T, int64_t D, ssd_dtype) {
 
 ssd_status clear_words(GatedArgs &a, const GatedPlan &p, void *workspace, hipStream_t s) {
     a.cols = (int)p.cols;
+    a.share = (uint32_t)p.share;
+    a.tiles = (uint32_t)p.tiles;
     if (p.nchunks == 1) return SSD_OK;
     char *ws = static_cast<char *>(workspace);
     a.ticket = reinterpret_cast<uint32_t *>(ws);
@@ -190,17 +228,17 @@ ssd_status clear_words(GatedArgs &a, const GatedPlan &p, void *workspace, hipStr
 ssd_status launch_gated_fwd(GatedArgs a, const GatedPlan &p, ssd_dtype dtype, int decay, void *workspace, hipStream_t s) {
     const ssd_status st = clear_words(a, p, workspace, s);
     if (st != SSD_OK) return st;
-    return pick_gated(dtype, decay, a.i != nullptr, [&](auto t, auto dec, auto in) {
+    return pick_gated(dtype, decay, a.i != nullptr, a.reset != nullptr, [&](auto t, auto dec, auto in, auto reset) {
         using T = decltype(t);
         constexpr int DECAY = decltype(dec)::value, V = 16 / (int)sizeof(T);
-        constexpr bool IN = decltype(in)::value;
-        auto go = [&](auto k) { return status_of(launch(k, dim3((unsigned)p.tiles), dim3(kGatedThreads), s, a)); };
-        return a.D >= V ? go(k_gated_fwd<T, DECAY, IN, V>) : go(k_gated_fwd<T, DECAY, IN, 1>);
+        constexpr bool IN = decltype(in)::value, RESET = decltype(reset)::value;
+        auto go = [&](auto k) { return status_of(launch(k, dim3((unsigned)p.groups), dim3(kGatedThreads), s, a)); };
+        return a.D >= V ? go(k_gated_fwd<T, DECAY, IN, RESET, V>) : go(k_gated_fwd<T, DECAY, IN, RESET, 1>);
     });
 }
 
 ssd_status launch_gated_step(const GatedStepArgs &a, ssd_dtype dtype, int decay, hipStream_t s) {
-    return pick_gated(dtype, decay, a.i != nullptr, [&](auto t, auto dec, auto in) {
+    return pick_gated(dtype, decay, a.i != nullptr, false, [&](auto t, auto dec, auto in, auto) {
         return status_of(launch(k_gated_step<decltype(t), decltype(dec)::value, decltype(in)::value>,
                                 dim3((unsigned)((a.rows * a.D + kThreads - 1) / kThreads)), dim3(kThreads), s, a));
     });

@@ -12,15 +12,21 @@
 
 namespace ssd {
 
-template <typename T, int DECAY, bool IN, int V>
-__global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a) {
+template <typename T, int DECAY, bool IN, bool RESET, int V>
+__global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) void k_gated_bwd(GatedArgs a) {
     using S = Shape<T, V>;
     constexpr int R = S::R, LPR = S::LPR, GPW = S::GPW;
     constexpr bool kFine = sizeof(T) == 4, kRate = DECAY == SSD_DECAY_RATE;
     // the groups' decays, ends of h and of G; then the values that enter them
     __shared__ __attribute__((aligned(16))) float ga[S::G][kCols], gh[S::G][kCols], gg[S::G][kCols];
-    __shared__ float wa[kGatedWaves][kCols], wh[kGatedWaves][kCols], wg[kGatedWaves][kCols], carry[kCols];
-    const Tile tile = take_tile(a.ticket, a.batch, a.cols);
+    // by turns, since a wavefront that is done with a tile writes the next one's while others still read
+    __shared__ float wa2[2][kGatedWaves][kCols], wh2[2][kGatedWaves][kCols], wg2[2][kGatedWaves][kCols], carry2[2][kCols];
+    __shared__ uint32_t mine;
+    Way way(a, &mine);
+    for (uint32_t turn = 0; way.now < a.tiles; ++turn) {
+    const Tile tile = tile_of(way.now, (uint32_t)a.batch, (uint32_t)a.cols);
+    auto &wa = wa2[turn & 1], &wh = wh2[turn & 1], &wg = wg2[turn & 1];
+    auto &carry = carry2[turn & 1];
     const int chunk = (int)a.nchunks - 1 - tile.chunk;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int j = lane % LPR, g = w * GPW + lane / LPR;
@@ -29,7 +35,8 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a) {
     const int d = min(c0 + j * V, D - V);
     const int t0 = chunk * SSD_GATED_CHUNK + g * R;
     const int n = live ? min(R, (int)a.T - t0) : 0;
-    const int64_t row = tile.b * a.T + t0;
+    const int64_t row0 = tile.b * a.T + (int64_t)chunk * SSD_GATED_CHUNK;
+    const Tokens<T> px(a.x, row0, a.ldx, g * R, d), pf(a.f, row0, a.ldf, g * R, d), pi(a.i, row0, a.ldi, g * R, d), py(a.dy, row0, D, g * R, d);
     // the channel of this lane's column
     const int base = c0 + lane / V * V, ch = min(base, D - V) + lane % V;
     const bool there = base < D;
@@ -42,43 +49,46 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a) {
         if constexpr (IN) in[r] = {};
         keep[r] = ~0u;
         if (r < n) {
-            f[r].load(reinterpret_cast<const T *>(a.f) + (row + r) * a.ldf + d);
-            x[r].load(reinterpret_cast<const T *>(a.x) + (row + r) * a.ldx + d);
-            if constexpr (IN) in[r].load(reinterpret_cast<const T *>(a.i) + (row + r) * a.ldi + d);
-            dy[r].load(reinterpret_cast<const T *>(a.dy) + (row + r) * D + d);
+            f[r].load(pf[r]);
+            x[r].load(px[r]);
+            if constexpr (IN) in[r].load(pi[r]);
+            dy[r].load(py[r]);
         }
     }
     float enter = 0.f;  // the state before the chunk, of this lane's column
     if (there) enter = a.states[(tile.b * a.nchunks + chunk) * D + ch];
-    if (a.reset) {
+    if constexpr (RESET) {
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            if (r < n && a.reset[row + r]) keep[r] = 0u;
+            if (r < n && a.reset[row0 + g * R + r]) keep[r] = 0u;
     }
-    float rate[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) rate[e] = kRate && live ? a.rate[d + e] : 0.f;
-
+    // read where it is needed, twice, and not kept
+    auto rate = [&](int e) { return kRate ? base2(a.rate[d + e]) : 0.f; };
+    const uint32_t next = way.ask(a);
     float dec[R][V], c[R][V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
+        const float rate2 = rate(e);
         float h = 0.f, p = 1.f, back = 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const Decay q = decay_of<DECAY, kFine, false>(f[r].get(e), rate[e]);
+            const Decay q = decay_of<DECAY, kFine>(f[r].get(e), rate2);
             float v = x[r].get(e);
             if constexpr (IN) v *= sigmoid_of<kFine>(in[r].get(e));
-            // tokens behind the end pass both on
-            dec[r][e] = r < n ? q.a : 1.f;
-            c[r][e] = r < n ? q.c : 0.f;
-            h = __builtin_fmaf(dec[r][e], masked(h, keep[r]), c[r][e] * v);
-            p = masked(p * dec[r][e], keep[r]);
+            // tokens behind the last one, with x and dy zero, hand G on as it is
+            const float dec_r = r < n ? q.a : 1.f;
+            dec[r][e] = dec_r;
+            c[r][e] = q.c;
+            h = r ? __builtin_fmaf(dec_r, cut<RESET>(h, keep[r]), q.c * v) : q.c * v;
+            p = cut<RESET>(r ? p * dec_r : dec_r, keep[r]);
         }
 #pragma unroll
-        for (int r = R - 1; r >= 0; --r) back = masked(dec[r][e] * (dy[r].get(e) + back), keep[r]);
+        for (int r = R - 1; r >= 0; --r)
+            back = cut<RESET>(dec[r][e] * (dy[r].get(e) + back), keep[r]);
         ga[g][j * V + e] = p;
         gh[g][j * V + e] = h;
         gg[g][j * V + e] = back;
+        if (e & 1) __builtin_amdgcn_sched_barrier(0);
     }
     __builtin_amdgcn_wave_barrier();
     // this wavefront's groups, a column to a lane
@@ -86,112 +96,112 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a) {
 #pragma unroll
     for (int k = 0; k < GPW; ++k) {
         const float q = ga[w * GPW + k][lane];
-        ph = pass(q, gh[w * GPW + k][lane], ph);
+        ph = pass<RESET>(q, gh[w * GPW + k][lane], ph);
         pa *= q;
     }
 #pragma unroll
-    for (int k = GPW - 1; k >= 0; --k) pg = pass(ga[w * GPW + k][lane], gg[w * GPW + k][lane], pg);
+    for (int k = GPW - 1; k >= 0; --k) pg = pass<RESET>(ga[w * GPW + k][lane], gg[w * GPW + k][lane], pg);
     wa[w][lane] = pa;
     wh[w][lane] = ph;
     wg[w][lane] = pg;
+    way.tell(next, &mine);
     __syncthreads();
+    way.go_on(a, &mine);
     if (w == 0) {
         const int64_t at = tile.b * D + ch;
         float first = 0.f, ca = 1.f, cg = 0.f;
         if (a.dfinal && there) first = a.dfinal[at];
 #pragma unroll
         for (int k = kGatedWaves - 1; k >= 0; --k) {
-            cg = pass(wa[k][lane], wg[k][lane], cg);
+            cg = pass<RESET>(wa[k][lane], wg[k][lane], cg);
             ca *= wa[k][lane];
         }
         if (a.nchunks > 1) {
-            const int64_t stride = (int64_t)a.cols * kCols;
-            uint64_t *pieces = a.pieces + tile.b * a.nchunks * stride + c0 + lane;
-            uint32_t *ends = a.ends + tile.b * a.nchunks * stride + c0 + lane;
+            const int64_t stride = (int64_t)a.cols * kCols, words = tile.b * a.nchunks * stride + c0;
             const int k = tile.chunk;
-            publish(pieces + k * stride, ca, cg);
-            first = entering(pieces, ends, stride, k, first);
-            publish(ends + k * stride, pass(ca, cg, first));
+            publish(a.pieces + words + k * stride + lane, ca, cg);
+            Entering<RESET> entering;
+            entering.look(a.pieces + words, a.ends + words, stride, lane, k);
+            first = entering.state(a.pieces + words, a.ends + words, stride, lane, k, first);
+            publish(a.ends + words + k * stride + lane, pass<RESET>(ca, cg, first));
         }
         carry[lane] = first;
-        if (chunk == 0 && a.dinit && there) a.dinit[at] = pass(ca, cg, first);
+        if (chunk == 0 && a.dinit && there) a.dinit[at] = pass<RESET>(ca, cg, first);
     }
     // the states that enter this wavefront's groups
-    for (int k = 0; k < w; ++k) enter = pass(wa[k][lane], wh[k][lane], enter);
+    for (int k = 0; k < w; ++k) enter = pass<RESET>(wa[k][lane], wh[k][lane], enter);
 #pragma unroll
     for (int k = 0; k < GPW; ++k) {
         const float own = gh[w * GPW + k][lane];
         gh[w * GPW + k][lane] = enter;
-        enter = pass(ga[w * GPW + k][lane], own, enter);
+        enter = pass<RESET>(ga[w * GPW + k][lane], own, enter);
     }
     __syncthreads();
     float back = carry[lane];
-    for (int k = kGatedWaves - 1; k > w; --k) back = pass(wa[k][lane], wg[k][lane], back);
+    for (int k = kGatedWaves - 1; k > w; --k) back = pass<RESET>(wa[k][lane], wg[k][lane], back);
 #pragma unroll
     for (int k = GPW - 1; k >= 0; --k) {
         const float own = gg[w * GPW + k][lane];
         gg[w * GPW + k][lane] = back;
-        back = pass(ga[w * GPW + k][lane], own, back);
+        back = pass<RESET>(ga[w * GPW + k][lane], own, back);
     }
     __builtin_amdgcn_wave_barrier();
-
+    // ga is read for the last time above
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+        x[r].forget();
         f[r].forget();
         if constexpr (IN) in[r].forget();
     }
-    float before[R][V], later[V], sum[V];
+    // channel by channel (in pairs, where two make a stored word), so that its inputs' registers become its outputs'
+    Packed<T, V> dx[R], di[R], df[R];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        sum[e] = 0.f;
-        later[e] = gg[g][j * V + e];
-        before[0][e] = masked(gh[g][j * V + e], keep[0]);
+        float before[R], later = gg[g][j * V + e];
+        before[0] = cut<RESET>(gh[g][j * V + e], keep[0]);
 #pragma unroll
         for (int r = 1; r < R; ++r) {
             float v = x[r - 1].get(e);
             if constexpr (IN) v *= sigmoid_of<kFine>(in[r - 1].get(e));
-            before[r][e] = masked(__builtin_fmaf(dec[r - 1][e], before[r - 1][e], c[r - 1][e] * v), keep[r]);
+            before[r] = cut<RESET>(__builtin_fmaf(dec[r - 1][e], before[r - 1], c[r - 1][e] * v), keep[r]);
         }
-    }
+        const float by_rate = rate(e) * kLn2;
+        float sum = 0.f;
 #pragma unroll
-    for (int r = R - 1; r >= 0; --r) {
-        float dx[V], di[V], df[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float dh = dy[r].get(e) + later[e], xv = x[r].get(e), cc = c[r][e], aa = dec[r][e];
-            later[e] = masked(aa * dh, keep[r]);
+        for (int r = R - 1; r >= 0; --r) {
+            const float dh = dy[r].get(e) + later;
+            const float cc = c[r][e], aa = dec[r][e], u = dh * cc;
+            later = cut<RESET>(aa * dh, keep[r]);
             Gate gi = {1.f, 0.f};
             if constexpr (IN) gi = gate_of<kFine>(in[r].get(e));
-            const float v = xv * gi.s, u = dh * cc;
-            dx[e] = u * gi.s;
-            di[e] = u * v * gi.n;
-            float dla = aa * before[r][e];
+            const float v = x[r].get(e) * gi.s;
+            dx[r].set(e, u * gi.s);
+            if constexpr (IN) di[r].set(e, u * v * gi.n);
+            float dla = aa * before[r];
             if constexpr (DECAY == SSD_DECAY_LOG) {
-                dla *= dh;
-                df[e] = dla;
+                df[r].set(e, dla * dh);
             } else if constexpr (DECAY == SSD_DECAY_SIGMOID) {  // c = sigmoid(-f)
-                dla = dh * __builtin_fmaf(-aa, v, dla);
-                df[e] = dla * cc;
+                df[r].set(e, u * __builtin_fmaf(-aa, v, dla));
             } else {
                 // dc / d log a = -a^2 / c; none where c is 0
                 const float slope = cc > 0.f ? -aa * aa * __builtin_amdgcn_rcpf(cc) : 0.f;
-                dla = dh * __builtin_fmaf(slope, v, dla);
                 const Gate q = gate_of<kFine>(f[r].get(e));
-                const float by = dla * q.s;
-                df[e] = by * q.n * rate[e];
-                sum[e] += r < n ? by : 0.f;
+                const float by = dh * __builtin_fmaf(slope, v, dla) * q.s;
+                df[r].set(e, by * q.n * by_rate);
+                sum += r < n ? by : 0.f;
             }
         }
-        if (r < n) {
-            const int64_t at = (row + r) * D + d;
-            Packed<T, V>::store(reinterpret_cast<T *>(a.dx) + at, dx);
-            if constexpr (IN) Packed<T, V>::store(reinterpret_cast<T *>(a.di) + at, di);
-            Packed<T, V>::store(reinterpret_cast<T *>(a.df) + at, df);
-        }
+        if constexpr (kRate) ga[g][j * V + e] = sum;  // its decays have been read, by this wavefront alone
+        if (e & 1) __builtin_amdgcn_sched_barrier(0);
     }
-    if constexpr (kRate) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) ga[g][j * V + e] = sum[e];  // read so far by this wavefront alone
+    for (int r = 0; r < R; ++r)
+        if (r < n) {
+            dx[r].store(Tokens<T>(a.dx, row0, D, g * R, d).out(r));
+            if constexpr (IN) di[r].store(Tokens<T>(a.di, row0, D, g * R, d).out(r));
+            df[r].store(Tokens<T>(a.df, row0, D, g * R, d).out(r));
+        }
+    if constexpr (kRate) {
         __builtin_amdgcn_wave_barrier();
         float s = 0.f;
 #pragma unroll
@@ -206,18 +216,19 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a) {
             a.part[(tile.b * a.nchunks + chunk) * D + ch] = s;
         }
     }
+    }
 }
 
 ssd_status launch_gated_bwd(GatedArgs a, const GatedPlan &p, ssd_dtype dtype, int decay, void *workspace, hipStream_t s) {
     ssd_status st = clear_words(a, p, workspace, s);
     if (st != SSD_OK) return st;
     a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.word_bytes);
-    st = pick_gated(dtype, decay, a.i != nullptr, [&](auto t, auto dec, auto in) {
+    st = pick_gated(dtype, decay, a.i != nullptr, a.reset != nullptr, [&](auto t, auto dec, auto in, auto reset) {
         using T = decltype(t);
         constexpr int DECAY = decltype(dec)::value, V = 16 / (int)sizeof(T);
-        constexpr bool IN = decltype(in)::value;
-        auto go = [&](auto k) { return status_of(launch(k, dim3((unsigned)p.tiles), dim3(kGatedThreads), s, a)); };
-        return a.D >= V ? go(k_gated_bwd<T, DECAY, IN, V>) : go(k_gated_bwd<T, DECAY, IN, 1>);
+        constexpr bool IN = decltype(in)::value, RESET = decltype(reset)::value;
+        auto go = [&](auto k) { return status_of(launch(k, dim3((unsigned)p.groups), dim3(kGatedThreads), s, a)); };
+        return a.D >= V ? go(k_gated_bwd<T, DECAY, IN, RESET, V>) : go(k_gated_bwd<T, DECAY, IN, RESET, 1>);
     });
     if (st != SSD_OK || !a.drate) return st;
     return launch_column_sums(a.part, a.drate, (int)(a.batch * a.nchunks), a.D, s);

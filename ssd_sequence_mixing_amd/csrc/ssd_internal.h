@@ -276,6 +276,7 @@ struct GatedArgs {
     float *part;                 // backward: shares of drate, (batch, nchunks, D)
     int64_t batch, T, D, nchunks;
     int cols;                    // pieces of 64 channels
+    uint32_t tiles, share;       // chunks of all of those and sequences, and how many a work-group takes
     uint32_t *ticket;            // workspace, cleared before: the next chunk to take; per (batch, chunk, column) ...
     uint64_t *pieces;            // ... its decay and its own state's end,
     uint32_t *ends;              // ... and the state behind it
@@ -283,6 +284,7 @@ struct GatedArgs {
 struct GatedPlan {
     bool fits;
     int64_t cols, nchunks, tiles;  // pieces of 64 channels, chunks, and chunks of all sequences and columns
+    int64_t share, groups;         // chunks of a work-group, and work-groups
     int64_t word_bytes;            // workspace of either pass
     int64_t rate_bytes;            // the backward's, behind that, for the rates' gradient
 };
