@@ -203,7 +203,7 @@ GatedPlan gated_plan(int64_t batch, int64_t T, int64_t D, ssd_dtype) {
     if (!p.fits) return p;
     p.tiles = batch * p.cols * p.nchunks;
     // tiles of a ticket, and work-groups: 2 for each CU
-    p.share = p.nchunks > 1 && p.tiles > 1024 ? 2 : 1;
+    p.share = p.nchunks > 1 && p.tiles > 4096 ? 2 : 1;
     p.groups = (p.tiles + p.share - 1) / p.share;
     if (p.nchunks > 1 && p.groups > 512) p.groups = 512;
     // the ticket, then a chunk's (a, h) and its end for each column
