@@ -673,7 +673,7 @@ ssd_status ssd_embedding_bwd(const void *dy, const int32_t *tokens, float scale,
  *   repetition, presence, frequency (rows)  float32 or NULL (1, 0, 0); repetition > 0
  *   bias (bias_rows, vocab)  float32 or NULL;  mask (mask_rows, ceil(vocab / 32))  int32 or NULL;
  *                         bias_rows, mask_rows: 1 (for all rows) or rows
- * vocab at most 2^28, capacity below 2^31, and rows * ceil((vocab + 7) / 4096) at most 2^24 - 1.
+ * vocab at most 2^28, capacity below 2^31, and rows * ceil((vocab + 7) / 2048) below 2^24.
  */
 ssd_status ssd_logits_process(const void *logits, void *out, const int32_t *tokens, int64_t capacity, const int32_t *lengths,
                               const int32_t *prompt, const float *repetition, const float *presence, const float *frequency,

@@ -6,10 +6,10 @@
 // in a fixed order, r ascending, so that the same inputs give the same bits. A
 // token outside the table is a row of zeros, and adds to no gradient.
 //
-// k_sort: a work-group sorts up to 16384 tokens in LDS (stable, by digits of at
-// most 8 bits); the other work-groups of the launch clear the table meanwhile.
-// More tokens are sorted piece by piece and merged, 8 pieces at a time, each value
-// finding its place by binary search (k_merge). k_sums: a wavefront adds
+// k_sort: a work-group sorts up to 4096 tokens in LDS (stable, by digits of at
+// most 8 bits). More tokens are merged, 8 sorted pieces at a time, each value
+// finding its place by binary search (k_merge). The other work-groups of these launches clear the table
+// meanwhile, each launch a share of it. k_sums: a wavefront adds
 // the rows of `len` places of the sorted list, 256 channels of them; a token whose
 // rows lie within writes its sum to the table, the first and the last one's may go on
 // beyond it, and are kept apart for k_join. Bound: HBM, the table's write.
@@ -20,7 +20,7 @@
 
 namespace ssd {
 
-constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64, kSortKeys = 16;
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64, kSortKeys = 4;
 
 // 4 consecutive values (V: aligned and whole) or one.
 template <typename T, int V>
@@ -67,16 +67,26 @@ __global__ __launch_bounds__(256) void k_embed(const int *tokens, const TT *tabl
     }
 }
 
+// A share of the table to clear: n16 pieces of 16 bytes, and `rest` of 2 behind them.
+struct Share {
+    u32x4 *p;
+    int64_t n16;
+    int rest;
+};
+template <int THREADS>
+__device__ __forceinline__ void clear_share(const Share &c, int64_t block, int64_t blocks) {
+    const int64_t i0 = block * THREADS + threadIdx.x;
+    for (int64_t i = i0; i < c.n16; i += blocks * THREADS) c.p[i] = u32x4{0, 0, 0, 0};
+    if (i0 < c.rest) reinterpret_cast<uint16_t *>(c.p + c.n16)[i0] = 0;
+}
+
 // Work-groups below `tiles` sort a piece of 2^bits tokens each: keys are
 // token << bits | place in the piece, in order of their tokens; out: token << 32 | row.
-// The others clear n16 pieces of 16 bytes, and the rest behind them.
+// The others clear.
 __global__ __launch_bounds__(kSortThreads) void k_sort(const int *tokens, uint64_t *out, int64_t rows, int vocab, int bits, int passes,
-                                                       int digit, int tiles, u32x4 *clear, int64_t n16, int rest) {
+                                                       int digit, int tiles, Share clear) {
     if ((int)blockIdx.x >= tiles) {
-        const int64_t hop = (int64_t)(gridDim.x - tiles) * kSortThreads;
-        const int64_t i0 = (int64_t)((int)blockIdx.x - tiles) * kSortThreads + threadIdx.x;
-        for (int64_t i = i0; i < n16; i += hop) clear[i] = u32x4{0, 0, 0, 0};
-        if (i0 < rest) reinterpret_cast<uint16_t *>(clear + n16)[i0] = 0;
+        clear_share<kSortThreads>(clear, blockIdx.x - tiles, gridDim.x - tiles);
         return;
     }
     __shared__ uint32_t keys[kSortThreads * kSortKeys];
@@ -111,9 +121,8 @@ __global__ __launch_bounds__(kSortThreads) void k_sort(const int *tokens, uint64
                 const uint32_t d = (key[e] >> shift) & (bins - 1);
                 uint64_t same = ~(uint64_t)0;
                 for (int b = 0; b < digit; ++b) {
-                    const bool one = (d >> b) & 1;
-                    const uint64_t ones = __ballot(one);
-                    same &= one ? ones : ~ones;
+                    const int64_t one = -(int64_t)((d >> b) & 1);
+                    same &= ~(__ballot(one != 0) ^ (uint64_t)one);
                 }
                 const uint32_t before = count[w][d];
                 __builtin_amdgcn_wave_barrier();
@@ -163,7 +172,12 @@ __global__ __launch_bounds__(kSortThreads) void k_sort(const int *tokens, uint64
 
 // Sorted runs of `run` values (the last one shorter) merged 8 at a time: a value's place is its own in its run
 // and, of each other run, the number of values below it (no two are equal).
-__global__ __launch_bounds__(256) void k_merge(const uint64_t *in, uint64_t *out, int64_t n, int64_t run) {
+// Work-groups from `blocks` on clear.
+__global__ __launch_bounds__(256) void k_merge(const uint64_t *in, uint64_t *out, int64_t n, int64_t run, int64_t blocks, Share clear) {
+    if (blockIdx.x >= blocks) {
+        clear_share<256>(clear, blockIdx.x - blocks, gridDim.x - blocks);
+        return;
+    }
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
     const uint64_t v = in[i];
@@ -201,7 +215,7 @@ __device__ __forceinline__ void put(const EmbedBwdArgs &a, int64_t token, int d,
 
 template <typename TY, typename TG, int V>
 __global__ __launch_bounds__(64) void k_sums(EmbedBwdArgs a) {
-    constexpr int U = 8;  // rows on their way
+    constexpr int U = 16;  // rows on their way
     const int d = ((int)blockIdx.y * 64 + (int)threadIdx.x) * V;
     const int64_t s = (int64_t)blockIdx.x * a.len, end = min(s + a.len, a.rows);
     const bool live = d < a.dim;
@@ -254,14 +268,15 @@ __global__ __launch_bounds__(256) void k_join(EmbedBwdArgs a) {
     const uint64_t mine = a.sorted[end - 1] >> 32;
     if (mine >= (uint64_t)a.vocab || mine != a.sorted[end] >> 32) return;
     if (mine == a.sorted[s] >> 32 && s > 0 && mine == a.sorted[s - 1] >> 32) return;  // it began earlier
-    // the first place behind the token's rows, and the piece of its last one
-    int64_t lo = end, hi = a.rows;
-    while (lo < hi) {
-        const int64_t m = (lo + hi) >> 1;
-        if (a.sorted[m] >> 32 <= mine) lo = m + 1;
-        else hi = m;
+    // the pieces behind this one that begin with the token: it ends in the last of them
+    int64_t pieces = 0;
+    for (;;) {
+        const int64_t next = (p + 1 + pieces + lane) * a.len;
+        const int n = __popcll(__ballot(next < a.rows && a.sorted[next < a.rows ? next : 0] >> 32 == mine));
+        pieces += n;
+        if (n < 64) break;
     }
-    const int64_t pieces = (lo - 1) / a.len - p, each = (pieces + 3) / 4;  // behind the first
+    const int64_t each = (pieces + 3) / 4;
     const int d = ((int)blockIdx.y * 64 + lane) * V;
     float sum[V];
 #pragma unroll
@@ -269,7 +284,7 @@ __global__ __launch_bounds__(256) void k_join(EmbedBwdArgs a) {
     if (d < a.dim) {
         if (w == 0) load<float, V>(sum, a.part + (p * 2 + 1) * a.dim + d);
         const int64_t to = min((w + 1) * each, pieces);
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t q = w * each; q < to; ++q) {
             float v[V];
             load<float, V>(v, a.part + (p + 1 + q) * 2 * a.dim + d);
@@ -317,7 +332,7 @@ EmbedPlan embed_plan(int64_t rows, int64_t vocab) {
     while ((vocab >> bits) != 0) ++bits;  // of `vocab` itself, which stands for tokens outside the table
     p.passes = (bits + 7) / 8;
     p.digit = (bits + p.passes - 1) / p.passes;
-    p.bits = 32 - bits < 14 ? 32 - bits : 14;
+    p.bits = 32 - bits < 12 ? 32 - bits : 12;
     p.tiles = (rows + ((int64_t)1 << p.bits) - 1) >> p.bits;
     p.len = 16;
     while (p.len < 256 && rows / p.len > 1024) p.len *= 2;
@@ -327,16 +342,31 @@ EmbedPlan embed_plan(int64_t rows, int64_t vocab) {
 
 ssd_status launch_embed_bwd(EmbedBwdArgs a, const EmbedPlan &p, const int *tokens, uint64_t *one, uint64_t *two, ssd_dtype dy_dtype,
                             ssd_dtype dtype, hipStream_t s) {
+    int merges = 0;
+    for (int64_t run = (int64_t)1 << p.bits; run < a.rows; run *= 8) ++merges;
+    // the table is cleared by shares of whole 16 bytes, one beside the sort and each merge
     const int64_t bytes = a.accumulate ? 0 : (int64_t)a.vocab * a.dim * (dtype == SSD_BF16 ? 2 : 4);
-    const int64_t n16 = bytes / 16, rest = bytes % 16 / 2;
-    int64_t fill = (n16 + 4 * kSortThreads - 1) / (4 * kSortThreads);
-    fill = bytes ? (fill < 1 ? 1 : fill > 2048 ? 2048 : fill) : 0;
-    if (p.tiles + fill == 0) return SSD_OK;
-    ssd_status st = status_of(launch(k_sort, dim3((unsigned)(p.tiles + fill)), dim3(kSortThreads), s, tokens, one, a.rows, a.vocab, p.bits,
-                                     p.passes, p.digit, (int)p.tiles, (u32x4 *)a.dtable, n16, (int)rest));
+    const int64_t all = bytes / 16, each = (all + merges) / (merges + 1);
+    auto share = [&](int k) {
+        const int64_t from = k * each < all ? k * each : all, to = k < merges && from + each < all ? from + each : all;
+        return Share{reinterpret_cast<u32x4 *>(a.dtable) + from, to - from, k == merges ? (int)(bytes % 16 / 2) : 0};
+    };
+    auto fill = [&](const Share &c, int64_t per) {  // work-groups, of `per` pieces of 16 bytes each, or up to 2048
+        const int64_t n = (c.n16 + per - 1) / per;
+        return n > 2048 ? 2048 : n > 0 ? n : c.rest ? 1 : 0;
+    };
+    Share c = share(0);
+    int64_t more = fill(c, 4 * kSortThreads);
+    if (p.tiles + more == 0) return SSD_OK;
+    ssd_status st = status_of(launch(k_sort, dim3((unsigned)(p.tiles + more)), dim3(kSortThreads), s, tokens, one, a.rows, a.vocab, p.bits,
+                                     p.passes, p.digit, (int)p.tiles, c));
     if (st != SSD_OK || a.rows == 0) return st;
-    for (int64_t run = (int64_t)1 << p.bits; run < a.rows; run *= 8) {
-        st = status_of(launch(k_merge, dim3((unsigned)((a.rows + 255) / 256)), dim3(256), s, one, two, a.rows, run));
+    for (int k = 1; k <= merges; ++k) {
+        c = share(k);
+        more = fill(c, 4 * 256);
+        const int64_t blocks = (a.rows + 255) / 256;
+        st = status_of(launch(k_merge, dim3((unsigned)(blocks + more)), dim3(256), s, one, two, a.rows, ((int64_t)1 << p.bits) << (3 * (k - 1)),
+                              blocks, c));
         if (st != SSD_OK) return st;
         uint64_t *t = one;
         one = two;

@@ -1,6 +1,11 @@
 // Rows in 8-bit integers for gfx950: scale = max |x| / 127 of the row, and
 // q the integer nearest to x / scale (ties to even). A row of zeros has scale 0; one that holds an
 // infinity or a NaN has scale NaN, and codes 0.
+//
+// A row stays in the registers of one wavefront (many rows) or of 4 or 16, 8 values a lane and load, at any
+// alignment; rows of more than 65536 values are read twice. Bound: HBM, one read and one write.
+// A quotient is formed by the scale's inverse; it is off by 1.5e-5 at most, so that only those within 1e-4
+// of the middle between two codes (one in 5000) need the exact remainder to be decided.
 #include <type_traits>
 
 #include "ssd_common.h"
@@ -8,52 +13,159 @@
 
 namespace ssd {
 
-// The integer nearest to x / s, |x| <= 127 s (1 + 2^-24): the rounded quotient's, put right by
-// the remainder x - q s, which is exact in one fused operation (a multiple of the smaller operand's last place below s).
-__device__ __forceinline__ int code_of(float x, float s) {
+// The integer nearest to x / s, ties to even: one that is at most 1 off, put right by the remainder x - q s, which one
+// fused operation gives exactly (a multiple of the smaller operand's last place, and below 2 s).
+__device__ __forceinline__ float nearest(float x, float s) {
     float q = rintf(x / s);
     const float r = __builtin_fmaf(-q, s, x), half = 0.5f * s;
     const bool odd = ((int)q & 1) != 0;
     if (r > half || (r == half && odd)) q += 1.f;
     else if (r < -half || (r == -half && odd)) q -= 1.f;
-    return (int)fminf(fmaxf(q, -127.f), 127.f);
+    return q;
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void k_int_quantize(const T *x, int8_t *q, float *scale, int64_t rows, int dim) {
-    __shared__ float tops[4];
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const T *p = x + r * dim;
+struct Eight {
+    float v[8];
+    // values from p on, zeros from n on
+    __device__ __forceinline__ void load(const T *p, int n) {
+        typedef uint32_t word __attribute__((ext_vector_type(4), aligned(2)));
+        if (n >= 8) {
+            if constexpr (sizeof(T) == 2) {
+                const word w = *reinterpret_cast<const word *>(p);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+            } else {
+                const word a = *reinterpret_cast<const word *>(p), b = *reinterpret_cast<const word *>(p + 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(a[e]), v[4 + e] = __uint_as_float(b[e]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = e < n ? (float)p[e] : 0.f;
+        }
+    }
+    __device__ __forceinline__ void largest(float &top, bool &bad) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            bad |= !(fabsf(v[e]) < INFINITY);
+            top = fmaxf(top, fabsf(v[e]));
+        }
+    }
+    // Their codes to q, n of them. inv: 1 / s, where that is an ordinary number, or 0.
+    __device__ __forceinline__ void store(int8_t *q, int n, float s, float inv, bool zero) const {
+        constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, which is the sum's lowest byte
+        uint32_t u[8];
+        float far = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float t = v[e] * inv, r = t + kMagic;
+            far = fmaxf(far, fabsf(t - (r - kMagic)));
+            u[e] = __float_as_uint(r);
+        }
+        if (__any(far > 0.4999f || inv == 0.f)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(nearest(v[e], s) + kMagic);
+        }
+        uint32_t w[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t lo = __builtin_amdgcn_perm(u[4 * k + 1], u[4 * k], 0x0c0c0400u);
+            const uint32_t hi = __builtin_amdgcn_perm(u[4 * k + 3], u[4 * k + 2], 0x04000c0cu);
+            w[k] = zero ? 0u : lo | hi;
+        }
+        typedef uint32_t pair __attribute__((ext_vector_type(2), aligned(1)));
+        if (n >= 8) {
+            *reinterpret_cast<pair *>(q) = pair{w[0], w[1]};
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n) q[e] = (int8_t)(w[e >> 2] >> (8 * (e & 3)));
+        }
+    }
+};
+
+// W wavefronts a row (at most 4 of them: 4 / W rows a work-group), NC loads a lane. NC = 0: rows read twice.
+template <typename T, int W, int NC>
+__global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_int_quantize(const T *x, int8_t *q, float *scale, int64_t rows, int dim) {
+    constexpr int RPB = W > 4 ? 1 : 4 / W, kStep = 64 * W * 8;
+    __shared__ float tops[W > 1 ? W : 1];
+    const int t = threadIdx.x % (64 * W), slot = threadIdx.x / (64 * W);
+    const int64_t hop = (int64_t)gridDim.x * RPB;
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += hop) {
+        const int64_t r = r0 + slot;
+        const bool in = r < rows;
+        const T *p = x + (in ? r : 0) * dim;
+        const int n = in ? dim : 0;
+        Eight<T> v[NC ? NC : 1];
         float top = 0.f;
         bool bad = false;
-        for (int d = threadIdx.x; d < dim; d += 256) {
-            const float v = fabsf((float)p[d]);
-            bad |= !(v < INFINITY);
-            top = fmaxf(top, v);
+        if constexpr (NC > 0) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) v[c].load(p + min(c * kStep + t * 8, dim), n - (c * kStep + t * 8));
+#pragma unroll
+            for (int c = 0; c < NC; ++c) v[c].largest(top, bad);
+        } else {
+            for (int d = t * 8; d < n; d += kStep) {
+                v[0].load(p + d, n - d);
+                v[0].largest(top, bad);
+            }
         }
         top = bad ? INFINITY : top;
+#pragma unroll
         for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-        __syncthreads();
-        if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
-        __syncthreads();
-        top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+        if constexpr (W > 1) {
+            if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < W; ++k) top = fmaxf(top, tops[k]);
+            __syncthreads();
+        }
         bad = top == INFINITY;
-        const float s = top / 127.f;
-        for (int d = threadIdx.x; d < dim; d += 256) q[r * dim + d] = bad || s == 0.f ? 0 : (int8_t)code_of((float)p[d], s);
-        if (threadIdx.x == 0) scale[r] = bad ? __builtin_nanf("") : s;
+        const float s = top / 127.f, inv = s > 0x1p-100f ? 1.f / s : 0.f;
+        const bool zero = bad || s == 0.f;
+        int8_t *o = q + (in ? r : 0) * dim;
+        if constexpr (NC > 0) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) v[c].store(o + min(c * kStep + t * 8, dim), n - (c * kStep + t * 8), s, inv, zero);
+        } else {
+            for (int d = t * 8; d < n; d += kStep) {
+                v[0].load(p + d, n - d);
+                v[0].store(o + d, n - d, s, inv, zero);
+            }
+        }
+        if (in && t == 0) scale[r] = bad ? __builtin_nanf("") : s;
     }
 }
 
 ssd_status launch_int_quantize(const void *x, int8_t *q, float *scale, int64_t rows, int64_t dim, ssd_dtype dtype, hipStream_t s) {
-    auto go = [&](auto t) {
+    auto of = [&](auto t) {
         using T = decltype(t);
-        const int64_t most = 1 << 20;
-        return launch(k_int_quantize<T>, dim3((unsigned)(rows < most ? rows : most)), dim3(256), s, (const T *)x, q, scale, rows, (int)dim) ==
-                       hipSuccess
-                   ? SSD_OK
-                   : SSD_ERR_HIP;
+        auto go = [&](auto k, int W) {
+            const int64_t per = W > 4 ? 1 : 4 / W, blocks = (rows + per - 1) / per, most = 1 << 20;
+            return launch(k, dim3((unsigned)(blocks < most ? blocks : most)), dim3(W > 4 ? 64 * W : 256), s, (const T *)x, q, scale, rows,
+                          (int)dim) == hipSuccess
+                       ? SSD_OK
+                       : SSD_ERR_HIP;
+        };
+        // one wavefront a row while a row fits 8 loads a lane (fp32: 4) and there are rows for every SIMD; else 4
+        // of them, whose chain is shorter, or 16
+        const int64_t c = (dim + 511) / 512;
+        const int most = sizeof(T) == 2 ? 8 : 4;
+        if (c == 1) return go(k_int_quantize<T, 1, 1>, 1);
+        if (rows >= 1024 && c <= most) {
+            if (c <= 2) return go(k_int_quantize<T, 1, 2>, 1);
+            if (c <= 4) return go(k_int_quantize<T, 1, 4>, 1);
+            return go(k_int_quantize<T, 1, 8>, 1);
+        }
+        if (c <= 4) return go(k_int_quantize<T, 4, 1>, 4);
+        if (c <= 16) return go(k_int_quantize<T, 4, 4>, 4);
+        if (c <= 32) return go(k_int_quantize<T, 16, 2>, 16);
+        if (c <= 64) return go(k_int_quantize<T, 16, 4>, 16);
+        if (c <= 128) return go(k_int_quantize<T, 16, 8>, 16);
+        return go(k_int_quantize<T, 16, 0>, 16);
     };
-    return dtype == SSD_BF16 ? go(bf16{}) : go(float{});
+    return dtype == SSD_BF16 ? of(bf16{}) : of(float{});
 }
 
 }  // namespace ssd

@@ -276,13 +276,22 @@ __device__ __forceinline__ void bias4(const LinearArgs &a, int n, float (&v)[4])
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = (a.bias && n + i < a.N) ? a.bias[n + i] : 0.f;
 }
-// Sums of integers in 4 consecutive columns of row m, with their scales.
-template <int KIND>
-__device__ __forceinline__ void scale4(const LinearArgs &a, int m, int n, float (&v)[4]) {
-    if constexpr (KIND == kInt) {
-        const float xs = m < a.M ? a.xs[m] : 0.f;
+// Integers: the scales of row m and of 4 consecutive columns, and sums with them.
+__device__ __forceinline__ float row_scale(const LinearArgs &a, int m) { return m < a.M ? a.xs[m] : 0.f; }
+__device__ __forceinline__ void column_scales4(const LinearArgs &a, int n, float (&v)[4]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = (float)__float_as_int(v[i]) * xs * (n + i < a.N ? a.ws[n + i] : 0.f);
+    for (int i = 0; i < 4; ++i) v[i] = n + i < a.N ? a.ws[n + i] : 0.f;
+}
+__device__ __forceinline__ void scale4(float xs, const float (&ws)[4], float (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (float)__float_as_int(v[i]) * xs * ws[i];
+}
+template <int KIND>
+__device__ __forceinline__ void scale4_any(const LinearArgs &a, int m, int n, float (&v)[4]) {
+    if constexpr (KIND == kInt) {
+        float ws[4];
+        column_scales4(a, n, ws);
+        scale4(row_scale(a, m), ws, v);
     }
 }
 template <typename TO, bool kWhole>
@@ -590,11 +599,10 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
         for (int j = 0; j < TN; ++j) *reinterpret_cast<f32x4 *>(piece + r * LDC + j * 16 + kg * 4) = acc[i][j];
         __builtin_amdgcn_wave_barrier();
     };
-    auto staged = [&](int i, int p, float (&v)[4]) {
+    auto staged = [&](int p, float (&v)[4]) {
         const f32x4 c = *reinterpret_cast<const f32x4 *>(piece + row_of(p) * LDC + col_of(p));
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = c[e];
-        scale4<KIND>(a, mw + i * 16 + row_of(p), nw + col_of(p), v);
     };
     if constexpr (EPI == kParts) {
         const bool whole = (a.N & 3) == 0;
@@ -604,8 +612,9 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
                 float v[4];
-                staged(i, p, v);
+                staged(p, v);
                 const int m = mw + i * 16 + row_of(p), n = nw + col_of(p);
+                scale4_any<KIND>(a, m, n, v);
                 if (m < a.M && n < a.N) put4<float>(a.part + blockIdx.y * part_stride(a.M, a.N) + (int64_t)m * a.N + n, v, a.N - n, whole);
             }
             __builtin_amdgcn_wave_barrier();
@@ -614,9 +623,13 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
     }
     if (EPI == SSD_ACT_NONE && a.whole) {
         // the next 16 rows' residual is on its way while 16 rows are finished
-        float bias[NP][4], res[2][NP][4];
+        float bias[NP][4], res[2][NP][4], ws[KIND == kInt ? NP : 1][4], xs[2][KIND == kInt ? NP : 1];
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
+            if constexpr (KIND == kInt) {
+                column_scales4(a, nw + col_of(p), ws[p]);
+                xs[0][p] = row_scale(a, mw + row_of(p));
+            }
             bias4(a, nw + col_of(p), bias[p]);
             res4<TO, true>(a, mw + row_of(p), nw + col_of(p), res[0][p]);
         }
@@ -625,13 +638,16 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
             stage(i);
             if (i + 1 < TM) {
 #pragma unroll
-                for (int p = 0; p < NP; ++p)
+                for (int p = 0; p < NP; ++p) {
                     res4<TO, true>(a, mw + (i + 1) * 16 + row_of(p), nw + col_of(p), res[(i + 1) & 1][p]);
+                    if constexpr (KIND == kInt) xs[(i + 1) & 1][p] = row_scale(a, mw + (i + 1) * 16 + row_of(p));
+                }
             }
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
                 float v[4];
-                staged(i, p, v);
+                staged(p, v);
+                if constexpr (KIND == kInt) scale4(xs[i & 1][p], ws[p], v);
                 finish4<TO, SSD_ACT_NONE, true>(a, mw + i * 16 + row_of(p), nw + col_of(p), v, bias[p], res[i & 1][p]);
             }
             __builtin_amdgcn_wave_barrier();
@@ -647,7 +663,8 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
             const int m = mw + i * 16 + row_of(p), n = nw + col_of(p);
             bias4(a, n, bias);
             res4<TO, kWhole>(a, m, n, res);
-            staged(i, p, v);
+            staged(p, v);
+            scale4_any<KIND>(a, m, n, v);
             finish4<TO, EPI, kWhole>(a, m, n, v, bias, res);
         }
     };
@@ -812,7 +829,7 @@ __global__ __launch_bounds__(512) void k_skinny(LinearArgs a) {
                     else v[e] += q[e];
                 }
             }
-            scale4<KIND>(a, r, n0 + c * 16 + kg * 4, v);
+            scale4_any<KIND>(a, r, n0 + c * 16 + kg * 4, v);
             finish4_any<TO>(a, r, n0 + c * 16 + kg * 4, v);
         }
     }
