@@ -4,8 +4,8 @@
 //
 // A row stays in the registers of one wavefront (many rows) or of 4 or 16, 8 values a lane and load, at any
 // alignment; rows of more than 65536 values are read twice. Bound: HBM, one read and one write.
-// A quotient is formed by the scale's inverse; it is off by 1.5e-5 at most, so that only those within 1e-4
-// of the middle between two codes (one in 5000) need the exact remainder to be decided.
+// A quotient is formed by the scale's inverse; it is off by 1.5e-5 at most, so that only those within 2e-5
+// of the middle between two codes (one in 25000) need the exact remainder to be decided.
 #include <type_traits>
 
 #include "ssd_common.h"
@@ -24,32 +24,42 @@ __device__ __forceinline__ float nearest(float x, float s) {
     return q;
 }
 
+// 8 values of a row, as stored.
 template <typename T>
 struct Eight {
-    float v[8];
+    static constexpr int kWords = 2 * (int)sizeof(T);
+    uint32_t w[kWords];
+    __device__ __forceinline__ float get(int e) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+        return __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+    }
+    // Hides from the compiler that the values are those loaded: it would keep them unpacked, in twice the registers.
+    __device__ __forceinline__ void forget() {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) asm volatile("" : "+v"(w[k]));
+    }
     // values from p on, zeros from n on
     __device__ __forceinline__ void load(const T *p, int n) {
         typedef uint32_t word __attribute__((ext_vector_type(4), aligned(2)));
         if (n >= 8) {
-            if constexpr (sizeof(T) == 2) {
-                const word w = *reinterpret_cast<const word *>(p);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
-            } else {
-                const word a = *reinterpret_cast<const word *>(p), b = *reinterpret_cast<const word *>(p + 4);
+            for (int k = 0; k < kWords; k += 4) {
+                const word q = *reinterpret_cast<const word *>(reinterpret_cast<const char *>(p) + 4 * k);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(a[e]), v[4 + e] = __uint_as_float(b[e]);
+                for (int e = 0; e < 4; ++e) w[k + e] = q[e];
             }
         } else {
+            T v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = e < n ? (float)p[e] : 0.f;
+            for (int e = 0; e < 8; ++e) v[e] = e < n ? p[e] : (T)0.f;
+            __builtin_memcpy(w, v, sizeof v);
         }
     }
     __device__ __forceinline__ void largest(float &top, bool &bad) const {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            bad |= !(fabsf(v[e]) < INFINITY);
-            top = fmaxf(top, fabsf(v[e]));
+            bad |= !(fabsf(get(e)) < INFINITY);
+            top = fmaxf(top, fabsf(get(e)));
         }
     }
     // Their codes to q, n of them. inv: 1 / s, where that is an ordinary number, or 0.
@@ -59,28 +69,28 @@ struct Eight {
         float far = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float t = v[e] * inv, r = t + kMagic;
+            const float t = get(e) * inv, r = t + kMagic;
             far = fmaxf(far, fabsf(t - (r - kMagic)));
             u[e] = __float_as_uint(r);
         }
-        if (__any(far > 0.4999f || inv == 0.f)) {
+        if (__any(far > 0.49998f || inv == 0.f)) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(nearest(v[e], s) + kMagic);
+            for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(nearest(get(e), s) + kMagic);
         }
-        uint32_t w[2];
+        uint32_t o[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const uint32_t lo = __builtin_amdgcn_perm(u[4 * k + 1], u[4 * k], 0x0c0c0400u);
             const uint32_t hi = __builtin_amdgcn_perm(u[4 * k + 3], u[4 * k + 2], 0x04000c0cu);
-            w[k] = zero ? 0u : lo | hi;
+            o[k] = zero ? 0u : lo | hi;
         }
         typedef uint32_t pair __attribute__((ext_vector_type(2), aligned(1)));
         if (n >= 8) {
-            *reinterpret_cast<pair *>(q) = pair{w[0], w[1]};
+            *reinterpret_cast<pair *>(q) = pair{o[0], o[1]};
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (e < n) q[e] = (int8_t)(w[e >> 2] >> (8 * (e & 3)));
+                if (e < n) q[e] = (int8_t)(o[e >> 2] >> (8 * (e & 3)));
         }
     }
 };
@@ -121,6 +131,10 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_int_quantize(const T *
             for (int k = 0; k < W; ++k) top = fmaxf(top, tops[k]);
             __syncthreads();
         }
+        if constexpr (NC > 0) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) v[c].forget();
+        }
         bad = top == INFINITY;
         const float s = top / 127.f, inv = s > 0x1p-100f ? 1.f / s : 0.f;
         const bool zero = bad || s == 0.f;
@@ -148,17 +162,13 @@ ssd_status launch_int_quantize(const void *x, int8_t *q, float *scale, int64_t r
                        ? SSD_OK
                        : SSD_ERR_HIP;
         };
-        // one wavefront a row while a row fits 8 loads a lane (fp32: 4) and there are rows for every SIMD; else 4
-        // of them, whose chain is shorter, or 16
+        // short rows: one wavefront each, if there are rows for every SIMD. Else 4 wavefronts a row, of 1 to 4 loads a
+        // lane (8192 x 4096 in bf16: 27 us, with one wavefront of 8 loads 37), or 16 of them
         const int64_t c = (dim + 511) / 512;
-        const int most = sizeof(T) == 2 ? 8 : 4;
         if (c == 1) return go(k_int_quantize<T, 1, 1>, 1);
-        if (rows >= 1024 && c <= most) {
-            if (c <= 2) return go(k_int_quantize<T, 1, 2>, 1);
-            if (c <= 4) return go(k_int_quantize<T, 1, 4>, 1);
-            return go(k_int_quantize<T, 1, 8>, 1);
-        }
+        if (c == 2 && rows >= 1024) return go(k_int_quantize<T, 1, 2>, 1);
         if (c <= 4) return go(k_int_quantize<T, 4, 1>, 4);
+        if (c <= 8) return go(k_int_quantize<T, 4, 2>, 4);
         if (c <= 16) return go(k_int_quantize<T, 4, 4>, 4);
         if (c <= 32) return go(k_int_quantize<T, 16, 2>, 16);
         if (c <= 64) return go(k_int_quantize<T, 16, 4>, 16);

@@ -29,6 +29,22 @@ __global__ __launch_bounds__(kLogitThreads) void k_logits(LogitsArgs a) {
     // slices begin where a row has 16 aligned bytes: the first one is shorter by what lies before that
     const int lead = (int)(at & (E - 1));
     const int64_t v0 = (int64_t)(blockIdx.x - row * a.slices) * SLICE - lead;  // the slice's place 0
+    const T *in = reinterpret_cast<const T *>(a.logits) + at;
+    T *out = reinterpret_cast<T *>(a.out) + at;
+    union Group {
+        T e[E];
+        u32x4 q;
+    };
+    // every whole group of the slice is on its way before the history is looked at
+    constexpr int N = SLICE / (kLogitThreads * E);
+    const int64_t left = V - v0;
+    const int whole_from = v0 < 0 ? E : 0, whole_to = (int)(left < SLICE ? left / E * E : SLICE);
+    auto place = [&](int k) { return (k * kLogitThreads + (int)threadIdx.x) * E; };
+    auto whole = [&](int p) { return p >= whole_from && p + E <= whole_to; };
+    Group x[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (whole(place(k))) x[k].q = *reinterpret_cast<const u32x4 *>(in + v0 + place(k));
     float rep = 1.f, inv = 1.f, pres = 0.f, freq = 0.f;
     if constexpr (HISTORY) {
         for (int i = threadIdx.x * 4; i < SLICE; i += kLogitThreads * 4) *reinterpret_cast<u32x4 *>(count + i) = u32x4{0, 0, 0, 0};
@@ -58,16 +74,11 @@ __global__ __launch_bounds__(kLogitThreads) void k_logits(LogitsArgs a) {
         for (int64_t k = i; k < len && k < i + 4; ++k) seen(h[k], k);
         __syncthreads();
     }
-    const T *in = reinterpret_cast<const T *>(a.logits) + at;
-    T *out = reinterpret_cast<T *>(a.out) + at;
     const float *bias = DENSE && a.bias ? a.bias + (a.bias_rows > 1 ? at : 0) : nullptr;
     const uint32_t *mask = DENSE && a.mask ? a.mask + (a.mask_rows > 1 ? row * a.words : 0) : nullptr;
-    union Group {
-        T e[E];
-        u32x4 q;
-    };
     // what becomes of the logits of places i .. i + E - 1 of the slice, tokens v and on; others keep their bits
-    auto apply = [&](Group &x, int i, int64_t v, bool whole) {
+    auto apply = [&](Group &x, int i, int64_t v, auto all) {
+        constexpr bool kAll = decltype(all)::value;
         float l[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) l[e] = (float)x.e[e];
@@ -83,7 +94,7 @@ __global__ __launch_bounds__(kLogitThreads) void k_logits(LogitsArgs a) {
         }
         if constexpr (DENSE) {
             if (bias) {
-                if (whole) {
+                if constexpr (kAll) {
 #pragma unroll
                     for (int k = 0; k < E; k += 4) {
                         const u32x4_any b = *reinterpret_cast<const u32x4_any *>(bias + v + k);
@@ -114,28 +125,12 @@ __global__ __launch_bounds__(kLogitThreads) void k_logits(LogitsArgs a) {
 #pragma unroll
         for (int e = 0; e < E; ++e) x.e[e] = touched[e] ? (T)l[e] : x.e[e];
     };
-    const int64_t left = V - v0;
-    // whole groups, two on their way at a time, then the row's ends
-    constexpr int kHop = kLogitThreads * E;
-    const int i0 = (int)threadIdx.x * E;
-    const int whole_from = v0 < 0 ? E : 0, whole_to = (int)(left < SLICE ? left / E * E : SLICE);
-#pragma unroll 1
-    for (int i = i0; i < SLICE; i += 2 * kHop) {
-        Group x[2];
-        bool ok[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int p = i + k * kHop;
-            ok[k] = p >= whole_from && p + E <= whole_to;
-            if (ok[k]) x[k].q = *reinterpret_cast<const u32x4 *>(in + v0 + p);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int p = i + k * kHop;
-            if (ok[k]) {
-                apply(x[k], p, v0 + p, true);
-                *reinterpret_cast<u32x4 *>(out + v0 + p) = x[k].q;
-            }
+    for (int k = 0; k < N; ++k) {
+        const int p = place(k);
+        if (whole(p)) {
+            apply(x[k], p, v0 + p, std::true_type{});
+            *reinterpret_cast<u32x4 *>(out + v0 + p) = x[k].q;
         }
     }
     // a group that the row begins or ends in
@@ -143,13 +138,13 @@ __global__ __launch_bounds__(kLogitThreads) void k_logits(LogitsArgs a) {
     const int mine = threadIdx.x == 0 && whole_from ? 0 : threadIdx.x == 1 && tail >= 0 ? tail : -1;
     if (mine >= 0) {
         const int64_t v = v0 + mine;
-        Group x;
+        Group y;
 #pragma unroll
-        for (int e = 0; e < E; ++e) x.e[e] = v + e >= 0 && v + e < V ? in[v + e] : (T)0.f;
-        apply(x, mine, v, false);
+        for (int e = 0; e < E; ++e) y.e[e] = v + e >= 0 && v + e < V ? in[v + e] : (T)0.f;
+        apply(y, mine, v, std::false_type{});
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            if (v + e >= 0 && v + e < V) out[v + e] = x.e[e];
+            if (v + e >= 0 && v + e < V) out[v + e] = y.e[e];
     }
 }
 
