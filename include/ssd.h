@@ -590,9 +590,12 @@ ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, int act,
  *   states (batch, ceil(seqlen / SSD_GATED_CHUNK), dim)  float32, or NULL: h before
  *                   the first token of each SSD_GATED_CHUNK, for the backward pass
  *
- * Everything in fp32, the gates to a few 2^-24 of themselves. dim at most 2^20, seqlen below 2^31, batch * dim below 2^31. An
+ * Everything in fp32: gates and decays within 2^-22 of themselves for ordinary gates (|f|, |i| to 8; beyond, |f| 2^-24
+ * with bf16 tensors), a sigmoid below 2^-126 is 0 or 2^-126. The same inputs give the same bits. dim at most 2^20, seqlen
+ * and batch * dim below 2^31, and batch * ceil(dim / 64) * ceil(seqlen / 128) at most 2^23 - 1. An
  * output that overlaps an input is refused (SSD_ERR_UNSUPPORTED). The
- * workspace is 256-byte aligned; the query returns (size_t)-1 for a shape that is not supported.
+ * workspace is 256-byte aligned; the query returns (size_t)-1 for a shape that is not supported. Work-groups exchange
+ * chunks' states in it: calls that run at the same time need one each (else they end, but with any results).
  */
 typedef enum { SSD_DECAY_LOG = 0, SSD_DECAY_SIGMOID = 1, SSD_DECAY_RATE = 2 } ssd_decay;
 #define SSD_GATED_CHUNK 128

@@ -168,6 +168,9 @@ __device__ __forceinline__ float cut(float v, uint32_t keep) { return RESET ? ma
 // which no published word is.
 // ---------------------------------------------------------------------------
 constexpr int kWindow = 4;
+// Looks that a wait gives up after, some seconds: it ends by the order of the tickets, unless the words are overwritten
+// while the kernel runs (a workspace that another call uses at the same time). Results are NaN then.
+constexpr int kMostLooks = 1 << 22;
 
 struct Tile {
     int64_t b;
@@ -247,11 +250,12 @@ struct Entering {
     }
     // first: what enters chunk 0
     __device__ __forceinline__ float state(const uint64_t *pieces, const uint32_t *ends, int64_t stride, int lane, int k, float first) {
-        for (;;) {
+        for (int looks = 0;; ++looks) {
             bool all = end != ~0u;
 #pragma unroll
             for (int j = 0; j < kWindow; ++j) all = all && w[j] != ~(uint64_t)0;
             if (all) break;
+            if (looks == kMostLooks) return __builtin_nanf("");
             __builtin_amdgcn_s_sleep(1);
             look(pieces, ends, stride, lane, k);
         }

@@ -12,6 +12,22 @@
 
 namespace ssd {
 
+template <int N>
+__device__ __forceinline__ void put(float *p, const float (&v)[N]) {
+    if constexpr (N == 4) *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    else p[0] = v[0];
+}
+template <int N>
+__device__ __forceinline__ void get(const float *p, float (&v)[N]) {
+    if constexpr (N == 4) {
+        const f32x4 q = *reinterpret_cast<const f32x4 *>(p);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = q[k];
+    } else {
+        v[0] = p[0];
+    }
+}
+
 template <typename T, int DECAY, bool IN, bool RESET, int V>
 __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) void k_gated_bwd(GatedArgs a) {
     using S = Shape<T, V>;
@@ -66,29 +82,37 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) voi
     auto rate = [&](int e) { return kRate ? base2(a.rate[d + e]) : 0.f; };
     const uint32_t next = way.ask(a);
     float dec[R][V], c[R][V];
+    constexpr int B = V < 4 ? V : 4;  // channels that go to LDS together: one by one, 8 lanes would meet in one bank
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        const float rate2 = rate(e);
-        float h = 0.f, p = 1.f, back = 0.f;
+    for (int b = 0; b < V; b += B) {
+        float ps[B], hs[B], backs[B];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const Decay q = decay_of<DECAY, kFine>(f[r].get(e), rate2);
-            float v = x[r].get(e);
-            if constexpr (IN) v *= sigmoid_of<kFine>(in[r].get(e));
-            // tokens behind the last one, with x and dy zero, hand G on as it is
-            const float dec_r = r < n ? q.a : 1.f;
-            dec[r][e] = dec_r;
-            c[r][e] = q.c;
-            h = r ? __builtin_fmaf(dec_r, cut<RESET>(h, keep[r]), q.c * v) : q.c * v;
-            p = cut<RESET>(r ? p * dec_r : dec_r, keep[r]);
+        for (int k = 0; k < B; ++k) {
+            const int e = b + k;
+            const float rate2 = rate(e);
+            float h = 0.f, p = 1.f, back = 0.f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const Decay q = decay_of<DECAY, kFine>(f[r].get(e), rate2);
+                float v = x[r].get(e);
+                if constexpr (IN) v *= sigmoid_of<kFine>(in[r].get(e));
+                // tokens behind the last one, with x and dy zero, hand G on as it is
+                const float dec_r = r < n ? q.a : 1.f;
+                dec[r][e] = dec_r;
+                c[r][e] = q.c;
+                h = r ? __builtin_fmaf(dec_r, cut<RESET>(h, keep[r]), q.c * v) : q.c * v;
+                p = cut<RESET>(r ? p * dec_r : dec_r, keep[r]);
+            }
+#pragma unroll
+            for (int r = R - 1; r >= 0; --r) back = cut<RESET>(dec[r][e] * (dy[r].get(e) + back), keep[r]);
+            ps[k] = p;
+            hs[k] = h;
+            backs[k] = back;
+            if (k & 1) __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int r = R - 1; r >= 0; --r)
-            back = cut<RESET>(dec[r][e] * (dy[r].get(e) + back), keep[r]);
-        ga[g][j * V + e] = p;
-        gh[g][j * V + e] = h;
-        gg[g][j * V + e] = back;
-        if (e & 1) __builtin_amdgcn_sched_barrier(0);
+        put<B>(&ga[g][j * V + b], ps);
+        put<B>(&gh[g][j * V + b], hs);
+        put<B>(&gg[g][j * V + b], backs);
     }
     __builtin_amdgcn_wave_barrier();
     // this wavefront's groups, a column to a lane
@@ -156,43 +180,47 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) voi
     // channel by channel (in pairs, where two make a stored word), so that its inputs' registers become its outputs'
     Packed<T, V> dx[R], di[R], df[R];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        float before[R], later = gg[g][j * V + e];
-        before[0] = cut<RESET>(gh[g][j * V + e], keep[0]);
+    for (int b = 0; b < V; b += B) {
+        float enters[B], returns[B], sums[B];
+        get<B>(&gh[g][j * V + b], enters);
+        get<B>(&gg[g][j * V + b], returns);
 #pragma unroll
-        for (int r = 1; r < R; ++r) {
-            float v = x[r - 1].get(e);
-            if constexpr (IN) v *= sigmoid_of<kFine>(in[r - 1].get(e));
-            before[r] = cut<RESET>(__builtin_fmaf(dec[r - 1][e], before[r - 1], c[r - 1][e] * v), keep[r]);
-        }
-        const float by_rate = rate(e) * kLn2;
-        float sum = 0.f;
+        for (int k = 0; k < B; ++k) {
+            const int e = b + k;
+            Gate gi[R];
+            float before[R], v[R], later = returns[k], sum = 0.f;
 #pragma unroll
-        for (int r = R - 1; r >= 0; --r) {
-            const float dh = dy[r].get(e) + later;
-            const float cc = c[r][e], aa = dec[r][e], u = dh * cc;
-            later = cut<RESET>(aa * dh, keep[r]);
-            Gate gi = {1.f, 0.f};
-            if constexpr (IN) gi = gate_of<kFine>(in[r].get(e));
-            const float v = x[r].get(e) * gi.s;
-            dx[r].set(e, u * gi.s);
-            if constexpr (IN) di[r].set(e, u * v * gi.n);
-            float dla = aa * before[r];
-            if constexpr (DECAY == SSD_DECAY_LOG) {
-                df[r].set(e, dla * dh);
-            } else if constexpr (DECAY == SSD_DECAY_SIGMOID) {  // c = sigmoid(-f)
-                df[r].set(e, u * __builtin_fmaf(-aa, v, dla));
-            } else {
-                // dc / d log a = -a^2 / c; none where c is 0
-                const float slope = cc > 0.f ? -aa * aa * __builtin_amdgcn_rcpf(cc) : 0.f;
-                const Gate q = gate_of<kFine>(f[r].get(e));
-                const float by = dh * __builtin_fmaf(slope, v, dla) * q.s;
-                df[r].set(e, by * q.n * by_rate);
-                sum += r < n ? by : 0.f;
+            for (int r = 0; r < R; ++r) {
+                gi[r] = {1.f, 0.f};
+                if constexpr (IN) gi[r] = gate_of<kFine>(in[r].get(e));
+                v[r] = x[r].get(e) * gi[r].s;
+                before[r] = cut<RESET>(r ? __builtin_fmaf(dec[r ? r - 1 : 0][e], before[r ? r - 1 : 0], c[r ? r - 1 : 0][e] * v[r ? r - 1 : 0]) : enters[k], keep[r]);
             }
+            const float by_rate = rate(e) * kLn2;
+#pragma unroll
+            for (int r = R - 1; r >= 0; --r) {
+                const float dh = dy[r].get(e) + later, cc = c[r][e], aa = dec[r][e], u = dh * cc;
+                later = cut<RESET>(aa * dh, keep[r]);
+                dx[r].set(e, u * gi[r].s);
+                if constexpr (IN) di[r].set(e, u * v[r] * gi[r].n);
+                const float own = aa * before[r];
+                if constexpr (DECAY == SSD_DECAY_LOG) {
+                    df[r].set(e, own * dh);
+                } else if constexpr (DECAY == SSD_DECAY_SIGMOID) {  // c = sigmoid(-f)
+                    df[r].set(e, u * __builtin_fmaf(-aa, v[r], own));
+                } else {
+                    // dc / d log a = -a^2 / c; none where c is 0
+                    const float slope = cc > 0.f ? -aa * aa * __builtin_amdgcn_rcpf(cc) : 0.f;
+                    const Gate q = gate_of<kFine>(f[r].get(e));
+                    const float by = dh * __builtin_fmaf(slope, v[r], own) * q.s;
+                    df[r].set(e, by * q.n * by_rate);
+                    sum += r < n ? by : 0.f;
+                }
+            }
+            sums[k] = sum;
+            if (k & 1) __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (kRate) ga[g][j * V + e] = sum;  // its decays have been read, by this wavefront alone
-        if (e & 1) __builtin_amdgcn_sched_barrier(0);
+        if constexpr (kRate) put<B>(&ga[g][j * V + b], sums);  // its decays have been read, by this wavefront alone
     }
 #pragma unroll
     for (int r = 0; r < R; ++r)
