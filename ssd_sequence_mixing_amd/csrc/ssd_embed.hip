@@ -8,7 +8,7 @@
 //
 // k_sort: a work-group sorts up to 4096 tokens in LDS (stable, by digits of at
 // most 8 bits). More tokens are merged, 8 sorted pieces at a time, each value
-// finding its place by binary search (k_merge). The other work-groups of these launches clear the table
+// finding its place by binary search (k_merge). Other work-groups of these launches clear the table
 // meanwhile, each launch a share of it. k_sums: a wavefront adds
 // the rows of `len` places of the sorted list, 256 channels of them; a token whose
 // rows lie within writes its sum to the table, the first and the last one's may go on
@@ -22,30 +22,46 @@ namespace ssd {
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64, kSortKeys = 4;
 
-// 4 consecutive values (V: aligned and whole) or one.
-template <typename T, int V>
-__device__ __forceinline__ void load(float (&v)[V], const T *p) {
-    if constexpr (V == 1) {
-        v[0] = (float)p[0];
-    } else if constexpr (sizeof(T) == 2) {
-        const bf16x4 q = *reinterpret_cast<const bf16x4 *>(p);
+// 4 consecutive values of a row at any alignment of their type; n of them where the row ends before that (zeros behind it).
+constexpr int V = 4;
+template <typename T>
+__device__ __forceinline__ void load(float (&v)[V], const T *p, int n) {
+    if (n >= V) {
+        if constexpr (sizeof(T) == 2) {
+            typedef uint32_t word __attribute__((ext_vector_type(2), aligned(2)));
+            const word q = *reinterpret_cast<const word *>(p);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = (float)q[e];
+            for (int e = 0; e < V; ++e) v[e] = __uint_as_float(e & 1 ? q[e >> 1] & 0xffff0000u : q[e >> 1] << 16);
+        } else {
+            typedef float word __attribute__((ext_vector_type(4), aligned(4)));
+            const word q = *reinterpret_cast<const word *>(p);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = q[e];
+        }
     } else {
-        const f32x4 q = *reinterpret_cast<const f32x4 *>(p);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = q[e];
+        for (int e = 0; e < V; ++e) v[e] = e < n ? (float)p[e] : 0.f;
     }
 }
-template <typename T, int V>
-__device__ __forceinline__ void store(T *p, const float (&v)[V]) {
-    if constexpr (V == 1) p[0] = (T)v[0];
-    else if constexpr (sizeof(T) == 2) *reinterpret_cast<bf16x4 *>(p) = bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
-    else *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
+template <typename T>
+__device__ __forceinline__ void store(T *p, const float (&v)[V], int n) {
+    if (n >= V) {
+        if constexpr (sizeof(T) == 2) {
+            typedef uint32_t word __attribute__((ext_vector_type(2), aligned(2)));
+            *reinterpret_cast<word *>(p) = __builtin_bit_cast(u32x2, bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]});
+        } else {
+            typedef float word __attribute__((ext_vector_type(4), aligned(4)));
+            *reinterpret_cast<word *>(p) = word{v[0], v[1], v[2], v[3]};
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if (e < n) p[e] = (T)v[e];
+    }
 }
 
-// V values a lane, 64 lanes to a slice of a row. Work-groups go over the rows' slices in turn.
-template <typename TT, typename TY, int V>
+// 4 values a lane, 64 lanes to a slice of a row. Work-groups go over the rows' slices in turn.
+template <typename TT, typename TY>
 __global__ __launch_bounds__(256) void k_embed(const int *tokens, const TT *table, TY *y, float scale, int64_t rows, int vocab, int dim) {
     const int slices = (dim + 64 * V - 1) / (64 * V);
     const int64_t n = rows * slices, hop = (int64_t)gridDim.x * 4;
@@ -59,11 +75,11 @@ __global__ __launch_bounds__(256) void k_embed(const int *tokens, const TT *tabl
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] = 0.f;
         if ((uint32_t)t < (uint32_t)vocab) {
-            load<TT, V>(v, table + (int64_t)t * dim + d);
+            load(v, table + (int64_t)t * dim + d, dim - d);
 #pragma unroll
             for (int e = 0; e < V; ++e) v[e] *= scale;
         }
-        store<TY, V>(y + r * dim + d, v);
+        store(y + r * dim + d, v, dim - d);
     }
 }
 
@@ -76,7 +92,7 @@ struct Share {
 template <int THREADS>
 __device__ __forceinline__ void clear_share(const Share &c, int64_t block, int64_t blocks) {
     const int64_t i0 = block * THREADS + threadIdx.x;
-    for (int64_t i = i0; i < c.n16; i += blocks * THREADS) c.p[i] = u32x4{0, 0, 0, 0};
+    for (int64_t i = i0; i < c.n16; i += blocks * THREADS) __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, c.p + i);  // past the caches: nothing reads the table soon (71 -> 58 us)
     if (i0 < c.rest) reinterpret_cast<uint16_t *>(c.p + c.n16)[i0] = 0;
 }
 
@@ -199,25 +215,26 @@ __global__ __launch_bounds__(256) void k_merge(const uint64_t *in, uint64_t *out
 }
 
 // The row of the table that a token's sum goes to.
-template <typename TG, int V>
+template <typename TG>
 __device__ __forceinline__ void put(const EmbedBwdArgs &a, int64_t token, int d, float (&sum)[V]) {
     TG *p = reinterpret_cast<TG *>(a.dtable) + token * a.dim + d;
 #pragma unroll
     for (int e = 0; e < V; ++e) sum[e] *= a.scale;
     if (a.accumulate) {
         float old[V];
-        load<TG, V>(old, p);
+        load(old, p, a.dim - d);
 #pragma unroll
         for (int e = 0; e < V; ++e) sum[e] += old[e];
     }
-    store<TG, V>(p, sum);
+    store(p, sum, a.dim - d);
 }
 
-template <typename TY, typename TG, int V>
+template <typename TY, typename TG>
 __global__ __launch_bounds__(64) void k_sums(EmbedBwdArgs a) {
+    const int64_t piece = blockIdx.x;
     constexpr int U = 16;  // rows on their way
     const int d = ((int)blockIdx.y * 64 + (int)threadIdx.x) * V;
-    const int64_t s = (int64_t)blockIdx.x * a.len, end = min(s + a.len, a.rows);
+    const int64_t s = piece * a.len, end = min(s + a.len, a.rows);
     const bool live = d < a.dim;
     auto token = [&](int64_t i) { return (uint32_t)(a.sorted[i] >> 32); };
     uint32_t now = token(s);
@@ -227,8 +244,8 @@ __global__ __launch_bounds__(64) void k_sums(EmbedBwdArgs a) {
     for (int e = 0; e < V; ++e) sum[e] = 0.f;
     auto flush = [&](bool tail) {
         if (!live || now >= (uint32_t)a.vocab) return;
-        if (head || tail) store<float, V>(a.part + ((int64_t)blockIdx.x * 2 + (head ? 0 : 1)) * a.dim + d, sum);
-        else put<TG, V>(a, now, d, sum);
+        if (head || tail) store(a.part + (piece * 2 + (head ? 0 : 1)) * a.dim + d, sum, a.dim - d);
+        else put<TG>(a, now, d, sum);
     };
     for (int64_t i = s; i < end; i += U) {
         float v[U][V];
@@ -239,7 +256,7 @@ __global__ __launch_bounds__(64) void k_sums(EmbedBwdArgs a) {
             t[u] = (uint32_t)(k >> 32);
 #pragma unroll
             for (int e = 0; e < V; ++e) v[u][e] = 0.f;
-            if (live && t[u] < (uint32_t)a.vocab) load<TY, V>(v[u], reinterpret_cast<const TY *>(a.dy) + (int64_t)(uint32_t)k * a.dim + d);
+            if (live && t[u] < (uint32_t)a.vocab) load(v[u], reinterpret_cast<const TY *>(a.dy) + (int64_t)(uint32_t)k * a.dim + d, a.dim - d);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -260,7 +277,7 @@ __global__ __launch_bounds__(64) void k_sums(EmbedBwdArgs a) {
 
 // The sums of a token whose rows begin in piece blockIdx.x and go on beyond it, in order.
 // 4 wavefronts take a quarter of the pieces each.
-template <typename TG, int V>
+template <typename TG>
 __global__ __launch_bounds__(256) void k_join(EmbedBwdArgs a) {
     __shared__ float share[4][64][V];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -282,12 +299,12 @@ __global__ __launch_bounds__(256) void k_join(EmbedBwdArgs a) {
 #pragma unroll
     for (int e = 0; e < V; ++e) sum[e] = 0.f;
     if (d < a.dim) {
-        if (w == 0) load<float, V>(sum, a.part + (p * 2 + 1) * a.dim + d);
+        if (w == 0) load(sum, a.part + (p * 2 + 1) * a.dim + d, a.dim - d);
         const int64_t to = min((w + 1) * each, pieces);
 #pragma unroll 8
         for (int64_t q = w * each; q < to; ++q) {
             float v[V];
-            load<float, V>(v, a.part + (p + 1 + q) * 2 * a.dim + d);
+            load(v, a.part + (p + 1 + q) * 2 * a.dim + d, a.dim - d);
 #pragma unroll
             for (int e = 0; e < V; ++e) sum[e] += v[e];
         }
@@ -300,7 +317,7 @@ __global__ __launch_bounds__(256) void k_join(EmbedBwdArgs a) {
         for (int k = 1; k < 4; ++k)
 #pragma unroll
             for (int e = 0; e < V; ++e) sum[e] += share[k][lane][e];
-        put<TG, V>(a, (int64_t)mine, d, sum);
+        put<TG>(a, (int64_t)mine, d, sum);
     }
 }
 
@@ -316,12 +333,9 @@ ssd_status launch_embed(const int *tokens, const void *table, void *y, float sca
         return pick_type(y_dtype, [&](auto ty) {
             using TT = decltype(tt);
             using TY = decltype(ty);
-            auto go = [&](auto k, int v) {
-                const int64_t n = rows * ((dim + 64 * v - 1) / (64 * v)), blocks = (n + 3) / 4, most = 1 << 20;
-                return status_of(launch(k, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), s, tokens, (const TT *)table,
-                                        (TY *)y, scale, rows, (int)vocab, (int)dim));
-            };
-            return dim % 4 == 0 ? go(k_embed<TT, TY, 4>, 4) : go(k_embed<TT, TY, 1>, 1);
+            const int64_t n = rows * ((dim + 64 * V - 1) / (64 * V)), blocks = (n + 3) / 4, most = 1 << 20;
+            return status_of(launch(k_embed<TT, TY>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), s, tokens, (const TT *)table,
+                                    (TY *)y, scale, rows, (int)vocab, (int)dim));
         });
     });
 }
@@ -374,17 +388,14 @@ ssd_status launch_embed_bwd(EmbedBwdArgs a, const EmbedPlan &p, const int *token
     }
     a.sorted = one;
     a.len = p.len;
+    const unsigned slices = (unsigned)((a.dim + 64 * V - 1) / (64 * V));
     return pick_type(dy_dtype, [&](auto ty) {
         return pick_type(dtype, [&](auto tg) {
             using TY = decltype(ty);
             using TG = decltype(tg);
-            auto go = [&](auto sums, auto join, int v) {
-                const unsigned slices = (unsigned)((a.dim + 64 * v - 1) / (64 * v));
-                const ssd_status e = status_of(launch(sums, dim3((unsigned)p.pieces, slices), dim3(64), s, a));
-                if (e != SSD_OK || p.pieces < 2) return e;
-                return status_of(launch(join, dim3((unsigned)(p.pieces - 1), slices), dim3(256), s, a));
-            };
-            return a.dim % 4 == 0 ? go(k_sums<TY, TG, 4>, k_join<TG, 4>, 4) : go(k_sums<TY, TG, 1>, k_join<TG, 1>, 1);
+            const ssd_status e = status_of(launch(k_sums<TY, TG>, dim3((unsigned)p.pieces, slices), dim3(64), s, a));
+            if (e != SSD_OK || p.pieces < 2) return e;
+            return status_of(launch(k_join<TG>, dim3((unsigned)(p.pieces - 1), slices), dim3(256), s, a));
         });
     });
 }

@@ -44,7 +44,9 @@ struct Eight {
         if (n >= 8) {
 #pragma unroll
             for (int k = 0; k < kWords; k += 4) {
-                const word q = *reinterpret_cast<const word *>(reinterpret_cast<const char *>(p) + 4 * k);
+                // past the caches: the product that follows then finds more of the codes there (8192 x 4096, and 4096 x 2048
+                // behind it: 116 us without, 106 so, though this alone takes 30 and not 27)
+                const word q = __builtin_nontemporal_load(reinterpret_cast<const word *>(reinterpret_cast<const char *>(p) + 4 * k));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[k + e] = q[e];
             }

@@ -35,7 +35,8 @@ __global__ __launch_bounds__(kLogitThreads) void k_logits(LogitsArgs a) {
         T e[E];
         u32x4 q;
     };
-    // every whole group of the slice is on its way before the history is looked at
+    // every whole group of the slice is on its way before the history is looked at (loads and stores past the caches,
+    // which 64 x 8 x 65536 logits do not fit: 80 us without, 65 so)
     constexpr int N = SLICE / (kLogitThreads * E);
     const int64_t left = V - v0;
     const int whole_from = v0 < 0 ? E : 0, whole_to = (int)(left < SLICE ? left / E * E : SLICE);
@@ -44,7 +45,7 @@ __global__ __launch_bounds__(kLogitThreads) void k_logits(LogitsArgs a) {
     Group x[N];
 #pragma unroll
     for (int k = 0; k < N; ++k)
-        if (whole(place(k))) x[k].q = *reinterpret_cast<const u32x4 *>(in + v0 + place(k));
+        if (whole(place(k))) x[k].q = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(in + v0 + place(k)));
     float rep = 1.f, inv = 1.f, pres = 0.f, freq = 0.f;
     if constexpr (HISTORY) {
         for (int i = threadIdx.x * 4; i < SLICE; i += kLogitThreads * 4) *reinterpret_cast<u32x4 *>(count + i) = u32x4{0, 0, 0, 0};
@@ -130,7 +131,7 @@ __global__ __launch_bounds__(kLogitThreads) void k_logits(LogitsArgs a) {
         const int p = place(k);
         if (whole(p)) {
             apply(x[k], p, v0 + p, std::true_type{});
-            *reinterpret_cast<u32x4 *>(out + v0 + p) = x[k].q;
+            __builtin_nontemporal_store(x[k].q, reinterpret_cast<u32x4 *>(out + v0 + p));
         }
     }
     // a group that the row begins or ends in
