@@ -574,7 +574,7 @@ ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, int act,
  *
  *   h_t = a_t h_{t-1} + c_t v_t;   v_t = sigmoid(i_t) x_t;   y_t = h_t
  *
- *   SSD_DECAY_LOG      a = e^f, c = 1 (f <= 0: log-decays)
+ *   SSD_DECAY_LOG      a = e^f, c = 1 (f <= 0: log-decays; products of 128 decays above 1 may overflow)
  *   SSD_DECAY_SIGMOID  a = sigmoid(f), c = 1 - a
  *   SSD_DECAY_RATE     a = e^(rate[d] sigmoid(f)), c = sqrt(1 - a^2) (a positive rate counts as 0; c = 0 where 1 - a^2 is)
  *

@@ -140,8 +140,10 @@ struct Tokens {
     const char *p;
     uint32_t ld, at;  // bytes
     __device__ __forceinline__ Tokens(const void *q, int64_t row, int64_t ld_, int i, int d)
-        : p(reinterpret_cast<const char *>(q) + row * ld_ * (int64_t)sizeof(T)), ld((uint32_t)ld_ * (uint32_t)sizeof(T)),
-          at((uint32_t)i * ld + (uint32_t)d * (uint32_t)sizeof(T)) {}
+        : p(reinterpret_cast<const char *>(q) + row * ld_ * (int64_t)sizeof(T)), ld((uint32_t)ld_ * (uint32_t)sizeof(T)) {
+        asm volatile("" : "+v"(i));  // made for every tile: kept over them, the tensors' offsets would not fit the registers
+        at = (uint32_t)i * ld + (uint32_t)d * (uint32_t)sizeof(T);
+    }
     __device__ __forceinline__ const T *operator[](int r) const { return reinterpret_cast<const T *>(p + (uint32_t)r * ld + at); }
     __device__ __forceinline__ T *out(int r) const { return const_cast<T *>((*this)[r]); }
 };
@@ -167,7 +169,7 @@ __device__ __forceinline__ float cut(float v, uint32_t keep) { return RESET ? ma
 // store that nothing else has to be ordered with, into memory that k_gated_clear has filled with ones,
 // which no published word is.
 // ---------------------------------------------------------------------------
-constexpr int kWindow = 4;
+constexpr int kWindow = 3;
 // Looks that a wait gives up after, some seconds: it ends by the order of the tickets, unless the words are overwritten
 // while the kernel runs (a workspace that another call uses at the same time). Results are NaN then.
 constexpr int kMostLooks = 1 << 22;
@@ -176,10 +178,10 @@ struct Tile {
     int64_t b;
     int chunk, col;  // along the order of the walk; first channel / kCols
 };
-// A work-group's way through its tiles, `share` to a ticket (no ticket: one tile, of a single chunk, which waits for
-// none). Every thread holds the same.
+// A work-group's way through its tiles, `share` to a ticket, of one chunk (no ticket: one tile, of a single chunk, which
+// waits for none). Every thread holds the same.
 struct Way {
-    uint32_t now, end;
+    uint32_t chunk, now, end;  // of the chunk's tiles of all sequences and columns: this one, and the ticket's end
     __device__ __forceinline__ Way(const GatedArgs &a, uint32_t *mine) {
         uint32_t t = blockIdx.x;
         if (a.ticket) {
@@ -191,8 +193,13 @@ struct Way {
         set(a, t);
     }
     __device__ __forceinline__ void set(const GatedArgs &a, uint32_t t) {
-        now = t * a.share;
-        end = min(now + a.share, a.tiles);
+        chunk = t / a.tickets;
+        now = (t - chunk * a.tickets) * a.share;
+        end = min(now + a.share, a.wide);
+    }
+    __device__ __forceinline__ Tile tile(uint32_t cols) const {
+        const uint32_t b = now / cols;
+        return {b, (int)chunk, (int)(now - b * cols)};
     }
     // The next ticket, where the last tile of one is under way: ask() for it early (thread 0 holds the answer),
     // tell() it to the others in front of a barrier, go_on() behind that.
@@ -207,13 +214,9 @@ struct Way {
     __device__ __forceinline__ void go_on(const GatedArgs &a, const uint32_t *mine) {
         if (++now < end) return;
         if (a.ticket) set(a, __builtin_amdgcn_readfirstlane(*mine));
-        else now = a.tiles;
+        else chunk = (uint32_t)a.nchunks;
     }
 };
-__device__ __forceinline__ Tile tile_of(uint32_t t, uint32_t batch, uint32_t cols) {
-    const uint32_t wide = batch * cols, chunk = t / wide, in = t - chunk * wide, b = in / cols;
-    return {b, (int)chunk, (int)(in - b * cols)};
-}
 
 __device__ __forceinline__ void publish(uint32_t *word, float v) {
     uint32_t u = __float_as_uint(v);
@@ -240,6 +243,7 @@ struct Entering {
     uint32_t end;
     __device__ __forceinline__ void look(const uint64_t *pieces, const uint32_t *ends, int64_t stride, int lane, int k) {
         const int from = max(k - kWindow, 0);
+        asm volatile("" : "+v"(lane));  // the addresses are made here: in front of the tiles' loop they took registers all the way
         end = 0;
         if (from > 0) end = peek(ends + (from - 1) * stride + lane);
 #pragma unroll

@@ -21,8 +21,12 @@ __global__ __launch_bounds__(256) void k_gated_clear(u32x4 *words, int64_t n16) 
         words[i] = i < 16 ? u32x4{0, 0, 0, 0} : u32x4{~0u, ~0u, ~0u, ~0u};
 }
 
+// What bounds it: 3 work-groups share a CU, whose vector unit is busy 60% of the time; a tile's way is its loads, the walk, two
+// exchanges through LDS and one look at the chunks before. 4 x 2048 x 4096 in bf16, rates and input gates (268 MB): 70 us
+// and 5 for the words' clearing (3.6 TB/s); 16384 x 4096 with resets (403 MB) 98 us. The next tile's loads under the exchange,
+// at 2 work-groups a CU: 70 and 105.
 template <typename T, int DECAY, bool IN, bool RESET, int V>
-__global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) void k_gated_fwd(GatedArgs a) {
+__global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 6 : 2) void k_gated_fwd(GatedArgs a) {
     using S = Shape<T, V>;
     constexpr int R = S::R, LPR = S::LPR, GPW = S::GPW;
     constexpr bool kFine = sizeof(T) == 4;
@@ -34,15 +38,22 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) voi
     const int j = lane % LPR, g = w * GPW + lane / LPR;
     const int D = (int)a.D;
 
-    // a tile's inputs, as stored; the next tile's are asked for as soon as this one's have been used
+    Way way(a, &mine);
+    for (uint32_t turn = 0; way.chunk < a.nchunks; ++turn) {
+    const Tile tile = way.tile((uint32_t)a.cols);
+    auto &wa = wa2[turn & 1], &wh = wh2[turn & 1];
+    auto &carry = carry2[turn & 1];
+    const int c0 = tile.col * kCols;
+    const bool live = c0 + j * V < D;
+    const int d = min(c0 + j * V, D - V);  // this lane's channels
+    const int t0 = tile.chunk * SSD_GATED_CHUNK + g * R;
+    const int n = live ? min(R, (int)a.T - t0) : 0;  // its tokens
+    const int64_t row0 = tile.b * a.T + (int64_t)tile.chunk * SSD_GATED_CHUNK;
     Packed<T, V> x[R], f[R], in[IN ? R : 1];
     uint8_t marks[RESET ? R : 1];
-    float rate[V];
-    auto load = [&](const Tile &tile) {
-        const int c0 = tile.col * kCols, d = min(c0 + j * V, D - V);
-        const int n = c0 + j * V < D ? min(R, (int)a.T - tile.chunk * SSD_GATED_CHUNK - g * R) : 0;
-        const int64_t row0 = tile.b * a.T + (int64_t)tile.chunk * SSD_GATED_CHUNK;
+    {
         const Tokens<T> px(a.x, row0, a.ldx, g * R, d), pf(a.f, row0, a.ldf, g * R, d), pi(a.i, row0, a.ldi, g * R, d);
+        const Tokens<uint8_t> pz(a.reset, row0, 1, g * R, 0);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             x[r] = {}; f[r] = {};
@@ -52,33 +63,19 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) voi
                 f[r].load(pf[r]);
                 x[r].load(px[r]);
                 if constexpr (IN) in[r].load(pi[r]);
-                if constexpr (RESET) marks[r] = a.reset[row0 + g * R + r];
+                if constexpr (RESET) marks[r] = *pz[r];
             }
         }
-        if constexpr (DECAY == SSD_DECAY_RATE) {
+    }
+    float rate[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) rate[e] = a.rate[d + e];
-        }
-    };
-    Way way(a, &mine);
-    if (way.now >= a.tiles) return;
-    Tile tile = tile_of(way.now, (uint32_t)a.batch, (uint32_t)a.cols);
-    load(tile);
-    for (uint32_t turn = 0;; ++turn) {
-    auto &wa = wa2[turn & 1], &wh = wh2[turn & 1];
-    auto &carry = carry2[turn & 1];
-    const int c0 = tile.col * kCols;
-    const bool live = c0 + j * V < D;
-    const int d = min(c0 + j * V, D - V);  // this lane's channels
-    const int t0 = tile.chunk * SSD_GATED_CHUNK + g * R;
-    const int n = live ? min(R, (int)a.T - t0) : 0;  // its tokens
-    uint32_t bits = 0;
+    for (int e = 0; e < V; ++e) rate[e] = DECAY == SSD_DECAY_RATE ? base2(a.rate[d + e]) : 0.f;
+    uint32_t resets = 0;  // one register for all R
     if constexpr (RESET) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) bits |= marks[r] ? 1u << r : 0u;
+        for (int r = 0; r < R; ++r) resets |= marks[r] ? 1u << r : 0u;
     }
-    auto keep = [&](int r) { return bits >> r & 1 ? 0u : ~0u; };
-
+    auto keep = [&](int r) { return resets >> r & 1 ? 0u : ~0u; };
     const uint32_t next = way.ask(a);
 
     float h[R][V], p[R][V];
@@ -87,7 +84,7 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) voi
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             // (behind the last token these are of no use, and of no harm: nobody takes what follows it)
-            const Decay q = decay_of<DECAY, kFine>(f[r].get(e), DECAY == SSD_DECAY_RATE ? base2(rate[e]) : 0.f);
+            const Decay q = decay_of<DECAY, kFine>(f[r].get(e), rate[e]);
             float v = x[r].get(e);
             if constexpr (IN) v *= sigmoid_of<kFine>(in[r].get(e));
             const float u = q.c * v;
@@ -109,11 +106,10 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) voi
     wh[w][lane] = ph;
     way.tell(next, &mine);
     __syncthreads();
-    const Tile here = tile;
     // wavefront 0 takes the chunk as a whole, a column to a lane: of the channel ch
     const int base = c0 + lane / V * V, ch = min(base, D - V) + lane % V;
     const bool there = base < D;
-    const int64_t stride = (int64_t)a.cols * kCols, words = here.b * a.nchunks * stride + c0;
+    const int64_t stride = (int64_t)a.cols * kCols, words = tile.b * a.nchunks * stride + c0;
     float ca = 1.f, chunk_h = 0.f;
     Entering<RESET> entering;
     if (w == 0 && a.nchunks > 1) {
@@ -122,24 +118,19 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) voi
             chunk_h = pass<RESET>(wa[k][lane], wh[k][lane], chunk_h);
             ca *= wa[k][lane];
         }
-        publish(a.pieces + words + here.chunk * stride + lane, ca, chunk_h);
-        entering.look(a.pieces + words, a.ends + words, stride, lane, here.chunk);
+        publish(a.pieces + words + tile.chunk * stride + lane, ca, chunk_h);
+        entering.look(a.pieces + words, a.ends + words, stride, lane, tile.chunk);
     }
     way.go_on(a, &mine);
-    const bool more = way.now < a.tiles;
-    if (more) {
-        tile = tile_of(way.now, (uint32_t)a.batch, (uint32_t)a.cols);
-        load(tile);
-    }
     if (w == 0) {
         float first = 0.f;
-        if (a.init && there) first = a.init[here.b * D + ch];
+        if (a.init && there) first = a.init[tile.b * D + ch];
         if (a.nchunks > 1) {
-            first = entering.state(a.pieces + words, a.ends + words, stride, lane, here.chunk, first);
-            publish(a.ends + words + here.chunk * stride + lane, pass<RESET>(ca, chunk_h, first));
+            first = entering.state(a.pieces + words, a.ends + words, stride, lane, tile.chunk, first);
+            publish(a.ends + words + tile.chunk * stride + lane, pass<RESET>(ca, chunk_h, first));
         }
         carry[lane] = first;
-        if (a.states && there) a.states[(here.b * a.nchunks + here.chunk) * D + ch] = first;
+        if (a.states && there) a.states[(tile.b * a.nchunks + tile.chunk) * D + ch] = first;
     }
     __syncthreads();
     float s = carry[lane];
@@ -151,7 +142,7 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) voi
         s = pass<RESET>(ga[w * GPW + k][lane], own, s);
     }
     __builtin_amdgcn_wave_barrier();
-    const Tokens<T> py(a.y, here.b * a.T + (int64_t)here.chunk * SSD_GATED_CHUNK, D, g * R, d);
+    const Tokens<T> py(a.y, row0, D, g * R, d);
     uint32_t open = ~0u;
     float from[V];
 #pragma unroll
@@ -164,12 +155,11 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) voi
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const float v = __builtin_fmaf(p[r][e], cut<RESET>(from[e], open), h[r][e]);
-            if (last) a.final[here.b * D + d + e] = v;
+            if (last) a.final[tile.b * D + d + e] = v;
             o.set(e, v);
         }
         if (r < n) o.store(py.out(r));
     }
-    if (!more) return;
     }
 }
 
@@ -202,10 +192,11 @@ GatedPlan gated_plan(int64_t batch, int64_t T, int64_t D, ssd_dtype) {
     p.fits = batch == 0 || T == 0 || (batch <= most / p.cols && batch * p.cols <= most / p.nchunks);
     if (!p.fits) return p;
     p.tiles = batch * p.cols * p.nchunks;
-    // tiles of a ticket, and work-groups: 2 for each CU
+    // tiles of a ticket: of two neighbouring columns where there are many, never of two chunks (a ticket that ended one
+    // chunk and began the next would have each chunk wait for a second tile of the one before)
     p.share = p.nchunks > 1 && p.tiles > 4096 ? 2 : 1;
-    p.groups = (p.tiles + p.share - 1) / p.share;
-    if (p.nchunks > 1 && p.groups > 512) p.groups = 512;
+    const int64_t tickets = (batch * p.cols + p.share - 1) / p.share * p.nchunks;
+    p.groups = p.nchunks > 1 && tickets > 768 ? 768 : tickets;  // 3 for each CU
     // the ticket, then a chunk's (a, h) and its end for each column
     p.word_bytes = p.nchunks > 1 && p.tiles ? 256 + p.tiles * kCols * 12 : 0;
     p.rate_bytes = batch * p.nchunks * D * 4;
@@ -215,7 +206,8 @@ GatedPlan gated_plan(int64_t batch, int64_t T, int64_t D, ssd_dtype) {
 ssd_status clear_words(GatedArgs &a, const GatedPlan &p, void *workspace, hipStream_t s) {
     a.cols = (int)p.cols;
     a.share = (uint32_t)p.share;
-    a.tiles = (uint32_t)p.tiles;
+    a.wide = (uint32_t)(a.batch * p.cols);
+    a.tickets = (uint32_t)((a.batch * p.cols + p.share - 1) / p.share);
     if (p.nchunks == 1) return SSD_OK;
     char *ws = static_cast<char *>(workspace);
     a.ticket = reinterpret_cast<uint32_t *>(ws);

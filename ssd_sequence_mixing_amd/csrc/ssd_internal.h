@@ -276,7 +276,7 @@ struct GatedArgs {
     float *part;                 // backward: shares of drate, (batch, nchunks, D)
     int64_t batch, T, D, nchunks;
     int cols;                    // pieces of 64 channels
-    uint32_t tiles, share;       // chunks of all of those and sequences, and how many a work-group takes
+    uint32_t wide, share, tickets;  // a chunk's tiles of all columns and sequences, how many a ticket is for, tickets a chunk
     uint32_t *ticket;            // workspace, cleared before: the next chunk to take; per (batch, chunk, column) ...
     uint64_t *pieces;            // ... its decay and its own state's end,
     uint32_t *ends;              // ... and the state behind it

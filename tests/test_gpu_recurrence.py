@@ -168,6 +168,34 @@ def test_many_chunks(ssd, T):
         _check(ssd, s, dtype, f"T {T} {dtype}")
 
 
+@pytest.mark.parametrize("shape", [(2, 700, 3), (1, 513, 5), (3, 260, 1), (1, 1300, 9), (2, 400, 65)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_narrow_rows_of_several_chunks(ssd, shape, dtype):
+    for decay in ("log", "sigmoid", "rate"):
+        _check(ssd, _draw(*shape, dtype, decay, True, True, True, seed=13), dtype, f"{shape} {decay} {dtype}")
+
+
+@pytest.mark.parametrize("B,T,D", [(1, 16384, 4160), (3, 9000, 1500), (5, 4000, 2600)])
+def test_more_chunks_than_tickets(ssd, B, T, D):
+    """So many chunks that a ticket is for two of them, with odd numbers of columns: parts have the bits of a call alone."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x, f, dy = (torch.randn(B, T, D, device="cuda", generator=g).bfloat16() for _ in range(3))
+    rate = torch.log(0.9 + 0.099 * torch.rand(D, device="cuda", generator=g))
+    reset = torch.rand(B, T, device="cuda", generator=g) < 0.001
+    y, final, st = ssd.ssd_gated_scan_fwd(x, f, decay="rate", rate=rate, reset=reset, want_states=True)
+    grads = ssd.ssd_gated_scan_bwd(dy, x, f, st, decay="rate", rate=rate, reset=reset)
+    for d in (0, D // 2 // 8 * 8, D - 40):
+        part = [t[..., d:d + 40].contiguous() for t in (x, f, dy)]
+        r = rate[d:d + 40].contiguous()
+        yp, fp, sp = ssd.ssd_gated_scan_fwd(part[0], part[1], decay="rate", rate=r, reset=reset, want_states=True)
+        gp = ssd.ssd_gated_scan_bwd(part[2], part[0], part[1], sp, decay="rate", rate=r, reset=reset)
+        torch.cuda.synchronize()
+        assert torch.equal(y[..., d:d + 40], yp) and torch.equal(final[:, d:d + 40], fp) and torch.equal(st[..., d:d + 40], sp)
+        for a, b in ((grads[0], gp[0]), (grads[1], gp[1]), (grads[3], gp[3]), (grads[4], gp[4])):
+            assert torch.equal(a[..., d:d + 40], b)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("dim", [64, 72, 37])
 def test_views_of_one_projection(ssd, dtype, dim):
