@@ -7,7 +7,7 @@
 // token outside the table is a row of zeros, and adds to no gradient.
 //
 // k_sort: a work-group sorts up to 4096 tokens in LDS (stable, by digits of at
-// most 8 bits). More tokens are merged, 8 sorted pieces at a time, each value
+// most 9 bits). More tokens are merged, 8 sorted pieces at a time, each value
 // finding its place by binary search (k_merge). Other work-groups of these launches clear the table
 // meanwhile, each launch a share of it. k_sums: a wavefront adds
 // the rows of `len` places of the sorted list, 256 channels of them; a token whose
@@ -20,7 +20,9 @@
 
 namespace ssd {
 
-constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64, kSortKeys = 4;
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64, kSortKeys = 4, kBins = 512;
+constexpr int kTileBits = 12;  // tokens of a sorted piece: 2^12 at most
+static_assert(kSortThreads * kSortKeys == 1 << kTileBits, "a piece fits the registers");
 
 // 4 consecutive values of a row at any alignment of their type; n of them where the row ends before that (zeros behind it).
 constexpr int V = 4;
@@ -106,7 +108,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort(const int *tokens, uint64
         return;
     }
     __shared__ uint32_t keys[kSortThreads * kSortKeys];
-    __shared__ uint32_t count[kSortWaves][256];
+    __shared__ uint32_t count[kSortWaves][kBins];
     __shared__ uint32_t sums[kSortWaves];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int64_t first = (int64_t)blockIdx.x << bits;
@@ -126,7 +128,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort(const int *tokens, uint64
     const uint32_t bins = 1u << digit;
     for (int p = 0; p < passes; ++p) {
         const int shift = bits + p * digit;
-        for (uint32_t i = threadIdx.x; i < kSortWaves * 256; i += kSortThreads) (&count[0][0])[i] = 0;
+        for (uint32_t i = threadIdx.x; i < kSortWaves * kBins; i += kSortThreads) (&count[0][0])[i] = 0;
         __syncthreads();
         // a key's place among its wavefront's keys of the same digit
         uint32_t place[kSortKeys];
@@ -149,11 +151,12 @@ __global__ __launch_bounds__(kSortThreads) void k_sort(const int *tokens, uint64
         }
         __syncthreads();
         // the counts' exclusive sums, digit by digit and within it wavefront by wavefront: thread t takes
-        // 4 wavefronts' counts of digit t / 4
-        const uint32_t dd = threadIdx.x >> 2, w0 = (threadIdx.x & 3) * 4;
-        uint32_t c[4], s = 0;
+        // 8 wavefronts' counts of digit t / 2
+        constexpr int kEach = kSortWaves * kBins / kSortThreads;
+        const uint32_t dd = threadIdx.x / (kSortWaves / kEach), w0 = threadIdx.x % (kSortWaves / kEach) * kEach;
+        uint32_t c[kEach], s = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[j] = count[w0 + j][dd], s += c[j];
+        for (int j = 0; j < kEach; ++j) c[j] = count[w0 + j][dd], s += c[j];
         uint32_t up = s;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
@@ -165,7 +168,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort(const int *tokens, uint64
         uint32_t base = up - s;
         for (int j = 0; j < w; ++j) base += sums[j];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kEach; ++j) {
             count[w0 + j][dd] = base;
             base += c[j];
         }
@@ -184,6 +187,47 @@ __global__ __launch_bounds__(kSortThreads) void k_sort(const int *tokens, uint64
         const int i = (w * each + e) * 64 + lane;
         if (e < each && i < n) out[first + i] = (uint64_t)(key[e] >> bits) << 32 | (uint64_t)(first + (key[e] & ((1u << bits) - 1)));
     }
+}
+
+// The same for the first pieces' runs, where all 8 fit LDS as tokens (128 KB): a work-group takes 1024 places, and a step of its
+// searches is one of LDS instead of the L2 (16384 tokens: 10 us with k_merge, 8 so). Between two runs the
+// earlier one's rows go first where tokens are equal.
+__global__ __launch_bounds__(1024) void k_merge_lds(const uint64_t *in, uint64_t *out, int64_t n, int run, int64_t blocks, Share clear) {
+    if (blockIdx.x >= blocks) {
+        clear_share<1024>(clear, blockIdx.x - blocks, gridDim.x - blocks);
+        return;
+    }
+    __shared__ uint32_t tokens[8 << kTileBits];
+    const int64_t first = (int64_t)blockIdx.x * 1024, group = first / (8 * run) * (8 * run);
+    const int many = (int)min((int64_t)8 * run, n - group);
+    for (int i0 = threadIdx.x; i0 < many; i0 += 8 * 1024) {  // 8 on their way
+        uint64_t k[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) k[u] = i0 + u * 1024 < many ? in[group + i0 + u * 1024] : 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (i0 + u * 1024 < many) tokens[i0 + u * 1024] = (uint32_t)(k[u] >> 32);
+    }
+    __syncthreads();
+    const int me = (int)(first - group) + (int)threadIdx.x;
+    if (me >= many) return;
+    const uint64_t v = in[group + me];
+    const uint32_t t = (uint32_t)(v >> 32);
+    const int mine = me / run;
+    int at = me - mine * run;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (j == mine || j * run >= many) continue;
+        int lo = 0, hi = min(run, many - j * run);
+        while (lo < hi) {
+            const int m = (lo + hi) >> 1;
+            const uint32_t o = tokens[j * run + m];
+            if (o < t || (o == t && j < mine)) lo = m + 1;
+            else hi = m;
+        }
+        at += lo;
+    }
+    out[group + at] = v;
 }
 
 // Sorted runs of `run` values (the last one shorter) merged 8 at a time: a value's place is its own in its run
@@ -344,9 +388,9 @@ EmbedPlan embed_plan(int64_t rows, int64_t vocab) {
     EmbedPlan p = {};
     int bits = 0;
     while ((vocab >> bits) != 0) ++bits;  // of `vocab` itself, which stands for tokens outside the table
-    p.passes = (bits + 7) / 8;
+    p.passes = (bits + 8) / 9;
     p.digit = (bits + p.passes - 1) / p.passes;
-    p.bits = 32 - bits < 12 ? 32 - bits : 12;
+    p.bits = 32 - bits < kTileBits ? 32 - bits : kTileBits;
     p.tiles = (rows + ((int64_t)1 << p.bits) - 1) >> p.bits;
     p.len = 16;
     while (p.len < 256 && rows / p.len > 1024) p.len *= 2;
@@ -370,17 +414,21 @@ ssd_status launch_embed_bwd(EmbedBwdArgs a, const EmbedPlan &p, const int *token
         return n > 2048 ? 2048 : n > 0 ? n : c.rest ? 1 : 0;
     };
     Share c = share(0);
-    int64_t more = fill(c, 4 * kSortThreads);
+    const int64_t more = fill(c, 4 * kSortThreads);
     if (p.tiles + more == 0) return SSD_OK;
     ssd_status st = status_of(launch(k_sort, dim3((unsigned)(p.tiles + more)), dim3(kSortThreads), s, tokens, one, a.rows, a.vocab, p.bits,
                                      p.passes, p.digit, (int)p.tiles, c));
     if (st != SSD_OK || a.rows == 0) return st;
     for (int k = 1; k <= merges; ++k) {
         c = share(k);
-        more = fill(c, 4 * 256);
-        const int64_t blocks = (a.rows + 255) / 256;
-        st = status_of(launch(k_merge, dim3((unsigned)(blocks + more)), dim3(256), s, one, two, a.rows, ((int64_t)1 << p.bits) << (3 * (k - 1)),
-                              blocks, c));
+        const int64_t run = ((int64_t)1 << p.bits) << (3 * (k - 1));
+        if (k == 1) {
+            const int64_t blocks = (a.rows + 1023) / 1024;
+            st = status_of(launch(k_merge_lds, dim3((unsigned)(blocks + fill(c, 4 * 1024))), dim3(1024), s, one, two, a.rows, (int)run, blocks, c));
+        } else {
+            const int64_t blocks = (a.rows + 255) / 256;
+            st = status_of(launch(k_merge, dim3((unsigned)(blocks + fill(c, 4 * 256))), dim3(256), s, one, two, a.rows, run, blocks, c));
+        }
         if (st != SSD_OK) return st;
         uint64_t *t = one;
         one = two;
