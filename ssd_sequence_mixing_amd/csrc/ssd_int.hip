@@ -45,7 +45,7 @@ struct Eight {
 #pragma unroll
             for (int k = 0; k < kWords; k += 4) {
                 // past the caches: the product that follows then finds more of the codes there (8192 x 4096, and 4096 x 2048
-                // behind it: 116 us without, 106 so, though this alone takes 30 and not 27)
+                // behind it: 116 us without, 106 so, though this alone took 30 and not 27)
                 const word q = __builtin_nontemporal_load(reinterpret_cast<const word *>(reinterpret_cast<const char *>(p) + 4 * k));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[k + e] = q[e];
@@ -75,9 +75,17 @@ struct Eight {
             far = fmaxf(far, fabsf(t - (r - kMagic)));
             u[e] = __float_as_uint(r);
         }
-        if (__any(far > 0.49998f || inv == 0.f)) {
+        if (__any(inv == 0.f)) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(nearest(get(e), s) + kMagic);
+        } else if (__any(far > 0.49998f)) {
+            // as nearest(), from the code at hand (in bf16 half the rows' largest value is common, and lies in the middle)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float rest = __builtin_fmaf(-(__uint_as_float(u[e]) - kMagic), s, get(e)), half = 0.5f * s;
+                const bool next = fabsf(rest) > half || (fabsf(rest) == half && (u[e] & 1));
+                u[e] += next ? (rest > 0.f ? 1u : ~0u) : 0u;
+            }
         }
         uint32_t o[2];
 #pragma unroll
@@ -165,7 +173,7 @@ ssd_status launch_int_quantize(const void *x, int8_t *q, float *scale, int64_t r
                        : SSD_ERR_HIP;
         };
         // short rows: one wavefront each, if there are rows for every SIMD. Else 4 wavefronts a row, of 1 to 4 loads a
-        // lane (8192 x 4096 in bf16: 27 us, with one wavefront of 8 loads 37), or 16 of them
+        // lane (8192 x 4096 in bf16: 26 us, 3.9 TB/s; with one wavefront of 8 loads 37), or 16 of them
         const int64_t c = (dim + 511) / 512;
         if (c == 1) return go(k_int_quantize<T, 1, 1>, 1);
         if (c == 2 && rows >= 1024) return go(k_int_quantize<T, 1, 2>, 1);
