@@ -269,7 +269,7 @@ ssd_status ssd_int_quantize(const void *x, int8_t *q, float *scale, int64_t rows
 
 static ssd_status check_int(int64_t rows, int64_t in, int64_t out) {
     if (rows < 0 || in <= 0 || out <= 0 || in % 16 != 0) return SSD_ERR_SHAPE;
-    // 127 * 127 * 131072 < 2^31
+    // 127 * 128 * 131072 < 2^31
     return rows > ((int64_t)1 << 24) || in > 131072 || out > kMostDim ? SSD_ERR_UNSUPPORTED : SSD_OK;
 }
 

@@ -4,8 +4,9 @@
 //
 // A row stays in the registers of one wavefront (many rows) or of 4 or 16, 8 values a lane and load, at any
 // alignment; rows of more than 65536 values are read twice. Bound: HBM, one read and one write.
-// A quotient is formed by the scale's inverse; it is off by 1.5e-5 at most, so that only those within 2e-5
-// of the middle between two codes (one in 25000) need the exact remainder to be decided.
+// A code is formed by the scale's inverse, and is at most 1 off; the exact remainder, half a scale or more, says where.
+// (With the maximum in fp32 and every value of a wavefront's decided again where one lay in the middle, 30 operations a
+// value, the vector unit was busy 94% of the time.)
 #include <type_traits>
 
 #include "ssd_common.h"
@@ -57,34 +58,47 @@ struct Eight {
             __builtin_memcpy(w, v, sizeof v);
         }
     }
-    __device__ __forceinline__ void largest(float &top, bool &bad) const {
+    // The larger of top and their magnitudes' bits (in 16 bits: two by two), in which an infinity or a NaN lies above all others.
+    __device__ __forceinline__ void largest(uint32_t &top) const {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            bad |= !(fabsf(get(e)) < INFINITY);
-            top = fmaxf(top, fabsf(get(e)));
+        for (int k = 0; k < kWords; ++k) {
+            if constexpr (sizeof(T) == 4) {
+                top = max(top, w[k] & 0x7fffffffu);
+            } else {
+                typedef uint16_t two __attribute__((ext_vector_type(2)));
+                top = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(two, top), __builtin_bit_cast(two, w[k] & 0x7fff7fffu)));
+            }
         }
     }
-    // Their codes to q, n of them. inv: 1 / s, where that is an ordinary number, or 0.
+    static __device__ __forceinline__ uint32_t as_float(uint32_t top) {
+        if constexpr (sizeof(T) == 4) return top;
+        return max(top >> 16, top & 0xffffu) << 16;
+    }
+    // Their codes to q, n of them. inv: 1 / s or next to it, where that is an ordinary number, or 0.
     __device__ __forceinline__ void store(int8_t *q, int n, float s, float inv, bool zero) const {
         constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, which is the sum's lowest byte
         uint32_t u[8];
-        float far = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float t = get(e) * inv, r = t + kMagic;
-            far = fmaxf(far, fabsf(t - (r - kMagic)));
-            u[e] = __float_as_uint(r);
-        }
         if (__any(inv == 0.f)) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(nearest(get(e), s) + kMagic);
-        } else if (__any(far > 0.49998f)) {
-            // as nearest(), from the code at hand (in bf16 half the rows' largest value is common, and lies in the middle)
+        } else {
+            const float half = 0.5f * s;
+            float rest[8], far = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float rest = __builtin_fmaf(-(__uint_as_float(u[e]) - kMagic), s, get(e)), half = 0.5f * s;
-                const bool next = fabsf(rest) > half || (fabsf(rest) == half && (u[e] & 1));
-                u[e] += next ? (rest > 0.f ? 1u : ~0u) : 0u;
+                const float r = __builtin_fmaf(get(e), inv, kMagic);
+                rest[e] = __builtin_fmaf(-(r - kMagic), s, get(e));
+                far = fmaxf(far, fabsf(rest[e]));
+                u[e] = __float_as_uint(r);
+            }
+            // as nearest(); value by value, since they are few (in bf16 half the rows' largest value, which lies in the middle)
+            if (__any(far >= half)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (__any(fabsf(rest[e]) >= half)) {
+                        const bool next = fabsf(rest[e]) > half || (fabsf(rest[e]) == half && (u[e] & 1));
+                        u[e] += next ? (rest[e] > 0.f ? 1u : ~0u) : 0u;
+                    }
             }
         }
         uint32_t o[2];
@@ -109,7 +123,7 @@ struct Eight {
 template <typename T, int W, int NC>
 __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_int_quantize(const T *x, int8_t *q, float *scale, int64_t rows, int dim) {
     constexpr int RPB = W > 4 ? 1 : 4 / W, kStep = 64 * W * 8;
-    __shared__ float tops[W > 1 ? W : 1];
+    __shared__ uint32_t tops[W > 1 ? W : 1];
     const int t = threadIdx.x % (64 * W), slot = threadIdx.x / (64 * W);
     const int64_t hop = (int64_t)gridDim.x * RPB;
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += hop) {
@@ -118,35 +132,34 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_int_quantize(const T *
         const T *p = x + (in ? r : 0) * dim;
         const int n = in ? dim : 0;
         Eight<T> v[NC ? NC : 1];
-        float top = 0.f;
-        bool bad = false;
+        uint32_t top = 0;
         if constexpr (NC > 0) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) v[c].load(p + min(c * kStep + t * 8, dim), n - (c * kStep + t * 8));
 #pragma unroll
-            for (int c = 0; c < NC; ++c) v[c].largest(top, bad);
+            for (int c = 0; c < NC; ++c) v[c].largest(top);
         } else {
             for (int d = t * 8; d < n; d += kStep) {
                 v[0].load(p + d, n - d);
-                v[0].largest(top, bad);
+                v[0].largest(top);
             }
         }
-        top = bad ? INFINITY : top;
+        top = Eight<T>::as_float(top);
 #pragma unroll
-        for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+        for (int o = 32; o; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
         if constexpr (W > 1) {
             if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
             __syncthreads();
 #pragma unroll
-            for (int k = 0; k < W; ++k) top = fmaxf(top, tops[k]);
+            for (int k = 0; k < W; ++k) top = max(top, tops[k]);
             __syncthreads();
         }
         if constexpr (NC > 0) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) v[c].forget();
         }
-        bad = top == INFINITY;
-        const float s = top / 127.f, inv = s > 0x1p-100f ? 1.f / s : 0.f;
+        const bool bad = top >= 0x7f800000u;
+        const float s = __uint_as_float(top) / 127.f, inv = s > 0x1p-100f && !bad ? __builtin_amdgcn_rcpf(s) : 0.f;
         const bool zero = bad || s == 0.f;
         int8_t *o = q + (in ? r : 0) * dim;
         if constexpr (NC > 0) {
@@ -173,7 +186,7 @@ ssd_status launch_int_quantize(const void *x, int8_t *q, float *scale, int64_t r
                        : SSD_ERR_HIP;
         };
         // short rows: one wavefront each, if there are rows for every SIMD. Else 4 wavefronts a row, of 1 to 4 loads a
-        // lane (8192 x 4096 in bf16: 26 us, 3.9 TB/s; with one wavefront of 8 loads 37), or 16 of them
+        // lane (8192 x 4096 in bf16: 22 us, 4.6 TB/s; with one wavefront of 8 loads 37 where this took 26), or 16 of them
         const int64_t c = (dim + 511) / 512;
         if (c == 1) return go(k_int_quantize<T, 1, 1>, 1);
         if (c == 2 && rows >= 1024) return go(k_int_quantize<T, 1, 2>, 1);
