@@ -276,13 +276,14 @@ __device__ __forceinline__ void put(const EmbedBwdArgs &a, int64_t token, int d,
 template <typename TY, typename TG>
 __global__ __launch_bounds__(64) void k_sums(EmbedBwdArgs a) {
     const int64_t piece = blockIdx.x;
-    constexpr int U = 16;  // rows on their way
+    constexpr int U = 8;  // rows on their way (with 16, half the wavefronts: 1.5 us more of 54)
     const int d = ((int)blockIdx.y * 64 + (int)threadIdx.x) * V;
     const int64_t s = piece * a.len, end = min(s + a.len, a.rows);
     const bool live = d < a.dim;
     auto token = [&](int64_t i) { return (uint32_t)(a.sorted[i] >> 32); };
     uint32_t now = token(s);
     bool head = s > 0 && token(s - 1) == now;
+    const uint32_t after = end < a.rows ? token(end) : ~0u;
     float sum[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) sum[e] = 0.f;
@@ -316,26 +317,31 @@ __global__ __launch_bounds__(64) void k_sums(EmbedBwdArgs a) {
             for (int e = 0; e < V; ++e) sum[e] += v[u][e];
         }
     }
-    flush(end < a.rows && token(end) == now);
+    flush(end < a.rows && after == now);
 }
 
 // The sums of a token whose rows begin in piece blockIdx.x and go on beyond it, in order.
 // 4 wavefronts take a quarter of the pieces each.
 template <typename TG>
-__global__ __launch_bounds__(256) void k_join(EmbedBwdArgs a) {
+__global__ __launch_bounds__(256, 8) void k_join(EmbedBwdArgs a) {
     __shared__ float share[4][64][V];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int64_t p = blockIdx.x, s = p * a.len, end = s + a.len;  // never the last piece
-    const uint64_t mine = a.sorted[end - 1] >> 32;
-    if (mine >= (uint64_t)a.vocab || mine != a.sorted[end] >> 32) return;
-    if (mine == a.sorted[s] >> 32 && s > 0 && mine == a.sorted[s - 1] >> 32) return;  // it began earlier
+    // all at once: one wait
+    const int64_t after = (p + 1 + lane) * a.len;
+    const uint64_t k0 = a.sorted[s > 0 ? s - 1 : 0], k1 = a.sorted[s], k2 = a.sorted[end - 1], k3 = a.sorted[end];
+    uint64_t begins = a.sorted[after < a.rows ? after : 0];
+    const uint64_t mine = k2 >> 32;
+    if (mine >= (uint64_t)a.vocab || mine != k3 >> 32) return;
+    if (mine == k1 >> 32 && s > 0 && mine == k0 >> 32) return;  // it began earlier
     // the pieces behind this one that begin with the token: it ends in the last of them
     int64_t pieces = 0;
-    for (;;) {
-        const int64_t next = (p + 1 + pieces + lane) * a.len;
-        const int n = __popcll(__ballot(next < a.rows && a.sorted[next < a.rows ? next : 0] >> 32 == mine));
+    for (int64_t next = after;;) {
+        const int n = __popcll(__ballot(next < a.rows && begins >> 32 == mine));
         pieces += n;
         if (n < 64) break;
+        next += 64 * a.len;
+        begins = a.sorted[next < a.rows ? next : 0];
     }
     const int64_t each = (pieces + 3) / 4;
     const int d = ((int)blockIdx.y * 64 + lane) * V;
@@ -345,7 +351,7 @@ __global__ __launch_bounds__(256) void k_join(EmbedBwdArgs a) {
     if (d < a.dim) {
         if (w == 0) load(sum, a.part + (p * 2 + 1) * a.dim + d, a.dim - d);
         const int64_t to = min((w + 1) * each, pieces);
-#pragma unroll 8
+#pragma unroll 4
         for (int64_t q = w * each; q < to; ++q) {
             float v[V];
             load(v, a.part + (p + 1 + q) * 2 * a.dim + d, a.dim - d);
