@@ -30,7 +30,7 @@ __device__ __forceinline__ void get(const float *p, float (&v)[N]) {
 
 // What bounds it: the vector unit is busy two thirds of the time (some 85 operations a value, 12 of them transcendental) and
 // the registers leave 2 work-groups a CU, so that a tile's loads, walks and exchanges overlap little. 8 x 2048 x 1536 in bf16, rates
-// and input gates (353 MB): 108 us, and 5 each for the words' clearing and the rates' sums (2.9 TB/s). No kernel here spills: with
+// and input gates (353 MB): 118 us, 122 with the words' clearing and the rates' sums (2.9 TB/s). No kernel here spills: with
 // 18 to 60 registers spilled it took 170 to 190.
 template <typename T, int DECAY, bool IN, bool RESET, int V>
 __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) void k_gated_bwd(GatedArgs a) {
