@@ -61,7 +61,7 @@ __device__ __forceinline__ Decay decay_of(float f, float rate2) {
     }
     const float y = rate2 * sigmoid_of<kFine>(f), a = fast_exp2(y);
     const float c2 = one_minus_square<kFine>(y, a);
-    return {a, c2 * __builtin_amdgcn_rsqf(fmaxf(c2, 0x1p-100f))};
+    return {a, c2 * __builtin_amdgcn_rsqf(c2 + 0x1p-126f)};  // 0 where c2 is
 }
 // A positive rate counts as 0; in two steps, so that its rounding does not follow that of the product.
 __device__ __forceinline__ float base2(float rate) { return (rate > 0.f ? 0.f : rate) * kLog2e; }
@@ -178,24 +178,31 @@ struct Tile {
     int64_t b;
     int chunk, col;  // along the order of the walk; first channel / kCols
 };
+// A kernel's arguments where the launch put them, its only ones. They are read where they are needed, again() and
+// again: over the tiles' loop they are more than the scalar registers hold, and a hundred of a tile's vector instructions
+// moved them to lanes and back.
+typedef const __attribute__((address_space(4))) GatedArgs *Args;
+__device__ __forceinline__ Args args() { return (Args)__builtin_amdgcn_kernarg_segment_ptr(); }
+__device__ __forceinline__ void again(Args &a) { asm volatile("" : "+s"(a)); }
+
 // A work-group's way through its tiles, `share` to a ticket, of one chunk (no ticket: one tile, of a single chunk, which
 // waits for none). Every thread holds the same.
 struct Way {
     uint32_t chunk, now, end;  // of the chunk's tiles of all sequences and columns: this one, and the ticket's end
-    __device__ __forceinline__ Way(const GatedArgs &a, uint32_t *mine) {
+    __device__ __forceinline__ Way(Args a, uint32_t *mine) {
         uint32_t t = blockIdx.x;
-        if (a.ticket) {
-            if (threadIdx.x == 0) *mine = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (a->ticket) {
+            if (threadIdx.x == 0) *mine = __hip_atomic_fetch_add(a->ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             __syncthreads();
             t = __builtin_amdgcn_readfirstlane(*mine);
             __syncthreads();
         }
         set(a, t);
     }
-    __device__ __forceinline__ void set(const GatedArgs &a, uint32_t t) {
-        chunk = t / a.tickets;
-        now = (t - chunk * a.tickets) * a.share;
-        end = min(now + a.share, a.wide);
+    __device__ __forceinline__ void set(Args a, uint32_t t) {
+        chunk = t / a->tickets;
+        now = (t - chunk * a->tickets) * a->share;
+        end = min(now + a->share, a->wide);
     }
     __device__ __forceinline__ Tile tile(uint32_t cols) const {
         const uint32_t b = now / cols;
@@ -203,18 +210,18 @@ struct Way {
     }
     // The next ticket, where the last tile of one is under way: ask() for it early (thread 0 holds the answer),
     // tell() it to the others in front of a barrier, go_on() behind that.
-    __device__ __forceinline__ uint32_t ask(const GatedArgs &a) const {
-        if (a.ticket && now + 1 >= end && threadIdx.x == 0)
-            return __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __device__ __forceinline__ uint32_t ask(Args a) const {
+        if (a->ticket && now + 1 >= end && threadIdx.x == 0)
+            return __hip_atomic_fetch_add(a->ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         return 0;
     }
     __device__ __forceinline__ void tell(uint32_t next, uint32_t *mine) const {
         if (now + 1 >= end && threadIdx.x == 0) *mine = next;
     }
-    __device__ __forceinline__ void go_on(const GatedArgs &a, const uint32_t *mine) {
+    __device__ __forceinline__ void go_on(Args a, const uint32_t *mine) {
         if (++now < end) return;
-        if (a.ticket) set(a, __builtin_amdgcn_readfirstlane(*mine));
-        else chunk = (uint32_t)a.nchunks;
+        if (a->ticket) set(a, __builtin_amdgcn_readfirstlane(*mine));
+        else chunk = (uint32_t)a->nchunks;
     }
 };
 

@@ -23,10 +23,11 @@ __global__ __launch_bounds__(256) void k_gated_clear(u32x4 *words, int64_t n16) 
 
 // What bounds it: 3 work-groups share a CU, whose vector unit is busy 60% of the time; a tile's way is its loads, the walk, two
 // exchanges through LDS and one look at the chunks before. 4 x 2048 x 4096 in bf16, rates and input gates (268 MB): 72 us,
-// 75 with the words' clearing (3.6 TB/s); 16384 x 4096 with resets (403 MB) 102 us together. The next tile's loads under the exchange,
+// 75 with the words' clearing (3.6 TB/s); 16384 x 4096 with resets (403 MB) 99 us together. The next tile's loads under the exchange,
 // at 2 work-groups a CU: 70 and 105.
 template <typename T, int DECAY, bool IN, bool RESET, int V>
-__global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 6 : 2) void k_gated_fwd(GatedArgs a) {
+__global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 6 : 2) void k_gated_fwd(GatedArgs) {
+    Args a = args();
     using S = Shape<T, V>;
     constexpr int R = S::R, LPR = S::LPR, GPW = S::GPW;
     constexpr bool kFine = sizeof(T) == 4;
@@ -36,24 +37,25 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 6 : 2) voi
     __shared__ uint32_t mine;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int j = lane % LPR, g = w * GPW + lane / LPR;
-    const int D = (int)a.D;
+    const int D = (int)a->D;
 
     Way way(a, &mine);
-    for (uint32_t turn = 0; way.chunk < a.nchunks; ++turn) {
-    const Tile tile = way.tile((uint32_t)a.cols);
+    for (uint32_t turn = 0; way.chunk < a->nchunks; ++turn) {
+    again(a);
+    const Tile tile = way.tile((uint32_t)a->cols);
     auto &wa = wa2[turn & 1], &wh = wh2[turn & 1];
     auto &carry = carry2[turn & 1];
     const int c0 = tile.col * kCols;
     const bool live = c0 + j * V < D;
     const int d = min(c0 + j * V, D - V);  // this lane's channels
     const int t0 = tile.chunk * SSD_GATED_CHUNK + g * R;
-    const int n = live ? min(R, (int)a.T - t0) : 0;  // its tokens
-    const int64_t row0 = tile.b * a.T + (int64_t)tile.chunk * SSD_GATED_CHUNK;
+    const int n = live ? min(R, (int)a->T - t0) : 0;  // its tokens
+    const int64_t row0 = tile.b * a->T + (int64_t)tile.chunk * SSD_GATED_CHUNK;
     Packed<T, V> x[R], f[R], in[IN ? R : 1];
     uint8_t marks[RESET ? R : 1];
     {
-        const Tokens<T> px(a.x, row0, a.ldx, g * R, d), pf(a.f, row0, a.ldf, g * R, d), pi(a.i, row0, a.ldi, g * R, d);
-        const Tokens<uint8_t> pz(a.reset, row0, 1, g * R, 0);
+        const Tokens<T> px(a->x, row0, a->ldx, g * R, d), pf(a->f, row0, a->ldf, g * R, d), pi(a->i, row0, a->ldi, g * R, d);
+        const Tokens<uint8_t> pz(a->reset, row0, 1, g * R, 0);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             x[r] = {}; f[r] = {};
@@ -69,7 +71,7 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 6 : 2) voi
     }
     float rate[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) rate[e] = DECAY == SSD_DECAY_RATE ? base2(a.rate[d + e]) : 0.f;
+    for (int e = 0; e < V; ++e) rate[e] = DECAY == SSD_DECAY_RATE ? base2(a->rate[d + e]) : 0.f;
     uint32_t resets = 0;  // one register for all R
     if constexpr (RESET) {
 #pragma unroll
@@ -106,31 +108,32 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 6 : 2) voi
     wh[w][lane] = ph;
     way.tell(next, &mine);
     __syncthreads();
+    again(a);
     // wavefront 0 takes the chunk as a whole, a column to a lane: of the channel ch
     const int base = c0 + lane / V * V, ch = min(base, D - V) + lane % V;
     const bool there = base < D;
-    const int64_t stride = (int64_t)a.cols * kCols, words = tile.b * a.nchunks * stride + c0;
+    const int64_t stride = (int64_t)a->cols * kCols, words = tile.b * a->nchunks * stride + c0;
     float ca = 1.f, chunk_h = 0.f;
     Entering<RESET> entering;
-    if (w == 0 && a.nchunks > 1) {
+    if (w == 0 && a->nchunks > 1) {
 #pragma unroll
         for (int k = 0; k < kGatedWaves; ++k) {
             chunk_h = pass<RESET>(wa[k][lane], wh[k][lane], chunk_h);
             ca *= wa[k][lane];
         }
-        publish(a.pieces + words + tile.chunk * stride + lane, ca, chunk_h);
-        entering.look(a.pieces + words, a.ends + words, stride, lane, tile.chunk);
+        publish(a->pieces + words + tile.chunk * stride + lane, ca, chunk_h);
+        entering.look(a->pieces + words, a->ends + words, stride, lane, tile.chunk);
     }
     way.go_on(a, &mine);
     if (w == 0) {
         float first = 0.f;
-        if (a.init && there) first = a.init[tile.b * D + ch];
-        if (a.nchunks > 1) {
-            first = entering.state(a.pieces + words, a.ends + words, stride, lane, tile.chunk, first);
-            publish(a.ends + words + tile.chunk * stride + lane, pass<RESET>(ca, chunk_h, first));
+        if (a->init && there) first = a->init[tile.b * D + ch];
+        if (a->nchunks > 1) {
+            first = entering.state(a->pieces + words, a->ends + words, stride, lane, tile.chunk, first);
+            publish(a->ends + words + tile.chunk * stride + lane, pass<RESET>(ca, chunk_h, first));
         }
         carry[lane] = first;
-        if (a.states && there) a.states[(tile.b * a.nchunks + tile.chunk) * D + ch] = first;
+        if (a->states && there) a->states[(tile.b * a->nchunks + tile.chunk) * D + ch] = first;
     }
     __syncthreads();
     float s = carry[lane];
@@ -142,7 +145,7 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 6 : 2) voi
         s = pass<RESET>(ga[w * GPW + k][lane], own, s);
     }
     __builtin_amdgcn_wave_barrier();
-    const Tokens<T> py(a.y, row0, D, g * R, d);
+    const Tokens<T> py(a->y, row0, D, g * R, d);
     uint32_t open = ~0u;
     float from[V];
 #pragma unroll
@@ -150,12 +153,12 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 6 : 2) voi
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         open &= keep(r);
-        const bool last = r < n && t0 + r == a.T - 1 && a.final;
+        const bool last = r < n && t0 + r == a->T - 1 && a->final;
         Packed<T, V> o;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const float v = __builtin_fmaf(p[r][e], cut<RESET>(from[e], open), h[r][e]);
-            if (last) a.final[tile.b * D + d + e] = v;
+            if (last) a->final[tile.b * D + d + e] = v;
             o.set(e, v);
         }
         if (r < n) o.store(py.out(r));

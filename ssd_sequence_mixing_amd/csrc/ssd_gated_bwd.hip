@@ -30,10 +30,11 @@ __device__ __forceinline__ void get(const float *p, float (&v)[N]) {
 
 // What bounds it: the vector unit is busy two thirds of the time (some 85 operations a value, 12 of them transcendental) and
 // the registers leave 2 work-groups a CU, so that a tile's loads, walks and exchanges overlap little. 8 x 2048 x 1536 in bf16, rates
-// and input gates (353 MB): 118 us, 122 with the words' clearing and the rates' sums (2.9 TB/s). No kernel here spills: with
+// and input gates (353 MB): 115 us, 119 with the words' clearing and the rates' sums (3.0 TB/s). No kernel here spills: with
 // 18 to 60 registers spilled it took 170 to 190.
 template <typename T, int DECAY, bool IN, bool RESET, int V>
-__global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) void k_gated_bwd(GatedArgs a) {
+__global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) void k_gated_bwd(GatedArgs) {
+    Args a = args();
     using S = Shape<T, V>;
     constexpr int R = S::R, LPR = S::LPR, GPW = S::GPW;
     constexpr bool kFine = sizeof(T) == 4, kRate = DECAY == SSD_DECAY_RATE;
@@ -43,20 +44,21 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) voi
     __shared__ float wa2[2][kGatedWaves][kCols], wh2[2][kGatedWaves][kCols], wg2[2][kGatedWaves][kCols], carry2[2][kCols];
     __shared__ uint32_t mine;
     Way way(a, &mine);
-    for (uint32_t turn = 0; way.chunk < a.nchunks; ++turn) {
-    const Tile tile = way.tile((uint32_t)a.cols);
+    for (uint32_t turn = 0; way.chunk < a->nchunks; ++turn) {
+    again(a);
+    const Tile tile = way.tile((uint32_t)a->cols);
     auto &wa = wa2[turn & 1], &wh = wh2[turn & 1], &wg = wg2[turn & 1];
     auto &carry = carry2[turn & 1];
-    const int chunk = (int)a.nchunks - 1 - tile.chunk;
+    const int chunk = (int)a->nchunks - 1 - tile.chunk;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int j = lane % LPR, g = w * GPW + lane / LPR;
-    const int D = (int)a.D, c0 = tile.col * kCols;
+    const int D = (int)a->D, c0 = tile.col * kCols;
     const bool live = c0 + j * V < D;
     const int d = min(c0 + j * V, D - V);
     const int t0 = chunk * SSD_GATED_CHUNK + g * R;
-    const int n = live ? min(R, (int)a.T - t0) : 0;
-    const int64_t row0 = tile.b * a.T + (int64_t)chunk * SSD_GATED_CHUNK;
-    const Tokens<T> px(a.x, row0, a.ldx, g * R, d), pf(a.f, row0, a.ldf, g * R, d), pi(a.i, row0, a.ldi, g * R, d), py(a.dy, row0, D, g * R, d);
+    const int n = live ? min(R, (int)a->T - t0) : 0;
+    const int64_t row0 = tile.b * a->T + (int64_t)chunk * SSD_GATED_CHUNK;
+    const Tokens<T> px(a->x, row0, a->ldx, g * R, d), pf(a->f, row0, a->ldf, g * R, d), pi(a->i, row0, a->ldi, g * R, d), py(a->dy, row0, D, g * R, d);
     // the channel of this lane's column
     const int base = c0 + lane / V * V, ch = min(base, D - V) + lane % V;
     const bool there = base < D;
@@ -76,14 +78,14 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) voi
         }
     }
     float enter = 0.f;  // the state before the chunk, of this lane's column
-    if (there) enter = a.states[(tile.b * a.nchunks + chunk) * D + ch];
+    if (there) enter = a->states[(tile.b * a->nchunks + chunk) * D + ch];
     if constexpr (RESET) {
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            if (r < n && a.reset[row0 + g * R + r]) keep[r] = 0u;
+            if (r < n && a->reset[row0 + g * R + r]) keep[r] = 0u;
     }
     // read where it is needed, twice, and not kept
-    auto rate = [&](int e) { return kRate ? base2(a.rate[d + e]) : 0.f; };
+    auto rate = [&](int e) { return kRate ? base2(a->rate[d + e]) : 0.f; };
     const uint32_t next = way.ask(a);
     float dec[R][V], c[R][V];
     constexpr int B = V < 4 ? V : 4;  // channels that go to LDS together: one by one, 8 lanes would meet in one bank
@@ -135,26 +137,27 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) voi
     way.tell(next, &mine);
     __syncthreads();
     way.go_on(a, &mine);
+    again(a);
     if (w == 0) {
         const int64_t at = tile.b * D + ch;
         float first = 0.f, ca = 1.f, cg = 0.f;
-        if (a.dfinal && there) first = a.dfinal[at];
+        if (a->dfinal && there) first = a->dfinal[at];
 #pragma unroll
         for (int k = kGatedWaves - 1; k >= 0; --k) {
             cg = pass<RESET>(wa[k][lane], wg[k][lane], cg);
             ca *= wa[k][lane];
         }
-        if (a.nchunks > 1) {
-            const int64_t stride = (int64_t)a.cols * kCols, words = tile.b * a.nchunks * stride + c0;
+        if (a->nchunks > 1) {
+            const int64_t stride = (int64_t)a->cols * kCols, words = tile.b * a->nchunks * stride + c0;
             const int k = tile.chunk;
-            publish(a.pieces + words + k * stride + lane, ca, cg);
+            publish(a->pieces + words + k * stride + lane, ca, cg);
             Entering<RESET> entering;
-            entering.look(a.pieces + words, a.ends + words, stride, lane, k);
-            first = entering.state(a.pieces + words, a.ends + words, stride, lane, k, first);
-            publish(a.ends + words + k * stride + lane, pass<RESET>(ca, cg, first));
+            entering.look(a->pieces + words, a->ends + words, stride, lane, k);
+            first = entering.state(a->pieces + words, a->ends + words, stride, lane, k, first);
+            publish(a->ends + words + k * stride + lane, pass<RESET>(ca, cg, first));
         }
         carry[lane] = first;
-        if (chunk == 0 && a.dinit && there) a.dinit[at] = pass<RESET>(ca, cg, first);
+        if (chunk == 0 && a->dinit && there) a->dinit[at] = pass<RESET>(ca, cg, first);
     }
     // the states that enter this wavefront's groups
     for (int k = 0; k < w; ++k) enter = pass<RESET>(wa[k][lane], wh[k][lane], enter);
@@ -204,19 +207,19 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) voi
 #pragma unroll
             for (int r = R - 1; r >= 0; --r) {
                 const float dh = dy[r].get(e) + later, cc = c[r][e], aa = dec[r][e], u = dh * cc;
-                later = cut<RESET>(aa * dh, keep[r]);
+                const float back_r = aa * dh;
+                later = cut<RESET>(back_r, keep[r]);
                 dx[r].set(e, u * gi[r].s);
                 if constexpr (IN) di[r].set(e, u * v[r] * gi[r].n);
-                const float own = aa * before[r];
                 if constexpr (DECAY == SSD_DECAY_LOG) {
-                    df[r].set(e, own * dh);
+                    df[r].set(e, back_r * before[r]);
                 } else if constexpr (DECAY == SSD_DECAY_SIGMOID) {  // c = sigmoid(-f)
-                    df[r].set(e, u * __builtin_fmaf(-aa, v[r], own));
+                    df[r].set(e, cc * back_r * (before[r] - v[r]));
                 } else {
                     // dc / d log a = -a^2 / c; none where c is 0
-                    const float slope = cc > 0.f ? -aa * aa * __builtin_amdgcn_rcpf(cc) : 0.f;
+                    const float inv = cc > 0.f ? __builtin_amdgcn_rcpf(cc) : 0.f;
                     const Gate q = gate_of<kFine>(f[r].get(e));
-                    const float by = dh * __builtin_fmaf(slope, v[r], own) * q.s;
+                    const float by = back_r * __builtin_fmaf(-aa * v[r], inv, before[r]) * q.s;
                     df[r].set(e, by * q.n * by_rate);
                     sum += r < n ? by : 0.f;
                 }
@@ -229,9 +232,9 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) voi
 #pragma unroll
     for (int r = 0; r < R; ++r)
         if (r < n) {
-            dx[r].store(Tokens<T>(a.dx, row0, D, g * R, d).out(r));
-            if constexpr (IN) di[r].store(Tokens<T>(a.di, row0, D, g * R, d).out(r));
-            df[r].store(Tokens<T>(a.df, row0, D, g * R, d).out(r));
+            dx[r].store(Tokens<T>(a->dx, row0, D, g * R, d).out(r));
+            if constexpr (IN) di[r].store(Tokens<T>(a->di, row0, D, g * R, d).out(r));
+            df[r].store(Tokens<T>(a->df, row0, D, g * R, d).out(r));
         }
     if constexpr (kRate) {
         __builtin_amdgcn_wave_barrier();
@@ -245,7 +248,7 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) voi
             s = wa[0][lane];
 #pragma unroll
             for (int k = 1; k < kGatedWaves; ++k) s += wa[k][lane];
-            a.part[(tile.b * a.nchunks + chunk) * D + ch] = s;
+            a->part[(tile.b * a->nchunks + chunk) * D + ch] = s;
         }
     }
     }
