@@ -28,7 +28,7 @@ __device__ __forceinline__ void get(const float *p, float (&v)[N]) {
     }
 }
 
-// What bounds it: the vector unit is busy two thirds of the time (some 85 operations a value, 12 of them transcendental) and
+// What bounds it: the vector unit is busy 61% of the time (some 85 operations a value, 11 of them transcendental) and
 // the registers leave 2 work-groups a CU, so that a tile's loads, walks and exchanges overlap little. 8 x 2048 x 1536 in bf16, rates
 // and input gates (353 MB): 115 us, 119 with the words' clearing and the rates' sums (3.0 TB/s). No kernel here spills: with
 // 18 to 60 registers spilled it took 170 to 190.
