@@ -695,7 +695,8 @@ ssd_status ssd_logits_process(const void *logits, void *out, const int32_t *toke
  * -128, which the quantiser does not write, add up to 2^31, and wrap.)
  *
  * ssd_int_quantize writes operands so (weights once, activations): scale = max |x| / 127
- * of the row, rounded to fp32, q the integer nearest to x / scale (ties to even). A row of zeros has scale 0;
+ * of the row, as the fp32 product with the number nearest to 1 / 127, q the integer of -127 .. 127
+ * nearest to x / scale (ties to even). A row of zeros (or whose scale rounds to 0) has scale 0 and codes 0;
  * a row with an infinity or a NaN has scale NaN and codes 0. x (rows, dim) dtype, any dim up to 2^20.
  */
 ssd_status ssd_int_quantize(const void *x, int8_t *q, float *scale, int64_t rows, int64_t dim, ssd_dtype dtype, void *stream);

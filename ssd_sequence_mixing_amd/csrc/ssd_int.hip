@@ -1,4 +1,4 @@
-// Rows in 8-bit integers for gfx950: scale = max |x| / 127 of the row, and
+// Rows in 8-bit integers for gfx950: scale = max |x| / 127 of the row (times the fp32 number nearest to 1 / 127), and
 // q the integer nearest to x / scale (ties to even). A row of zeros has scale 0; one that holds an
 // infinity or a NaN has scale NaN, and codes 0.
 //
@@ -18,10 +18,10 @@ namespace ssd {
 // fused operation gives exactly (a multiple of the smaller operand's last place, and below 2 s).
 __device__ __forceinline__ float nearest(float x, float s) {
     float q = rintf(x / s);
-    const float r = __builtin_fmaf(-q, s, x), half = 0.5f * s;
+    const float r = 2.f * __builtin_fmaf(-q, s, x);  // (half of a scale of few bits would be rounded)
     const bool odd = ((int)q & 1) != 0;
-    if (r > half || (r == half && odd)) q += 1.f;
-    else if (r < -half || (r == -half && odd)) q -= 1.f;
+    if (r > s || (r == s && odd)) q += 1.f;
+    else if (r < -s || (r == -s && odd)) q -= 1.f;
     return q;
 }
 
@@ -80,7 +80,7 @@ struct Eight {
         uint32_t u[8];
         if (__any(inv == 0.f)) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(nearest(get(e), s) + kMagic);
+            for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(fminf(fmaxf(nearest(get(e), s), -127.f), 127.f) + kMagic);  // a scale of few bits may be far below its value
         } else {
             const float half = 0.5f * s;
             float rest[8], far = 0.f;
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_int_quantize(const T *
             for (int c = 0; c < NC; ++c) v[c].forget();
         }
         const bool bad = top >= 0x7f800000u;
-        const float s = __uint_as_float(top) / 127.f, inv = s > 0x1p-100f && !bad ? __builtin_amdgcn_rcpf(s) : 0.f;
+        const float s = __uint_as_float(top) * (1.f / 127.f), inv = s > 0x1p-100f && !bad ? __builtin_amdgcn_rcpf(s) : 0.f;
         const bool zero = bad || s == 0.f;
         int8_t *o = q + (in ? r : 0) * dim;
         if constexpr (NC > 0) {

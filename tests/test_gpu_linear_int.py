@@ -26,9 +26,9 @@ def _t(name):
 def _codes(x):
     x = x.float().cpu().numpy().astype(np.float32)
     top = np.abs(x).max(-1)
-    scale = (top / np.float32(127)).astype(np.float32)
+    scale = (top * np.float32(1 / 127)).astype(np.float32)
     q = np.rint(x.astype(np.float64) / np.where(scale > 0, scale, 1).astype(np.float64)[..., None])
-    return np.where(scale[..., None] > 0, q, 0), scale
+    return np.where(scale[..., None] > 0, np.clip(q, -127, 127), 0), scale
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -48,6 +48,19 @@ def test_codes_are_exact(ssd, rows, dim, dtype):
     want, scale = _codes(x)
     assert np.array_equal(s.cpu().numpy(), scale)
     assert np.array_equal(q.cpu().numpy().astype(np.float64), want)
+
+
+def test_codes_of_scales_of_few_bits(ssd):
+    """The largest value is k 2^-149, and its scale rounded to 1, 2, 3 of those: a quotient of up to 190 stays 127."""
+    import torch
+    tops = np.array([1, 63, 64, 100, 190, 191, 317, 318, 400, 5000], np.int64)
+    bits = np.stack([tops, tops // 2, np.zeros_like(tops)], 1).astype(np.int32)
+    bits[:, 1] |= np.int32(-2 ** 31)
+    x = torch.from_numpy(bits).cuda().view(torch.float32)
+    q, s = ssd.ssd_int_quantize(x)
+    torch.cuda.synchronize()
+    want, scale = _codes(x)
+    assert np.array_equal(s.cpu().numpy(), scale) and np.array_equal(q.cpu().numpy().astype(np.float64), want)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
