@@ -206,7 +206,7 @@ static int64_t embed_list(const ssd::EmbedPlan &p, int64_t rows) { return align2
 
 size_t ssd_embedding_bwd_workspace_bytes(int64_t rows, int64_t vocab, int64_t dim) {
     if (check_embed(rows, vocab, dim) != SSD_OK) return (size_t)-1;
-    const ssd::EmbedPlan p = ssd::embed_plan(rows, vocab);
+    const ssd::EmbedPlan p = ssd::embed_plan(rows, vocab, dim);
     return (size_t)(embed_list(p, rows) + align256(p.pieces * 2 * dim * 4));
 }
 
@@ -220,7 +220,7 @@ ssd_status ssd_embedding_bwd(const void *dy, const int32_t *tokens, float scale,
     if (misaligned((const char *)dy, (const char *)tokens, (const char *)dtable)) return SSD_ERR_ALIGN;
     if ((st = check_workspace((int64_t)ssd_embedding_bwd_workspace_bytes(rows, vocab, dim), workspace, workspace_bytes)) != SSD_OK) return st;
     if (any_overlap({{dtable, vocab * dim * esize(dtype)}}, {{dy, rows * dim * esize(dy_dtype)}, {tokens, rows * 4}})) return SSD_ERR_UNSUPPORTED;
-    const ssd::EmbedPlan p = ssd::embed_plan(rows, vocab);
+    const ssd::EmbedPlan p = ssd::embed_plan(rows, vocab, dim);
     char *ws = static_cast<char *>(workspace);
     ssd::EmbedBwdArgs a = {};
     a.dy = dy; a.dtable = dtable; a.part = reinterpret_cast<float *>(ws + embed_list(p, rows)); a.rows = rows; a.vocab = (int)vocab;

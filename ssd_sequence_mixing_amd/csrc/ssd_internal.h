@@ -313,7 +313,7 @@ struct EmbedPlan {
     int len;                     // rows of a piece of sums
     int64_t pieces;
 };
-EmbedPlan embed_plan(int64_t rows, int64_t vocab);
+EmbedPlan embed_plan(int64_t rows, int64_t vocab, int64_t dim);
 struct EmbedBwdArgs {
     const void *dy;              // (rows, dim)
     void *dtable;                // (vocab, dim)
