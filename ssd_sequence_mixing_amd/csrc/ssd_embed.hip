@@ -8,7 +8,7 @@
 //
 // k_sort: a work-group sorts up to 4096 tokens in LDS (stable, by digits of at
 // most 9 bits). More tokens are merged, 8 sorted pieces at a time, each value
-// finding its place by binary search (k_merge). Other work-groups of these launches clear the table
+// finding its place by binary search (k_merge_lds, then k_merge). Other work-groups of these launches clear the table
 // meanwhile, each launch a share of it. k_sums: a wavefront adds
 // the rows of `len` places of the sorted list, 256 channels of them; a token whose
 // rows lie within writes its sum to the table, the first and the last one's may go on
