@@ -150,6 +150,19 @@ struct Tokens {
 
 // v where keep is all ones, 0 where it is 0, whatever v.
 __device__ __forceinline__ float masked(float v, uint32_t keep) { return __uint_as_float(__float_as_uint(v) & keep); }
+// A piece's decay where a reset lies in it: -0, which no product of decays is. It stays that whatever the piece's other
+// decays are: a plain product with one that is undefined or infinite would not be zero, and would let in what a reset leaves out.
+constexpr uint32_t kMark = 0x80000000u;
+__device__ __forceinline__ bool marked(float a) { return __float_as_uint(a) == kMark; }
+// a where open is all ones, the mark where it is 0; and the decay of two pieces, one after the other
+template <bool RESET>
+__device__ __forceinline__ float mark(float a, uint32_t open) {
+    return RESET ? __uint_as_float((__float_as_uint(a) & open) | (kMark & ~open)) : a;
+}
+template <bool RESET>
+__device__ __forceinline__ float join(float a, float b) {
+    return RESET && (marked(a) || marked(b)) ? __uint_as_float(kMark) : a * b;
+}
 // A state passed through a piece: decay a, own state h. RESET: a is 0 where one lies in the piece, and then what
 // enters may be anything.
 template <bool RESET>

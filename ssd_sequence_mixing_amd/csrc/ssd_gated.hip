@@ -81,8 +81,10 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 6 : 2) voi
     const uint32_t next = way.ask(a);
 
     float h[R][V], p[R][V];
+    uint32_t open = ~0u;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r) {
+        open &= keep(r);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             // (behind the last token these are of no use, and of no harm: nobody takes what follows it)
@@ -91,8 +93,9 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 6 : 2) voi
             if constexpr (IN) v *= sigmoid_of<kFine>(in[r].get(e));
             const float u = q.c * v;
             h[r][e] = r ? __builtin_fmaf(q.a, cut<RESET>(h[r ? r - 1 : 0][e], keep(r)), u) : u;
-            p[r][e] = cut<RESET>(r ? p[r ? r - 1 : 0][e] * q.a : q.a, keep(r));
+            p[r][e] = mark<RESET>(r ? p[r ? r - 1 : 0][e] * q.a : q.a, open);
         }
+    }
 #pragma unroll
     for (int e = 0; e < V; ++e) ga[g][j * V + e] = p[R - 1][e], gh[g][j * V + e] = h[R - 1][e];
     __builtin_amdgcn_wave_barrier();
@@ -102,7 +105,7 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 6 : 2) voi
     for (int k = 0; k < GPW; ++k) {
         const float q = ga[w * GPW + k][lane];
         ph = pass<RESET>(q, gh[w * GPW + k][lane], ph);
-        pa *= q;
+        pa = join<RESET>(pa, q);
     }
     wa[w][lane] = pa;
     wh[w][lane] = ph;
@@ -119,7 +122,7 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 6 : 2) voi
 #pragma unroll
         for (int k = 0; k < kGatedWaves; ++k) {
             chunk_h = pass<RESET>(wa[k][lane], wh[k][lane], chunk_h);
-            ca *= wa[k][lane];
+            ca = join<RESET>(ca, wa[k][lane]);
         }
         publish(a->pieces + words + tile.chunk * stride + lane, ca, chunk_h);
         entering.look(a->pieces + words, a->ends + words, stride, lane, tile.chunk);
@@ -146,7 +149,7 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 6 : 2) voi
     }
     __builtin_amdgcn_wave_barrier();
     const Tokens<T> py(a->y, row0, D, g * R, d);
-    uint32_t open = ~0u;
+    open = ~0u;
     float from[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) from[e] = gh[g][j * V + e];

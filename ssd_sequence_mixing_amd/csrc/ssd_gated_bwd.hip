@@ -33,7 +33,7 @@ __device__ __forceinline__ void get(const float *p, float (&v)[N]) {
 // and input gates (353 MB): 115 us, 119 with the words' clearing and the rates' sums (3.0 TB/s). No kernel here spills: with
 // 18 to 60 registers spilled it took 170 to 190.
 template <typename T, int DECAY, bool IN, bool RESET, int V>
-__global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) void k_gated_bwd(GatedArgs) {
+__global__ __launch_bounds__(kGatedThreads, V > 1 && (sizeof(T) == 2 || !IN) ? 4 : 2) void k_gated_bwd(GatedArgs) {
     Args a = args();
     using S = Shape<T, V>;
     constexpr int R = S::R, LPR = S::LPR, GPW = S::GPW;
@@ -107,11 +107,14 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) voi
                 dec[r][e] = dec_r;
                 c[r][e] = q.c;
                 h = r ? __builtin_fmaf(dec_r, cut<RESET>(h, keep[r]), q.c * v) : q.c * v;
-                p = cut<RESET>(r ? p * dec_r : dec_r, keep[r]);
+                p = r ? p * dec_r : dec_r;
             }
 #pragma unroll
             for (int r = R - 1; r >= 0; --r) back = cut<RESET>(dec[r][e] * (dy[r].get(e) + back), keep[r]);
-            ps[k] = p;
+            uint32_t open = keep[0];
+#pragma unroll
+            for (int r = 1; r < R; ++r) open &= keep[r];
+            ps[k] = mark<RESET>(p, open);
             hs[k] = h;
             backs[k] = back;
             if (k & 1) __builtin_amdgcn_sched_barrier(0);
@@ -127,7 +130,7 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) voi
     for (int k = 0; k < GPW; ++k) {
         const float q = ga[w * GPW + k][lane];
         ph = pass<RESET>(q, gh[w * GPW + k][lane], ph);
-        pa *= q;
+        pa = join<RESET>(pa, q);
     }
 #pragma unroll
     for (int k = GPW - 1; k >= 0; --k) pg = pass<RESET>(ga[w * GPW + k][lane], gg[w * GPW + k][lane], pg);
@@ -145,7 +148,7 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 4 : 2) voi
 #pragma unroll
         for (int k = kGatedWaves - 1; k >= 0; --k) {
             cg = pass<RESET>(wa[k][lane], wg[k][lane], cg);
-            ca *= wa[k][lane];
+            ca = join<RESET>(ca, wa[k][lane]);
         }
         if (a->nchunks > 1) {
             const int64_t stride = (int64_t)a->cols * kCols, words = tile.b * a->nchunks * stride + c0;
