@@ -163,11 +163,11 @@ template <bool RESET>
 __device__ __forceinline__ float join(float a, float b) {
     return RESET && (marked(a) || marked(b)) ? __uint_as_float(kMark) : a * b;
 }
-// A state passed through a piece: decay a, own state h. RESET: a is 0 where one lies in the piece, and then what
-// enters may be anything.
+// A state passed through a piece: decay a, own state h. Where a is the mark, what enters may be anything; decays
+// that underflow are no reset, and an undefined state goes on through them.
 template <bool RESET>
 __device__ __forceinline__ float pass(float a, float h, float in) {
-    return RESET && a == 0.f ? h : __builtin_fmaf(a, in, h);
+    return RESET && marked(a) ? h : __builtin_fmaf(a, in, h);
 }
 template <bool RESET>
 __device__ __forceinline__ float cut(float v, uint32_t keep) { return RESET ? masked(v, keep) : v; }
