@@ -16,7 +16,7 @@ __device__ __forceinline__ float exp_of(float x) {
     const float y = x * kLog2e, e = fast_exp2(y);
     if constexpr (!kFine) return e;
     float rest = __builtin_fmaf(x, kLog2e, -y) + x * 1.925963033e-8f;
-    rest = fmaxf(rest, -1.f);  // x infinite: not a number until here
+    rest = fminf(fmaxf(rest, -1.f), 1.f);  // e is 0 or infinite where it is larger, or (x infinite) not a number
     return e * __builtin_fmaf(kLn2, rest, 1.f);
 }
 
