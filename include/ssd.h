@@ -690,7 +690,7 @@ ssd_status ssd_logits_process(const void *logits, void *out, const int32_t *toke
  *
  *   xq (rows, in), wq (out, in)  int8;  xscale (rows), wscale (out)  float32
  *   residual, y (rows, out)  dtype (bf16 or fp32);  others as ssd_linear
- * The sum over k is exact (32-bit integers) and rounded to fp32 once (split sums: once for each of up to 32 parts). in a
+ * The sum over k is exact (32-bit integers) and rounded to fp32 once. in a
  * multiple of 16, at most 131072; rows at most 2^24, out at most 2^20. (Any codes: only 131072 products of -128 and
  * -128, which the quantiser does not write, add up to 2^31, and wrap.)
  *

@@ -282,10 +282,12 @@ __device__ __forceinline__ void column_scales4(const LinearArgs &a, int n, float
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = n + i < a.N ? a.ws[n + i] : 0.f;
 }
+__device__ __forceinline__ float scaled(float bits, float xs, float ws) { return (float)__float_as_int(bits) * xs * ws; }
 __device__ __forceinline__ void scale4(float xs, const float (&ws)[4], float (&v)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = (float)__float_as_int(v[i]) * xs * ws[i];
+    for (int i = 0; i < 4; ++i) v[i] = scaled(v[i], xs, ws[i]);
 }
+__device__ __forceinline__ float add_bits(float a, float b) { return __int_as_float(__float_as_int(a) + __float_as_int(b)); }
 template <int KIND>
 __device__ __forceinline__ void scale4_any(const LinearArgs &a, int m, int n, float (&v)[4]) {
     if constexpr (KIND == kInt) {
@@ -631,7 +633,6 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
                 float v[4];
                 staged(p, v);
                 const int m = mw + i * 16 + row_of(p), n = nw + col_of(p);
-                scale4_any<KIND>(a, m, n, v);
                 if (m < a.M && n < a.N) put4<float>(a.part + blockIdx.y * part_stride(a.M, a.N) + (int64_t)m * a.N + n, v, a.N - n, whole);
             }
             __builtin_amdgcn_wave_barrier();
@@ -704,7 +705,8 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void k_tile(LinearA
 
 // The splits' parts of y, added in order, and the epilogue. y, the residual,
 // z and a part are each one run of M N values, of which a thread takes 4; a
-// part's stride is a multiple of 4. INT: a name of its own in each of the two builds of this file.
+// part's stride is a multiple of 4. INT: the parts are integers, whose sum the row's and the column's scale then
+// multiply, and a name of its own in each of the two builds of this file.
 template <bool INT, typename TO>
 __global__ __launch_bounds__(256) void k_join(LinearArgs a) {
     const int64_t total = (int64_t)a.M * a.N, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
@@ -717,13 +719,15 @@ __global__ __launch_bounds__(256) void k_join(LinearArgs a) {
     for (int s = 0; s < a.splits; ++s, p += step) {
         const f32x4 c = *reinterpret_cast<const f32x4 *>(p);  // behind the last value: the stride's rest
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += c[e];
+        for (int e = 0; e < 4; ++e) v[e] = INT ? add_bits(v[e], c[e]) : v[e] + c[e];
     }
-    int n = (int)(i % a.N);
+    int64_t m = i / a.N;
+    int n = (int)(i - m * a.N);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
+        if (INT && e < left) v[e] = scaled(v[e], a.xs[m], a.ws[n]);
         if (a.bias && e < left) v[e] += a.bias[n];
-        n = n + 1 < a.N ? n + 1 : 0;
+        if (++n == a.N) n = 0, ++m;
         z[e] = v[e];
     }
     if (a.pre) put4<TO>(reinterpret_cast<TO *>(a.pre) + i, z, left, left == 4);
@@ -849,10 +853,7 @@ __global__ __launch_bounds__(512) void k_skinny(LinearArgs a) {
             for (int k = 0; k < 8; ++k) {
                 const f32x4 q = *reinterpret_cast<const f32x4 *>(red[k][lane]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (KIND == kInt) v[e] = __int_as_float(__float_as_int(v[e]) + __float_as_int(q[e]));
-                    else v[e] += q[e];
-                }
+                for (int e = 0; e < 4; ++e) v[e] = KIND == kInt ? add_bits(v[e], q[e]) : v[e] + q[e];
             }
             scale4_any<KIND>(a, r, n0 + c * 16 + kg * 4, v);
             finish4_any<TO>(a, r, n0 + c * 16 + kg * 4, v);
