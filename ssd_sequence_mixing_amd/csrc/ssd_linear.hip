@@ -282,10 +282,21 @@ __device__ __forceinline__ void column_scales4(const LinearArgs &a, int n, float
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = n + i < a.N ? a.ws[n + i] : 0.f;
 }
-__device__ __forceinline__ float scaled(float bits, float xs, float ws) { return (float)__float_as_int(bits) * xs * ws; }
+// The sum goes by the row's scale first, but where that may be beyond 2^127: sums are at most 2^31, so what is infinite then
+// is so with both scales (and nothing is lost below: the product of an integer and a number has its places).
+__device__ __forceinline__ bool far(float xs) { return fabsf(xs) > 0x1p96f; }
+__device__ __forceinline__ float scaled(float bits, float xs, float ws) {
+    return (float)__float_as_int(bits) * (far(xs) ? ws : xs) * (far(xs) ? xs : ws);
+}
+// A branch: to choose value by value took 3% longer (8192 x 2048 x 8512: 162 us, 168 so).
 __device__ __forceinline__ void scale4(float xs, const float (&ws)[4], float (&v)[4]) {
+    if (__builtin_expect(__any(far(xs)), 0)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = scaled(v[i], xs, ws[i]);
+        for (int i = 0; i < 4; ++i) v[i] = scaled(v[i], xs, ws[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = (float)__float_as_int(v[i]) * xs * ws[i];
+    }
 }
 __device__ __forceinline__ float add_bits(float a, float b) { return __int_as_float(__float_as_int(a) + __float_as_int(b)); }
 template <int KIND>
