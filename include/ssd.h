@@ -673,7 +673,8 @@ ssd_status ssd_embedding_bwd(const void *dy, const int32_t *tokens, float scale,
  *                         count for nothing
  *   lengths, prompt (rows)  int32 or NULL: how much of a row's history there is (NULL: capacity; clamped to
  *                         [0, capacity]), and how much of that is its prompt (NULL: 0)
- *   repetition, presence, frequency (rows)  float32 or NULL (1, 0, 0); repetition > 0
+ *   repetition, presence, frequency (rows)  float32 or NULL (1, 0, 0); repetition > 0 (l / repetition is l times
+ *                         the number nearest to 1 / repetition, where that is a normal one)
  *   bias (bias_rows, vocab)  float32 or NULL;  mask (mask_rows, ceil(vocab / 32))  int32 or NULL;
  *                         bias_rows, mask_rows: 1 (for all rows) or rows
  * vocab at most 2^28, capacity below 2^31, and rows * ceil((vocab + 7) / 2048) below 2^24.
