@@ -582,16 +582,20 @@ ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, int act,
  *                   from one token to the next, dim to 2^22, tokens of one sequence behind the last
  *                   one's (the parts of one projection's output need no copies); aligned to their type only
  *   rate (dim)      float32, with SSD_DECAY_RATE (else NULL)
- *   reset (batch, seqlen)  uint8 or NULL: where it is not 0, h_{t-1} is left out (a document
- *                   begins; several laid end to end)
+ *   reset (batch, seqlen)  uint8 or NULL: where it is not 0, h_{t-1} is left out, whatever it is (a document
+ *                   begins; several laid end to end). c_t stays: models in which a document's first
+ *                   input is not weighted by sqrt(1 - a^2) are not expressed by this
  *   initial_state (batch, dim)  float32 or NULL (zero)
  *   y (batch, seqlen, dim)  dtype    output, contiguous
  *   final_state (batch, dim)  float32, or NULL: h of the last token (initial_state, or zero, with seqlen == 0)
  *   states (batch, ceil(seqlen / SSD_GATED_CHUNK), dim)  float32, or NULL: h before
  *                   the first token of each SSD_GATED_CHUNK, for the backward pass
  *
- * Everything in fp32: gates and decays within 2^-22 of themselves for ordinary gates (|f|, |i| to 8; beyond, |f| 2^-24
- * with bf16 tensors), a sigmoid below 2^-126 is 0 or 2^-126. The same inputs give the same bits. dim at most 2^20, seqlen
+ * Everything in fp32. In steps of 2^-24 of the value, e^f is within 4, sigmoid(f) within s = 7 and 1 - sigmoid(f)
+ * within 14; with a rate, a is within 2 + (s + 2.3) |log a| and c within s / 2 + 14. With bf16 tensors e^f is
+ * within 2 + 1.3 |f| instead, and s = 5 + 1.3 |f| (1 - sigmoid(f): twice that), but for ssd_gated_step. A sigmoid below 2^-126 is
+ * 0 or 2^-126. An infinite state becomes undefined where its decays underflow to zero within a chunk. The same inputs
+ * give the same bits. dim at most 2^20, seqlen
  * and batch * dim below 2^31, and batch * ceil(dim / 64) * ceil(seqlen / 128) at most 2^23 - 1. An
  * output that overlaps an input is refused (SSD_ERR_UNSUPPORTED). The
  * workspace is 256-byte aligned; the query returns (size_t)-1 for a shape that is not supported. Work-groups exchange
@@ -618,7 +622,7 @@ ssd_status ssd_gated_scan_fwd(const void *x, int64_t ldx, const void *f, int64_t
  *   x ... reset: as the forward had them; states: as it wrote them (with initial_state in the first)
  *   dy (batch, seqlen, dim) dtype;  d_final_state (batch, dim) float32 or NULL (zero)
  *   dx, df, d_in_gate (batch, seqlen, dim) dtype  outputs, contiguous; d_in_gate exactly where in_gate is
- *   drate (dim) float32  output with SSD_DECAY_RATE (else NULL), summed in a fixed order
+ *   drate (dim) float32  output with SSD_DECAY_RATE (else NULL), summed in a fixed order; of a positive rate that at 0
  *   d_initial_state (batch, dim) float32  output, or NULL
  * With batch or seqlen 0, drate = 0 and d_initial_state = d_final_state (or zero).
  */
