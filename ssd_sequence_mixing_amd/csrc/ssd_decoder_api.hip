@@ -60,7 +60,7 @@ ssd_status check_gated(int64_t batch, int64_t seqlen, int64_t dim, int decay, in
     if (!valid_dtype(dtype) || decay < SSD_DECAY_LOG || decay > SSD_DECAY_RATE) return SSD_ERR_UNSUPPORTED;
     if (batch < 0 || seqlen < 0 || dim <= 0) return SSD_ERR_SHAPE;
     if (dim > kMostDim || seqlen > INT32_MAX || batch > INT32_MAX / dim) return SSD_ERR_UNSUPPORTED;
-    return ssd::gated_plan(batch, seqlen, dim, (ssd_dtype)dtype).fits ? SSD_OK : SSD_ERR_UNSUPPORTED;
+    return ssd::gated_plan(batch, seqlen, dim, (ssd_dtype)dtype, false).fits ? SSD_OK : SSD_ERR_UNSUPPORTED;
 }
 
 // The inputs of a recurrence, `rows` tokens of them: present, far enough apart, aligned to their type.
@@ -82,7 +82,7 @@ extern "C" {
 
 size_t ssd_gated_scan_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, ssd_dtype dtype) {
     if (check_gated(batch, seqlen, dim, SSD_DECAY_LOG, (int)dtype) != SSD_OK) return (size_t)-1;
-    return (size_t)ssd::gated_plan(batch, seqlen, dim, dtype).word_bytes;
+    return (size_t)ssd::gated_plan(batch, seqlen, dim, dtype, false).word_bytes;
 }
 
 ssd_status ssd_gated_scan_fwd(const void *x, int64_t ldx, const void *f, int64_t ldf, const void *in_gate, int64_t ldi,
@@ -99,7 +99,7 @@ ssd_status ssd_gated_scan_fwd(const void *x, int64_t ldx, const void *f, int64_t
     if (misaligned((const char *)y, (const char *)rate, (const char *)reset, (const char *)initial_state,
                    (const char *)final_state, (const char *)states))
         return SSD_ERR_ALIGN;
-    const ssd::GatedPlan plan = ssd::gated_plan(batch, seqlen, dim, dtype);
+    const ssd::GatedPlan plan = ssd::gated_plan(batch, seqlen, dim, dtype, false);
     if ((st = check_workspace(plan.word_bytes, workspace, workspace_bytes)) != SSD_OK) return st;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const int64_t nb = batch * dim * 4;
@@ -117,7 +117,7 @@ ssd_status ssd_gated_scan_fwd(const void *x, int64_t ldx, const void *f, int64_t
 
 size_t ssd_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int decay, ssd_dtype dtype) {
     if (check_gated(batch, seqlen, dim, decay, (int)dtype) != SSD_OK) return (size_t)-1;
-    const ssd::GatedPlan p = ssd::gated_plan(batch, seqlen, dim, dtype);
+    const ssd::GatedPlan p = ssd::gated_plan(batch, seqlen, dim, dtype, true);
     return (size_t)(p.word_bytes + (decay == SSD_DECAY_RATE ? p.rate_bytes : 0));
 }
 
@@ -137,7 +137,7 @@ ssd_status ssd_gated_scan_bwd(const void *dy, const void *x, int64_t ldx, const 
     if (misaligned((const char *)dy, (const char *)rate, (const char *)reset, (const char *)states, (const char *)d_final_state,
                    (const char *)dx, (const char *)df, (const char *)d_in_gate, (const char *)drate, (const char *)d_initial_state))
         return SSD_ERR_ALIGN;
-    const ssd::GatedPlan plan = ssd::gated_plan(batch, seqlen, dim, dtype);
+    const ssd::GatedPlan plan = ssd::gated_plan(batch, seqlen, dim, dtype, true);
     const int64_t need = plan.word_bytes + (has_rate ? plan.rate_bytes : 0);
     if ((st = check_workspace(need, workspace, workspace_bytes)) != SSD_OK) return st;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);

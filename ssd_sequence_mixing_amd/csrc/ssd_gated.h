@@ -175,8 +175,8 @@ __device__ __forceinline__ float cut(float v, uint32_t keep) { return RESET ? ma
 // ---------------------------------------------------------------------------
 // Handing states on. Work-groups take their chunks by ticket, those of all sequences and columns before the
 // next ones along the sequence, so a chunk's predecessors belong to work-groups that have begun whenever it does, and
-// that wait for earlier chunks only: every wait ends. A ticket is for several chunks in this order, one after the
-// other: tickets are given out one each 13 ns, which for 4096 chunks would be as long as reading them. Each publishes its chunk's
+// that wait for earlier chunks only: every wait ends. Tickets are given out one each 13 ns, as long as a small tile takes the
+// memory; where tiles are so small a ticket is for two of a chunk, one after the other. Each publishes its chunk's
 // (a, h), waits for the state kWindow chunks back, and passes it through the (a, h) of
 // those between, always in this order: the same inputs give the same bits. A word is published once, by one
 // store that nothing else has to be ordered with, into memory that k_gated_clear has filled with ones,

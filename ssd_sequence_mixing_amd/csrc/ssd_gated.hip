@@ -190,7 +190,7 @@ __global__ __launch_bounds__(kThreads) void k_gated_step(GatedStepArgs a) {
     reinterpret_cast<T *>(a.y)[k] = (T)h;
 }
 
-GatedPlan gated_plan(int64_t batch, int64_t T, int64_t D, ssd_dtype) {
+GatedPlan gated_plan(int64_t batch, int64_t T, int64_t D, ssd_dtype dtype, bool backward) {
     GatedPlan p = {};
     p.cols = (D + kCols - 1) / kCols;
     p.nchunks = (T + SSD_GATED_CHUNK - 1) / SSD_GATED_CHUNK;
@@ -198,9 +198,13 @@ GatedPlan gated_plan(int64_t batch, int64_t T, int64_t D, ssd_dtype) {
     p.fits = batch == 0 || T == 0 || (batch <= most / p.cols && batch * p.cols <= most / p.nchunks);
     if (!p.fits) return p;
     p.tiles = batch * p.cols * p.nchunks;
-    // tiles of a ticket: of two neighbouring columns where there are many, never of two chunks (a ticket that ended one
-    // chunk and began the next would have each chunk wait for a second tile of the one before)
-    p.share = p.nchunks > 1 && p.tiles > 4096 ? 2 : 1;
+    // Tiles of a ticket: two of neighbouring columns where a tile takes the memory no longer than a ticket takes (13 ns): the
+    // forward pass's in 16 bits, of 48 or 64 KB (with one, and with two: 2048 x 1536 20.3 and 18.3 us, 4 x 2048 x 4096 75 and
+    // 72, 16384 x 4096 without input gates 124 and 105). Those in fp32 and the gradients' are larger (4 x 2048 x 4096 in fp32 107 and
+    // 114, gradients in bf16 143 and 151), and below 384 tiles two in a row take a chunk longer than the tickets of two (2 x 8192 x
+    // 64 18 and 22). Never of two chunks: a ticket that ended one and began the next would have each chunk wait for a second tile
+    // of the one before.
+    p.share = p.nchunks > 1 && !backward && dtype == SSD_BF16 && p.tiles >= 384 ? 2 : 1;
     const int64_t tickets = (batch * p.cols + p.share - 1) / p.share * p.nchunks;
     p.groups = p.nchunks > 1 && tickets > 768 ? 768 : tickets;  // 3 for each CU
     // the ticket, then a chunk's (a, h) and its end for each column

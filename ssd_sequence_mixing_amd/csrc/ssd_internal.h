@@ -284,11 +284,11 @@ struct GatedArgs {
 struct GatedPlan {
     bool fits;
     int64_t cols, nchunks, tiles;  // pieces of 64 channels, chunks, and chunks of all sequences and columns
-    int64_t share, groups;         // chunks of a work-group, and work-groups
+    int64_t share, groups;         // a chunk's tiles of a ticket, and work-groups
     int64_t word_bytes;            // workspace of either pass
     int64_t rate_bytes;            // the backward's, behind that, for the rates' gradient
 };
-GatedPlan gated_plan(int64_t batch, int64_t T, int64_t D, ssd_dtype dtype);
+GatedPlan gated_plan(int64_t batch, int64_t T, int64_t D, ssd_dtype dtype, bool backward);
 ssd_status launch_gated_fwd(GatedArgs a, const GatedPlan &p, ssd_dtype dtype, int decay, void *workspace, hipStream_t s);
 ssd_status launch_gated_bwd(GatedArgs a, const GatedPlan &p, ssd_dtype dtype, int decay, void *workspace, hipStream_t s);
 struct GatedStepArgs {
