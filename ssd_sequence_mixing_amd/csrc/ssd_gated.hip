@@ -21,9 +21,9 @@ __global__ __launch_bounds__(256) void k_gated_clear(u32x4 *words, int64_t n16) 
         words[i] = i < 16 ? u32x4{0, 0, 0, 0} : u32x4{~0u, ~0u, ~0u, ~0u};
 }
 
-// What bounds it: 3 work-groups share a CU, whose vector unit is busy 60% of the time; a tile's way is its loads, the walk, two
-// exchanges through LDS and one look at the chunks before. 4 x 2048 x 4096 in bf16, rates and input gates (268 MB): 72 us,
-// 75 with the words' clearing (3.6 TB/s); 16384 x 4096 with resets (403 MB) 99 us together. With the next tile's loads under the
+// What bounds it: 3 work-groups share a CU, whose vector unit is busy 56 to 67% of the time; a tile's way is its loads, the walk, two
+// exchanges through LDS and one look at the chunks before. 4 x 2048 x 4096 in bf16, rates and input gates (268 MB): 69 us,
+// 72 with the words' clearing (3.7 TB/s); 16384 x 4096 with resets (403 MB) 99 us together. With the next tile's loads under the
 // exchange, at 2 work-groups a CU, they took 77 and 110 where this took 75 and 102.
 template <typename T, int DECAY, bool IN, bool RESET, int V>
 __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 6 : 2) void k_gated_fwd(GatedArgs) {

@@ -29,9 +29,10 @@ __device__ __forceinline__ void get(const float *p, float (&v)[N]) {
 }
 
 // What bounds it: the vector unit is busy 61% of the time (some 85 operations a value, 11 of them transcendental) and
-// the registers leave 2 work-groups a CU, so that a tile's loads, walks and exchanges overlap little. 8 x 2048 x 1536 in bf16, rates
-// and input gates (353 MB): 115 us, 119 with the words' clearing and the rates' sums (3.0 TB/s). No kernel here spills: with
-// 18 to 60 registers spilled it took 170 to 190.
+// the registers leave 2 work-groups a CU, so that a tile's loads, walks and exchanges overlap little. In fp32 with input gates, decays
+// from sigmoids or rates leave 1 (140 to 152 registers). 8 x 2048 x 1536 in bf16, rates
+// and input gates (353 MB): 115 us, 119 with the words' clearing and the rates' sums (3.0 TB/s); in fp32 177. No kernel here spills
+// vector registers: with 18 to 60 of them spilled it took 170 to 190. (V = 1 spills 14 to 68 scalar ones.)
 template <typename T, int DECAY, bool IN, bool RESET, int V>
 __global__ __launch_bounds__(kGatedThreads, V > 1 && (sizeof(T) == 2 || !IN) ? 4 : 2) void k_gated_bwd(GatedArgs) {
     Args a = args();
