@@ -583,7 +583,7 @@ ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, int act,
  *                   one's (the parts of one projection's output need no copies); aligned to their type only
  *   rate (dim)      float32, with SSD_DECAY_RATE (else NULL)
  *   reset (batch, seqlen)  uint8 or NULL: where it is not 0, h_{t-1} is left out, whatever it is (a document
- *                   begins; several laid end to end). c_t stays: models in which a document's first
+ *                   begins; several laid end to end), and a_t with it. c_t stays: models in which a document's first
  *                   input is not weighted by sqrt(1 - a^2) are not expressed by this
  *   initial_state (batch, dim)  float32 or NULL (zero)
  *   y (batch, seqlen, dim)  dtype    output, contiguous

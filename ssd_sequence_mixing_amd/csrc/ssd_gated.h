@@ -9,6 +9,9 @@
 
 namespace ssd {
 
+// v where keep is all ones, 0 where it is 0, whatever v.
+__device__ __forceinline__ float masked(float v, uint32_t keep) { return __uint_as_float(__float_as_uint(v) & keep); }
+
 // e^x. kFine (fp32): x log2 e in two parts, since the rounding of the first is 2^-24 of it, some 1e-6 of the
 // result far from zero; within 2^-22 of itself. Else that rounding stays: |x| 2^-24 of the result.
 template <bool kFine>
@@ -52,6 +55,12 @@ __device__ __forceinline__ float one_minus_square(float y, float e) {
 struct Decay {
     float a, c;
 };
+// At a reset (keep 0) nothing passes the decay, whatever the gate. (Of sigmoids and rates c goes by the gate too, and the
+// token is undefined where that is.)
+template <int DECAY, bool RESET>
+__device__ __forceinline__ Decay passed(Decay q, uint32_t keep) {
+    return {RESET && DECAY == SSD_DECAY_LOG ? masked(q.a, keep) : q.a, q.c};
+}
 template <int DECAY, bool kFine>
 __device__ __forceinline__ Decay decay_of(float f, float rate2) {
     if constexpr (DECAY == SSD_DECAY_LOG) return {exp_of<kFine>(f), 1.f};
@@ -148,8 +157,6 @@ struct Tokens {
     __device__ __forceinline__ T *out(int r) const { return const_cast<T *>((*this)[r]); }
 };
 
-// v where keep is all ones, 0 where it is 0, whatever v.
-__device__ __forceinline__ float masked(float v, uint32_t keep) { return __uint_as_float(__float_as_uint(v) & keep); }
 // A piece's decay where a reset lies in it: -0, which no product of decays is. It stays that whatever the piece's other
 // decays are: a plain product with one that is undefined or infinite would not be zero, and would let in what a reset leaves out.
 constexpr uint32_t kMark = 0x80000000u;

@@ -88,7 +88,7 @@ __global__ __launch_bounds__(kGatedThreads, sizeof(T) == 2 && V > 1 ? 6 : 2) voi
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             // (behind the last token these are of no use, and of no harm: nobody takes what follows it)
-            const Decay q = decay_of<DECAY, kFine>(f[r].get(e), rate[e]);
+            const Decay q = passed<DECAY, RESET>(decay_of<DECAY, kFine>(f[r].get(e), rate[e]), keep(r));
             float v = x[r].get(e);
             if constexpr (IN) v *= sigmoid_of<kFine>(in[r].get(e));
             const float u = q.c * v;

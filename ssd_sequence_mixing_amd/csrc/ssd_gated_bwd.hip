@@ -100,7 +100,7 @@ __global__ __launch_bounds__(kGatedThreads, V > 1 && (sizeof(T) == 2 || !IN) ? 4
             float h = 0.f, p = 1.f, back = 0.f;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const Decay q = decay_of<DECAY, kFine>(f[r].get(e), rate2);
+                const Decay q = passed<DECAY, RESET>(decay_of<DECAY, kFine>(f[r].get(e), rate2), keep[r]);
                 float v = x[r].get(e);
                 if constexpr (IN) v *= sigmoid_of<kFine>(in[r].get(e));
                 // tokens behind the last one, with x and dy zero, hand G on as it is
